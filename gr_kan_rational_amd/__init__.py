@@ -1,8 +1,9 @@
 """MI355X-native GR-KAN (Group-Rational KAN) safe Pade activation.
 
 The compute path is the HIP library ``libgrkan.so`` (hand-written gfx950
-kernels behind a C ABI declared in ``include/grkan.h``); the names below are
-its thin Python binding.  Importing this package loads nothing: the library
+kernels behind a C ABI declared in ``include/grkan.h`` and, for the operators
+around the activation in a transformer block, ``include/grkan_block.h``); the
+names below are its thin Python binding.  Importing this package loads nothing: the library
 is loaded on first use and a missing or unloadable library raises.
 """
 __all__ = [
@@ -20,9 +21,19 @@ __all__ = [
     "grkan_pau_supported",
     "load_library",
 ]
+_BLOCK = [
+    "grkan_group_norm_forward",
+    "grkan_group_norm_backward",
+    "GRKANGroupNorm",
+]
+__all__ += _BLOCK
 
 
 def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+
+        return getattr(block, name)
     if name in __all__:
         from . import binding
 

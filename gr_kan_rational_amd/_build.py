@@ -46,6 +46,11 @@ def units() -> list[tuple[str, list[str], str]]:
            ("grkan_layer.hip", [], "grkan_layer.o"),
            ("grkan_probe.hip", [], "grkan_probe.o"),
            ("grkan_naive.hip", ["-mllvm", "-amdgpu-atomic-optimizer-strategy=None"], "grkan_naive.o")]
+    out.append(("grkan_block_api.hip", [], "grkan_block_api.o"))
+    for bf16 in (0, 1):
+        for backward in (0, 1):
+            out.append(("grkan_norm.hip", [f"-DGRKAN_NORM_BF16={bf16}", f"-DGRKAN_NORM_BACKWARD={backward}"],
+                        f"grkan_norm_{bf16}_{backward}.o"))
     for m, n in degree_pairs():
         out.append(("grkan_kernels.hip", [f"-DGRKAN_M={m}", f"-DGRKAN_N={n}"], f"grkan_kernels_{m}_{n}.o"))
     return out

@@ -1,0 +1,389 @@
+// grkan_block_api.hip -- the C ABI of include/grkan_block.h: argument
+// validation, plans and dispatch.  Plans depend on shapes, types and the
+// activation alone, so results have the same bits on every device.
+#include <limits.h>
+#include <stdint.h>
+
+#include "grkan_block.h"
+#include "grkan_launch.h"
+#include "grkan_norm.h"
+
+using namespace grkan;
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A byte range an argument covers; empty if absent.
+struct Range {
+    const void *p;
+    size_t n;
+};
+
+bool overlap(const Range &a, const Range &b) {
+    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.n && y < x + a.n;
+}
+
+// Every output apart from every other argument.
+bool outputs_overlap(const Range *outs, int no, const Range *ins, int ni) {
+    for (int i = 0; i < no; ++i) {
+        for (int j = 0; j < ni; ++j)
+            if (overlap(outs[i], ins[j])) return true;
+        for (int j = i + 1; j < no; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+grkan_status_t from_hip(hipError_t e) { return e == hipSuccess ? GRKAN_OK : GRKAN_ERR_HIP; }
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+__global__ __launch_bounds__(256) void grkan_norm_empty_kernel(float *mean, float *rstd, int64_t n, float value) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    mean[i] = 0.0f;
+    rstd[i] = value;
+}
+
+// Statistics of samples without positions.
+hipError_t launch_norm_empty(const NormArgs &a, hipStream_t s) {
+    const int64_t n = a.N * a.G;
+    hipLaunchKernelGGL(grkan_norm_empty_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.mean, a.rstd, n,
+                       1.0f / sqrtf(a.eps));
+    return hipGetLastError();
+}
+
+int io_bytes(grkan_dtype_t io) { return io == GRKAN_BF16 ? 2 : 4; }
+
+bool act_valid(grkan_act_t act) {
+    return act == GRKAN_ACT_NONE || act == GRKAN_ACT_SILU || act == GRKAN_ACT_GELU || act == GRKAN_ACT_RATIONAL;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int pow2_at_most(int64_t v) {
+    int p = 1;
+    while (2 * (int64_t)p <= v) p *= 2;
+    return p;
+}
+
+// ------------------------------------------------------------ norm plans
+
+constexpr int kTokenMaxLanes = 512, kTokenMaxAccesses = 4;
+constexpr int64_t kNormWorkgroups = 2048;  // target of the looping kernels: 8 workgroups a CU
+
+// The elements of one access: 16 bytes, unless a group's segment wastes more
+// than an eighth of its lanes on ragged accesses, or an access would straddle
+// two activation groups (which would need two sets of coefficients).
+int norm_vec(int64_t D, int64_t dga, bool rational, int es) {
+    for (int v = 16 / es; v > 1; v /= 2) {
+        if (D % v != 0 && D < 8 * (int64_t)v) continue;
+        if (rational && !((D % v == 0 && dga % v == 0) || dga % D == 0)) continue;
+        return v;
+    }
+    return 1;
+}
+
+void norm_columns(NormPlan *p, int64_t G, int threads) {
+    if (p->vpg <= threads) {
+        p->bpg = 1;
+        if (p->gpb > G) p->gpb = (int32_t)G;
+        p->TX = p->gpb * p->vpg;
+        p->ncb = (int32_t)ceil_div(G, p->gpb);
+    } else {
+        p->gpb = 1;
+        p->bpg = (int32_t)ceil_div(p->vpg, threads);
+        p->TX = (int32_t)ceil_div(p->vpg, p->bpg);
+        p->ncb = (int32_t)(G * p->bpg);
+    }
+}
+
+grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng, grkan_act_t act, grkan_dtype_t io,
+                         bool backward, NormPlan *p) {
+    if (io != GRKAN_F32 && io != GRKAN_BF16) return GRKAN_ERR_INVALID_ARG;
+    if (!act_valid(act)) return GRKAN_ERR_INVALID_ARG;
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    if (N < 0 || S < 0 || C < 1 || G < 1 || C % G != 0) return GRKAN_ERR_INVALID_ARG;
+    if (rational && (ng < 1 || C % ng != 0)) return GRKAN_ERR_INVALID_ARG;
+    if (C >= (1 << 24) || S > INT32_MAX) return GRKAN_ERR_UNSUPPORTED;
+    if (N > INT32_MAX / G) return GRKAN_ERR_UNSUPPORTED;
+    const int es = io_bytes(io);
+    const int64_t D = C / G;
+    *p = NormPlan{};
+    p->vec = norm_vec(D, rational ? C / ng : 1, rational, es);
+    p->vpg = (int32_t)ceil_div(D, p->vec);
+    p->cv = (int64_t)G * p->vpg;
+    if (N == 0 || S == 0) return GRKAN_OK;
+
+    const int64_t row_values = norm_partial_row(*p, C, rational);
+    if (S == 1 && p->vpg <= kTokenMaxLanes * kTokenMaxAccesses) {
+        p->kind = kNormToken;
+        // The fewest lane places (T lanes x K accesses) that hold the group,
+        // then the fewest accesses a lane.
+        int64_t best = INT64_MAX;
+        for (int K = 1; K <= kTokenMaxAccesses; ++K) {
+            int T = 1;
+            while ((int64_t)T * K < p->vpg) T *= 2;
+            if (T > kTokenMaxLanes) continue;
+            if ((int64_t)T * K < best) best = (int64_t)T * K, p->T = T, p->K = K;
+        }
+        int spw = p->T < 256 && p->T <= 64 ? 256 / p->T : 1;
+        while (spw % G != 0 && G % spw != 0) --spw;
+        p->spw = spw;
+        p->block = spw * p->T;
+        const int64_t unit = spw < G ? G / spw : 1;  // workgroups that cover one sample
+        int64_t blocks = ceil_div(N * G, spw);
+        const int64_t cap = backward ? kNormWorkgroups / 2 : kNormWorkgroups;
+        if (blocks > cap) blocks = cap;
+        p->blocks = ceil_div(blocks, unit) * unit;
+        p->prows = spw > G ? p->blocks : p->blocks * spw / G;
+        p->lds = (size_t)p->block * 13 * 4 + 256;
+    } else {
+        // A slab: whole groups side by side until their segments make 64
+        // bytes or more of every row and the rows a lane has to hold allow.
+        const int threads = backward ? 512 : 1024, regs = backward ? 8 : 16;
+        const int64_t seg = D * es;
+        int64_t gpb = ceil_div(64, seg);
+        if (gpb > G) gpb = G;
+        const bool fits = S > 1 && (int64_t)p->vpg * gpb <= threads && S <= (threads / (p->vpg * gpb)) * regs;
+        if (fits) {
+            p->kind = kNormSlab;
+            // wider blocks while many workgroups remain and segments are short
+            while (gpb * 2 <= G && (int64_t)p->vpg * gpb * 2 <= 64 && gpb * seg < 256 &&
+                   S <= (threads / (p->vpg * gpb * 2)) * regs && N * ceil_div(G, gpb * 2) >= kNormWorkgroups)
+                gpb *= 2;
+            p->gpb = (int32_t)gpb;
+            norm_columns(p, G, threads);
+            // the fewest row lanes that hold S rows in the registers a lane has
+            // (more of them while a workgroup stays within 256 threads)
+            int64_t ty = ceil_div(S, regs);
+            const int64_t wide = 256 / p->TX;
+            if (ty < wide) ty = wide < S ? wide : S;
+            p->TY = (int32_t)ty;
+            p->regs = (int32_t)ceil_div(S, ty);
+            p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
+            if (!backward) {
+                p->blocks = (N >= 8 ? ceil_div(N, 8) * 8 : N) * p->ncb;
+            } else {
+                int64_t chunks = kNormWorkgroups / p->ncb;
+                if (chunks < 1) chunks = 1;
+                if (chunks > N) chunks = N;
+                if (chunks >= 8) chunks = chunks / 8 * 8;
+                p->chunks = chunks;
+                p->blocks = chunks * p->ncb;
+                p->prows = chunks;
+            }
+        } else {
+            p->kind = kNormSplit;
+            const int threads2 = 256;
+            gpb = threads2 / (p->vpg < threads2 ? p->vpg : threads2);
+            p->gpb = (int32_t)(gpb < 1 ? 1 : gpb);
+            norm_columns(p, G, threads2);
+            int64_t ty = threads2 / p->TX;
+            if (ty > S) ty = S;
+            p->TY = (int32_t)ty;
+            p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
+            // chunks of at least 4 rows a lane
+            int64_t chunks = ceil_div(kNormWorkgroups, N * p->ncb);
+            const int64_t most = ceil_div(S, 4 * ty);
+            if (chunks > most) chunks = most;
+            p->chunk_rows = ceil_div(S, chunks);
+            p->chunks = ceil_div(S, p->chunk_rows);
+            p->blocks = N * p->chunks * p->ncb;
+            p->prows = N * p->chunks;
+        }
+        p->L = pow2_at_most(p->block / p->gpb < 64 ? p->block / p->gpb : 64);
+        const size_t vals = p->kind == kNormSplit ? 2 * sizeof(double) : 2 * sizeof(float);
+        p->lds = vals * ((size_t)p->block + p->gpb);
+        if (backward && p->lds < (size_t)p->block * 13 * 4) p->lds = (size_t)p->block * 13 * 4;
+    }
+    size_t at = 0;
+    if (p->kind == kNormSplit) {
+        p->off_stats = at;
+        at += align256((size_t)N * G * p->chunks * p->bpg * 16);
+        p->off_means = at;
+        if (backward) at += align256((size_t)N * G * 8);
+    }
+    p->off_partials = at;
+    if (backward) at += align256((size_t)p->prows * row_values * 4);
+    p->total = at;
+    return GRKAN_OK;
+}
+
+// Elements from the first to the last of a strided [N][S][C] tensor, or -1 if
+// that does not fit an address.
+int64_t span(int64_t N, int64_t S, int64_t C, int64_t sample, int64_t row) {
+    if (N == 0 || S == 0) return 0;
+    __int128 v = (__int128)(N - 1) * sample + (__int128)(S - 1) * row + C;
+    return v > INT64_MAX / 8 ? -1 : (int64_t)v;
+}
+
+grkan_status_t strides_ok(int64_t N, int64_t S, int64_t C, int64_t sample, int64_t row) {
+    if (row < C || sample < 0) return GRKAN_ERR_INVALID_ARG;
+    if (span(N, S, C, sample, row) < 0) return GRKAN_ERR_INVALID_ARG;
+    return GRKAN_OK;
+}
+
+bool dense(int64_t N, int64_t S, int64_t C, int64_t sample, int64_t row) {
+    return (row == C || S <= 1) && (sample == S * C || N <= 1);
+}
+
+// What both directions check of the coefficients.
+grkan_status_t coefs_ok(const float *A, const float *B, grkan_act_t act) {
+    if (act != GRKAN_ACT_RATIONAL) return A || B ? GRKAN_ERR_INVALID_ARG : GRKAN_OK;
+    if (!A || !B) return GRKAN_ERR_INVALID_ARG;
+    return aligned(A, 4) && aligned(B, 4) ? GRKAN_OK : GRKAN_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" size_t grkan_group_norm_forward_workspace_size(int64_t samples, int64_t positions, int64_t channels,
+                                                          int32_t norm_groups, int32_t n_groups, grkan_act_t act,
+                                                          grkan_dtype_t io) {
+    NormPlan p;
+    return norm_plan(samples, positions, channels, norm_groups, n_groups, act, io, false, &p) == GRKAN_OK ? p.total
+                                                                                                          : 0;
+}
+
+extern "C" size_t grkan_group_norm_backward_workspace_size(int64_t samples, int64_t positions, int64_t channels,
+                                                           int32_t norm_groups, int32_t n_groups, grkan_act_t act,
+                                                           grkan_dtype_t io) {
+    NormPlan p;
+    return norm_plan(samples, positions, channels, norm_groups, n_groups, act, io, true, &p) == GRKAN_OK ? p.total
+                                                                                                         : 0;
+}
+
+extern "C" grkan_status_t grkan_group_norm_forward(const void *x, void *y, float *mean, float *rstd,
+                                                   const float *weight, const float *bias, const float *A,
+                                                   const float *B, int64_t samples, int64_t positions,
+                                                   int64_t channels, int64_t x_sample, int64_t x_row,
+                                                   int32_t norm_groups, int32_t n_groups, float eps, grkan_act_t act,
+                                                   grkan_dtype_t io, void *workspace, size_t workspace_bytes,
+                                                   hipStream_t stream) {
+    NormArgs a{};
+    grkan_status_t st = norm_plan(samples, positions, channels, norm_groups, n_groups, act, io, false, &a.p);
+    if (st != GRKAN_OK) return st;
+    if (!(eps > 0.0f) || eps > 3.0e38f) return GRKAN_ERR_INVALID_ARG;
+    if ((st = coefs_ok(A, B, act)) != GRKAN_OK) return st;
+    if ((st = strides_ok(samples, positions, channels, x_sample, x_row)) != GRKAN_OK) return st;
+    const int es = io_bytes(io);
+    if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(x, es) ||
+        !aligned(y, es))
+        return GRKAN_ERR_UNSUPPORTED;
+    if (samples == 0) return GRKAN_OK;
+    if (!mean || !rstd) return GRKAN_ERR_INVALID_ARG;
+    if (positions > 0 && (!x || !y)) return GRKAN_ERR_INVALID_ARG;
+    const size_t sg = (size_t)samples * norm_groups * 4;
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    const Range rx{x, (size_t)span(samples, positions, channels, x_sample, x_row) * es};
+    const Range ry{y, (size_t)samples * positions * channels * es};
+    const Range ins[] = {{weight, (size_t)channels * 4}, {bias, (size_t)channels * 4},
+                         {A, rational ? (size_t)n_groups * 24 : 0}, {B, rational ? (size_t)n_groups * 16 : 0}, rx};
+    const Range outs[] = {{mean, sg}, {rstd, sg}, {workspace, a.p.total}, ry};
+    const bool in_place = x == y && dense(samples, positions, channels, x_sample, x_row);
+    if (outputs_overlap(outs, 3, ins, 5) || outputs_overlap(outs, 4, ins, 4) || (!in_place && overlap(rx, ry)))
+        return GRKAN_ERR_INVALID_ARG;
+    if (a.p.total && (!workspace || workspace_bytes < a.p.total)) return GRKAN_ERR_INVALID_ARG;
+    if (a.p.total && !aligned(workspace, 256)) return GRKAN_ERR_UNSUPPORTED;
+    // ---- validation done; HIP calls from here on
+    a.x = x;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.w = weight;
+    a.b = bias;
+    a.A = A;
+    a.B = B;
+    a.N = samples;
+    a.S = positions;
+    a.xs = x_sample;
+    a.xr = x_row;
+    a.C = (int32_t)channels;
+    a.G = norm_groups;
+    a.D = (int32_t)(channels / norm_groups);
+    a.ng = n_groups;
+    a.dga = rational ? (int32_t)(channels / n_groups) : 1;
+    a.act = act;
+    a.eps = eps;
+    if (positions == 0) return from_hip(launch_norm_empty(a, stream));
+    a.stats = reinterpret_cast<double *>(static_cast<char *>(workspace) + a.p.off_stats);
+    return from_hip(io == GRKAN_BF16 ? launch_norm_forward<bf16io>(a, stream) : launch_norm_forward<float>(a, stream));
+}
+
+extern "C" grkan_status_t grkan_group_norm_backward(
+    const void *x, const void *dy, const float *mean, const float *rstd, const float *weight, const float *bias,
+    const float *A, const float *B, void *dx, float *dweight, float *dbias, float *dA, float *dB, int64_t samples,
+    int64_t positions, int64_t channels, int64_t x_sample, int64_t x_row, int64_t dy_sample, int64_t dy_row,
+    int32_t norm_groups, int32_t n_groups, grkan_act_t act, grkan_dtype_t io, void *workspace,
+    size_t workspace_bytes, hipStream_t stream) {
+    NormArgs a{};
+    grkan_status_t st = norm_plan(samples, positions, channels, norm_groups, n_groups, act, io, true, &a.p);
+    if (st != GRKAN_OK) return st;
+    if ((st = coefs_ok(A, B, act)) != GRKAN_OK) return st;
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    if (rational ? (!dA || !dB) : (dA || dB)) return GRKAN_ERR_INVALID_ARG;
+    if ((st = strides_ok(samples, positions, channels, x_sample, x_row)) != GRKAN_OK) return st;
+    if ((st = strides_ok(samples, positions, channels, dy_sample, dy_row)) != GRKAN_OK) return st;
+    const int es = io_bytes(io);
+    if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
+        !aligned(dbias, 4) || !aligned(dA, 4) || !aligned(dB, 4) || !aligned(x, es) || !aligned(dy, es) ||
+        !aligned(dx, es))
+        return GRKAN_ERR_UNSUPPORTED;
+    const bool empty = samples == 0 || positions == 0;
+    if (!empty && (!x || !dy || !dx || !mean || !rstd)) return GRKAN_ERR_INVALID_ARG;
+    const size_t sg = (size_t)samples * norm_groups * 4, cb = (size_t)channels * 4;
+    const size_t ab = rational ? (size_t)n_groups * 24 : 0, bb = rational ? (size_t)n_groups * 16 : 0;
+    const Range rx{x, (size_t)span(samples, positions, channels, x_sample, x_row) * es};
+    const Range rdy{dy, (size_t)span(samples, positions, channels, dy_sample, dy_row) * es};
+    const Range rdx{dx, (size_t)samples * positions * channels * es};
+    const Range ins[] = {{mean, sg}, {rstd, sg}, {weight, cb}, {bias, cb}, {A, ab}, {B, bb}, rx, rdy};
+    const Range outs[] = {{dweight, cb}, {dbias, cb}, {dA, ab}, {dB, bb}, {workspace, a.p.total}, rdx};
+    if (outputs_overlap(outs, 5, ins, 8) || outputs_overlap(outs, 6, ins, 6)) return GRKAN_ERR_INVALID_ARG;
+    const bool on_x = dx == x && dense(samples, positions, channels, x_sample, x_row);
+    const bool on_dy = dx == dy && dense(samples, positions, channels, dy_sample, dy_row);
+    if ((!on_x && overlap(rdx, rx)) || (!on_dy && overlap(rdx, rdy))) return GRKAN_ERR_INVALID_ARG;
+    if (a.p.total && (!workspace || workspace_bytes < a.p.total)) return GRKAN_ERR_INVALID_ARG;
+    if (a.p.total && !aligned(workspace, 256)) return GRKAN_ERR_UNSUPPORTED;
+    // ---- validation done; HIP calls from here on
+    a.x = x;
+    a.dy = dy;
+    a.y = dx;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.w = weight;
+    a.b = bias;
+    a.A = A;
+    a.B = B;
+    a.dw = dweight;
+    a.db = dbias;
+    a.dA = dA;
+    a.dB = dB;
+    a.N = samples;
+    a.S = positions;
+    a.xs = x_sample;
+    a.xr = x_row;
+    a.ds = dy_sample;
+    a.dr = dy_row;
+    a.C = (int32_t)channels;
+    a.G = norm_groups;
+    a.D = (int32_t)(channels / norm_groups);
+    a.ng = n_groups;
+    a.dga = rational ? (int32_t)(channels / n_groups) : 1;
+    a.act = act;
+    if (empty) {
+        hipError_t e = hipSuccess;
+        if (dweight) e = launch_zero(dweight, dweight, channels, 0, stream);
+        if (e == hipSuccess && dbias) e = launch_zero(dbias, dbias, channels, 0, stream);
+        if (e == hipSuccess && rational) e = launch_zero(dA, dB, (int64_t)n_groups * 6, (int64_t)n_groups * 4, stream);
+        return from_hip(e);
+    }
+    char *ws = static_cast<char *>(workspace);
+    a.stats = reinterpret_cast<double *>(ws + a.p.off_stats);
+    a.means = reinterpret_cast<float *>(ws + a.p.off_means);
+    a.partials = reinterpret_cast<float *>(ws + a.p.off_partials);
+    return from_hip(io == GRKAN_BF16 ? launch_norm_backward<bf16io>(a, stream)
+                                     : launch_norm_backward<float>(a, stream));
+}
