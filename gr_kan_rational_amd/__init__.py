@@ -25,6 +25,9 @@ _BLOCK = [
     "grkan_group_norm_forward",
     "grkan_group_norm_backward",
     "GRKANGroupNorm",
+    "grkan_linear_act_forward",
+    "grkan_linear_act_backward",
+    "GRKANLinearAct",
 ]
 __all__ += _BLOCK
 

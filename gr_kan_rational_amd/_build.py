@@ -51,6 +51,8 @@ def units() -> list[tuple[str, list[str], str]]:
         for backward in (0, 1):
             out.append(("grkan_norm.hip", [f"-DGRKAN_NORM_BF16={bf16}", f"-DGRKAN_NORM_BACKWARD={backward}"],
                         f"grkan_norm_{bf16}_{backward}.o"))
+    for al in (0, 1):
+        out.append(("grkan_linear.hip", [f"-DGRKAN_LINEAR_ALIGNED={al}"], f"grkan_linear_{al}.o"))
     for m, n in degree_pairs():
         out.append(("grkan_kernels.hip", [f"-DGRKAN_M={m}", f"-DGRKAN_N={n}"], f"grkan_kernels_{m}_{n}.o"))
     return out

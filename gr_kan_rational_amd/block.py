@@ -1,5 +1,6 @@
 """Thin Python binding of the block operators of libgrkan.so (C ABI in include/grkan_block.h):
-the group norm with an activation, channels last, and their autograd wrappers.
+the group norm with an activation, channels last, the linear map with bias, activation and residual in
+its epilogue, and their autograd wrappers.
 
 Argument marshalling only, as in binding.py: shapes, strides and pointers are
 checked and handed over; every step of the computation is a HIP kernel.
@@ -36,6 +37,14 @@ def _library() -> ctypes.CDLL:
     for name in ("forward", "backward"):
         size = getattr(lib, f"grkan_group_norm_{name}_workspace_size")
         size.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+        size.restype = sz
+    lib.grkan_linear_act_forward.argtypes = [vp] * 8 + [i64] * 5 + [i32, i32, vp, sz, vp]
+    lib.grkan_linear_act_forward.restype = ctypes.c_int
+    lib.grkan_linear_act_backward.argtypes = [vp] * 11 + [i64] * 5 + [i32, i32, vp, sz, vp]
+    lib.grkan_linear_act_backward.restype = ctypes.c_int
+    for name in ("forward", "backward"):
+        size = getattr(lib, f"grkan_linear_act_{name}_workspace_size")
+        size.argtypes = [i64, i64, i64, i32, i32]
         size.restype = sz
     _lib = lib
     return lib
@@ -210,6 +219,130 @@ def _coef_grads(code: int, dA, dB, n_groups: int, dev):
     return dA, dB
 
 
+def _rows(t: torch.Tensor, name: str, dev):
+    """(rows, width, row stride) of a bf16 tensor [..., width] whose rows are equally spaced."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must be [..., width]")
+    w = t.shape[-1]
+    rows = 1
+    for k in t.shape[:-1]:
+        rows *= k
+    if t.is_contiguous():
+        return rows, w, w
+    if w > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    row, run = None, 0
+    for k in range(t.dim() - 2, -1, -1):
+        if t.shape[k] == 1:
+            continue
+        if row is None:
+            row = t.stride(k)
+        elif t.stride(k) != run:
+            raise ValueError(f"the rows of {name} must be equally spaced")
+        run = t.stride(k) * t.shape[k]
+    if row is None:
+        row = w
+    if row < w:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return rows, w, row
+
+
+def _linear_dims(x: torch.Tensor, W: torch.Tensor):
+    _on_gpu(x)
+    dev = x.device
+    rows, d_in, ldx = _rows(x, "x", dev)
+    if W.dtype != torch.bfloat16:
+        raise TypeError(f"W must be bfloat16, got {W.dtype}")
+    if W.dim() != 2 or not W.is_contiguous() or W.device != dev or W.shape[1] != d_in:
+        raise ValueError(f"W must be a contiguous [d_out, {d_in}] tensor on {dev}")
+    return rows, d_in, W.shape[0], ldx, dev
+
+
+def grkan_linear_act_forward(x: torch.Tensor, W: torch.Tensor, bias=None, act: str = "none", A=None, B=None,
+                             n_groups: int = 8, residual=None, keep: bool = False, out=None, pre=None,
+                             workspace=None, stream=None):
+    """(z, pre): z = act(x W^T + bias) + residual (``grkan_linear_act_forward``).
+
+    bf16 x [..., d_in] and residual [..., d_out] with equally spaced rows, W [d_out, d_in]; float32 bias
+    [d_out].  ``pre`` is the bf16 product before the activation, for the backward, if ``keep`` (or a tensor
+    for it) is given, else None."""
+    code = _act(act)
+    rows, d_in, d_out, ldx, dev = _linear_dims(x, W)
+    _channel_vector(bias, "bias", d_out, dev)
+    A, B, ng = _act_coefs(code, A, B, n_groups, d_out, dev)
+    shape = (*x.shape[:-1], d_out)
+    ldr = 0
+    if residual is not None:
+        if residual.shape != shape:
+            raise ValueError(f"residual must be {list(shape)}")
+        ldr = _rows(residual, "residual", dev)[2]
+    lib = _library()
+    with _scope(stream, dev):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _check_out(out, "out", torch.bfloat16, rows * d_out, dev)
+        if pre is None and keep:
+            pre = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        if pre is not None:
+            _check_out(pre, "pre", torch.bfloat16, rows * d_out, dev)
+        need = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, ng, code)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wsp, wsn = _workspace(workspace, dev)
+        st = lib.grkan_linear_act_forward(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(A), _ptr(B), _ptr(out),
+                                          _ptr(pre), rows, d_in, d_out, ldx, ldr, ng, code, wsp, wsn,
+                                          _stream(stream))
+    if st != GRKAN_OK:
+        raise GRKANError(st, "grkan_linear_act_forward")
+    return out, pre
+
+
+def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor, pre=None, act: str = "none",
+                              A=None, B=None, n_groups: int = 8, dx=None, dW=None, dbias=None, dA=None, dB=None,
+                              workspace=None, stream=None):
+    """(dx, dW, dbias, dA, dB) of ``grkan_linear_act_forward`` from its pre (not needed for act "none")
+    (``grkan_linear_act_backward``): bf16 dx and dW, float32 dbias; dA and dB None but for the rational.
+    The residual's gradient is dz."""
+    code = _act(act)
+    rows, d_in, d_out, ldx, dev = _linear_dims(x, W)
+    if dz.shape != (*x.shape[:-1], d_out):
+        raise ValueError(f"dz must be {[*x.shape[:-1], d_out]}")
+    lddz = _rows(dz, "dz", dev)[2]
+    if code == GRKAN_ACT_NONE:
+        pre = None
+    elif pre is None:
+        raise ValueError("the backward of an activation needs the forward's pre")
+    else:
+        _check_out(pre, "pre", torch.bfloat16, rows * d_out, dev)
+    A, B, ng = _act_coefs(code, A, B, n_groups, d_out, dev)
+    lib = _library()
+    with _scope(stream, dev):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        _check_out(dx, "dx", torch.bfloat16, rows * d_in, dev)
+        if dW is None:
+            dW = torch.empty((d_out, d_in), dtype=torch.bfloat16, device=dev)
+        _check_out(dW, "dW", torch.bfloat16, d_out * d_in, dev)
+        if dbias is None:
+            dbias = torch.empty(d_out, dtype=torch.float32, device=dev)
+        _check_out(dbias, "dbias", torch.float32, d_out, dev)
+        dA, dB = _coef_grads(code, dA, dB, ng, dev)
+        need = lib.grkan_linear_act_backward_workspace_size(rows, d_in, d_out, ng, code)
+        if need and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wsp, wsn = _workspace(workspace, dev)
+        st = lib.grkan_linear_act_backward(_ptr(x), _ptr(W), _ptr(dz), _ptr(pre), _ptr(A), _ptr(B), _ptr(dx),
+                                           _ptr(dW), _ptr(dbias), _ptr(dA), _ptr(dB), rows, d_in, d_out, ldx, lddz,
+                                           ng, code, wsp, wsn, _stream(stream))
+    if st != GRKAN_OK:
+        raise GRKANError(st, "grkan_linear_act_backward")
+    return dx, dW, dbias, dA, dB
+
+
 class GRKANGroupNorm(torch.autograd.Function):
     """Autograd wrapper: y = act(group norm of x), ``apply(x, norm_groups, weight, bias, eps, act, A, B,
     n_groups)``."""
@@ -229,3 +362,23 @@ class GRKANGroupNorm(torch.autograd.Function):
                                                        act, A, B, n_groups)
         return (dx, None, None if weight is None else dw.view_as(weight), None if bias is None else db.view_as(bias),
                 None, None, None if dA is None else dA.view_as(A), None if dB is None else dB.view_as(B), None)
+
+
+class GRKANLinearAct(torch.autograd.Function):
+    """Autograd wrapper: z = act(x W^T + bias) + residual, ``apply(x, W, bias, act, A, B, n_groups, residual)``."""
+
+    @staticmethod
+    def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, residual=None):
+        z, pre = grkan_linear_act_forward(x, W, bias, act, A, B, n_groups, residual, keep=act != "none")
+        ctx.save_for_backward(x, W, bias, A, B, pre)
+        ctx.args = act, n_groups, residual is not None
+        return z
+
+    @staticmethod
+    def backward(ctx, dz):
+        x, W, bias, A, B, pre = ctx.saved_tensors
+        act, n_groups, residual = ctx.args
+        dz = dz.contiguous()
+        dx, dW, db, dA, dB = grkan_linear_act_backward(x, W, dz, pre, act, A, B, n_groups)
+        return (dx, dW, None if bias is None else db.view_as(bias), None, None if dA is None else dA.view_as(A),
+                None if dB is None else dB.view_as(B), None, dz if residual else None)

@@ -6,6 +6,7 @@
 
 #include "grkan_block.h"
 #include "grkan_launch.h"
+#include "grkan_linear.h"
 #include "grkan_norm.h"
 
 using namespace grkan;
@@ -386,4 +387,208 @@ extern "C" grkan_status_t grkan_group_norm_backward(
     a.partials = reinterpret_cast<float *>(ws + a.p.off_partials);
     return from_hip(io == GRKAN_BF16 ? launch_norm_backward<bf16io>(a, stream)
                                      : launch_norm_backward<float>(a, stream));
+}
+
+// ------------------------------------------------------------ linear map
+
+namespace {
+
+constexpr int64_t kMaxWidth = int64_t(1) << 22;
+
+grkan_status_t linear_shape(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act) {
+    if (!act_valid(act) || rows < 0 || d_in < 1 || d_out < 1) return GRKAN_ERR_INVALID_ARG;
+    if (act == GRKAN_ACT_RATIONAL && (n_groups < 1 || d_out % n_groups != 0)) return GRKAN_ERR_INVALID_ARG;
+    if (rows > INT32_MAX || d_in > kMaxWidth || d_out > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
+    // one thread per 8 elements of a result, one launch
+    if (rows * ceil_div(d_out, 8) >= (int64_t(1) << 32) || rows * ceil_div(d_in, 8) >= (int64_t(1) << 32) ||
+        d_in * ceil_div(d_out, 8) >= (int64_t(1) << 32))
+        return GRKAN_ERR_UNSUPPORTED;
+    return GRKAN_OK;
+}
+
+bool chunks_aligned(const void *p, int64_t ld, int64_t width) {
+    return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;
+}
+
+int64_t act_group(int64_t d_out, int32_t n_groups, grkan_act_t act) {
+    return act == GRKAN_ACT_RATIONAL ? d_out / n_groups : 8;
+}
+
+// Plans and workspace do not depend on alignment.
+struct LinearBwdPlan {
+    SlopePlan slope;
+    ProductPlan dx, dw;
+    size_t off_slope, off_sums, total;
+};
+
+void linear_bwd_plan(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act, LinearBwdPlan *p) {
+    p->slope = plan_slope(rows, d_out, act, act_group(d_out, n_groups, act));
+    p->dx = plan_product(kFormDx, rows, d_in, d_out, true, GRKAN_ACT_NONE, 8);
+    p->dw = plan_product(kFormDw, d_out, d_in, rows, true, GRKAN_ACT_NONE, 8);
+    p->off_slope = act == GRKAN_ACT_NONE ? 0 : align256((size_t)rows * d_out * 2);
+    p->off_sums = p->off_slope + align256(p->slope.partials_bytes);
+    const size_t sums = p->dx.partials_bytes > p->dw.partials_bytes ? p->dx.partials_bytes : p->dw.partials_bytes;
+    p->total = p->off_sums + align256(sums);
+}
+
+__global__ __launch_bounds__(256) void grkan_zero16_kernel(uint16_t *p, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
+}  // namespace
+
+extern "C" size_t grkan_linear_act_forward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
+                                                          int32_t n_groups, grkan_act_t act) {
+    if (linear_shape(rows, d_in, d_out, n_groups, act) != GRKAN_OK || rows == 0) return 0;
+    return align256(
+        plan_product(kFormForward, rows, d_out, d_in, true, act, act_group(d_out, n_groups, act)).partials_bytes);
+}
+
+extern "C" grkan_status_t grkan_linear_act_forward(const void *x, const void *W, const float *bias,
+                                                   const void *residual, const float *A, const float *B, void *z,
+                                                   void *pre, int64_t rows, int64_t d_in, int64_t d_out, int64_t ldx,
+                                                   int64_t ldr, int32_t n_groups, grkan_act_t act, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream) {
+    grkan_status_t st = linear_shape(rows, d_in, d_out, n_groups, act);
+    if (st != GRKAN_OK) return st;
+    if (ldx < d_in || (residual && ldr < d_out)) return GRKAN_ERR_INVALID_ARG;
+    if (ldx > kMaxWidth || (residual && ldr > kMaxWidth)) return GRKAN_ERR_UNSUPPORTED;
+    if ((st = coefs_ok(A, B, act)) != GRKAN_OK) return st;
+    if (!W) return GRKAN_ERR_INVALID_ARG;
+    if (!aligned(x, 2) || !aligned(W, 2) || !aligned(residual, 2) || !aligned(z, 2) || !aligned(pre, 2) ||
+        !aligned(bias, 4))
+        return GRKAN_ERR_UNSUPPORTED;
+    if (rows == 0) return GRKAN_OK;
+    if (!x || !z) return GRKAN_ERR_INVALID_ARG;
+    const int64_t dga = act_group(d_out, n_groups, act);
+    const bool al = chunks_aligned(x, ldx, d_in) && chunks_aligned(W, d_in, d_in);
+    const ProductPlan p = plan_product(kFormForward, rows, d_out, d_in, al, act, dga);
+    const size_t need = align256(p.partials_bytes), zb = (size_t)rows * d_out * 2;
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    const Range rr{residual, residual ? (size_t)((rows - 1) * ldr + d_out) * 2 : 0};
+    const Range ins[] = {{x, (size_t)((rows - 1) * ldx + d_in) * 2}, {W, (size_t)d_out * d_in * 2},
+                         {bias, (size_t)d_out * 4}, {A, rational ? (size_t)n_groups * 24 : 0},
+                         {B, rational ? (size_t)n_groups * 16 : 0}, rr};
+    const Range outs[] = {{workspace, need}, {pre, zb}, {z, zb}};
+    const bool in_place = residual == z && ldr == d_out;
+    if (outputs_overlap(outs, 2, ins, 6) || outputs_overlap(outs, 3, ins, 5) || (!in_place && overlap(outs[2], rr)))
+        return GRKAN_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need)) return GRKAN_ERR_INVALID_ARG;
+    if (need && !aligned(workspace, 256)) return GRKAN_ERR_UNSUPPORTED;
+    // ---- validation done; HIP calls from here on
+    ProductArgs a{};
+    a.q = Operand{x, ldx};
+    a.p = Operand{W, d_in};
+    a.M = (int32_t)rows;
+    a.N = (int32_t)d_out;
+    a.K = (int32_t)d_in;
+    a.partials = static_cast<float *>(workspace);
+    a.e = Epilogue{bias, A, B, residual, pre, z, ldr, act, (int32_t)dga};
+    return from_hip(launch_product(kFormForward, p, a, stream));
+}
+
+extern "C" size_t grkan_linear_act_backward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
+                                                           int32_t n_groups, grkan_act_t act) {
+    if (linear_shape(rows, d_in, d_out, n_groups, act) != GRKAN_OK || rows == 0) return 0;
+    LinearBwdPlan p;
+    linear_bwd_plan(rows, d_in, d_out, n_groups, act, &p);
+    return p.total;
+}
+
+extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W, const void *dz, const void *pre,
+                                                    const float *A, const float *B, void *dx, void *dW, float *dbias,
+                                                    float *dA, float *dB, int64_t rows, int64_t d_in, int64_t d_out,
+                                                    int64_t ldx, int64_t lddz, int32_t n_groups, grkan_act_t act,
+                                                    void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    grkan_status_t st = linear_shape(rows, d_in, d_out, n_groups, act);
+    if (st != GRKAN_OK) return st;
+    if (ldx < d_in || lddz < d_out) return GRKAN_ERR_INVALID_ARG;
+    if (ldx > kMaxWidth || lddz > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
+    if ((st = coefs_ok(A, B, act)) != GRKAN_OK) return st;
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    if (rational ? (!dA || !dB) : (dA || dB)) return GRKAN_ERR_INVALID_ARG;
+    if (!aligned(x, 2) || !aligned(W, 2) || !aligned(dz, 2) || !aligned(pre, 2) || !aligned(dx, 2) || !aligned(dW, 2) ||
+        !aligned(dbias, 4) || !aligned(dA, 4) || !aligned(dB, 4))
+        return GRKAN_ERR_UNSUPPORTED;
+    LinearBwdPlan p{};
+    if (rows > 0) {
+        if (!x || !W || !dz || (act != GRKAN_ACT_NONE && !pre)) return GRKAN_ERR_INVALID_ARG;
+        linear_bwd_plan(rows, d_in, d_out, n_groups, act, &p);
+    }
+    const size_t ab = rational ? (size_t)n_groups * 24 : 0, bb = rational ? (size_t)n_groups * 16 : 0;
+    const size_t wb = (size_t)d_out * d_in * 2;
+    const size_t rows1 = rows > 0 ? (size_t)rows - 1 : 0, some = rows > 0;
+    const Range ins[] = {{x, (rows1 * ldx + d_in) * 2 * some}, {W, wb * some}, {dz, (rows1 * lddz + d_out) * 2 * some},
+                         {pre, act == GRKAN_ACT_NONE ? 0 : (size_t)rows * d_out * 2}, {A, ab}, {B, bb}};
+    const Range outs[] = {{dx, (size_t)rows * d_in * 2}, {dW, wb}, {dbias, (size_t)d_out * 4}, {dA, ab}, {dB, bb},
+                          {workspace, p.total}};
+    if (outputs_overlap(outs, 6, ins, 6)) return GRKAN_ERR_INVALID_ARG;
+    if (p.total && (!workspace || workspace_bytes < p.total)) return GRKAN_ERR_INVALID_ARG;
+    if (p.total && !aligned(workspace, 256)) return GRKAN_ERR_UNSUPPORTED;
+    // ---- validation done; HIP calls from here on
+    if (rows == 0) {
+        hipError_t e = hipSuccess;
+        if (dW) {
+            const int64_t n = d_out * d_in;
+            hipLaunchKernelGGL(grkan_zero16_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, stream,
+                               static_cast<uint16_t *>(dW), n);
+            e = hipGetLastError();
+        }
+        if (e == hipSuccess && dbias) e = launch_zero(dbias, dbias, d_out, 0, stream);
+        if (e == hipSuccess && rational) e = launch_zero(dA, dB, (int64_t)n_groups * 6, (int64_t)n_groups * 4, stream);
+        return from_hip(e);
+    }
+    char *ws = static_cast<char *>(workspace);
+    const void *dpre = act == GRKAN_ACT_NONE ? dz : ws;
+    const int64_t ldp = act == GRKAN_ACT_NONE ? lddz : d_out;
+    if (act != GRKAN_ACT_NONE || dbias) {
+        SlopeArgs s{};
+        s.dz = dz;
+        s.pre = pre;
+        s.dpre = ws;
+        s.A = A;
+        s.B = B;
+        s.dbias = dbias;
+        s.dA = dA;
+        s.dB = dB;
+        s.partials = reinterpret_cast<float *>(ws + p.off_slope);
+        s.rows = rows;
+        s.lddz = lddz;
+        s.ldp = ldp;
+        s.N = (int32_t)d_out;
+        s.act = act;
+        s.ng = n_groups;
+        s.dga = (int32_t)act_group(d_out, n_groups, act);
+        s.vec = p.slope.vec;
+        s.vpr = p.slope.vpr;
+        s.chunks = p.slope.chunks;
+        s.chunk_rows = p.slope.chunk_rows;
+        st = from_hip(launch_slope(s, stream));
+        if (st != GRKAN_OK) return st;
+    }
+    const bool q_ok = chunks_aligned(dpre, ldp, d_out);
+    ProductArgs a{};
+    a.partials = reinterpret_cast<float *>(ws + p.off_sums);
+    a.q = Operand{dpre, ldp};
+    if (dx) {
+        p.dx.aligned = q_ok && chunks_aligned(W, d_in, d_in);
+        a.p = Operand{W, d_in};
+        a.M = (int32_t)rows;
+        a.N = (int32_t)d_in;
+        a.K = (int32_t)d_out;
+        a.e.z = dx;
+        st = from_hip(launch_product(kFormDx, p.dx, a, stream));
+        if (st != GRKAN_OK) return st;
+    }
+    if (dW) {
+        p.dw.aligned = q_ok && chunks_aligned(x, ldx, d_in);
+        a.p = Operand{x, ldx};
+        a.M = (int32_t)d_out;
+        a.N = (int32_t)d_in;
+        a.K = (int32_t)rows;
+        a.e.z = dW;
+        return from_hip(launch_product(kFormDw, p.dw, a, stream));
+    }
+    return GRKAN_OK;
 }

@@ -1,0 +1,782 @@
+// grkan_linear.hip -- the linear map z = act(x W^T + b) + r and its gradients
+// on the matrix cores (gfx950): bf16 operands, fp32 sums.
+//
+// Compiled twice: GRKAN_LINEAR_ALIGNED 1 (every 16-byte chunk of the operands
+// aligned and whole) and 0 (any widths, strides and alignment).
+//
+// Bound: many rows, the matrix cores; few rows, the bytes of W.
+//
+// The tile kernel.  A workgroup of 4 waves (2 x 2) forms a BM x BN tile of
+// the result; a wave BM/2 x BN/2 of it in 32 x 32 blocks of
+// v_mfma_f32_32x32x16_bf16.  The instruction's row operand is P (columns of
+// the result) and its column operand Q (rows of the result), so a lane's
+// accumulators run along n within one row of the result, and exchanging them
+// with the lane 32 away leaves 8 consecutive columns in a lane: bias,
+// activation, residual and stores take 16-byte accesses and no LDS.
+// k advances BK at a time through three LDS stages.  While step t is
+// multiplied, the chunks of step t + 2 travel from memory straight into LDS
+// (no registers); one barrier a step, before the step's last group of matrix
+// instructions, whose fragments are already in registers, covers both the
+// arrival of step t + 1 and the release of step t's stage.  Two workgroups
+// fit on a CU, so one's epilogue and barriers overlap the other's products.
+//
+// LDS layouts.  Chunks are 16 bytes and land in the order of the lanes, so
+// bank conflicts are avoided by choosing which chunk a lane fetches:
+//   K contiguous   [row][BK]: chunk c of row r sits at c ^ f(r), f(r) = r mod 8
+//                  for BK = 64 and (r / 2) mod 4 for BK = 32: 8 consecutive
+//                  rows of one chunk column touch 8 different 16-byte banks
+//   K strided      [k][rows]: chunk c of row k sits at c ^ s(k), s = 2 (j + 4 (j
+//                  mod 2)), j = k mod 4 (2 j for 64 rows, whose k rows are half
+//                  as long); fragments are read with the transposing
+//                  ds_read_b64_tr_b16, whose 16 lanes touch rows k..k+3 of 32
+//                  bytes: four different 32-byte banks, and the two groups of
+//                  16 side by side eight different ones
+#include "grkan_linear.h"
+
+#include "grkan_act.h"
+
+namespace grkan {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+constexpr bool kAligned = GRKAN_LINEAR_ALIGNED != 0;
+
+// nv (0..8) elements at p, the rest zeros; p is aligned to an element.
+__device__ static inline u32x4 load8(const uint16_t *p, int nv) {
+    if (nv >= 8) return *reinterpret_cast<const u32x4_any *>(p);
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < nv) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+    return v;
+}
+__device__ static inline void store8(uint16_t *p, int nv, u32x4 v) {
+    if (nv >= 8) {
+        *reinterpret_cast<u32x4_any *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < nv) p[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+}
+
+// ------------------------------------------------------------ epilogue
+
+// RAT: 0 an activation without coefficients, 1 the rational with 8-column
+// chunks inside one activation group, 2 the rational with any groups.
+template <int RAT> struct ChunkParams {
+    float bias[8];
+    Coefs<5, 4> c;
+    int n, nv;
+    __device__ inline void init(const Epilogue &e, int n_, int N) {
+        n = n_;
+        nv = N - n < 8 ? N - n : 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = e.bias && i < nv ? e.bias[n + i] : 0.0f;
+        if constexpr (RAT == 1) c = load_coefs<5, 4>(e.A, e.B, nv > 0 ? n / e.dga : 0);
+    }
+};
+
+// 8 sums of row m, columns n.. -> pre, z.
+template <int RAT>
+__device__ static inline void finish8(float (&h)[8], const Epilogue &e, const ChunkParams<RAT> &k, int64_t m, int N) {
+    if (k.nv <= 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += k.bias[i];
+    const int64_t at = m * N + k.n;
+    if (e.pre) store8(static_cast<uint16_t *>(e.pre) + at, k.nv, Io<bf16io>::pack(h));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (RAT == 2) {
+            if (i < k.nv) h[i] = rational<5, 4>(h[i], load_coefs<5, 4>(e.A, e.B, (k.n + i) / e.dga));
+        } else {
+            h[i] = act_value<RAT == 1>(h[i], e.act, k.c);
+        }
+    }
+    if (e.residual) {
+        float r[8];
+        Io<bf16io>::unpack(load8(static_cast<const uint16_t *>(e.residual) + m * e.ldr + k.n, k.nv), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] += r[i];
+    }
+    store8(static_cast<uint16_t *>(e.z) + at, k.nv, Io<bf16io>::pack(h));
+}
+
+// ------------------------------------------------------------ staging
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer: reads zeros
+constexpr int kThreads = 256;
+
+// One operand's tile of ROWS x BK, as this thread's chunks: chunk id i * 256 +
+// thread, at byte 16 id of its stage.
+template <int ROWS, int BK, bool STRIDED> struct Stager {
+    static constexpr int kChunks = ROWS * BK / 8 / kThreads;
+    static constexpr int kBytes = ROWS * BK * 2;
+    static constexpr int kPerRow = STRIDED ? ROWS / 8 : BK / 8;  // chunks per LDS row
+    static_assert(ROWS * BK / 8 % kThreads == 0 && kThreads % kPerRow == 0, "whole chunks");
+
+    const char *base;    // first row of the tile at its first k
+    int64_t step;        // bytes from one k step to the next
+    int64_t ld;
+    uint32_t off[kChunks];   // byte offset of the chunk from base, or kNowhere
+    int k0;              // K contiguous: k of the chunks; strided: k of chunk 0
+    int valid;           // unaligned: elements of a chunk inside the operand's own range (strided)
+    u32x4 r[kAligned ? 1 : kChunks];
+
+    __device__ static inline int f(int row) { return BK == 64 ? row & 7 : (row >> 1) & 3; }
+    __device__ static inline int s(int k) { return ROWS >= 128 ? 2 * ((k & 3) + 4 * (k & 1)) : 2 * (k & 3); }
+
+    __device__ inline void init(const Operand &o, int row0, int rows, int kstart) {
+        const int t = (int)threadIdx.x;
+        ld = o.ld;
+        const int slot = t % kPerRow, r0 = t / kPerRow;
+        if constexpr (STRIDED) {
+            base = static_cast<const char *>(o.p) + ((int64_t)kstart * ld + row0) * 2;
+            step = (int64_t)BK * ld * 2;
+            k0 = r0;
+            // the rows of a thread's chunks are a multiple of 4 apart, so s() is one value
+            static_assert(kThreads / kPerRow % 4 == 0, "one swizzle per thread");
+            const int c = slot ^ s(r0);
+            valid = min(max(rows - row0 - c * 8, 0), 8);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                off[i] = valid > 0 ? (uint32_t)((r0 + i * (kThreads / kPerRow)) * ld * 2 + c * 16) : kNowhere;
+        } else {
+            base = static_cast<const char *>(o.p) + ((int64_t)row0 * ld + kstart) * 2;
+            step = BK * 2;
+            static_assert(kThreads / kPerRow % 8 == 0, "one swizzle per thread");
+            const int c = slot ^ f(r0);
+            k0 = c * 8;
+            valid = 8;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int row = r0 + i * (kThreads / kPerRow);
+                off[i] = row0 + row < rows ? (uint32_t)(row * ld * 2 + c * 16) : kNowhere;
+            }
+        }
+    }
+
+    // Chunks of step t (k from kt on, `left` of them in this split) into the
+    // stage at LDS byte offset `stage`; past the end zeros.
+    __device__ inline void fetch(char *lds, int stage, int t, int left) {
+        const char *src = base + t * step;
+        if constexpr (kAligned) {
+            __amdgpu_buffer_rsrc_t rsrc =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, 0x7ffffff0, 0x00020000);
+            const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
+                const uint32_t o = k < left ? off[i] : kNowhere;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (__attribute__((address_space(3))) void *)(lds + stage + (i * kThreads + wave * 64) * 16), 16, o,
+                    0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
+                int nv = STRIDED ? (k < left ? valid : 0) : min(max(left - k, 0), 8);
+                if (off[i] == kNowhere) nv = 0;
+                r[i] = load8(reinterpret_cast<const uint16_t *>(src + (nv ? off[i] : 0)), nv);
+            }
+        }
+    }
+    // Unaligned: the fetched chunks into their stage.
+    __device__ inline void put(char *lds, int stage) {
+        if constexpr (!kAligned) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                *reinterpret_cast<u32x4 *>(lds + stage + (i * kThreads + (int)threadIdx.x) * 16) = r[i];
+        }
+    }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Fragments of NB blocks of 32 rows from row `row0` of the tile, k from 16 ks.
+template <int ROWS, int BK, bool STRIDED, int NB> struct Reader {
+    int at[STRIDED ? NB : BK / 16];
+    __device__ inline void init(int row0) {
+        const int lane = (int)threadIdx.x & 63;
+        if constexpr (STRIDED) {
+            const int k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+            const int col = row0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int c = (col + 32 * i) >> 3;
+                at[i] = k * ROWS * 2 + ((c ^ Stager<ROWS, BK, true>::s(k)) << 4) + (col & 4) * 2;
+            }
+        } else {
+            const int row = row0 + (lane & 31);
+#pragma unroll
+            for (int ks = 0; ks < BK / 16; ++ks)
+                at[ks] = row * BK * 2 + (((2 * ks + (lane >> 5)) ^ Stager<ROWS, BK, false>::f(row)) << 4);
+        }
+    }
+    __device__ inline void read(const char *stage, int ks, bf16x8 (&f)[NB]) const {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            if constexpr (STRIDED) {
+                typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+                const char *p = stage + at[i] + ks * 16 * ROWS * 2;
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * ROWS * 2));
+                f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                f[i] = *reinterpret_cast<const bf16x8 *>(stage + at[ks] + i * 32 * BK * 2);
+            }
+        }
+    }
+};
+
+// s_waitcnt vmcnt(n), lgkmcnt(0).
+template <int N> __device__ static inline void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+__device__ static inline void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------ tile kernel
+
+template <int BM, int BN, int BK> struct TileShape {
+    static constexpr int kStage = (BM + BN) * BK * 2;
+    static constexpr size_t kLds = 3 * (size_t)kStage;
+};
+
+// FORM as in ProductForm; PARTIAL: fp32 sums of a split to memory.
+template <int BM, int BN, int BK, int FORM, bool PARTIAL, int RAT>
+__global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr bool QS = FORM == kFormDw, PS = FORM != kFormForward;
+    constexpr int NM = BM / 64, NN = BN / 64;  // 32 x 32 blocks of a wave
+    constexpr int kStage = TileShape<BM, BN, BK>::kStage, kQ = BM * BK * 2;
+    constexpr int KS = BK / 16;
+
+    const int nb = (a.N + BN - 1) / BN, mb = (a.M + BM - 1) / BM;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    // Workgroups go to the 8 XCDs in turn.  Without splits each XCD takes whole
+    // panels of BM rows, column tiles of a panel one after another, so that a
+    // panel of Q stays in one L2; with splits, consecutive workgroups of an XCD
+    // share a split's k range.
+    int m0, n0, split = 0;
+    if constexpr (PARTIAL) {
+        const int tiles = mb * nb, b = (int)blockIdx.x;
+        split = b / tiles;
+        const int tile = b - split * tiles;
+        m0 = tile / nb * BM;
+        n0 = tile % nb * BN;
+    } else {
+        const int b = (int)blockIdx.x, idx = b >> 3;
+        m0 = (idx / nb * 8 + (b & 7)) * BM;
+        n0 = idx % nb * BN;
+        if (m0 >= a.M) return;
+    }
+    const int kb = split * a.k_split, ke = min(a.K, kb + a.k_split), len = ke - kb;
+    const int steps = (len + BK - 1) / BK;
+
+    Stager<BM, BK, QS> sq;
+    Stager<BN, BK, PS> sp;
+    sq.init(a.q, m0, a.M, kb);
+    sp.init(a.p, n0, a.N, kb);
+    Reader<BM, BK, QS, NM> rq;
+    Reader<BN, BK, PS, NN> rp;
+    rq.init((wave >> 1) * (BM / 2));
+    rp.init((wave & 1) * (BN / 2));
+    constexpr int kInFlight = Stager<BM, BK, QS>::kChunks + Stager<BN, BK, PS>::kChunks;
+
+    f32x16 acc[NN][NM];
+#pragma unroll
+    for (int j = 0; j < NN; ++j)
+#pragma unroll
+        for (int i = 0; i < NM; ++i) acc[j][i] = f32x16{};
+
+    auto fetch = [&](int stage, int t) {
+        sq.fetch(lds, stage, t, len - t * BK);
+        sp.fetch(lds, stage + kQ, t, len - t * BK);
+    };
+    auto put = [&](int stage) {
+        sq.put(lds, stage);
+        sp.put(lds, stage + kQ);
+    };
+    bf16x8 fq[2][NM], fp[2][NN];
+    auto multiply = [&](int set) {
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+#pragma unroll
+            for (int i = 0; i < NM; ++i)
+                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[set][j], fq[set][i], acc[j][i], 0, 0, 0);
+    };
+
+    // Stages of steps t, t + 1, t + 2.
+    int s0 = 0, s1 = kStage, s2 = 2 * kStage;
+    fetch(s0, 0);
+    put(s0);
+    if constexpr (kAligned) fetch(s1, 1);
+    wait_loads<kAligned ? kInFlight : 0>();
+    barrier();
+    rq.read(lds + s0, 0, fq[0]);
+    rp.read(lds + s0 + kQ, 0, fp[0]);
+    for (int t = 0; t < steps; ++t) {
+        // Fetches past the last step read zeros, so the count in flight is fixed.
+        if constexpr (kAligned)
+            fetch(s2, t + 2);
+        else
+            fetch(s1, t + 1);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const int set = ks & 1;
+            if (ks + 1 < KS) {
+                rq.read(lds + s0, ks + 1, fq[set ^ 1]);
+                rp.read(lds + s0 + kQ, ks + 1, fp[set ^ 1]);
+            } else {
+                // step t + 1 has arrived, and every wave holds its last
+                // fragments of step t in registers
+                put(s1);
+                wait_loads<kAligned ? kInFlight : 0>();
+                barrier();
+                rq.read(lds + s1, 0, fq[set ^ 1]);
+                rp.read(lds + s1 + kQ, 0, fp[set ^ 1]);
+            }
+            multiply(set);
+        }
+        const int s = s0;
+        s0 = s1;
+        s1 = s2;
+        s2 = s;
+    }
+    wait_loads<0>();  // nothing may still be on its way into LDS when the workgroup ends
+    static_assert(KS % 2 == 0, "the first fragments of a step are always set 0");
+
+    // A lane's 16 accumulators of a block: row of the result lane mod 32,
+    // columns 8 (v / 4) + 4 (lane / 32) + v mod 4.  Swapping the upper lanes of
+    // quad 2 p with the lower lanes of quad 2 p + 1 leaves the lower lanes
+    // columns 16 p + 0..7 and the upper ones 16 p + 8..15 of the same rows.
+    const int mw = m0 + (wave >> 1) * (BM / 2) + (lane & 31), nw = n0 + (wave & 1) * (BN / 2) + 8 * (lane >> 5);
+#pragma unroll
+    for (int j = 0; j < NN; ++j)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int n = nw + 32 * j + 16 * p;
+            ChunkParams<RAT> k;
+            if constexpr (!PARTIAL) k.init(a.e, n, a.N);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                float h[8];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[j][i][8 * p + v]),
+                                                                    __float_as_uint(acc[j][i][8 * p + 4 + v]), false, false);
+                    h[v] = __uint_as_float(w[0]);
+                    h[4 + v] = __uint_as_float(w[1]);
+                }
+                const int m = mw + 32 * i;
+                if (m >= a.M) continue;
+                if constexpr (PARTIAL) {
+                    float *o = a.partials + ((int64_t)split * a.M + m) * a.N + n;
+                    if (n + 8 <= a.N) {
+                        *reinterpret_cast<f32x4_any *>(o) = f32x4{h[0], h[1], h[2], h[3]};
+                        *reinterpret_cast<f32x4_any *>(o + 4) = f32x4{h[4], h[5], h[6], h[7]};
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (n + e < a.N) o[e] = h[e];
+                    }
+                } else {
+                    finish8<RAT>(h, a.e, k, m, a.N);
+                }
+            }
+        }
+}
+
+// ------------------------------------------------------------ skinny kernel
+
+// Few rows of x: a workgroup takes 16 columns of the result (16 rows of W)
+// and 16 MT rows; its waves share the k range in turns of 64, each lane
+// reading 32 consecutive bytes of a row of W (a line per row and turn) and of
+// x, straight into the operand registers of v_mfma_f32_16x16x32_bf16: the
+// order of k inside a turn is the lanes' own, the same for both operands.  The
+// waves' sums meet in LDS, where one thread finishes 8 columns of a row.
+constexpr int kSkinnyWaves = 8;
+
+template <int MT, int RAT>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void grkan_linear_skinny_kernel(ProductArgs a) {
+    __shared__ float red[kSkinnyWaves][MT * 16][17];
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16 * MT;
+    const uint16_t *W = static_cast<const uint16_t *>(a.p.p) + (int64_t)min(n0 + (lane & 15), a.N - 1) * a.p.ld;
+    const uint16_t *x[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        x[i] = static_cast<const uint16_t *>(a.q.p) + (int64_t)min(m0 + 16 * i + (lane & 15), a.M - 1) * a.q.ld;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
+    const int kl = (lane >> 4) * 16;
+#pragma unroll 2
+    for (int k0 = wave * 64; k0 < a.K; k0 += kSkinnyWaves * 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = k0 + kl + 8 * h, nv = min(max(a.K - k, 0), 8);
+            // rows past the end are clamped (their results are not stored); past K both operands are zeros
+            const bf16x8 w = __builtin_bit_cast(bf16x8, load8(W + (nv ? k : 0), nv));
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const bf16x8 q = __builtin_bit_cast(bf16x8, load8(x[i] + (nv ? k : 0), nv));
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, q, acc[i], 0, 0, 0);
+            }
+        }
+    }
+    // lane: row lane mod 16, columns 4 (lane / 16) + v
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[wave][16 * i + (lane & 15)][4 * (lane >> 4) + v] = acc[i][v];
+    __syncthreads();
+    for (int q = t; q < MT * 32; q += kSkinnyWaves * 64) {
+        const int m = q >> 1, c = (q & 1) * 8;
+        if (m0 + m >= a.M) continue;
+        ChunkParams<RAT> k;
+        k.init(a.e, n0 + c, a.N);
+        float h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kSkinnyWaves; ++w) s += red[w][m][c + e];
+            h[e] = s;
+        }
+        finish8<RAT>(h, a.e, k, m0 + m, a.N);
+    }
+}
+
+// ------------------------------------------------------------ second step
+
+// The splits' sums added in order, then the epilogue; a thread keeps its 8
+// columns over its rows.
+template <int RAT>
+__global__ __launch_bounds__(256) void grkan_linear_finish_kernel(ProductArgs a) {
+    const int chunks = (a.N + 7) / 8;
+    const int64_t total = (int64_t)chunks * a.M, plane = (int64_t)a.M * a.N;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const int64_t m = i / chunks;
+    const int n = (int)(i - m * chunks) * 8;
+    ChunkParams<RAT> k;
+    k.init(a.e, n, a.N);
+    const float *p = a.partials + m * a.N + n;
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+    for (int s = 0; s < a.splits; ++s, p += plane) {
+        if (k.nv == 8) {
+            const f32x4 u = *reinterpret_cast<const f32x4_any *>(p), v = *reinterpret_cast<const f32x4_any *>(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h[e] += u[e];
+                h[4 + e] += v[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < k.nv) h[e] += p[e];
+        }
+    }
+    finish8<RAT>(h, a.e, k, m, a.N);
+}
+
+// ------------------------------------------------------------ dispatch
+
+template <int BM, int BN, int BK, int FORM, bool PARTIAL, int RAT>
+hipError_t launch_tile(const ProductArgs &a, hipStream_t s) {
+    auto kern = grkan_linear_tile_kernel<BM, BN, BK, FORM, PARTIAL, RAT>;
+    constexpr size_t lds = TileShape<BM, BN, BK>::kLds;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (attr != hipSuccess) return attr;
+    const int64_t mb = (a.M + BM - 1) / BM, nb = (a.N + BN - 1) / BN;
+    const int64_t grid = PARTIAL ? mb * nb * a.splits : (mb + 7) / 8 * 8 * nb;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int BK>
+hipError_t launch_shape(int form, bool partial, bool rational, const ProductArgs &a, hipStream_t s) {
+    if (form == kFormDw)
+        return partial ? launch_tile<BM, BN, BK, kFormDw, true, 0>(a, s) : launch_tile<BM, BN, BK, kFormDw, false, 0>(a, s);
+    if (form == kFormDx)
+        return partial ? launch_tile<BM, BN, BK, kFormDx, true, 0>(a, s) : launch_tile<BM, BN, BK, kFormDx, false, 0>(a, s);
+    if (partial) return launch_tile<BM, BN, BK, kFormForward, true, 0>(a, s);
+    return rational ? launch_tile<BM, BN, BK, kFormForward, false, 1>(a, s)
+                    : launch_tile<BM, BN, BK, kFormForward, false, 0>(a, s);
+}
+
+}  // namespace
+
+// The tile kernels of this translation unit's alignment.
+#if GRKAN_LINEAR_ALIGNED
+#define GRKAN_LAUNCH_TILES launch_tiles_aligned
+#else
+#define GRKAN_LAUNCH_TILES launch_tiles_any
+#endif
+hipError_t GRKAN_LAUNCH_TILES(int tile, int form, bool partial, bool rational, const ProductArgs &a, hipStream_t s) {
+    switch (tile) {
+        case 0: return launch_shape<256, 128, 32>(form, partial, rational, a, s);
+        case 1: return launch_shape<128, 128, 32>(form, partial, rational, a, s);
+        case 2: return launch_shape<64, 64, 64>(form, partial, rational, a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+#if !GRKAN_LINEAR_ALIGNED
+hipError_t launch_tiles_aligned(int tile, int form, bool partial, bool rational, const ProductArgs &a, hipStream_t s);
+
+namespace {
+template <int RAT> hipError_t launch_skinny(int mt, const ProductArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * mt - 1) / (16 * mt))), block(kSkinnyWaves * 64);
+    switch (mt) {
+        case 1: hipLaunchKernelGGL((grkan_linear_skinny_kernel<1, RAT>), grid, block, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((grkan_linear_skinny_kernel<2, RAT>), grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL((grkan_linear_skinny_kernel<4, RAT>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError();
+}
+}  // namespace
+
+constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {128, 128, 64}, kTileK[] = {32, 32, 64};
+constexpr int64_t kSlots = 512;  // workgroups resident at once, two a CU
+
+ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga) {
+    ProductPlan p{};
+    p.aligned = aligned;
+    p.splits = 1;
+    const bool any_groups = act == GRKAN_ACT_RATIONAL && dga % 8 != 0;
+    if (form == kFormForward && M <= 64) {
+        p.kind = kSkinny;
+        p.mt = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+        p.k_split = (int32_t)K;
+        return p;
+    }
+    p.kind = kTile;
+    // the largest tile that still gives every CU two workgroups, else the smallest
+    p.tile = 2;
+    for (int i = 0; i < 2; ++i)
+        if (((M + kTileM[i] - 1) / kTileM[i]) * ((N + kTileN[i] - 1) / kTileN[i]) >= kSlots) {
+            p.tile = i;
+            break;
+        }
+    if (p.tile == 2 && K >= 4096) p.tile = (M >= 256 && N >= 128) ? 0 : 2;  // a long k range: split it
+    const int64_t tiles = ((M + kTileM[p.tile] - 1) / kTileM[p.tile]) * ((N + kTileN[p.tile] - 1) / kTileN[p.tile]);
+    const int bk = kTileK[p.tile];
+    const int64_t steps = (K + bk - 1) / bk;
+    int64_t splits = tiles >= kSlots ? 1 : kSlots / tiles;
+    const int64_t most = steps / 8;  // at least 8 steps a split
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    // fp32 sums of one split run over at most 16384 k
+    const int64_t least = (K + 16383) / 16384;
+    if (splits < least) splits = least;
+    const int64_t per = (steps + splits - 1) / splits;
+    p.k_split = (int32_t)(per * bk < K ? per * bk : (K > 0 ? K : 1));
+    p.splits = (int32_t)((K + p.k_split - 1) / p.k_split);
+    if (p.splits < 1) p.splits = 1;
+    p.two_steps = p.splits > 1 || any_groups;
+    if (p.two_steps) p.partials_bytes = (size_t)p.splits * (size_t)M * (size_t)N * 4;
+    return p;
+}
+
+hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &args, hipStream_t s) {
+    ProductArgs a = args;
+    a.splits = p.splits;
+    a.k_split = p.k_split;
+    const int rat = a.e.act != GRKAN_ACT_RATIONAL ? 0 : (a.e.dga % 8 == 0 ? 1 : 2);
+    if (p.kind == kSkinny)
+        return rat == 0 ? launch_skinny<0>(p.mt, a, s) : (rat == 1 ? launch_skinny<1>(p.mt, a, s) : launch_skinny<2>(p.mt, a, s));
+    hipError_t e = p.aligned ? launch_tiles_aligned(p.tile, form, p.two_steps, rat == 1, a, s)
+                             : launch_tiles_any(p.tile, form, p.two_steps, rat == 1, a, s);
+    if (e != hipSuccess || !p.two_steps) return e;
+    const int64_t work = (int64_t)((a.N + 7) / 8) * a.M;
+    const dim3 grid((unsigned)((work + 255) / 256));
+    if (rat == 0) hipLaunchKernelGGL((grkan_linear_finish_kernel<0>), grid, dim3(256), 0, s, a);
+    if (rat == 1) hipLaunchKernelGGL((grkan_linear_finish_kernel<1>), grid, dim3(256), 0, s, a);
+    if (rat == 2) hipLaunchKernelGGL((grkan_linear_finish_kernel<2>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------ dpre, dbias
+
+namespace {
+
+constexpr int kSlopeTx = 32, kSlopeTy = 8;
+
+template <int V, bool RAT>
+__global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel(SlopeArgs a) {
+    __shared__ float red[kSlopeTy][kSlopeTx * V + 1];
+    __shared__ float redc[RAT ? kSlopeTy : 1][RAT ? 10 * kSlopeTx : 1];
+    const int t = (int)threadIdx.x, tx = t % kSlopeTx, ty = t / kSlopeTx;
+    const int vi = (int)blockIdx.x * kSlopeTx + tx, n = vi * V, nv = min(max(a.N - n, 0), V);
+    const int64_t r0 = (int64_t)blockIdx.y * a.chunk_rows, r1 = min(a.rows, r0 + a.chunk_rows);
+    const uint16_t *dz = static_cast<const uint16_t *>(a.dz) + n, *pre = static_cast<const uint16_t *>(a.pre) + n;
+    uint16_t *out = static_cast<uint16_t *>(a.dpre) + n;
+    float sum[V], coef[RAT ? 10 : 1] = {};
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+    BwdCoefs<5, 4> kc;
+    QWide<4> kw;
+    if constexpr (RAT) {
+        const Coefs<5, 4> c = load_coefs<5, 4>(a.A, a.B, nv > 0 ? n / a.dga : 0);
+        kc = derive<5, 4>(c);
+        kw = widen<5, 4, false>(c);
+    }
+    auto value = [](u32x4 v, int e) { return __uint_as_float((e & 1) ? (v[e / 2] & 0xffff0000u) : (v[e / 2] << 16)); };
+    if (nv > 0) {
+        for (int64_t r = r0 + ty; r < r1; r += kSlopeTy) {
+            const u32x4 g = V == 8 ? load8(dz + r * a.lddz, nv) : u32x4{dz[r * a.lddz], 0u, 0u, 0u};
+            float d[8] = {};
+            if (a.act == GRKAN_ACT_NONE) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] += value(g, e);
+                continue;
+            }
+            const u32x4 h = V == 8 ? load8(pre + r * a.N, nv) : u32x4{pre[r * a.N], 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float he = value(h, e), ge = value(g, e);
+                if constexpr (RAT) {
+                    // pre is what the forward kept, an exact input: the sign of Q is decided as by the
+                    // activation's own backward
+                    const Pow<5> X(he);
+                    const ElemBwd el = sign_fixed_element<5, 4, 5>(X, ge, kc, kw);
+                    accumulate<5, 4, 5>(el.w, el.sv, X, coef);
+                    d[e] = el.dx;
+                } else {
+                    d[e] = ge * act_slope(he, a.act);
+                }
+                sum[e] += d[e];
+            }
+            if constexpr (V == 8)
+                store8(out + r * a.ldp, nv, Io<bf16io>::pack(d));
+            else
+                out[r * a.ldp] = __builtin_bit_cast(uint16_t, (__bf16)d[0]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) red[ty][tx * V + e] = sum[e];
+    if constexpr (RAT) {
+#pragma unroll
+        for (int k = 0; k < 10; ++k) redc[ty][k * kSlopeTx + tx] = coef[k];
+    }
+    __syncthreads();
+    float *p = a.partials + (int64_t)blockIdx.y * (a.N + (RAT ? 10 * (int64_t)a.vpr : 0));
+    for (int i = t; i < kSlopeTx * V; i += kSlopeTx * kSlopeTy) {
+        const int c = (int)blockIdx.x * kSlopeTx * V + i;
+        if (c >= a.N) continue;
+        float s = 0.0f;
+        for (int q = 0; q < kSlopeTy; ++q) s += red[q][i];
+        p[c] = s;
+    }
+    if constexpr (RAT) {
+        for (int i = t; i < 10 * kSlopeTx; i += kSlopeTx * kSlopeTy) {
+            const int v = (int)blockIdx.x * kSlopeTx + i % kSlopeTx, k = i / kSlopeTx;
+            if (v >= a.vpr) continue;
+            float s = 0.0f;
+            for (int q = 0; q < kSlopeTy; ++q) s += redc[q][i];
+            p[a.N + (int64_t)k * a.vpr + v] = s;
+        }
+    }
+}
+
+// Column partials over their rows in fp64: 64 columns x 16 row lanes a
+// workgroup, then one workgroup per (activation group, coefficient).
+template <bool RAT>
+__global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a) {
+    __shared__ double red[1024];
+    const int t = (int)threadIdx.x;
+    const int64_t row = a.N + (RAT ? 10 * (int64_t)a.vpr : 0);
+    const int colblocks = (a.N + 63) / 64;
+    double s = 0.0;
+    if ((int)blockIdx.x < colblocks) {
+        const int c = (int)blockIdx.x * 64 + (t & 63);
+        if (c < a.N) {
+#pragma unroll 8
+            for (int r = t >> 6; r < a.chunks; r += 16) s += (double)a.partials[r * row + c];
+        }
+        red[t] = s;
+        __syncthreads();
+        if (t < 64 && c < a.N && a.dbias) {
+            for (int q = 1; q < 16; ++q) s += red[t + 64 * q];
+            a.dbias[c] = (float)s;
+        }
+        return;
+    }
+    if constexpr (RAT) {
+        const int gk = (int)blockIdx.x - colblocks, g = gk / 10, k = gk % 10;
+        const int v0 = g * a.dga / a.vec, w = a.dga / a.vec;
+#pragma unroll 8
+        for (int64_t i = t; i < (int64_t)a.chunks * w; i += 1024) {
+            const int64_t r = i / w;
+            s += (double)a.partials[r * row + a.N + (int64_t)k * a.vpr + v0 + (i - r * w)];
+        }
+        red[t] = s;
+        __syncthreads();
+        for (int o = 512; o > 0; o >>= 1) {
+            if (t < o) red[t] += red[t + o];
+            __syncthreads();
+        }
+        if (t == 0) {
+            if (k < 6)
+                a.dA[g * 6 + k] = (float)red[0];
+            else
+                a.dB[g * 4 + k - 6] = (float)red[0];
+        }
+    }
+}
+
+}  // namespace
+
+SlopePlan plan_slope(int64_t rows, int64_t N, int32_t act, int64_t dga) {
+    SlopePlan p{};
+    const bool rational = act == GRKAN_ACT_RATIONAL;
+    p.vec = rational && dga % 8 != 0 ? 1 : 8;
+    p.vpr = (int32_t)((N + p.vec - 1) / p.vec);
+    const int64_t blocks = (p.vpr + kSlopeTx - 1) / kSlopeTx;
+    int64_t chunks = (2048 + blocks - 1) / blocks;
+    const int64_t most = (rows + 4 * kSlopeTy - 1) / (4 * kSlopeTy);
+    if (chunks > most) chunks = most;
+    if (chunks < 1) chunks = 1;
+    p.chunk_rows = (rows + chunks - 1) / chunks;
+    if (p.chunk_rows < 1) p.chunk_rows = 1;
+    p.chunks = (int32_t)((rows + p.chunk_rows - 1) / p.chunk_rows);
+    p.partials_bytes = (size_t)p.chunks * (size_t)(N + (rational ? 10 * (int64_t)p.vpr : 0)) * 4;
+    return p;
+}
+
+hipError_t launch_slope(const SlopeArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.vpr + kSlopeTx - 1) / kSlopeTx), (unsigned)a.chunks), block(kSlopeTx * kSlopeTy);
+    const bool rational = a.act == GRKAN_ACT_RATIONAL;
+    if (!rational)
+        hipLaunchKernelGGL((grkan_linear_slope_kernel<8, false>), grid, block, 0, s, a);
+    else if (a.vec == 8)
+        hipLaunchKernelGGL((grkan_linear_slope_kernel<8, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((grkan_linear_slope_kernel<1, true>), grid, block, 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (!a.dbias && !rational)) return e;
+    const dim3 rgrid((unsigned)((a.N + 63) / 64 + (rational ? a.ng * 10 : 0)));
+    if (rational)
+        hipLaunchKernelGGL((grkan_linear_columns_kernel<true>), rgrid, dim3(1024), 0, s, a);
+    else
+        hipLaunchKernelGGL((grkan_linear_columns_kernel<false>), rgrid, dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+#endif
+
+}  // namespace grkan

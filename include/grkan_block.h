@@ -121,6 +121,69 @@ GRKAN_API size_t grkan_group_norm_backward_workspace_size(
     int64_t samples, int64_t positions, int64_t channels, int32_t norm_groups, int32_t n_groups,
     grkan_act_t act, grkan_dtype_t io);
 
+/*
+ * Linear map with bias, activation and residual in its epilogue:
+ *
+ *     h = x W^T + bias        z = act(h) + residual
+ *
+ * bf16 x, W, residual, z, fp32 bias; products accumulate in fp32, the
+ * epilogue is fp32 and z is rounded once to nearest-even bf16.
+ *   x         bf16 [rows][d_in], row r at x + r ldx (ldx >= d_in).
+ *   W         bf16 [d_out][d_in], dense.
+ *   bias      fp32 [d_out], or NULL.
+ *   residual  bf16 [rows][d_out], row r at residual + r ldr (ldr >= d_out), or
+ *             NULL (ldr is then ignored).
+ *   z         bf16 [rows][d_out], dense; may be the residual itself if that is
+ *             dense; any other overlap is GRKAN_ERR_INVALID_ARG.
+ *   pre       bf16 [rows][d_out], dense: h, for the backward; or NULL.
+ *   A, B      with GRKAN_ACT_RATIONAL, channel groups of d_out / n_groups.
+ *   rows >= 0 (0 is a no-op), d_in, d_out >= 1; any sizes, strides and element
+ *   alignment are served, whole 16-byte vectors in both widths fastest.
+ *   workspace grkan_linear_act_forward_workspace_size() bytes (may be 0),
+ *             256-byte aligned.
+ * GRKAN_ERR_UNSUPPORTED: rows >= 2^31, a width or stride above 2^22, rows x
+ * d_out past the launch limits, a misaligned pointer.
+ */
+GRKAN_API grkan_status_t grkan_linear_act_forward(
+    const void *x, const void *W, const float *bias, const void *residual, const float *A,
+    const float *B, void *z, void *pre, int64_t rows, int64_t d_in, int64_t d_out, int64_t ldx,
+    int64_t ldr, int32_t n_groups, grkan_act_t act, void *workspace, size_t workspace_bytes,
+    hipStream_t stream);
+
+GRKAN_API size_t grkan_linear_act_forward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
+                                                         int32_t n_groups, grkan_act_t act);
+
+/*
+ * Its backward, given dz = dL/dz and the forward's pre:
+ *
+ *     dpre = dz act'(pre)     (bf16, internal; dz itself for GRKAN_ACT_NONE)
+ *     dx   = dpre W           bf16 [rows][d_in]
+ *     dW   = dpre^T x         bf16 [d_out][d_in]
+ *     dbias = sum of dpre     fp32 [d_out], from dpre before its rounding
+ *     dA, dB                  as grkan_backward's, at pre (its sign decision
+ *                             for Q included)
+ *
+ * and dL/dresidual is dz.  dpre is rounded to bf16 as the operand of the
+ * matrix cores; that error is relative to each term, as that of any bf16
+ * operand.
+ *   dz        bf16 [rows][d_out], row r at dz + r lddz.
+ *   pre       bf16 [rows][d_out], dense; not read for GRKAN_ACT_NONE.
+ *   dx, dW,   outputs, dense, overwritten; each may be NULL (not computed).
+ *   dbias
+ *   dA, dB    required with GRKAN_ACT_RATIONAL.
+ *   rows == 0 writes zeros to dW, dbias, dA and dB.
+ *   workspace grkan_linear_act_backward_workspace_size() bytes, 256-byte
+ *             aligned.
+ */
+GRKAN_API grkan_status_t grkan_linear_act_backward(
+    const void *x, const void *W, const void *dz, const void *pre, const float *A, const float *B,
+    void *dx, void *dW, float *dbias, float *dA, float *dB, int64_t rows, int64_t d_in,
+    int64_t d_out, int64_t ldx, int64_t lddz, int32_t n_groups, grkan_act_t act, void *workspace,
+    size_t workspace_bytes, hipStream_t stream);
+
+GRKAN_API size_t grkan_linear_act_backward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
+                                                          int32_t n_groups, grkan_act_t act);
+
 #ifdef __cplusplus
 }
 #endif

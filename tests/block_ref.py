@@ -164,10 +164,57 @@ def norm_backward(x, dy, mean, rstd, groups, weight, bias, act, A=None, B=None):
 
 def check(what, got, ref, bound):
     """Every element within its bound (and finite where the reference is)."""
-    g = got.detach().double().cpu().reshape(ref.shape)
+    g = got.detach().double().to(ref.device).reshape(ref.shape)
     err = (g - ref).abs()
     bad = ~(err <= bound + 1e-37)
     if bad.any():
         i = int(torch.argmax(torch.where(bad, err / (bound + 1e-37), torch.zeros_like(err)).reshape(-1)))
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} out of bounds; worst at {i}: got "
                              f"{g.reshape(-1)[i]!r}, reference {ref.reshape(-1)[i]!r}, bound {bound.reshape(-1)[i]!r}")
+
+
+def bf16_neighbours(v, e):
+    """(nearest bf16 of v, allowance): 0 where every value within e of v rounds the same way, else the
+    distance between the two candidates."""
+    lo, hi = (v - e).to(torch.bfloat16).double(), (v + e).to(torch.bfloat16).double()
+    return v.to(torch.bfloat16).double(), (hi - lo).abs()
+
+
+def linear_forward(x, W, bias, act, A=None, B=None, residual=None):
+    """{name: (value, bound)} of z and pre; K exact products summed in fp32 cost at most (K + 8) u of the
+    sum of their absolute values."""
+    xd, wd = x.double(), W.double()
+    h, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+    eh = (x.shape[-1] + 8) * U * mag
+    if bias is not None:
+        h = h + bias.double()
+        eh = eh + 2 * U * (h.abs() + bias.double().abs())
+    y, ey, _, _, _ = activation(h, eh, act, A, B)
+    if residual is not None:
+        y = y + residual.double()
+        ey = ey + U * (y.abs() + residual.double().abs())
+    return {"z": (y, ey + rounding(y.abs() + ey, torch.bfloat16)), "pre": (h, eh + rounding(h.abs() + eh, torch.bfloat16))}
+
+
+def linear_backward(x, W, dz, pre, act, A=None, B=None):
+    """{name: (value, bound)} of dx, dW, dbias (dA, dB).  dpre is rounded to bf16 as the products' operand:
+    the reference rounds its own and allows for the elements whose rounding its error does not settle."""
+    g = dz.double()
+    d, e = g, torch.zeros_like(g)
+    out = {}
+    if act != "none":
+        h = pre.double()
+        zero = torch.zeros_like(h)
+        _, _, slope, es, extra = activation(h, zero, act, A, B)
+        d, e = g * slope, g.abs() * es + 2 * U * (g * slope).abs()
+        if act == "rational":
+            dA, dB, eA, eB = coefficient_sums(h, zero, g, A, extra, A.shape[0])
+            out["dA"], out["dB"] = (dA, eA), (dB, eB)
+    out["dbias"] = (d.sum(0), e.sum(0) + SUM * d.abs().sum(0))
+    q, amb = bf16_neighbours(d, e)
+    xd, wd = x.double(), W.double()
+    for name, v, mag, a, k in (("dx", q @ wd, q.abs() @ wd.abs(), amb @ wd.abs(), W.shape[0]),
+                               ("dW", q.t() @ xd, q.abs().t() @ xd.abs(), amb.t() @ xd.abs(), x.shape[0])):
+        err = a + (k + 8) * U * mag
+        out[name] = (v, err + rounding(v.abs() + err, torch.bfloat16))
+    return out
