@@ -11,20 +11,30 @@
 // v_mfma_f32_32x32x16_bf16.  The instruction's row operand is P (columns of
 // the result) and its column operand Q (rows of the result), so a lane's
 // accumulators run along n within one row of the result, and exchanging them
-// with the lane 32 away leaves 8 consecutive columns in a lane: bias,
-// activation, residual and stores take 16-byte accesses and no LDS.
+// with the lane 32 away leaves 8 consecutive columns in a lane, which take bias,
+// activation and residual together and leave through LDS as whole rows.
 // k advances BK at a time through three LDS stages.  While step t is
 // multiplied, the chunks of step t + 2 travel from memory straight into LDS
 // (no registers); one barrier a step, before the step's last group of matrix
 // instructions, whose fragments are already in registers, covers both the
-// arrival of step t + 1 and the release of step t's stage.  Two workgroups
-// fit on a CU, so one's epilogue and barriers overlap the other's products.
+// arrival of step t + 1 and the release of step t's stage.  The launch has as
+// many workgroups as the CUs hold at once (two or three a CU, so that one's
+// epilogue and barriers overlap another's products); each walks over its
+// tiles, and the fetches run on into the next tile while a result leaves.
+//
+// Measured on MI355X at 50,432 rows (238 GFLOP a product): 293-302 us for d =
+// 768 -> 3,072 and 267-280 us for 3,072 -> 768 (790-890 TFLOP/s; the library's
+// product on the first takes 297 us).  LDS bounds the products: without the
+// fetches (64 bytes a cycle into LDS beside the fragments' 128 out of it) the
+// same loop runs 1.5 times as fast.  A 256 x 256 tile of 4 waves, which reads a
+// third less, needs 352 registers and ran at 376 TFLOP/s with one wave a SIMD.
 //
 // LDS layouts.  Chunks are 16 bytes and land in the order of the lanes, so
 // bank conflicts are avoided by choosing which chunk a lane fetches:
-//   K contiguous   [row][BK]: chunk c of row r sits at c ^ f(r), f(r) = r mod 8
-//                  for BK = 64 and (r / 2) mod 4 for BK = 32: 8 consecutive
-//                  rows of one chunk column touch 8 different 16-byte banks
+//   K contiguous   [row][BK]: chunk c of row r sits at c ^ f(r), with f(r) = r mod
+//                  8 for BK = 64 and (r / 2) mod 4 for BK = 32, bit 0 flipped in
+//                  every other 8 rows: 8 consecutive rows of one chunk column
+//                  cover 128 bytes of banks and 16 cover 256
 //   K strided      [k][rows]: chunk c of row k sits at c ^ s(k), s = 2 (j + 4 (j
 //                  mod 2)), j = k mod 4 (2 j for 64 rows, whose k rows are half
 //                  as long); fragments are read with the transposing
@@ -65,6 +75,16 @@ __device__ static inline void store8(uint16_t *p, int nv, u32x4 v) {
         if (e < nv) p[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
 }
 
+// store8 for results larger than the caches: non-temporal, so that they do not
+// drive the operands out (50,432 x 768 -> 3,072: 355 us with ordinary stores,
+// 323 with these).
+__device__ static inline void stream8(uint16_t *p, int nv, u32x4 v) {
+    if (nv >= 8)
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(p));
+    else
+        store8(p, nv, v);
+}
+
 // ------------------------------------------------------------ epilogue
 
 // RAT: 0 an activation without coefficients, 1 the rational with 8-column
@@ -82,14 +102,9 @@ template <int RAT> struct ChunkParams {
     }
 };
 
-// 8 sums of row m, columns n.. -> pre, z.
+// act(h) of 8 columns, in place.
 template <int RAT>
-__device__ static inline void finish8(float (&h)[8], const Epilogue &e, const ChunkParams<RAT> &k, int64_t m, int N) {
-    if (k.nv <= 0) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] += k.bias[i];
-    const int64_t at = m * N + k.n;
-    if (e.pre) store8(static_cast<uint16_t *>(e.pre) + at, k.nv, Io<bf16io>::pack(h));
+__device__ static inline void activate8(float (&h)[8], const Epilogue &e, const ChunkParams<RAT> &k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if constexpr (RAT == 2) {
@@ -98,6 +113,17 @@ __device__ static inline void finish8(float (&h)[8], const Epilogue &e, const Ch
             h[i] = act_value<RAT == 1>(h[i], e.act, k.c);
         }
     }
+}
+
+// 8 sums of row m, columns n.. -> pre, z.
+template <int RAT>
+__device__ static inline void finish8(float (&h)[8], const Epilogue &e, const ChunkParams<RAT> &k, int64_t m, int N) {
+    if (k.nv <= 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += k.bias[i];
+    const int64_t at = m * N + k.n;
+    if (e.pre) store8(static_cast<uint16_t *>(e.pre) + at, k.nv, Io<bf16io>::pack(h));
+    activate8<RAT>(h, e, k);
     if (e.residual) {
         float r[8];
         Io<bf16io>::unpack(load8(static_cast<const uint16_t *>(e.residual) + m * e.ldr + k.n, k.nv), r);
@@ -128,7 +154,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
     int valid;           // unaligned: elements of a chunk inside the operand's own range (strided)
     u32x4 r[kAligned ? 1 : kChunks];
 
-    __device__ static inline int f(int row) { return BK == 64 ? row & 7 : (row >> 1) & 3; }
+    __device__ static inline int f(int row) { return ((BK == 64 ? row : row >> 1) & (BK / 8 - 1)) ^ ((row >> 3) & 1); }
     __device__ static inline int s(int k) { return ROWS >= 128 ? 2 * ((k & 3) + 4 * (k & 1)) : 2 * (k & 3); }
 
     __device__ inline void init(const Operand &o, int row0, int rows, int kstart) {
@@ -149,7 +175,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
         } else {
             base = static_cast<const char *>(o.p) + ((int64_t)row0 * ld + kstart) * 2;
             step = BK * 2;
-            static_assert(kThreads / kPerRow % 8 == 0, "one swizzle per thread");
+            static_assert(kThreads / kPerRow % 16 == 0, "one swizzle per thread");
             const int c = slot ^ f(r0);
             k0 = c * 8;
             valid = 8;
@@ -249,64 +275,95 @@ __device__ static inline void barrier() {
 
 template <int BM, int BN, int BK> struct TileShape {
     static constexpr int kStage = (BM + BN) * BK * 2;
-    static constexpr size_t kLds = 3 * (size_t)kStage;
+    static constexpr size_t kLds = 3 * (size_t)kStage + BN * 4 + BN / 8 * 12 * 4;
 };
+
+// The epilogue's parameters of a tile's BN columns in LDS: bias, then for each
+// 8-column chunk the rational's coefficients (a_0..a_5, b_1..b_4, two unused).
+template <int RAT, int BN>
+__device__ static inline void load_params(float *params, const Epilogue &e, int n0, int N) {
+    const int t = (int)threadIdx.x;
+    if (t < BN) params[t] = e.bias && n0 + t < N ? e.bias[n0 + t] : 0.0f;
+    if constexpr (RAT == 1) {
+        for (int i = t; i < BN / 8 * 12; i += kThreads) {
+            const int c = i / 12, k = i - 12 * c, n = n0 + 8 * c, g = n < N ? n / e.dga : 0;
+            params[BN + i] = k < 6 ? e.A[g * 6 + k] : (k < 10 ? e.B[g * 4 + k - 6] : 0.0f);
+        }
+    }
+}
+template <int BN> __device__ static inline void add_bias(float (&h)[8], const float *params, int chunk) {
+    const f32x4 u = *reinterpret_cast<const f32x4 *>(params + 8 * chunk);
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(params + 8 * chunk + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] += u[i];
+        h[4 + i] += v[i];
+    }
+}
+template <int RAT, int BN>
+__device__ static inline void activate_tile(float (&h)[8], const float *params, int chunk, int act) {
+    Coefs<5, 4> c;
+    if constexpr (RAT == 1) {
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(params + BN + 12 * chunk);
+        const f32x4 u = p[0], v = p[1], w = p[2];
+        c = Coefs<5, 4>{{u[0], u[1], u[2], u[3], v[0], v[1]}, {v[2], v[3], w[0], w[1]}};
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = act_value<RAT == 1>(h[i], act, c);
+}
 
 // FORM as in ProductForm; PARTIAL: fp32 sums of a split to memory.
 template <int BM, int BN, int BK, int FORM, bool PARTIAL, int RAT>
 __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    float *params = reinterpret_cast<float *>(lds + 3 * TileShape<BM, BN, BK>::kStage);
     constexpr bool QS = FORM == kFormDw, PS = FORM != kFormForward;
     constexpr int NM = BM / 64, NN = BN / 64;  // 32 x 32 blocks of a wave
     constexpr int kStage = TileShape<BM, BN, BK>::kStage, kQ = BM * BK * 2;
     constexpr int KS = BK / 16;
 
-    const int nb = (a.N + BN - 1) / BN, mb = (a.M + BM - 1) / BM;
+    const int nb = (a.N + BN - 1) / BN, mb = (a.M + BM - 1) / BM, tiles = mb * nb;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    // Workgroups go to the 8 XCDs in turn.  Without splits each XCD takes whole
-    // panels of BM rows, column tiles of a panel one after another, so that a
-    // panel of Q stays in one L2; with splits, consecutive workgroups of an XCD
-    // share a split's k range.
-    int m0, n0, split = 0;
-    if constexpr (PARTIAL) {
-        const int tiles = mb * nb, b = (int)blockIdx.x;
-        split = b / tiles;
-        const int tile = b - split * tiles;
-        m0 = tile / nb * BM;
-        n0 = tile % nb * BN;
-    } else {
-        const int b = (int)blockIdx.x, idx = b >> 3;
-        m0 = (idx / nb * 8 + (b & 7)) * BM;
-        n0 = idx % nb * BN;
-        if (m0 >= a.M) return;
-    }
-    const int kb = split * a.k_split, ke = min(a.K, kb + a.k_split), len = ke - kb;
-    const int steps = (len + BK - 1) / BK;
+    constexpr int WM = BM / 2, WN = BN / 2;
+    const int mrow = (wave >> 1) * WM, ncol = (wave & 1) * WN;
+
+    // Tile b of the launch.  Workgroups go to the 8 XCDs in turn.  Without
+    // splits each XCD takes whole panels of BM rows, column tiles of a panel one
+    // after another, so that a panel of Q stays in one L2; with splits, tiles
+    // of one k range come one after another.
+    const int count = PARTIAL ? tiles * a.splits : (mb + 7) / 8 * 8 * nb;
+    int m0, n0, split = 0, kb = 0, len = a.K;
+    auto place = [&](int b) {
+        if constexpr (PARTIAL) {
+            split = b / tiles;
+            const int tile = b - split * tiles;
+            m0 = tile / nb * BM;
+            n0 = tile % nb * BN;
+            kb = split * a.k_split;
+            len = min(a.K - kb, a.k_split);
+        } else {
+            const int idx = b >> 3;
+            m0 = (idx / nb * 8 + (b & 7)) * BM;
+            n0 = idx % nb * BN;
+        }
+    };
+    // The next tile of this workgroup from b on, or `count`.
+    auto next = [&](int b) {
+        if constexpr (!PARTIAL)
+            while (b < count && ((b >> 3) / nb * 8 + (b & 7)) * BM >= a.M) b += (int)gridDim.x;
+        return b;
+    };
 
     Stager<BM, BK, QS> sq;
     Stager<BN, BK, PS> sp;
-    sq.init(a.q, m0, a.M, kb);
-    sp.init(a.p, n0, a.N, kb);
     Reader<BM, BK, QS, NM> rq;
     Reader<BN, BK, PS, NN> rp;
-    rq.init((wave >> 1) * (BM / 2));
-    rp.init((wave & 1) * (BN / 2));
+    rq.init(mrow);
+    rp.init(ncol);
     constexpr int kInFlight = Stager<BM, BK, QS>::kChunks + Stager<BN, BK, PS>::kChunks;
+    constexpr int kAhead = kAligned ? 2 : 1;  // steps between a fetch and its use
 
     f32x16 acc[NN][NM];
-#pragma unroll
-    for (int j = 0; j < NN; ++j)
-#pragma unroll
-        for (int i = 0; i < NM; ++i) acc[j][i] = f32x16{};
-
-    auto fetch = [&](int stage, int t) {
-        sq.fetch(lds, stage, t, len - t * BK);
-        sp.fetch(lds, stage + kQ, t, len - t * BK);
-    };
-    auto put = [&](int stage) {
-        sq.put(lds, stage);
-        sp.put(lds, stage + kQ);
-    };
     bf16x8 fq[2][NM], fp[2][NN];
     auto multiply = [&](int set) {
 #pragma unroll
@@ -316,85 +373,209 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                 acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[set][j], fq[set][i], acc[j][i], 0, 0, 0);
     };
 
+    // The fetches run kAhead steps ahead of the products, on through the tiles
+    // of this workgroup: fetch_tile, fetch_step say what comes next.  Past
+    // the last tile they read zeros, so the count in flight is fixed.
+    int fetch_tile = next((int)blockIdx.x), fetch_step = 0, fetch_len = 0;
+    if (fetch_tile >= count) return;
+    auto start_tile = [&]() {
+        if (fetch_tile < count) {
+            place(fetch_tile);
+            sq.init(a.q, m0, a.M, kb);
+            sp.init(a.p, n0, a.N, kb);
+            fetch_len = len;
+        } else {
+            fetch_len = 0;
+        }
+        fetch_step = 0;
+    };
+    auto fetch = [&](int stage) {
+        const int left = fetch_len - fetch_step * BK;
+        sq.fetch(lds, stage, fetch_step, left);
+        sp.fetch(lds, stage + kQ, fetch_step, left);
+        ++fetch_step;
+        if (fetch_step * BK >= fetch_len && fetch_tile < count) {
+            fetch_tile = next(fetch_tile + (int)gridDim.x);
+            start_tile();
+        }
+    };
+    auto put = [&](int stage) {
+        sq.put(lds, stage);
+        sp.put(lds, stage + kQ);
+    };
+
     // Stages of steps t, t + 1, t + 2.
     int s0 = 0, s1 = kStage, s2 = 2 * kStage;
-    fetch(s0, 0);
+    int tile = fetch_tile;
+    bool whole = false;  // the last tile stored by this workgroup had no edge
+    constexpr int kStores = WM * WN / 512;
+    start_tile();
+    fetch(s0);
     put(s0);
-    if constexpr (kAligned) fetch(s1, 1);
+    if constexpr (kAligned) fetch(s1);
     wait_loads<kAligned ? kInFlight : 0>();
     barrier();
     rq.read(lds + s0, 0, fq[0]);
     rp.read(lds + s0 + kQ, 0, fp[0]);
-    for (int t = 0; t < steps; ++t) {
-        // Fetches past the last step read zeros, so the count in flight is fixed.
-        if constexpr (kAligned)
-            fetch(s2, t + 2);
-        else
-            fetch(s1, t + 1);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const int set = ks & 1;
-            if (ks + 1 < KS) {
-                rq.read(lds + s0, ks + 1, fq[set ^ 1]);
-                rp.read(lds + s0 + kQ, ks + 1, fp[set ^ 1]);
-            } else {
-                // step t + 1 has arrived, and every wave holds its last
-                // fragments of step t in registers
-                put(s1);
-                wait_loads<kAligned ? kInFlight : 0>();
-                barrier();
-                rq.read(lds + s1, 0, fq[set ^ 1]);
-                rp.read(lds + s1 + kQ, 0, fp[set ^ 1]);
-            }
-            multiply(set);
-        }
-        const int s = s0;
-        s0 = s1;
-        s1 = s2;
-        s2 = s;
-    }
-    wait_loads<0>();  // nothing may still be on its way into LDS when the workgroup ends
     static_assert(KS % 2 == 0, "the first fragments of a step are always set 0");
+    for (; tile < count; tile = next(tile + (int)gridDim.x)) {
+        place(tile);
+        const int steps = (len + BK - 1) / BK;
+        const int tm0 = m0, tn0 = n0, tsplit = split;
+        if constexpr (!PARTIAL) load_params<RAT, BN>(params, a.e, tn0, a.N);
+#pragma unroll
+        for (int j = 0; j < NN; ++j)
+#pragma unroll
+            for (int i = 0; i < NM; ++i) acc[j][i] = f32x16{};
+        for (int t = 0; t < steps; ++t) {
+            fetch(kAhead == 2 ? s2 : s1);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const int set = ks & 1;
+                if (ks + 1 < KS) {
+                    rq.read(lds + s0, ks + 1, fq[set ^ 1]);
+                    rp.read(lds + s0 + kQ, ks + 1, fp[set ^ 1]);
+                } else {
+                    // step t + 1 has arrived, and every wave holds its last
+                    // fragments of step t in registers
+                    put(s1);
+                    // memory operations end in the order of their issue: after a
+                    // whole tile its kStores stores stand between step 1's fetch
+                    // and step 2's, and need not be waited for
+                    if (kAligned && !PARTIAL && t == 0 && whole)
+                        wait_loads<kInFlight + kStores>();
+                    else
+                        wait_loads<kAligned ? kInFlight : 0>();
+                    barrier();
+                    rq.read(lds + s1, 0, fq[set ^ 1]);
+                    rp.read(lds + s1 + kQ, 0, fp[set ^ 1]);
+                }
+                multiply(set);
+            }
+            const int s = s0;
+            s0 = s1;
+            s1 = s2;
+            s2 = s;
+        }
+        // Here s0 holds the next tile's first step (its first fragments are in
+        // registers), s1 receives its second, and s2 is free.
 
-    // A lane's 16 accumulators of a block: row of the result lane mod 32,
-    // columns 8 (v / 4) + 4 (lane / 32) + v mod 4.  Swapping the upper lanes of
-    // quad 2 p with the lower lanes of quad 2 p + 1 leaves the lower lanes
-    // columns 16 p + 0..7 and the upper ones 16 p + 8..15 of the same rows.
-    const int mw = m0 + (wave >> 1) * (BM / 2) + (lane & 31), nw = n0 + (wave & 1) * (BN / 2) + 8 * (lane >> 5);
+        // A lane's 16 accumulators of a block: row of the result lane mod 32,
+        // columns 8 (v / 4) + 4 (lane / 32) + v mod 4.  Swapping the upper lanes of
+        // quad 2 p with the lower lanes of quad 2 p + 1 leaves the lower lanes
+        // columns 16 p + 0..7 and the upper ones 16 p + 8..15 of the same rows.
+        const int mw = tm0 + mrow, nw = tn0 + ncol;
+        auto take8 = [&](int j, int p, int i, float (&h)[8]) {
 #pragma unroll
-    for (int j = 0; j < NN; ++j)
+            for (int v = 0; v < 4; ++v) {
+                const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[j][i][8 * p + v]),
+                                                                __float_as_uint(acc[j][i][8 * p + 4 + v]), false, false);
+                h[v] = __uint_as_float(w[0]);
+                h[4 + v] = __uint_as_float(w[1]);
+            }
+        };
+        if constexpr (PARTIAL) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int n = nw + 32 * j + 16 * p;
-            ChunkParams<RAT> k;
-            if constexpr (!PARTIAL) k.init(a.e, n, a.N);
+            for (int j = 0; j < NN; ++j)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int i = 0; i < NM; ++i) {
+                        float h[8];
+                        take8(j, p, i, h);
+                        const int m = mw + 32 * i + (lane & 31), n = nw + 32 * j + 16 * p + 8 * (lane >> 5);
+                        if (m >= a.M) continue;
+                        float *o = a.partials + ((int64_t)tsplit * a.M + m) * a.N + n;
+                        if (n + 8 <= a.N) {
+                            *reinterpret_cast<f32x4_any *>(o) = f32x4{h[0], h[1], h[2], h[3]};
+                            *reinterpret_cast<f32x4_any *>(o + 4) = f32x4{h[4], h[5], h[6], h[7]};
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (n + e < a.N) o[e] = h[e];
+                        }
+                    }
+        } else {
+            // bf16 results pass through the wave's own corner of stage s2, 32 rows
+            // of WN columns at a time, so that memory sees whole rows: from the
+            // accumulators a lane holds 8 columns of 32 different rows (32-byte
+            // pieces; storing those took 110 us of 420 at 50,432 x 768 ->
+            // 3,072).  Chunk c of row r sits at c ^ g(r), conflict-free both
+            // ways.  The residual comes the same way, into the slot its result
+            // will take.
+            constexpr int CP = WN / 8, RP = 64 / CP;
+            static_assert(4 * 32 * WN * 2 <= kStage, "staging fits");
+            char *own = lds + s2 + wave * (32 * WN * 2);
+            auto slot = [&](int r, int c) {
+                const int g = ((CP == 8 ? r : r >> 1) & (CP - 1)) ^ ((r >> 3) & 1);
+                return reinterpret_cast<u32x4 *>(own + r * (WN * 2) + ((c ^ g) << 4));
+            };
+            const int row = lane / CP, chunk = lane % CP;
+            const int cn = nw + chunk * 8, cnv = min(max(a.N - cn, 0), 8);
+            auto fence = [] { asm volatile("" ::: "memory"); };  // LDS serves a wave in order
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
-                float h[8];
+                const int mh = mw + 32 * i;
+                auto store_rows = [&](void *out) {
+                    fence();
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[j][i][8 * p + v]),
-                                                                    __float_as_uint(acc[j][i][8 * p + 4 + v]), false, false);
-                    h[v] = __uint_as_float(w[0]);
-                    h[4 + v] = __uint_as_float(w[1]);
-                }
-                const int m = mw + 32 * i;
-                if (m >= a.M) continue;
-                if constexpr (PARTIAL) {
-                    float *o = a.partials + ((int64_t)split * a.M + m) * a.N + n;
-                    if (n + 8 <= a.N) {
-                        *reinterpret_cast<f32x4_any *>(o) = f32x4{h[0], h[1], h[2], h[3]};
-                        *reinterpret_cast<f32x4_any *>(o + 4) = f32x4{h[4], h[5], h[6], h[7]};
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (n + e < a.N) o[e] = h[e];
+                    for (int it = 0; it < 32 / RP; ++it) {
+                        const int r = it * RP + row;
+                        if (mh + r < a.M && cnv > 0)
+                            stream8(static_cast<uint16_t *>(out) + (int64_t)(mh + r) * a.N + cn, cnv, *slot(r, chunk));
                     }
-                } else {
-                    finish8<RAT>(h, a.e, k, m, a.N);
+                    fence();
+                };
+                if (a.e.pre) {
+#pragma unroll
+                    for (int j = 0; j < NN; ++j)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const int c = 4 * j + 2 * p + (lane >> 5);
+                            float h[8];
+                            take8(j, p, i, h);
+                            add_bias<BN>(h, params, ncol / 8 + c);
+                            *slot(lane & 31, c) = Io<bf16io>::pack(h);
+                        }
+                    store_rows(a.e.pre);
                 }
+                if (a.e.residual) {
+#pragma unroll
+                    for (int it = 0; it < 32 / RP; ++it) {
+                        const int r = it * RP + row;
+                        const int nv = mh + r < a.M ? cnv : 0;
+                        *slot(r, chunk) = load8(
+                            static_cast<const uint16_t *>(a.e.residual) + (nv ? (int64_t)(mh + r) * a.e.ldr + cn : 0), nv);
+                    }
+                    fence();
+                }
+#pragma unroll
+                for (int j = 0; j < NN; ++j)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int c = 4 * j + 2 * p + (lane >> 5);
+                        float h[8];
+                        take8(j, p, i, h);
+                        add_bias<BN>(h, params, ncol / 8 + c);
+                        activate_tile<RAT, BN>(h, params, ncol / 8 + c, a.e.act);
+                        u32x4 *to = slot(lane & 31, c);
+                        if (a.e.residual) {
+                            float r[8];
+                            Io<bf16io>::unpack(*to, r);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] += r[e];
+                        }
+                        *to = Io<bf16io>::pack(h);
+                    }
+                store_rows(a.e.z);
             }
+            whole = tm0 + BM <= a.M && tn0 + BN <= a.N;
+            // the stage goes back to the fetches, the parameters to the next tile
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+            barrier();
         }
+    }
+    wait_loads<0>();  // nothing may still be on its way into LDS when the workgroup ends
 }
 
 // ------------------------------------------------------------ skinny kernel
@@ -503,7 +684,10 @@ hipError_t launch_tile(const ProductArgs &a, hipStream_t s) {
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (attr != hipSuccess) return attr;
     const int64_t mb = (a.M + BM - 1) / BM, nb = (a.N + BN - 1) / BN;
-    const int64_t grid = PARTIAL ? mb * nb * a.splits : (mb + 7) / 8 * 8 * nb;
+    int64_t grid = PARTIAL ? mb * nb * a.splits : (mb + 7) / 8 * 8 * nb;
+    // as many workgroups as fit on the 256 CUs at once; each walks over its tiles
+    constexpr int64_t resident = 256 * (BM * BN >= 256 * 128 ? 2 : 3);
+    if (grid > resident) grid = resident;
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, s, a);
     return hipGetLastError();
 }
