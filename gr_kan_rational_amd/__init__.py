@@ -36,7 +36,8 @@ def __getattr__(name):
     if name in _BLOCK:
         from . import block
 
-        return getattr(block, name)
+        globals()[name] = getattr(block, name)  # the next access finds it without this function
+        return globals()[name]
     if name in __all__:
         from . import binding
 

@@ -9,13 +9,12 @@ call runs on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 from . import binding
-from .binding import GRKAN_OK, GRKANError, _check_coefs, _check_out, _io, _on_gpu, _ptr, _stream, _workspace
+from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_coefs, _check_out, _on_gpu
 
 GRKAN_ACT_NONE, GRKAN_ACT_SILU, GRKAN_ACT_GELU, GRKAN_ACT_RATIONAL = 0, 1, 2, 3
 _ACTS = {"none": GRKAN_ACT_NONE, "silu": GRKAN_ACT_SILU, "gelu": GRKAN_ACT_GELU, "rational": GRKAN_ACT_RATIONAL}
@@ -56,15 +55,58 @@ def _act(act: str) -> int:
     return _ACTS[act]
 
 
-def _scope(stream, dev):
-    """Allocations and the launch belong to `stream` (the current one if None) of device dev."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+# The handle of a device's current stream without a Stream object around it, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_stream(stream, dev, launch):
+    """launch(handle) with allocations and kernels on `stream` (the current one if None) of device dev."""
     if stream is None:
-        return torch.cuda.device(dev)
+        if dev.index == torch.cuda.current_device():
+            return launch(_raw_stream(dev.index))
+        with torch.cuda.device(dev):
+            return launch(_raw_stream(dev.index))
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return launch(stream.cuda_stream)
+
+
+_IO = {torch.float32: GRKAN_F32, torch.bfloat16: GRKAN_BF16}
+
+
+def _io(t: torch.Tensor) -> int:
+    io = _IO.get(t.dtype)
+    if io is None:
+        raise TypeError(f"GR-KAN I/O dtype must be float32 or bfloat16, got {t.dtype}")
+    return io
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _given(t, name: str, shape, dtype, dev):
+    """A caller's output checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    numel = 1
+    for k in shape:
+        numel *= k
+    _check_out(t, name, dtype, numel, dev)
+    return t
+
+
+def _space(ws, need: int, dev):
+    """(tensor, pointer, size in bytes) of the workspace: the caller's, or a new one of `need` bytes."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not ws.is_contiguous() or ws.device != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _act_coefs(act: int, A, B, n_groups: int, channels: int, dev):
@@ -134,29 +176,24 @@ def grkan_group_norm_forward(x: torch.Tensor, norm_groups: int, weight=None, bia
     _channel_vector(weight, "weight", c, dev)
     _channel_vector(bias, "bias", c, dev)
     A, B, ng = _act_coefs(code, A, B, n_groups, c, dev)
+    if out is not None and out.shape != x.shape:
+        raise ValueError("out must match x")
     lib = _library()
-    with _scope(stream, dev):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif out.shape != x.shape:
-            raise ValueError("out must match x")
-        _check_out(out, "out", x.dtype, x.numel(), dev)
-        if mean is None:
-            mean = torch.empty((n, norm_groups), dtype=torch.float32, device=dev)
-        _check_out(mean, "mean", torch.float32, n * norm_groups, dev)
-        if rstd is None:
-            rstd = torch.empty((n, norm_groups), dtype=torch.float32, device=dev)
-        _check_out(rstd, "rstd", torch.float32, n * norm_groups, dev)
-        need = lib.grkan_group_norm_forward_workspace_size(n, s, c, norm_groups, ng, code, io)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _workspace(workspace, dev)
-        st = lib.grkan_group_norm_forward(_ptr(x), _ptr(out), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
-                                          _ptr(A), _ptr(B), n, s, c, xs, xr, norm_groups, ng, eps, code, io, wsp,
-                                          wsn, _stream(stream))
-    if st != GRKAN_OK:
-        raise GRKANError(st, "grkan_group_norm_forward")
-    return out, mean, rstd
+    need = lib.grkan_group_norm_forward_workspace_size(n, s, c, norm_groups, ng, code, io)
+
+    def launch(handle):
+        y = _given(out, "out", x.shape, x.dtype, dev)
+        mu = _given(mean, "mean", (n, norm_groups), torch.float32, dev)
+        rs = _given(rstd, "rstd", (n, norm_groups), torch.float32, dev)
+        ws, wsp, wsn = _space(workspace, need, dev)
+        st = lib.grkan_group_norm_forward(x.data_ptr(), y.data_ptr(), mu.data_ptr(), rs.data_ptr(), _ptr(weight),
+                                          _ptr(bias), _ptr(A), _ptr(B), n, s, c, xs, xr, norm_groups, ng, eps, code,
+                                          io, wsp, wsn, handle)
+        if st != GRKAN_OK:
+            raise GRKANError(st, "grkan_group_norm_forward")
+        return y, mu, rs
+
+    return _on_stream(stream, dev, launch)
 
 
 def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -180,43 +217,32 @@ def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Ten
     _check_out(mean, "mean", torch.float32, n * norm_groups, dev)
     _check_out(rstd, "rstd", torch.float32, n * norm_groups, dev)
     A, B, ng = _act_coefs(code, A, B, n_groups, c, dev)
+    if dx is not None and dx.shape != x.shape:
+        raise ValueError("dx must match x")
     lib = _library()
-    with _scope(stream, dev):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif dx.shape != x.shape:
-            raise ValueError("dx must match x")
-        _check_out(dx, "dx", x.dtype, x.numel(), dev)
-        if dweight is None:
-            dweight = torch.empty(c, dtype=torch.float32, device=dev)
-        _check_out(dweight, "dweight", torch.float32, c, dev)
-        if dbias is None:
-            dbias = torch.empty(c, dtype=torch.float32, device=dev)
-        _check_out(dbias, "dbias", torch.float32, c, dev)
-        dA, dB = _coef_grads(code, dA, dB, ng, dev)
-        need = lib.grkan_group_norm_backward_workspace_size(n, s, c, norm_groups, ng, code, io)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _workspace(workspace, dev)
-        st = lib.grkan_group_norm_backward(_ptr(x), _ptr(dy), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
-                                           _ptr(A), _ptr(B), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dA),
-                                           _ptr(dB), n, s, c, xs, xr, ds, dr, norm_groups, ng, code, io, wsp, wsn,
-                                           _stream(stream))
-    if st != GRKAN_OK:
-        raise GRKANError(st, "grkan_group_norm_backward")
-    return dx, dweight, dbias, dA, dB
+    need = lib.grkan_group_norm_backward_workspace_size(n, s, c, norm_groups, ng, code, io)
+
+    def launch(handle):
+        gx = _given(dx, "dx", x.shape, x.dtype, dev)
+        gw = _given(dweight, "dweight", (c,), torch.float32, dev)
+        gb = _given(dbias, "dbias", (c,), torch.float32, dev)
+        gA, gB = _coef_grads(code, dA, dB, ng, dev)
+        ws, wsp, wsn = _space(workspace, need, dev)
+        st = lib.grkan_group_norm_backward(x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                           _ptr(weight), _ptr(bias), _ptr(A), _ptr(B), gx.data_ptr(), gw.data_ptr(),
+                                           gb.data_ptr(), _ptr(gA), _ptr(gB), n, s, c, xs, xr, ds, dr, norm_groups,
+                                           ng, code, io, wsp, wsn, handle)
+        if st != GRKAN_OK:
+            raise GRKANError(st, "grkan_group_norm_backward")
+        return gx, gw, gb, gA, gB
+
+    return _on_stream(stream, dev, launch)
 
 
 def _coef_grads(code: int, dA, dB, n_groups: int, dev):
     if code != GRKAN_ACT_RATIONAL:
         return None, None
-    if dA is None:
-        dA = torch.empty((n_groups, 6), dtype=torch.float32, device=dev)
-    _check_out(dA, "dA", torch.float32, n_groups * 6, dev)
-    if dB is None:
-        dB = torch.empty((n_groups, 4), dtype=torch.float32, device=dev)
-    _check_out(dB, "dB", torch.float32, n_groups * 4, dev)
-    return dA, dB
+    return (_given(dA, "dA", (n_groups, 6), torch.float32, dev), _given(dB, "dB", (n_groups, 4), torch.float32, dev))
 
 
 def _rows(t: torch.Tensor, name: str, dev):
@@ -281,24 +307,20 @@ def grkan_linear_act_forward(x: torch.Tensor, W: torch.Tensor, bias=None, act: s
             raise ValueError(f"residual must be {list(shape)}")
         ldr = _rows(residual, "residual", dev)[2]
     lib = _library()
-    with _scope(stream, dev):
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        _check_out(out, "out", torch.bfloat16, rows * d_out, dev)
-        if pre is None and keep:
-            pre = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        if pre is not None:
-            _check_out(pre, "pre", torch.bfloat16, rows * d_out, dev)
-        need = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, ng, code)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _workspace(workspace, dev)
-        st = lib.grkan_linear_act_forward(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), _ptr(A), _ptr(B), _ptr(out),
-                                          _ptr(pre), rows, d_in, d_out, ldx, ldr, ng, code, wsp, wsn,
-                                          _stream(stream))
-    if st != GRKAN_OK:
-        raise GRKANError(st, "grkan_linear_act_forward")
-    return out, pre
+    need = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, ng, code)
+
+    def launch(handle):
+        z = _given(out, "out", shape, torch.bfloat16, dev)
+        h = _given(pre, "pre", shape, torch.bfloat16, dev) if keep or pre is not None else None
+        ws, wsp, wsn = _space(workspace, need, dev)
+        st = lib.grkan_linear_act_forward(x.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual), _ptr(A), _ptr(B),
+                                          z.data_ptr(), _ptr(h), rows, d_in, d_out, ldx, ldr, ng, code, wsp, wsn,
+                                          handle)
+        if st != GRKAN_OK:
+            raise GRKANError(st, "grkan_linear_act_forward")
+        return z, h
+
+    return _on_stream(stream, dev, launch)
 
 
 def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor, pre=None, act: str = "none",
@@ -320,27 +342,22 @@ def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor
         _check_out(pre, "pre", torch.bfloat16, rows * d_out, dev)
     A, B, ng = _act_coefs(code, A, B, n_groups, d_out, dev)
     lib = _library()
-    with _scope(stream, dev):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-        _check_out(dx, "dx", torch.bfloat16, rows * d_in, dev)
-        if dW is None:
-            dW = torch.empty((d_out, d_in), dtype=torch.bfloat16, device=dev)
-        _check_out(dW, "dW", torch.bfloat16, d_out * d_in, dev)
-        if dbias is None:
-            dbias = torch.empty(d_out, dtype=torch.float32, device=dev)
-        _check_out(dbias, "dbias", torch.float32, d_out, dev)
-        dA, dB = _coef_grads(code, dA, dB, ng, dev)
-        need = lib.grkan_linear_act_backward_workspace_size(rows, d_in, d_out, ng, code)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsp, wsn = _workspace(workspace, dev)
-        st = lib.grkan_linear_act_backward(_ptr(x), _ptr(W), _ptr(dz), _ptr(pre), _ptr(A), _ptr(B), _ptr(dx),
-                                           _ptr(dW), _ptr(dbias), _ptr(dA), _ptr(dB), rows, d_in, d_out, ldx, lddz,
-                                           ng, code, wsp, wsn, _stream(stream))
-    if st != GRKAN_OK:
-        raise GRKANError(st, "grkan_linear_act_backward")
-    return dx, dW, dbias, dA, dB
+    need = lib.grkan_linear_act_backward_workspace_size(rows, d_in, d_out, ng, code)
+
+    def launch(handle):
+        gx = _given(dx, "dx", x.shape, torch.bfloat16, dev)
+        gW = _given(dW, "dW", (d_out, d_in), torch.bfloat16, dev)
+        gb = _given(dbias, "dbias", (d_out,), torch.float32, dev)
+        gA, gB = _coef_grads(code, dA, dB, ng, dev)
+        ws, wsp, wsn = _space(workspace, need, dev)
+        st = lib.grkan_linear_act_backward(x.data_ptr(), W.data_ptr(), dz.data_ptr(), _ptr(pre), _ptr(A), _ptr(B),
+                                           gx.data_ptr(), gW.data_ptr(), gb.data_ptr(), _ptr(gA), _ptr(gB), rows, d_in,
+                                           d_out, ldx, lddz, ng, code, wsp, wsn, handle)
+        if st != GRKAN_OK:
+            raise GRKANError(st, "grkan_linear_act_backward")
+        return gx, gW, gb, gA, gB
+
+    return _on_stream(stream, dev, launch)
 
 
 class GRKANGroupNorm(torch.autograd.Function):

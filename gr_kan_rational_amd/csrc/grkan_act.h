@@ -83,37 +83,47 @@ __device__ static inline float act_slope(float h, int act) {
 // arithmetic (a normalised value): dy dF/dh, the ten coefficient terms added
 // to acc.  Q and its sign are taken in fp32 -- h carries its own rounding, so
 // deciding the sign of Q more exactly than h is known would mean nothing --
-// with sign(0) = 0.
-__device__ static inline float rational_slope(float h, float dy, const Coefs<5, 4> &c, float (&acc)[10]) {
-    float P = c.a[5], dP = 5.0f * c.a[5];
+// with sign(0) = 0.  The powers of h serve the polynomials and the sums (46
+// instructions; Horner's rule with running products for the sums takes 51).
+struct SlopeCoefs {
+    Coefs<5, 4> c;
+    float da[4], db[3];  // 2 a_2 .. 5 a_5, 2 b_2 .. 4 b_4
+    __device__ inline void init(const Coefs<5, 4> &k) {
+        c = k;
 #pragma unroll
-    for (int i = 4; i >= 0; --i) P = fmaf(P, h, c.a[i]);
+        for (int i = 2; i <= 5; ++i) da[i - 2] = (float)i * k.a[i];
 #pragma unroll
-    for (int i = 4; i >= 1; --i) dP = fmaf(dP, h, (float)i * c.a[i]);
-    float q = c.b[3], dQ = 4.0f * c.b[3];
-#pragma unroll
-    for (int j = 2; j >= 0; --j) q = fmaf(q, h, c.b[j]);
-#pragma unroll
-    for (int j = 2; j >= 0; --j) dQ = fmaf(dQ, h, (float)(j + 1) * c.b[j]);
-    const float Q = h * q;
+        for (int j = 2; j <= 4; ++j) db[j - 2] = (float)j * k.b[j - 1];
+    }
+};
+
+__device__ static inline float rational_slope(float h, float dy, const SlopeCoefs &k, float (&acc)[10]) {
+    // One element after another (the asm ties h to every sum so far): left
+    // alone, the compiler puts the sums off and holds the powers of all of a
+    // lane's elements (270 registers for 12 of them).
+    asm volatile("" : "+v"(h) : "v"(acc[0]), "v"(acc[1]), "v"(acc[2]), "v"(acc[3]), "v"(acc[4]), "v"(acc[5]), "v"(acc[6]),
+                 "v"(acc[7]), "v"(acc[8]), "v"(acc[9]));
+    const float *a = k.c.a, *b = k.c.b;
+    const float h2 = h * h, h3 = h2 * h, h4 = h2 * h2, h5 = h4 * h;
+    const float P = fmaf(a[5], h5, fmaf(a[4], h4, fmaf(a[3], h3, fmaf(a[2], h2, fmaf(a[1], h, a[0])))));
+    const float dP = fmaf(k.da[3], h4, fmaf(k.da[2], h3, fmaf(k.da[1], h2, fmaf(k.da[0], h, a[1]))));
+    const float Q = fmaf(b[3], h4, fmaf(b[2], h3, fmaf(b[1], h2, b[0] * h)));
+    const float dQ = fmaf(k.db[2], h3, fmaf(k.db[1], h2, fmaf(k.db[0], h, b[0])));
     const float r = __builtin_amdgcn_rcpf(1.0f + fabsf(Q));
     const float w = dy * r;
     const float v = w * (P * r);
-    float sv = Q == 0.0f ? 0.0f : __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(Q) & 0x80000000u));
-    const float dh = fmaf(-sv, dQ, w * dP);
-    float p = w;
-    acc[0] += p;
-#pragma unroll
-    for (int i = 1; i <= 5; ++i) {
-        p *= h;
-        acc[i] += p;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        sv *= h;
-        acc[6 + j] -= sv;
-    }
-    return dh;
+    const float sv = Q == 0.0f ? 0.0f : __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(Q) & 0x80000000u));
+    acc[0] += w;
+    acc[1] = fmaf(w, h, acc[1]);
+    acc[2] = fmaf(w, h2, acc[2]);
+    acc[3] = fmaf(w, h3, acc[3]);
+    acc[4] = fmaf(w, h4, acc[4]);
+    acc[5] = fmaf(w, h5, acc[5]);
+    acc[6] = fmaf(-sv, h, acc[6]);
+    acc[7] = fmaf(-sv, h2, acc[7]);
+    acc[8] = fmaf(-sv, h3, acc[8]);
+    acc[9] = fmaf(-sv, h4, acc[9]);
+    return fmaf(-sv, dQ, w * dP);
 }
 
 }  // namespace grkan

@@ -73,33 +73,16 @@ int pow2_at_most(int64_t v) {
 
 // ------------------------------------------------------------ norm plans
 
-constexpr int kTokenMaxLanes = 512, kTokenMaxAccesses = 4;
+constexpr int kTokenMaxLanes = 256, kTokenMaxAccesses = 4;
 constexpr int64_t kNormWorkgroups = 2048;  // target of the looping kernels: 8 workgroups a CU
+constexpr int64_t kSplitWorkgroups = 1024;
 
-// The elements of one access: 16 bytes, unless a group's segment wastes more
-// than an eighth of its lanes on ragged accesses, or an access would straddle
-// two activation groups (which would need two sets of coefficients).
-int norm_vec(int64_t D, int64_t dga, bool rational, int es) {
-    for (int v = 16 / es; v > 1; v /= 2) {
-        if (D % v != 0 && D < 8 * (int64_t)v) continue;
-        if (rational && !((D % v == 0 && dga % v == 0) || dga % D == 0)) continue;
-        return v;
-    }
-    return 1;
-}
-
-void norm_columns(NormPlan *p, int64_t G, int threads) {
-    if (p->vpg <= threads) {
-        p->bpg = 1;
-        if (p->gpb > G) p->gpb = (int32_t)G;
-        p->TX = p->gpb * p->vpg;
-        p->ncb = (int32_t)ceil_div(G, p->gpb);
-    } else {
-        p->gpb = 1;
-        p->bpg = (int32_t)ceil_div(p->vpg, threads);
-        p->TX = (int32_t)ceil_div(p->vpg, p->bpg);
-        p->ncb = (int32_t)(G * p->bpg);
-    }
+// Largest power of two <= v elements per access such that accesses that start
+// at multiples of `start` columns (and then every v) lie in one activation
+// group each.
+int rational_vec(int v, int64_t dga, int64_t start) {
+    while (v > 1 && (dga % v != 0 || start % v != 0)) v /= 2;
+    return v;
 }
 
 grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng, grkan_act_t act, grkan_dtype_t io,
@@ -111,61 +94,85 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
     if (rational && (ng < 1 || C % ng != 0)) return GRKAN_ERR_INVALID_ARG;
     if (C >= (1 << 24) || S > INT32_MAX) return GRKAN_ERR_UNSUPPORTED;
     if (N > INT32_MAX / G) return GRKAN_ERR_UNSUPPORTED;
-    const int es = io_bytes(io);
-    const int64_t D = C / G;
+    const int es = io_bytes(io), vmax = 16 / es;
+    const int64_t D = C / G, dga = rational ? C / ng : 0;
     *p = NormPlan{};
-    p->vec = norm_vec(D, rational ? C / ng : 1, rational, es);
-    p->vpg = (int32_t)ceil_div(D, p->vec);
-    p->cv = (int64_t)G * p->vpg;
     if (N == 0 || S == 0) return GRKAN_OK;
 
-    const int64_t row_values = norm_partial_row(*p, C, rational);
-    if (S == 1 && p->vpg <= kTokenMaxLanes * kTokenMaxAccesses) {
+    // Token: T lanes of K accesses of v elements with the fewest idle places for
+    // a group, then the widest accesses (16 bytes or 8), then the fewest.  The
+    // backward keeps two sums, a weight and a bias per element of a lane, so it
+    // takes at most 16 (768 channels in bf16: 64 lanes x 3 x 4).  A rational's
+    // lanes prefer runs inside one activation group; else a run may lie in two,
+    // and has to be no longer than a group for that.
+    int64_t best = INT64_MAX;
+    if (S == 1) {
+        for (int straddle = 0; straddle <= (rational ? 1 : 0) && best == INT64_MAX; ++straddle)
+            for (int v = vmax; v >= 1; v /= 2) {
+                if (!rational && v < vmax / 2) break;
+                for (int K = 1; K <= kTokenMaxAccesses; ++K) {
+                    const int run = K * v;
+                    if (backward && run > 16) break;
+                    if (rational && !straddle && dga % D != 0 && (dga % run != 0 || D % run != 0)) continue;
+                    if (straddle && (run > dga || run < 4)) continue;
+                    int T = 1;
+                    while ((int64_t)T * run < D) T *= 2;
+                    if (T > (run == 1 ? 1024 : kTokenMaxLanes) || (int64_t)T * run >= best) continue;
+                    best = (int64_t)T * run;
+                    p->vec = v;
+                    p->T = T;
+                    p->K = K;
+                    p->straddle = straddle != 0;
+                }
+            }
+    }
+    if (best != INT64_MAX) {
         p->kind = kNormToken;
-        // The fewest lane places (T lanes x K accesses) that hold the group,
-        // then the fewest accesses a lane.
-        int64_t best = INT64_MAX;
-        for (int K = 1; K <= kTokenMaxAccesses; ++K) {
-            int T = 1;
-            while ((int64_t)T * K < p->vpg) T *= 2;
-            if (T > kTokenMaxLanes) continue;
-            if ((int64_t)T * K < best) best = (int64_t)T * K, p->T = T, p->K = K;
-        }
-        int spw = p->T < 256 && p->T <= 64 ? 256 / p->T : 1;
+        p->vpg = (int32_t)ceil_div(D, p->K * p->vec);  // (read for a rational only)
+        p->cv = (int64_t)G * p->vpg;
+        int spw = p->T <= 64 ? 256 / p->T : 1;
         while (spw % G != 0 && G % spw != 0) --spw;
         p->spw = spw;
         p->block = spw * p->T;
+        // Enough workgroups to fill the GPU, walking over the samples in as
+        // many rounds each as the last of them needs.
         const int64_t unit = spw < G ? G / spw : 1;  // workgroups that cover one sample
-        int64_t blocks = ceil_div(N * G, spw);
-        const int64_t cap = backward ? kNormWorkgroups / 2 : kNormWorkgroups;
-        if (blocks > cap) blocks = cap;
-        p->blocks = ceil_div(blocks, unit) * unit;
+        const int64_t wanted = ceil_div(N * G, spw), cap = backward ? kNormWorkgroups / 2 : kNormWorkgroups;
+        const int64_t rounds = ceil_div(wanted, cap);
+        p->blocks = ceil_div(ceil_div(wanted, rounds), unit) * unit;
         p->prows = spw > G ? p->blocks : p->blocks * spw / G;
-        p->lds = (size_t)p->block * 13 * 4 + 256;
+        p->lds = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4 + 256;
     } else {
-        // A slab: whole groups side by side until their segments make 64
-        // bytes or more of every row and the rows a lane has to hold allow.
+        // A slab: whole groups side by side until they make 64 bytes or more of
+        // every row, if a workgroup's registers hold all rows of that.
         const int threads = backward ? 512 : 1024, regs = backward ? 8 : 16;
-        const int64_t seg = D * es;
-        int64_t gpb = ceil_div(64, seg);
+        int64_t gpb = ceil_div(64, D * es);
         if (gpb > G) gpb = G;
-        const bool fits = S > 1 && (int64_t)p->vpg * gpb <= threads && S <= (threads / (p->vpg * gpb)) * regs;
-        if (fits) {
+        auto vec_of = [&](int64_t groups) { return rational ? rational_vec(vmax, dga, groups * D) : vmax; };
+        auto rows_of = [&](int64_t groups) {  // rows a workgroup can hold
+            const int64_t tx = ceil_div(groups * D, vec_of(groups));
+            return tx <= threads ? threads / tx * regs : 0;
+        };
+        if (S > 1 && S <= rows_of(gpb)) {
             p->kind = kNormSlab;
-            // wider blocks while many workgroups remain and segments are short
-            while (gpb * 2 <= G && (int64_t)p->vpg * gpb * 2 <= 64 && gpb * seg < 256 &&
-                   S <= (threads / (p->vpg * gpb * 2)) * regs && N * ceil_div(G, gpb * 2) >= kNormWorkgroups)
+            // wider blocks while many workgroups remain and rows are short
+            while (gpb * 2 <= G && gpb * D * es < 256 && S <= rows_of(gpb * 2) && vec_of(gpb * 2) >= vec_of(gpb) &&
+                   N * ceil_div(G, gpb * 2) >= kNormWorkgroups)
                 gpb *= 2;
-            p->gpb = (int32_t)gpb;
-            norm_columns(p, G, threads);
-            // the fewest row lanes that hold S rows in the registers a lane has
-            // (more of them while a workgroup stays within 256 threads)
-            int64_t ty = ceil_div(S, regs);
-            const int64_t wide = 256 / p->TX;
-            if (ty < wide) ty = wide < S ? wide : S;
-            p->TY = (int32_t)ty;
+            p->vec = vec_of(gpb);
+            p->width = (int32_t)(gpb * D);
+            p->ncb = (int32_t)ceil_div(G, gpb);
+            p->groups = (int32_t)gpb;
+            p->TX = (int32_t)ceil_div(p->width, p->vec);
+            // Row lanes: 256 threads if many workgroups share a CU, all there are
+            // if not; at least what the registers need.
+            const int64_t want = N * p->ncb >= 1024 ? 256 : threads;
+            int64_t ty = want / p->TX;
+            if (ty < ceil_div(S, regs)) ty = ceil_div(S, regs);
+            if (ty > S) ty = S;
             p->regs = (int32_t)ceil_div(S, ty);
-            p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
+            p->TY = (int32_t)ceil_div(S, p->regs);
+            p->block = (int32_t)(ceil_div((int64_t)p->TX * p->TY, 64) * 64);
             if (!backward) {
                 p->blocks = (N >= 8 ? ceil_div(N, 8) * 8 : N) * p->ncb;
             } else {
@@ -179,37 +186,48 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
             }
         } else {
             p->kind = kNormSplit;
-            const int threads2 = 256;
-            gpb = threads2 / (p->vpg < threads2 ? p->vpg : threads2);
-            p->gpb = (int32_t)(gpb < 1 ? 1 : gpb);
-            norm_columns(p, G, threads2);
-            int64_t ty = threads2 / p->TX;
+            p->vec = rational ? rational_vec(vmax, dga, 0) : vmax;
+            const int64_t accesses = ceil_div(C, p->vec);
+            // (half the accesses where every column is a group, for the groups' sums in LDS)
+            p->ncb = (int32_t)ceil_div(accesses, D == 1 ? 128 : 256);
+            p->TX = (int32_t)ceil_div(accesses, p->ncb);
+            p->width = p->TX * p->vec;
+            p->ncb = (int32_t)ceil_div(C, p->width);
+            p->groups = (int32_t)(p->width / D + 2 < G ? p->width / D + 2 : G);
+            p->parts = (int32_t)(D / p->width + 2 < p->ncb ? D / p->width + 2 : p->ncb);
+            int64_t ty = 256 / p->TX;
             if (ty > S) ty = S;
             p->TY = (int32_t)ty;
             p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
-            // chunks of at least 4 rows a lane
-            int64_t chunks = ceil_div(kNormWorkgroups, N * p->ncb);
-            const int64_t most = ceil_div(S, 4 * ty);
+            // chunks of 4 to 64 rows a lane
+            int64_t chunks = ceil_div(kSplitWorkgroups, N * p->ncb);
+            const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 64 * ty);
             if (chunks > most) chunks = most;
+            if (chunks < least) chunks = least;
             p->chunk_rows = ceil_div(S, chunks);
             p->chunks = ceil_div(S, p->chunk_rows);
             p->blocks = N * p->chunks * p->ncb;
             p->prows = N * p->chunks;
         }
-        p->L = pow2_at_most(p->block / p->gpb < 64 ? p->block / p->gpb : 64);
-        const size_t vals = p->kind == kNormSplit ? 2 * sizeof(double) : 2 * sizeof(float);
-        p->lds = vals * ((size_t)p->block + p->gpb);
-        if (backward && p->lds < (size_t)p->block * 13 * 4) p->lds = (size_t)p->block * 13 * 4;
+        p->cv = (int64_t)p->ncb * p->TX;
+        p->mixed = D % p->vec != 0;
+        p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
+        const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
+        const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
+        p->lds = value * values * ((size_t)p->block * (p->mixed ? p->vec : 1) + p->groups);
+        const size_t cols = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4;
+        if (backward && p->lds < cols) p->lds = cols;
     }
+    p->row = 2 * C + (rational ? (p->straddle ? 20 : 10) * p->cv : 0);
     size_t at = 0;
     if (p->kind == kNormSplit) {
         p->off_stats = at;
-        at += align256((size_t)N * G * p->chunks * p->bpg * 16);
+        at += align256((size_t)N * G * p->chunks * p->parts * 16);
         p->off_means = at;
         if (backward) at += align256((size_t)N * G * 8);
     }
     p->off_partials = at;
-    if (backward) at += align256((size_t)p->prows * row_values * 4);
+    if (backward) at += align256((size_t)p->prows * p->row * 4);
     p->total = at;
     return GRKAN_OK;
 }

@@ -602,7 +602,6 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void grkan_linear_skinny_kernel(
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
     const int kl = (lane >> 4) * 16;
-#pragma unroll 2
     for (int k0 = wave * 64; k0 < a.K; k0 += kSkinnyWaves * 64) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -95,6 +95,17 @@ template <int V> struct Pack {
         }
         return k;
     }
+    // Keeps the compiler from holding the unpacked values from one use to the
+    // next: unpacking again costs an instruction an element, holding them up to
+    // twice the registers.
+    __device__ inline void repack() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t w = r[i];
+            asm volatile("" : "+v"(w));
+            r[i] = w;
+        }
+    }
     __device__ inline void store(char *p, int nv) const {
         if (nv == V) {
             if constexpr (kBytes == 2)
@@ -134,15 +145,23 @@ template <int V, bool RAT> struct Cols {
     }
 };
 
-// y of one access, the statistics folded into one multiplication and addition
-// after the subtraction of the mean (which is exact enough only when done
-// first).
-template <int V, bool RAT>
-__device__ static inline Pack<V> apply_forward(const Pack<V> &x, float mean, float rstd, const Cols<V, RAT> &k,
+// Statistics of a lane's elements: one pair, or one per element where accesses
+// straddle groups.
+template <int V, bool MIXED> struct Stats {
+    static constexpr int N = MIXED ? V : 1;
+    float mean[N], rstd[N];
+    __device__ inline float m(int e) const { return mean[MIXED ? e : 0]; }
+    __device__ inline float r(int e) const { return rstd[MIXED ? e : 0]; }
+};
+
+// y of one access.  The mean is subtracted first, which is exact for values
+// near it; rstd w is one factor.
+template <int V, bool RAT, bool MIXED>
+__device__ static inline Pack<V> apply_forward(const Pack<V> &x, const Stats<V, MIXED> &s, const Cols<V, RAT> &k,
                                                int act) {
     float f[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = act_value<RAT>(fmaf((x.get(e) - mean) * rstd, k.w[e], k.b[e]), act, k.c);
+    for (int e = 0; e < V; ++e) f[e] = act_value<RAT>(fmaf(x.get(e) - s.m(e), s.r(e) * k.w[e], k.b[e]), act, k.c);
     return Pack<V>::from(f);
 }
 
@@ -155,37 +174,102 @@ template <int V, bool RAT> struct ColSums {
 #pragma unroll
         for (int i = 0; i < (RAT ? 10 : 1); ++i) coef[i] = 0.0f;
     }
-    static constexpr int kValues = 2 * V + (RAT ? 10 : 0);
-    __device__ inline float get(int i) const {
-        return i < V ? dw[i] : (i < 2 * V ? db[i - V] : coef[i - 2 * V]);
+};
+
+// dh at xh of element e.
+template <int V, bool RAT>
+__device__ static inline float slope(float xh, float dy, const Cols<V, RAT> &k, const SlopeCoefs &sc, int e, int act,
+                                     float *coef) {
+    const float h = fmaf(xh, k.w[e], k.b[e]);
+    if constexpr (RAT)
+        return rational_slope(h, dy, sc, *reinterpret_cast<float (*)[10]>(coef));
+    else
+        return dy * act_slope(h, act);
+}
+
+// A token lane's K accesses: columns, weights, biases and the rational's
+// coefficients.  Without coefficients the accesses of a group's lanes
+// interleave (access l + i T), which coalesces best; with them a lane takes a
+// run of K V consecutive columns, so that one set of coefficients (RAT 1), or
+// two where runs straddle activation groups (RAT 2: the second from element
+// `split` of the run on), serves them all.
+template <int V, int RAT, int K> struct TokenCols {
+    static constexpr int kSets = RAT == 2 ? 2 : 1;
+    int col[K], nv[K], split;
+    float w[K][V], b[K][V];
+    Coefs<5, 4> c[kSets];
+
+    __device__ inline void init(const NormArgs &a, int g, int l) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const int first = (RAT ? l * K + i : l + i * a.p.T) * V;
+            nv[i] = min(max(a.D - first, 0), V);
+            col[i] = g * a.D + (nv[i] > 0 ? first : 0);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const bool in = e < nv[i];
+                w[i][e] = in ? (a.w ? a.w[col[i] + e] : 1.0f) : 0.0f;
+                b[i][e] = in && a.b ? a.b[col[i] + e] : 0.0f;
+            }
+        }
+        split = K * V;
+        if constexpr (RAT != 0) {
+            const int group = col[0] / a.dga;
+            c[0] = load_coefs<5, 4>(a.A, a.B, group);
+            if constexpr (RAT == 2) {
+                split = (group + 1) * a.dga - col[0];
+                c[1] = load_coefs<5, 4>(a.A, a.B, min(group + 1, a.ng - 1));
+            }
+        }
+    }
+    // the coefficients of element j of the run
+    __device__ inline Coefs<5, 4> coefs(int j) const {
+        if constexpr (RAT == 2) {
+            Coefs<5, 4> k;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) k.a[i] = j < split ? c[0].a[i] : c[1].a[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k.b[i] = j < split ? c[0].b[i] : c[1].b[i];
+            return k;
+        } else {
+            return c[0];
+        }
     }
 };
 
-// dh and xh of element e.
-template <int V, bool RAT>
-__device__ static inline float slope(float x, float dy, float mean, float rstd, const Cols<V, RAT> &k, int e, int act,
-                                     float *coef, float &xh) {
-    xh = (x - mean) * rstd;
-    const float h = fmaf(xh, k.w[e], k.b[e]);
-    if constexpr (RAT) {
-        return rational_slope(h, dy, k.c, *reinterpret_cast<float (*)[10]>(coef));
-    } else {
-        return dy * act_slope(h, act);
-    }
-}
-
 // ------------------------------------------------------------ reductions
 
-// Sum of v over the T lanes of a slot, in every one of them.  T <= 64: a
-// butterfly within the wave.  Larger T is the whole workgroup: one value per
-// wave through LDS (`lds` is 2 x 16 floats x NV used alternately, so that one
-// barrier per call is enough).
+// v of the lane that the DPP control names (all lanes are named by some lane).
+template <int CTRL> __device__ static inline float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum of v over aligned runs of T <= 64 lanes (T a power of two), in each of
+// them: within 16 lanes by DPP (quads by permutation, then the mirrored half and
+// the mirrored row, whose lanes already agree), beyond by swapping rows.
+__device__ static inline float lane_sum(float v, int T) {
+    if (T > 1) v += dpp<0xb1>(v);
+    if (T > 2) v += dpp<0x4e>(v);
+    if (T > 4) v += dpp<0x141>(v);
+    if (T > 8) v += dpp<0x140>(v);
+    if (T > 16) {
+        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
+    if (T > 32) {
+        const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
+    return v;
+}
+
+// Sum of v over the T lanes of a slot, in every one of them.  T > 64 is the
+// whole workgroup: one value per wave through LDS (two buffers of 16 NV floats
+// used in turn, so that one barrier per call is enough).
 template <int NV>
 __device__ static inline void slot_sum(float (&v)[NV], int T, float *lds, int &phase) {
-    const int top = T < 64 ? T : 64;
-    for (int o = top >> 1; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor(v[i], o, 64);
+    for (int i = 0; i < NV; ++i) v[i] = lane_sum(v[i], T);
     if (T > 64) {
         float *buf = lds + phase * 16 * NV;
         phase ^= 1;
@@ -204,73 +288,82 @@ __device__ static inline void slot_sum(float (&v)[NV], int T, float *lds, int &p
     }
 }
 
-// Sums of NV values over each group of a column block of TX x TY lanes, in
-// every lane of the group.  `lds` holds NV * (threads + groups) values.
-template <class R, int NV>
-__device__ static inline void group_sum(R (&v)[NV], const NormPlan &p, int vpg, int ngroups, int jg, char *ldsb) {
+// A lane's place in a column block.
+struct Place {
+    int c0, width;           // the block's columns
+    int g0, ngroups;         // its groups (the first and last may reach outside it)
+    int col, nv, tx, ty;
+    __device__ inline Place(const NormArgs &a, int cb) {
+        const NormPlan &p = a.p;
+        const int t = (int)threadIdx.x;
+        ty = t / p.TX;
+        tx = t - ty * p.TX;
+        c0 = cb * p.width;
+        width = min(p.width, a.C - c0);
+        g0 = c0 / a.D;
+        ngroups = (c0 + width - 1) / a.D - g0 + 1;
+        col = c0 + tx * p.vec;
+        nv = ty < p.TY ? min(max(width - tx * p.vec, 0), p.vec) : 0;
+    }
+    // group of element e, counted from g0 (clamped for absent elements)
+    __device__ inline int group(const NormArgs &a, int e) const {
+        return min(col + e, c0 + width - 1) / a.D - g0;
+    }
+};
+
+// Sums over each group of a column block: v[i][e] is value i of element e (of
+// the whole access unless MIXED) in this lane; afterwards the sum over the
+// element's group, of its columns in this block.  `lds` holds NV * (E *
+// threads + groups) values, E = V if MIXED else 1.
+template <class R, int NV, int V, bool MIXED>
+__device__ static inline void group_sum(R (&v)[NV][MIXED ? V : 1], const NormArgs &a, const Place &q, char *ldsb) {
+    constexpr int E = MIXED ? V : 1;
+    const NormPlan &p = a.p;
     R *red = reinterpret_cast<R *>(ldsb);
-    R *res = red + NV * p.block;
+    R *res = red + NV * E * p.block;
     const int t = (int)threadIdx.x, l = t & (p.L - 1);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) red[i * p.block + t] = v[i];
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) red[(i * E + e) * p.block + t] = v[i][e];
     __syncthreads();
-    const int count = vpg * p.TY;
-    for (int j = t / p.L; j < ngroups; j += p.block / p.L) {
+    for (int j = t / p.L; j < q.ngroups; j += p.block / p.L) {
+        // the group's columns in this block; accesses unless MIXED
+        int lo = max((q.g0 + j) * a.D - q.c0, 0), hi = min((q.g0 + j + 1) * a.D - q.c0, q.width);
+        if constexpr (!MIXED) lo /= V, hi /= V;
+        const int n = hi - lo, count = n * p.TY;
         R s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = 0;
-        for (int q = l; q < count; q += p.L) {
-            const int row = q / vpg, at = row * p.TX + j * vpg + (q - row * vpg);
+        for (int u = l; u < count; u += p.L) {
+            const int row = u / n, c = lo + (u - row * n);
+            const int at = MIXED ? (c % V) * p.block + row * p.TX + c / V : row * p.TX + c;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] += red[i * p.block + at];
+            for (int i = 0; i < NV; ++i) s[i] += red[i * E * p.block + at];
         }
         for (int o = p.L >> 1; o > 0; o >>= 1)
 #pragma unroll
             for (int i = 0; i < NV; ++i) s[i] += __shfl_xor(s[i], o, 64);
         if (l == 0) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) res[i * p.gpb + j] = s[i];
+            for (int i = 0; i < NV; ++i) res[i * p.groups + j] = s[i];
         }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = res[i * p.gpb + jg];
+    for (int e = 0; e < E; ++e) {
+        const int j = q.group(a, e);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i][e] = res[i * p.groups + j];
+    }
 }
 
-// A lane's place in a column block: columns, group within the block, row lane.
-struct Place {
-    int g0, ngroups, vpg;    // first group of the block, groups in it, accesses per group in it
-    int jg, col, nv, ty;
-    bool on;
-    __device__ inline Place(const NormArgs &a, int cb) {
-        const NormPlan &p = a.p;
-        const int t = (int)threadIdx.x, tx = t % p.TX;
-        ty = t / p.TX;
-        int vi;
-        if (p.bpg == 1) {
-            g0 = cb * p.gpb;
-            ngroups = min(p.gpb, a.G - g0);
-            vpg = p.vpg;
-            jg = tx / vpg;
-            vi = tx - jg * vpg;
-        } else {
-            g0 = cb / p.bpg;
-            ngroups = 1;
-            vpg = p.TX;
-            jg = 0;
-            vi = (cb - g0 * p.bpg) * p.TX + tx;
-        }
-        on = ty < p.TY && jg < ngroups && vi < p.vpg;
-        if (jg >= ngroups) jg = 0;
-        col = (g0 + jg) * a.D + vi * p.vec;
-        nv = on ? min(p.vec, a.D - vi * p.vec) : 0;
-    }
-    // index of the lane's access in a row of all groups
-    __device__ inline int64_t access(const NormArgs &a) const {
-        const int g = col / a.D;
-        return (int64_t)g * a.p.vpg + (col - g * a.D) / a.p.vec;
-    }
-};
+// The groups' sums of a block as group_sum left them in LDS, by the first
+// threads: split plans store them as one part of the group's.
+template <class R, int NV, int E>
+__device__ static inline const R *group_results(const NormPlan &p, const char *ldsb) {
+    return reinterpret_cast<const R *>(ldsb) + NV * E * p.block;
+}
 
 __device__ static inline const char *at(const void *base, int64_t e) {
     return static_cast<const char *>(base) + e * ES;
@@ -293,31 +386,79 @@ __device__ static inline void sample_block(int64_t b, int ncb, int64_t N, int64_
     }
 }
 
+// Split: the block's group sums (pairs in LDS after group_sum) as this chunk's
+// and block's part of each group.
+template <int E>
+__device__ static inline void store_parts(const NormArgs &a, const Place &q, int64_t n, int64_t c, int cb,
+                                          const char *lds) {
+    const NormPlan &p = a.p;
+    const double *res = group_results<double, 2, E>(p, lds);
+    for (int j = (int)threadIdx.x; j < q.ngroups; j += p.block) {
+        const int g = q.g0 + j, part = cb - g * a.D / p.width;
+        double *o = a.stats + 2 * (((n * a.G + g) * p.chunks + c) * p.parts + part);
+        o[0] = res[j];
+        o[1] = res[p.groups + j];
+    }
+}
+
+// Split: the sum of a group's parts, by a workgroup of 256; in thread 0.
+__device__ static inline void add_parts(const NormArgs &a, int64_t ng, double &s0, double &s1) {
+    __shared__ double red[2][4];
+    const NormPlan &p = a.p;
+    const int g = (int)(ng % a.G), t = (int)threadIdx.x;
+    const int parts = ((g + 1) * a.D - 1) / p.width - g * a.D / p.width + 1;  // blocks the group lies in
+    const int64_t count = p.chunks * p.parts;
+    s0 = s1 = 0.0;
+#pragma unroll 4
+    for (int64_t i = t; i < count; i += 256) {
+        if ((int)(i % p.parts) >= parts) continue;
+        const double *o = a.stats + 2 * (ng * count + i);
+        s0 += o[0];
+        s1 += o[1];
+    }
+    for (int o = 32; o > 0; o >>= 1) {
+        s0 += __shfl_xor(s0, o, 64);
+        s1 += __shfl_xor(s1, o, 64);
+    }
+    if ((t & 63) == 0) red[0][t >> 6] = s0, red[1][t >> 6] = s1;
+    __syncthreads();
+    if (t == 0) {
+        s0 = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+        s1 = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+    }
+}
+
 #if !GRKAN_NORM_BACKWARD
 // ============================================================ forward
 
-template <int V, bool RAT, int K>
-__global__ __launch_bounds__(512) void grkan_norm_token_fwd_kernel(NormArgs a) {
+template <int V, int RAT, int K>
+__global__ __launch_bounds__(K * V == 1 ? 1024 : 256) void grkan_norm_token_fwd_kernel(NormArgs a) {
     __shared__ float lds[2 * 16];
     const NormPlan &p = a.p;
     const int t = (int)threadIdx.x, l = t & (p.T - 1);
     const int64_t slot = (int64_t)blockIdx.x * p.spw + t / p.T;
     const int g = (int)(slot % a.G);
     const int64_t step = p.blocks * p.spw / a.G;
-    Cols<V, RAT> k[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int vi = l + i * p.T;
-        k[i].init(a, g * a.D + min(vi, p.vpg - 1) * V, vi < p.vpg ? min(V, a.D - vi * V) : 0);
-    }
     const float inv = 1.0f / (float)a.D;
     int phase = 0;
+    TokenCols<V, RAT, K> k;
+    k.init(a, g, l);
     // T <= 64: a slot ends when its samples do; larger T: the slot is the
-    // workgroup, and n is the same in all its lanes
-    for (int64_t n = slot / a.G; n < a.N; n += step) {
-        Pack<V> x[K];
+    // workgroup, and n is the same in all its lanes.  The next sample's values
+    // are on their way while this one's are reduced.
+    int64_t n = slot / a.G;
+    Pack<V> next[K];
 #pragma unroll
-        for (int i = 0; i < K; ++i) x[i] = Pack<V>::load(at(a.x, n * a.xs + k[i].col), k[i].nv);
+    for (int i = 0; i < K; ++i)
+        next[i] = Pack<V>::load(at(a.x, (n < a.N ? n : 0) * a.xs + k.col[i]), n < a.N ? k.nv[i] : 0);
+    for (; n < a.N; n += step) {
+        Pack<V> x[K];
+        const int64_t nn = n + step < a.N ? n + step : n;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            x[i] = next[i];
+            next[i] = Pack<V>::load(at(a.x, nn * a.xs + k.col[i]), k.nv[i]);
+        }
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < K; ++i)
@@ -327,12 +468,14 @@ __global__ __launch_bounds__(512) void grkan_norm_token_fwd_kernel(NormArgs a) {
         const float mean = s[0] * inv;
         float m2[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < K; ++i)
+        for (int i = 0; i < K; ++i) {
+            x[i].repack();
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float d = e < k[i].nv ? x[i].get(e) - mean : 0.0f;
+                const float d = e < k.nv[i] ? x[i].get(e) - mean : 0.0f;
                 m2[0] = fmaf(d, d, m2[0]);
             }
+        }
         slot_sum<1>(m2, p.T, lds, phase);
         const float rstd = rstd_of(m2[0] * inv, a.eps);
         if (l == 0) {
@@ -340,117 +483,134 @@ __global__ __launch_bounds__(512) void grkan_norm_token_fwd_kernel(NormArgs a) {
             a.rstd[n * a.G + g] = rstd;
         }
 #pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (k[i].nv > 0) apply_forward<V, RAT>(x[i], mean, rstd, k[i], a.act).store(at(a.y, n * a.C + k[i].col), k[i].nv);
+        for (int i = 0; i < K; ++i) {
+            x[i].repack();
+            if (k.nv[i] > 0) {
+                float f[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    f[e] = act_value<RAT != 0>(fmaf((x[i].get(e) - mean) * rstd, k.w[i][e], k.b[i][e]), a.act,
+                                               k.coefs(i * V + e));
+                Pack<V>::from(f).store(at(a.y, n * a.C + k.col[i]), k.nv[i]);
+            }
+        }
     }
 }
 
-template <int V, bool RAT, int R>
+template <int V, bool RAT, bool MIXED, int R>
 __global__ __launch_bounds__(1024) void grkan_norm_slab_fwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
-    const int64_t total = p.blocks;
     const float inv = 1.0f / ((float)a.D * (float)a.S);
-    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
         int64_t n;
         int cb;
         sample_block(b, p.ncb, a.N, n, cb);
         if (n >= a.N) continue;  // the same for the whole workgroup
         const Place q(a, cb);
-        Cols<V, RAT> k;
-        k.init(a, q.col, q.nv);
         const int S = (int)a.S;
         Pack<V> x[R];
-        float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = q.ty + i * p.TY;
-            x[i] = Pack<V>::load(at(a.x, n * a.xs + (r < S ? r : 0) * a.xr + k.col), r < S ? k.nv : 0);
+            x[i] = Pack<V>::load(at(a.x, n * a.xs + (r < S ? r : 0) * a.xr + q.col), r < S ? q.nv : 0);
         }
+        Cols<V, RAT> k;
+        k.init(a, q.col, q.nv);
+        // absent elements are zeros, and absent rows
+        float s[1][E] = {};
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int e = 0; e < V; ++e) s[0] += x[i].get(e);
-        group_sum<float, 1>(s, p, q.vpg, q.ngroups, q.jg, lds);
-        const float mean = s[0] * inv;
-        s[0] = 0.0f;
+            for (int e = 0; e < V; ++e) s[0][MIXED ? e : 0] += x[i].get(e);
+        group_sum<float, 1, V, MIXED>(s, a, q, lds);
+        Stats<V, MIXED> st;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            st.mean[e] = s[0][e] * inv;
+            s[0][e] = 0.0f;
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            x[i].repack();
             const int nv = q.ty + i * p.TY < S ? k.nv : 0;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float d = e < nv ? x[i].get(e) - mean : 0.0f;
-                s[0] = fmaf(d, d, s[0]);
+                const float d = e < nv ? x[i].get(e) - st.m(e) : 0.0f;
+                s[0][MIXED ? e : 0] = fmaf(d, d, s[0][MIXED ? e : 0]);
             }
         }
-        group_sum<float, 1>(s, p, q.vpg, q.ngroups, q.jg, lds);
-        const float rstd = rstd_of(s[0] * inv, a.eps);
-        if (q.on && q.ty == 0 && q.col % a.D == 0) {
-            a.mean[n * a.G + q.g0 + q.jg] = mean;
-            a.rstd[n * a.G + q.g0 + q.jg] = rstd;
+        group_sum<float, 1, V, MIXED>(s, a, q, lds);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            st.rstd[e] = rstd_of(s[0][e] * inv, a.eps);
+            if (q.ty == 0 && e < q.nv && (q.col + e) % a.D == 0) {
+                const int64_t ng = n * a.G + (q.col + e) / a.D;
+                a.mean[ng] = st.mean[e];
+                a.rstd[ng] = st.rstd[e];
+            }
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = q.ty + i * p.TY;
+            x[i].repack();
             if (r < S && k.nv > 0)
-                apply_forward<V, RAT>(x[i], mean, rstd, k, a.act).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
+                apply_forward<V, RAT, MIXED>(x[i], st, k, a.act).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
         }
     }
 }
 
-// Split, first pass: fp64 sums of x and x^2 of a row chunk of a column block.
-template <int V>
+// Split, first pass: sums of x and x^2 of a row chunk of a column block.  A
+// lane sums the differences from its first row (and their squares) in fp32,
+// column by column, over at most ~64 rows, and turns them into fp64 sums of x
+// and x^2 about zero at the end: three fp32 operations an element, with the
+// digits of a mean far from zero kept out of them.
+template <int V, bool MIXED>
 __global__ __launch_bounds__(256) void grkan_norm_sums_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int cb = (int)(b % p.ncb);
         const int64_t nc = b / p.ncb, n = nc / p.chunks, c = nc % p.chunks;
         const Place q(a, cb);
-        const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
-        double s[2] = {0.0, 0.0};
-        if (q.nv > 0) {
+        const int64_t r0 = c * p.chunk_rows + q.ty, r1 = min(a.S, (c + 1) * p.chunk_rows);
+        double s[2][E] = {};
+        if (q.nv > 0 && r0 < r1) {
             const char *src = at(a.x, n * a.xs + q.col);
+            const Pack<V> first = Pack<V>::load(src + r0 * a.xr * ES, q.nv);
+            float s1[V] = {}, s2[V] = {};
 #pragma unroll 4
-            for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
+            for (int64_t r = r0 + p.TY; r < r1; r += p.TY) {
                 const Pack<V> x = Pack<V>::load(src + r * a.xr * ES, q.nv);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const double f = (double)x.get(e);
-                    s[0] += f;
-                    s[1] = fma(f, f, s[1]);
+                    const float d = x.get(e) - first.get(e);
+                    s1[e] += d;
+                    s2[e] = fmaf(d, d, s2[e]);
                 }
             }
+            const double m = (double)((r1 - r0 + p.TY - 1) / p.TY);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const double f = (double)first.get(e), d = (double)s1[e];
+                s[0][MIXED ? e : 0] += fma(m, f, d);
+                s[1][MIXED ? e : 0] += fma(f, fma(m, f, 2.0 * d), (double)s2[e]);
+            }
         }
-        group_sum<double, 2>(s, p, q.vpg, q.ngroups, q.jg, lds);
-        const int first = p.bpg == 1 ? q.jg * p.vpg : 0;
-        if (q.ty == 0 && (int)threadIdx.x % p.TX == first && (int)threadIdx.x < p.TX && q.jg < q.ngroups) {
-            const int part = p.bpg == 1 ? 0 : cb % p.bpg;
-            double *o = a.stats + 2 * (((n * a.G + q.g0 + q.jg) * p.chunks + c) * p.bpg + part);
-            o[0] = s[0];
-            o[1] = s[1];
-        }
+        group_sum<double, 2, V, MIXED>(s, a, q, lds);
+        store_parts<E>(a, q, n, c, cb, lds);
     }
 }
 
-// Split, second step: one wave per (sample, group) adds the chunks' sums.
+// Split, second step: a workgroup per (sample, group) adds the parts.
 __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
-    const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (ng >= a.N * a.G) return;
-    const int lane = (int)threadIdx.x & 63;
-    const int64_t count = a.p.chunks * a.p.bpg;
-    double s0 = 0.0, s1 = 0.0;
-    for (int64_t i = lane; i < count; i += 64) {
-        const double *o = a.stats + 2 * (ng * count + i);
-        s0 += o[0];
-        s1 += o[1];
-    }
-    for (int o = 32; o > 0; o >>= 1) {
-        s0 += __shfl_xor(s0, o, 64);
-        s1 += __shfl_xor(s1, o, 64);
-    }
-    if (lane == 0) {
+    const int64_t ng = blockIdx.x;
+    double s0, s1;
+    add_parts(a, ng, s0, s1);
+    if (threadIdx.x == 0) {
         const double m = (double)a.D * (double)a.S, mean = s0 / m;
         a.mean[ng] = (float)mean;
         a.rstd[ng] = rstd_of((float)(s1 / m - mean * mean), a.eps);
@@ -458,7 +618,7 @@ __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
 }
 
 // Split, third step: y over a row chunk of a column block.
-template <int V, bool RAT>
+template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(256) void grkan_norm_apply_fwd_kernel(NormArgs a) {
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
@@ -469,123 +629,178 @@ __global__ __launch_bounds__(256) void grkan_norm_apply_fwd_kernel(NormArgs a) {
         if (q.nv == 0) continue;
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
-        const float mean = a.mean[n * a.G + q.g0 + q.jg], rstd = a.rstd[n * a.G + q.g0 + q.jg];
+        Stats<V, MIXED> st;
+#pragma unroll
+        for (int e = 0; e < Stats<V, MIXED>::N; ++e) {
+            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+            st.mean[e] = a.mean[ng];
+            st.rstd[e] = a.rstd[ng];
+        }
         const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
 #pragma unroll 4
         for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY)
-            apply_forward<V, RAT>(Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv), mean, rstd, k, a.act)
+            apply_forward<V, RAT, MIXED>(Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv), st, k, a.act)
                 .store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
     }
 }
 
-template <int V, bool RAT>
-hipError_t forward_vec(const NormArgs &a, hipStream_t s) {
+template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hipStream_t s) {
+    if constexpr (RAT == 2 && K * V < 4) {  // the plan straddles with runs of 4 or more only
+        return hipErrorInvalidValue;
+    } else {
+        hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, K>), dim3((unsigned)a.p.blocks), dim3((unsigned)a.p.block),
+                           0, s, a);
+        return hipGetLastError();
+    }
+}
+
+template <int V, int RAT> hipError_t launch_token(const NormArgs &a, hipStream_t s) {
+    switch (a.p.K) {
+        case 1: return launch_token_k<V, RAT, 1>(a, s);
+        case 2: return launch_token_k<V, RAT, 2>(a, s);
+        case 3: return launch_token_k<V, RAT, 3>(a, s);
+        default: return launch_token_k<V, RAT, 4>(a, s);
+    }
+}
+
+template <int V, bool RAT, bool MIXED>
+hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
     const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20))), block((unsigned)p.block);
-    if (p.kind == kNormToken) {
-        const dim3 tgrid((unsigned)p.blocks);
-        switch (p.K) {
-            case 1: hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, 1>), tgrid, block, 0, s, a); break;
-            case 2: hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, 2>), tgrid, block, 0, s, a); break;
-            case 3: hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, 3>), tgrid, block, 0, s, a); break;
-            default: hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, 4>), tgrid, block, 0, s, a); break;
-        }
-        return hipGetLastError();
-    }
     if (p.kind == kNormSlab) {
         if (p.regs <= 4)
-            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, 4>), grid, block, p.lds, s, a);
+            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 4>), grid, block, p.lds, s, a);
+        else if (p.regs <= 8)
+            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 8>), grid, block, p.lds, s, a);
         else
-            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, 16>), grid, block, p.lds, s, a);
+            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 16>), grid, block, p.lds, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((grkan_norm_sums_kernel<V>), grid, block, p.lds, s, a);
+    hipLaunchKernelGGL((grkan_norm_sums_kernel<V, MIXED>), grid, block, p.lds, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grkan_norm_stats_kernel, dim3((unsigned)((a.N * a.G + 3) / 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(grkan_norm_stats_kernel, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((grkan_norm_apply_fwd_kernel<V, RAT>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((grkan_norm_apply_fwd_kernel<V, RAT, MIXED>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
 #else
 // ============================================================ backward
 
-// Writes a lane's column sums, added over the row lanes of the workgroup (and,
-// for token plans, over its slots of one group), to row `prow` of the
-// partials.  `lds` holds block * min(values, kBatch) floats.
-constexpr int kBatch = 13;
-
-template <int V, bool RAT>
-__device__ static inline void store_col_sums(const NormArgs &a, const ColSums<V, RAT> &cs, int width, int depth,
-                                             int lane, int64_t prow, int col, int nv, int64_t access, float *lds) {
-    constexpr int NVAL = ColSums<V, RAT>::kValues;
+// Adds NVAL sums of a lane over `depth` lanes `width` apart (row lanes, or a
+// token plan's slots of one group) and writes the first n of them to row
+// `prow` of the partials, value i of lane x < width at its at + i * pitch.  All
+// threads share the additions.  `lds` holds block * (NVAL + 3) floats.
+template <int NVAL>
+__device__ static inline void store_sums(const NormArgs &a, const float (&v)[NVAL], int width, int depth, int64_t prow,
+                                         int64_t at, int n, int64_t pitch, float *lds) {
     const int t = (int)threadIdx.x, block = a.p.block;
-    const bool writer = lane == 0;
-    float *out = a.partials + prow * norm_partial_row(a.p, a.C, RAT);
+    int *where = reinterpret_cast<int *>(lds + NVAL * block);
+    __syncthreads();
 #pragma unroll
-    for (int i0 = 0; i0 < NVAL; i0 += kBatch) {
-        __syncthreads();
-#pragma unroll
-        for (int i = i0; i < NVAL && i < i0 + kBatch; ++i) lds[(i - i0) * block + t] = nv > 0 ? cs.get(i) : 0.0f;
-        __syncthreads();
-        if (writer && nv > 0) {
-#pragma unroll
-            for (int i = i0; i < NVAL && i < i0 + kBatch; ++i) {
-                float s = 0.0f;
-                for (int q = 0; q < depth; ++q) s += lds[(i - i0) * block + t + q * width];
-                if (i < V) {
-                    if (i < nv) out[col + i] = s;
-                } else if (i < 2 * V) {
-                    if (i - V < nv) out[a.C + col + i - V] = s;
-                } else {
-                    out[2 * (int64_t)a.C + (int64_t)(i - 2 * V) * a.p.cv + access] = s;
-                }
-            }
-        }
+    for (int i = 0; i < NVAL; ++i) lds[i * block + t] = v[i];
+    where[t] = n;
+    where[block + t] = (int)(uint32_t)at;
+    where[2 * block + t] = (int)(uint32_t)((uint64_t)at >> 32);
+    __syncthreads();
+    float *out = a.partials + prow * a.p.row;
+    for (int u = t; u < NVAL * width; u += block) {
+        const int i = u / width, x = u - i * width;
+        if (i >= where[x]) continue;
+        float s = 0.0f;
+        for (int q = 0; q < depth; ++q) s += lds[i * block + x + q * width];
+        const int64_t o = (int64_t)((uint64_t)(uint32_t)where[block + x] | (uint64_t)(uint32_t)where[2 * block + x] << 32);
+        out[o + i * pitch] = s;
     }
 }
 
-template <int V, bool RAT, int K>
-__global__ __launch_bounds__(512) void grkan_norm_token_bwd_kernel(NormArgs a) {
+template <int V, bool RAT>
+__device__ static inline void store_col_sums(const NormArgs &a, const ColSums<V, RAT> &cs, const Place &q, int cb,
+                                             int64_t prow, char *ldsb) {
+    float *lds = reinterpret_cast<float *>(ldsb);
+    const NormPlan &p = a.p;
+    store_sums<V>(a, cs.dw, p.TX, p.TY, prow, q.col, q.nv, 1, lds);
+    store_sums<V>(a, cs.db, p.TX, p.TY, prow, a.C + (int64_t)q.col, q.nv, 1, lds);
+    if constexpr (RAT)
+        store_sums<10>(a, cs.coef, p.TX, p.TY, prow, 2 * (int64_t)a.C + (int64_t)cb * p.TX + q.tx, q.nv > 0 ? 10 : 0,
+                       p.cv, lds);
+}
+
+// The second bound keeps two or three waves on a SIMD: left alone, the compiler
+// evaluates all of a lane's elements side by side, in 270 registers for 12.
+template <int V, int RAT, int K>
+__global__ __launch_bounds__(K * V == 1 ? 1024 : 256, K * V == 1 ? 1 : (RAT == 2 || K * V > 12 ? 2 : 3)) void
+grkan_norm_token_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char ldsb[];
     float *lds = reinterpret_cast<float *>(ldsb);
+    constexpr int kSets = RAT == 2 ? 2 : 1;
     const NormPlan &p = a.p;
     const int t = (int)threadIdx.x, l = t & (p.T - 1), sl = t / p.T;
     const int64_t slot = (int64_t)blockIdx.x * p.spw + sl;
     const int g = (int)(slot % a.G);
     const int64_t step = p.blocks * p.spw / a.G;
-    Cols<V, RAT> k[K];
-    ColSums<V, RAT> cs[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int vi = l + i * p.T;
-        k[i].init(a, g * a.D + min(vi, p.vpg - 1) * V, vi < p.vpg ? min(V, a.D - vi * V) : 0);
-        cs[i].clear();
-    }
     const float inv = 1.0f / (float)a.D;
     int phase = 0;
-    for (int64_t n = slot / a.G; n < a.N; n += step) {
-        const float mean = a.mean[n * a.G + g], rstd = a.rstd[n * a.G + g];
-        Pack<V> x[K], dy[K];
+    TokenCols<V, RAT, K> k;
+    k.init(a, g, l);
+    SlopeCoefs sc;
+    if constexpr (RAT == 1) sc.init(k.c[0]);
+    float dw[K][V] = {}, db[K][V] = {}, coef[kSets][RAT ? 10 : 1] = {};
+    int64_t n = slot / a.G;
+    Pack<V> nx[K], ndy[K];
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t m, bool any) {
+        nmean = any ? a.mean[m * a.G + g] : 0.0f;
+        nrstd = any ? a.rstd[m * a.G + g] : 0.0f;
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            x[i] = Pack<V>::load(at(a.x, n * a.xs + k[i].col), k[i].nv);
-            dy[i] = Pack<V>::load(at(a.dy, n * a.ds + k[i].col), k[i].nv);
+            nx[i] = Pack<V>::load(at(a.x, m * a.xs + k.col[i]), any ? k.nv[i] : 0);
+            ndy[i] = Pack<V>::load(at(a.dy, m * a.ds + k.col[i]), any ? k.nv[i] : 0);
         }
+    };
+    fetch(n < a.N ? n : 0, n < a.N);
+    for (; n < a.N; n += step) {
+        const float mean = nmean, rstd = nrstd;
+        Pack<V> x[K], dy[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) x[i] = nx[i], dy[i] = ndy[i];
+        fetch(n + step < a.N ? n + step : n, true);
         float m[2] = {0.0f, 0.0f};
         float tt[K][V], xh[K][V];
 #pragma unroll
         for (int i = 0; i < K; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const bool in = e < k[i].nv;
-                const float dh = slope<V, RAT>(in ? x[i].get(e) : mean, in ? dy[i].get(e) : 0.0f, mean, rstd, k[i], e,
-                                               a.act, cs[i].coef, xh[i][e]);
-                cs[i].db[e] += dh;
-                cs[i].dw[e] = fmaf(dh, xh[i][e], cs[i].dw[e]);
-                tt[i][e] = dh * k[i].w[e];
+                // absent elements: dy = 0, and xh = 0 in place of -mean rstd
+                xh[i][e] = e < k.nv[i] ? (x[i].get(e) - mean) * rstd : 0.0f;
+                float h = fmaf(xh[i][e], k.w[i][e], k.b[i][e]), dh;
+                const float gr = dy[i].get(e);
+                if constexpr (RAT == 0) {
+                    dh = gr * act_slope(h, a.act);
+                } else if constexpr (RAT == 1) {
+                    dh = rational_slope(h, gr, sc, *reinterpret_cast<float (*)[10]>(coef[0]));
+                } else {
+                    const int j = i * V + e;
+                    // (one element after another, as in rational_slope)
+                    asm volatile("" : "+v"(h) : "v"(coef[0][0]), "v"(coef[0][1]), "v"(coef[0][2]), "v"(coef[0][3]),
+                                 "v"(coef[0][4]), "v"(coef[0][5]), "v"(coef[0][6]), "v"(coef[0][7]), "v"(coef[0][8]),
+                                 "v"(coef[0][9]), "v"(coef[1][0]), "v"(coef[1][1]), "v"(coef[1][2]), "v"(coef[1][3]),
+                                 "v"(coef[1][4]), "v"(coef[1][5]), "v"(coef[1][6]), "v"(coef[1][7]), "v"(coef[1][8]),
+                                 "v"(coef[1][9]));
+                    sc.init(k.coefs(j));
+                    float term[10] = {};
+                    dh = rational_slope(h, gr, sc, term);
+#pragma unroll
+                    for (int q = 0; q < 10; ++q) {
+                        coef[0][q] += j < k.split ? term[q] : 0.0f;
+                        coef[1][q] += j < k.split ? 0.0f : term[q];
+                    }
+                }
+                db[i][e] += dh;
+                dw[i][e] = fmaf(dh, xh[i][e], dw[i][e]);
+                tt[i][e] = dh * k.w[i][e];
                 m[0] += tt[i][e];
                 m[1] = fmaf(tt[i][e], xh[i][e], m[1]);
             }
@@ -593,29 +808,37 @@ __global__ __launch_bounds__(512) void grkan_norm_token_bwd_kernel(NormArgs a) {
         const float m1 = m[0] * inv, m2 = m[1] * inv;
 #pragma unroll
         for (int i = 0; i < K; ++i)
-            if (k[i].nv > 0) {
+            if (k.nv[i] > 0) {
                 float f[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) f[e] = rstd * (tt[i][e] - m1 - xh[i][e] * m2);
-                Pack<V>::from(f).store(at(a.y, n * a.C + k[i].col), k[i].nv);
+                for (int e = 0; e < V; ++e) f[e] = rstd * (tt[i][e] - fmaf(xh[i][e], m2, m1));
+                Pack<V>::from(f).store(at(a.y, n * a.C + k.col[i]), k.nv[i]);
             }
     }
     // slots of one group in this workgroup: spw / G of them, G slots apart
-    // (slot = workgroup * spw + sl, spw a multiple of G), or each its own
-    const int depth = p.spw > a.G ? p.spw / a.G : 1;
-    const int64_t prow = p.spw > a.G ? (int64_t)blockIdx.x : slot / a.G;
-    const int first = p.spw > a.G ? (sl < a.G ? 0 : 1) : 0;
+    // (slot = workgroup * spw + sl, spw a multiple of G), or each its own;
+    // either way the workgroup's sums lie in one row of the partials
+    const bool shared = p.spw > a.G;
+    const int width = shared ? a.G * p.T : p.spw * p.T, depth = shared ? p.spw / a.G : 1;
+    const int64_t prow = shared ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * p.spw / a.G;
+    const int64_t coefs0 = 2 * (int64_t)a.C;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const int vi = l + i * p.T;
-        store_col_sums<V, RAT>(a, cs[i], a.G * p.T, depth, first, prow, k[i].col, k[i].nv,
-                               (int64_t)g * p.vpg + vi, lds);
+        store_sums<V>(a, dw[i], width, depth, prow, k.col[i], k.nv[i], 1, lds);
+        store_sums<V>(a, db[i], width, depth, prow, a.C + k.col[i], k.nv[i], 1, lds);
+    }
+    if constexpr (RAT != 0) {
+#pragma unroll
+        for (int q = 0; q < kSets; ++q)
+            store_sums<10>(a, coef[q], width, depth, prow, coefs0 + 10 * q * p.cv + (int64_t)g * p.vpg + l,
+                           k.nv[0] > 0 ? 10 : 0, p.cv, lds);
     }
 }
 
-template <int V, bool RAT, int R>
+template <int V, bool RAT, bool MIXED, int R>
 __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
     const float inv = 1.0f / ((float)a.D * (float)a.S);
     int64_t n0;
@@ -625,11 +848,12 @@ __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
     const Place q(a, cb);
     Cols<V, RAT> k;
     k.init(a, q.col, q.nv);
+    SlopeCoefs sc;
+    if constexpr (RAT) sc.init(k.c);
     ColSums<V, RAT> cs;
     cs.clear();
     const int S = (int)a.S;
     for (int64_t n = n0; n < a.N; n += p.chunks) {
-        const float mean = a.mean[n * a.G + q.g0 + q.jg], rstd = a.rstd[n * a.G + q.g0 + q.jg];
         Pack<V> x[R], dy[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -639,44 +863,58 @@ __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
             x[i] = Pack<V>::load(at(a.x, n * a.xs + rr * a.xr + k.col), nv);
             dy[i] = Pack<V>::load(at(a.dy, n * a.ds + rr * a.dr + k.col), nv);
         }
-        float m[2] = {0.0f, 0.0f};
-        float tt[R][V];
+        Stats<V, MIXED> st;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+            st.mean[e] = a.mean[ng];
+            st.rstd[e] = a.rstd[ng];
+        }
+        float dh[R][V], sdh[V] = {}, sdx[V] = {};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int nv = q.ty + i * p.TY < S ? k.nv : 0;
+            if (q.ty + i * p.TY < S) {  // rows past the end add nothing
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const bool in = e < nv;
-                float xh;
-                const float dh = slope<V, RAT>(in ? x[i].get(e) : mean, in ? dy[i].get(e) : 0.0f, mean, rstd, k, e,
-                                               a.act, cs.coef, xh);
-                cs.db[e] += dh;
-                cs.dw[e] = fmaf(dh, xh, cs.dw[e]);
-                tt[i][e] = dh * k.w[e];
-                m[0] += tt[i][e];
-                m[1] = fmaf(tt[i][e], xh, m[1]);
+                for (int e = 0; e < V; ++e) {
+                    const float xh = e < k.nv ? (x[i].get(e) - st.m(e)) * st.r(e) : 0.0f;
+                    dh[i][e] = slope<V, RAT>(xh, dy[i].get(e), k, sc, e, a.act, cs.coef);
+                    sdh[e] += dh[i][e];
+                    sdx[e] = fmaf(dh[i][e], xh, sdx[e]);
+                }
             }
         }
-        group_sum<float, 2>(m, p, q.vpg, q.ngroups, q.jg, lds);
-        const float m1 = m[0] * inv, m2 = m[1] * inv;
+        float m[2][E] = {};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            cs.db[e] += sdh[e];
+            cs.dw[e] += sdx[e];
+            m[0][MIXED ? e : 0] = fmaf(sdh[e], k.w[e], m[0][MIXED ? e : 0]);
+            m[1][MIXED ? e : 0] = fmaf(sdx[e], k.w[e], m[1][MIXED ? e : 0]);
+        }
+        group_sum<float, 2, V, MIXED>(m, a, q, lds);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = q.ty + i * p.TY;
+            x[i].repack();
             if (r < S && k.nv > 0) {
                 float f[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) f[e] = rstd * (tt[i][e] - m1 - (x[i].get(e) - mean) * rstd * m2);
+                for (int e = 0; e < V; ++e) {
+                    const float xh = (x[i].get(e) - st.m(e)) * st.r(e);
+                    f[e] = st.r(e) * (dh[i][e] * k.w[e] - fmaf(xh, m[1][MIXED ? e : 0] * inv, m[0][MIXED ? e : 0] * inv));
+                }
                 Pack<V>::from(f).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
             }
         }
     }
-    store_col_sums<V, RAT>(a, cs, p.TX, p.TY, q.ty, n0, k.col, k.nv, q.access(a), reinterpret_cast<float *>(lds));
+    store_col_sums<V, RAT>(a, cs, q, cb, n0, lds);
 }
 
 // Split, first pass: sums of t and t xh and the column sums of a row chunk.
-template <int V, bool RAT>
+template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(256) void grkan_norm_sums_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
@@ -685,64 +923,51 @@ __global__ __launch_bounds__(256) void grkan_norm_sums_bwd_kernel(NormArgs a) {
         const Place q(a, cb);
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
+        SlopeCoefs sc;
+        if constexpr (RAT) sc.init(k.c);
         ColSums<V, RAT> cs;
         cs.clear();
         const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
-        double s[2] = {0.0, 0.0};
         if (q.nv > 0) {
-            const float mean = a.mean[n * a.G + q.g0 + q.jg], rstd = a.rstd[n * a.G + q.g0 + q.jg];
-#pragma unroll 2
+            Stats<V, MIXED> st;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+                st.mean[e] = a.mean[ng];
+                st.rstd[e] = a.rstd[ng];
+            }
+#pragma unroll(RAT ? 1 : 2)
             for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
                 const Pack<V> x = Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv);
                 const Pack<V> dy = Pack<V>::load(at(a.dy, n * a.ds + r * a.dr + k.col), k.nv);
-                float m1 = 0.0f, m2 = 0.0f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const bool in = e < k.nv;
-                    float xh;
-                    const float dh = slope<V, RAT>(in ? x.get(e) : mean, in ? dy.get(e) : 0.0f, mean, rstd, k, e,
-                                                   a.act, cs.coef, xh);
+                    const float xh = e < k.nv ? (x.get(e) - st.m(e)) * st.r(e) : 0.0f;
+                    const float dh = slope<V, RAT>(xh, dy.get(e), k, sc, e, a.act, cs.coef);
                     cs.db[e] += dh;
                     cs.dw[e] = fmaf(dh, xh, cs.dw[e]);
-                    const float t = dh * k.w[e];
-                    m1 += t;
-                    m2 = fmaf(t, xh, m2);
                 }
-                s[0] += (double)m1;
-                s[1] += (double)m2;
             }
         }
-        group_sum<double, 2>(s, p, q.vpg, q.ngroups, q.jg, lds);
-        const int first = p.bpg == 1 ? q.jg * p.vpg : 0;
-        if (q.ty == 0 && (int)threadIdx.x % p.TX == first && (int)threadIdx.x < p.TX && q.jg < q.ngroups) {
-            const int part = p.bpg == 1 ? 0 : cb % p.bpg;
-            double *o = a.stats + 2 * (((n * a.G + q.g0 + q.jg) * p.chunks + c) * p.bpg + part);
-            o[0] = s[0];
-            o[1] = s[1];
+        double s[2][E] = {};
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            s[0][MIXED ? e : 0] += (double)cs.db[e] * (double)k.w[e];
+            s[1][MIXED ? e : 0] += (double)cs.dw[e] * (double)k.w[e];
         }
-        store_col_sums<V, RAT>(a, cs, p.TX, p.TY, q.ty, n * p.chunks + c, k.col, k.nv, q.access(a),
-                               reinterpret_cast<float *>(lds));
+        group_sum<double, 2, V, MIXED>(s, a, q, lds);
+        store_parts<E>(a, q, n, c, cb, lds);
+        store_col_sums<V, RAT>(a, cs, q, cb, n * p.chunks + c, lds);
         __syncthreads();
     }
 }
 
-// Split, second step: <t> and <t xh>, one wave per (sample, group).
+// Split, second step: <t> and <t xh>, a workgroup per (sample, group).
 __global__ __launch_bounds__(256) void grkan_norm_means_kernel(NormArgs a) {
-    const int64_t ng = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (ng >= a.N * a.G) return;
-    const int lane = (int)threadIdx.x & 63;
-    const int64_t count = a.p.chunks * a.p.bpg;
-    double s0 = 0.0, s1 = 0.0;
-    for (int64_t i = lane; i < count; i += 64) {
-        const double *o = a.stats + 2 * (ng * count + i);
-        s0 += o[0];
-        s1 += o[1];
-    }
-    for (int o = 32; o > 0; o >>= 1) {
-        s0 += __shfl_xor(s0, o, 64);
-        s1 += __shfl_xor(s1, o, 64);
-    }
-    if (lane == 0) {
+    const int64_t ng = blockIdx.x;
+    double s0, s1;
+    add_parts(a, ng, s0, s1);
+    if (threadIdx.x == 0) {
         const double m = (double)a.D * (double)a.S;
         a.means[2 * ng] = (float)(s0 / m);
         a.means[2 * ng + 1] = (float)(s1 / m);
@@ -751,7 +976,7 @@ __global__ __launch_bounds__(256) void grkan_norm_means_kernel(NormArgs a) {
 
 // Split, third step: dx over a row chunk.  The slope is formed again: keeping
 // it would cost a write and a read of a tensor.
-template <int V, bool RAT>
+template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(256) void grkan_norm_apply_bwd_kernel(NormArgs a) {
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
@@ -762,20 +987,29 @@ __global__ __launch_bounds__(256) void grkan_norm_apply_bwd_kernel(NormArgs a) {
         if (q.nv == 0) continue;
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
-        const int64_t ng = n * a.G + q.g0 + q.jg;
-        const float mean = a.mean[ng], rstd = a.rstd[ng], m1 = a.means[2 * ng], m2 = a.means[2 * ng + 1];
+        SlopeCoefs sc;
+        if constexpr (RAT) sc.init(k.c);
+        Stats<V, MIXED> st, mm;  // mm: <t> and <t xh>
+#pragma unroll
+        for (int e = 0; e < Stats<V, MIXED>::N; ++e) {
+            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+            st.mean[e] = a.mean[ng];
+            st.rstd[e] = a.rstd[ng];
+            mm.mean[e] = a.means[2 * ng];
+            mm.rstd[e] = a.means[2 * ng + 1];
+        }
         const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
         float unused[10] = {};
-#pragma unroll 2
+#pragma unroll(RAT ? 1 : 2)
         for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
             const Pack<V> x = Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv);
             const Pack<V> dy = Pack<V>::load(at(a.dy, n * a.ds + r * a.dr + k.col), k.nv);
             float f[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                float xh;
-                const float dh = slope<V, RAT>(x.get(e), dy.get(e), mean, rstd, k, e, a.act, unused, xh);
-                f[e] = rstd * (dh * k.w[e] - m1 - xh * m2);
+                const float xh = (x.get(e) - st.m(e)) * st.r(e);
+                const float dh = slope<V, RAT>(xh, dy.get(e), k, sc, e, a.act, unused);
+                f[e] = st.r(e) * (dh * k.w[e] - fmaf(xh, mm.r(e), mm.m(e)));
             }
             Pack<V>::from(f).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
         }
@@ -789,7 +1023,8 @@ template <bool RAT>
 __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
     __shared__ double red[1024];
     const int t = (int)threadIdx.x;
-    const int64_t row = norm_partial_row(a.p, a.C, RAT), P = a.p.prows;
+    const NormPlan &p = a.p;
+    const int64_t row = p.row, P = p.prows;
     const int64_t colblocks = (2 * (int64_t)a.C + 63) / 64;
     if ((int64_t)blockIdx.x < colblocks) {
         const int64_t c = (int64_t)blockIdx.x * 64 + (t & 63);
@@ -813,16 +1048,24 @@ __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
     if constexpr (RAT) {
         const int64_t gk = blockIdx.x - colblocks;
         const int g = (int)(gk / 10), k = (int)(gk % 10);
-        // accesses of columns [g dga, (g + 1) dga): they never straddle a boundary
-        const int64_t c0 = (int64_t)g * a.dga, c1 = c0 + a.dga;
-        const int64_t v0 = c0 / a.D * a.p.vpg + (c0 % a.D + a.p.vec - 1) / a.p.vec;
-        const int64_t v1 = c1 / a.D * a.p.vpg + (c1 % a.D + a.p.vec - 1) / a.p.vec;
-        const int64_t w = v1 - v0;
+        // The lanes whose first column lies in this group, counted over a row
+        // (token: runs of K V columns from each norm group on; else accesses
+        // from each block's first column on); where runs straddle groups also
+        // the second sums of the lanes of the group before.
+        const bool token = p.kind == kNormToken;
+        const int per = token ? a.D : p.width, lanes = token ? p.vpg : p.TX, len = token ? p.K * p.vec : p.vec;
+        auto lane = [&](int64_t c) { return c / per * lanes + (c % per + len - 1) / len; };
         double s = 0.0;
+        for (int set = 0; set <= (p.straddle ? 1 : 0); ++set) {
+            const int64_t g0 = (int64_t)g - set;
+            if (g0 < 0) continue;
+            const int64_t v0 = lane(g0 * a.dga), w = lane((g0 + 1) * a.dga) - v0;
+            const float *src = a.partials + 2 * (int64_t)a.C + (10 * set + k) * p.cv + v0;
 #pragma unroll 8
-        for (int64_t i = t; i < P * w; i += 1024) {
-            const int64_t r = i / w;
-            s += (double)a.partials[r * row + 2 * (int64_t)a.C + k * a.p.cv + v0 + (i - r * w)];
+            for (int64_t i = t; i < P * w; i += 1024) {
+                const int64_t r = i / w;
+                s += (double)src[r * row + (i - r * w)];
+            }
         }
         red[t] = s;
         __syncthreads();
@@ -839,49 +1082,69 @@ __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
     }
 }
 
-template <int V, bool RAT>
-hipError_t backward_vec(const NormArgs &a, hipStream_t s) {
+template <bool RAT> hipError_t launch_columns(const NormArgs &a, hipStream_t s) {
+    if (!a.dw && !a.db && !RAT) return hipSuccess;
+    const dim3 grid((unsigned)((2 * (int64_t)a.C + 63) / 64 + (RAT ? (int64_t)a.ng * 10 : 0)));
+    hipLaunchKernelGGL((grkan_norm_columns_kernel<RAT>), grid, dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hipStream_t s) {
+    // the plan gives a lane 16 elements at most, and straddles with runs of 4 or more only
+    if constexpr ((K > 1 && K * V > 16) || (RAT == 2 && K * V < 4)) {
+        return hipErrorInvalidValue;
+    } else {
+        hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, K>), dim3((unsigned)a.p.blocks), dim3((unsigned)a.p.block),
+                           a.p.lds, s, a);
+        const hipError_t e = hipGetLastError();
+        return e != hipSuccess ? e : launch_columns<RAT != 0>(a, s);
+    }
+}
+
+template <int V, int RAT> hipError_t launch_token(const NormArgs &a, hipStream_t s) {
+    switch (a.p.K) {
+        case 1: return launch_token_k<V, RAT, 1>(a, s);
+        case 2: return launch_token_k<V, RAT, 2>(a, s);
+        case 3: return launch_token_k<V, RAT, 3>(a, s);
+        default: return launch_token_k<V, RAT, 4>(a, s);
+    }
+}
+
+template <int V, bool RAT, bool MIXED>
+hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
     const dim3 block((unsigned)p.block);
     hipError_t e;
-    if (p.kind == kNormToken) {
+    if (p.kind == kNormSlab) {
         const dim3 grid((unsigned)p.blocks);
-        switch (p.K) {
-            case 1: hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, 1>), grid, block, p.lds, s, a); break;
-            case 2: hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, 2>), grid, block, p.lds, s, a); break;
-            case 3: hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, 3>), grid, block, p.lds, s, a); break;
-            default: hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, 4>), grid, block, p.lds, s, a); break;
-        }
-    } else if (p.kind == kNormSlab) {
-        const dim3 grid((unsigned)p.blocks);
-        if (p.regs <= 2)
-            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, 2>), grid, block, p.lds, s, a);
+        if (p.regs <= 3)
+            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 3>), grid, block, p.lds, s, a);
+        else if (p.regs <= 5)
+            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 5>), grid, block, p.lds, s, a);
         else
-            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, 8>), grid, block, p.lds, s, a);
+            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 8>), grid, block, p.lds, s, a);
     } else {
         const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20)));
-        hipLaunchKernelGGL((grkan_norm_sums_bwd_kernel<V, RAT>), grid, block, p.lds, s, a);
+        hipLaunchKernelGGL((grkan_norm_sums_bwd_kernel<V, RAT, MIXED>), grid, block, p.lds, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(grkan_norm_means_kernel, dim3((unsigned)((a.N * a.G + 3) / 4)), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(grkan_norm_means_kernel, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL((grkan_norm_apply_bwd_kernel<V, RAT>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((grkan_norm_apply_bwd_kernel<V, RAT, MIXED>), grid, block, 0, s, a);
     }
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t groups = RAT ? (int64_t)a.ng * 10 : 0;
-    if (!a.dw && !a.db && !RAT) return hipSuccess;
-    const dim3 rgrid((unsigned)((2 * (int64_t)a.C + 63) / 64 + groups));
-    hipLaunchKernelGGL((grkan_norm_columns_kernel<RAT>), rgrid, dim3(1024), 0, s, a);
-    return hipGetLastError();
+    e = hipGetLastError();
+    return e != hipSuccess ? e : launch_columns<RAT>(a, s);
 }
 #endif
 
-template <int V>
-hipError_t launch_vec(const NormArgs &a, hipStream_t s) {
-#if GRKAN_NORM_BACKWARD
-    return a.act == GRKAN_ACT_RATIONAL ? backward_vec<V, true>(a, s) : backward_vec<V, false>(a, s);
-#else
-    return a.act == GRKAN_ACT_RATIONAL ? forward_vec<V, true>(a, s) : forward_vec<V, false>(a, s);
-#endif
+template <int V, bool RAT> hipError_t launch_vec(const NormArgs &a, hipStream_t s) {
+    if (a.p.kind == kNormToken) {
+        if constexpr (RAT) return a.p.straddle ? launch_token<V, 2>(a, s) : launch_token<V, 1>(a, s);
+        return launch_token<V, 0>(a, s);
+    }
+    if constexpr (V > 1) {
+        if (a.p.mixed) return launch_blocks<V, RAT, true>(a, s);
+    }
+    return launch_blocks<V, RAT, false>(a, s);
 }
 
 }  // namespace
@@ -891,13 +1154,19 @@ template <> hipError_t launch_norm_backward<NormIo>(const NormArgs &a, hipStream
 #else
 template <> hipError_t launch_norm_forward<NormIo>(const NormArgs &a, hipStream_t s) {
 #endif
+    const bool rational = a.act == GRKAN_ACT_RATIONAL;
+    if (!rational) {
+        if (a.p.vec == kMaxV) return launch_vec<kMaxV, false>(a, s);
+        if (a.p.vec == kMaxV / 2 && a.p.kind == kNormToken) return launch_token<kMaxV / 2, 0>(a, s);
+        return hipErrorInvalidValue;
+    }
     switch (a.p.vec) {
         case 8:
-            if constexpr (kMaxV >= 8) return launch_vec<8>(a, s);
+            if constexpr (kMaxV >= 8) return launch_vec<8, true>(a, s);
             return hipErrorInvalidValue;
-        case 4: return launch_vec<4>(a, s);
-        case 2: return launch_vec<2>(a, s);
-        case 1: return launch_vec<1>(a, s);
+        case 4: return launch_vec<4, true>(a, s);
+        case 2: return launch_vec<2, true>(a, s);
+        case 1: return launch_vec<1, true>(a, s);
         default: return hipErrorInvalidValue;
     }
 }

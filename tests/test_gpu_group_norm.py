@@ -18,7 +18,11 @@ SHAPES = [
     # one position: lanes of a wave, of several waves, one lane; ragged accesses
     (1, 1, 768, 1, 8), (5, 1, 192, 8, 8), (3, 1, 37, 1, 1), (2, 1, 10, 10, 10), (7, 1, 48, 3, 8), (4, 1, 4096, 1, 8),
     (300, 1, 96, 1, 8), (130, 1, 1, 1, 1), (6, 1, 1500, 5, 10), (2, 1, 7000, 1, 8), (1100, 1, 64, 4, 8),
+    # one position, activation groups that end inside a lane's columns, or of few channels
+    (20, 1, 1000, 1, 8), (9, 1, 528, 1, 8), (6, 1, 296, 1, 8), (5, 1, 180, 2, 6), (3, 1, 300, 1, 300),
+    (4, 1, 640, 1, 128), (11, 1, 36, 2, 12),
     # one position, a group beyond one workgroup
+    (3, 1, 1100, 1, 1100),
     (2, 1, 20001, 1, 1),
     # several positions, a group in one workgroup
     (2, 7, 32, 4, 8), (3, 197, 96, 1, 8), (2, 49, 320, 32, 8), (9, 5, 33, 3, 3), (1, 2, 8, 8, 8), (17, 3, 24, 2, 4),
