@@ -75,7 +75,6 @@ int pow2_at_most(int64_t v) {
 
 constexpr int kTokenMaxLanes = 256, kTokenMaxAccesses = 4;
 constexpr int64_t kNormWorkgroups = 2048;  // target of the looping kernels: 8 workgroups a CU
-constexpr int64_t kSplitWorkgroups = 1024;
 
 // Largest power of two <= v elements per access such that accesses that start
 // at multiples of `start` columns (and then every v) lie in one activation
@@ -113,7 +112,9 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
                 for (int K = 1; K <= kTokenMaxAccesses; ++K) {
                     const int run = K * v;
                     if (backward && run > 16) break;
-                    if (rational && !straddle && dga % D != 0 && (dga % run != 0 || D % run != 0)) continue;
+                    // (the forward has coefficients per access, the backward per run)
+                    const int unit = backward ? run : v;
+                    if (rational && !straddle && dga % D != 0 && (dga % unit != 0 || D % unit != 0)) continue;
                     if (straddle && (run > dga || run < 4)) continue;
                     int T = 1;
                     while ((int64_t)T * run < D) T *= 2;
@@ -188,20 +189,23 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
             p->kind = kNormSplit;
             p->vec = rational ? rational_vec(vmax, dga, 0) : vmax;
             const int64_t accesses = ceil_div(C, p->vec);
-            // (half the accesses where every column is a group, for the groups' sums in LDS)
+            // Large workgroups, about one (forward) or two a CU, so that few sums
+            // are left to add.  At most 256 accesses across (128 where every column
+            // is a group, for the groups' sums in LDS).
+            const int64_t lanes = backward ? 512 : 1024, wanted = backward ? 512 : 256;
             p->ncb = (int32_t)ceil_div(accesses, D == 1 ? 128 : 256);
             p->TX = (int32_t)ceil_div(accesses, p->ncb);
             p->width = p->TX * p->vec;
             p->ncb = (int32_t)ceil_div(C, p->width);
             p->groups = (int32_t)(p->width / D + 2 < G ? p->width / D + 2 : G);
             p->parts = (int32_t)(D / p->width + 2 < p->ncb ? D / p->width + 2 : p->ncb);
-            int64_t ty = 256 / p->TX;
+            int64_t ty = lanes / p->TX;
             if (ty > S) ty = S;
             p->TY = (int32_t)ty;
             p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
-            // chunks of 4 to 64 rows a lane
-            int64_t chunks = ceil_div(kSplitWorkgroups, N * p->ncb);
-            const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 64 * ty);
+            // chunks of 4 to 32 rows a lane
+            int64_t chunks = ceil_div(wanted, N * p->ncb);
+            const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 32 * ty);
             if (chunks > most) chunks = most;
             if (chunks < least) chunks = least;
             p->chunk_rows = ceil_div(S, chunks);
@@ -212,9 +216,13 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
         p->cv = (int64_t)p->ncb * p->TX;
         p->mixed = D % p->vec != 0;
         p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
+        const int64_t cols_across = (int64_t)p->TX * (p->mixed ? p->vec : 1);
+        p->P = pow2_at_most(p->block / cols_across < 1 ? 1 : (p->block / cols_across < 64 ? p->block / cols_across : 64));
+        // (up to 16 sums a lane: 8 us for the pass that adds them alone, with its launch)
+        p->fused = p->kind == kNormSplit && ceil_div(p->chunks * p->parts, p->L) <= 16;
         const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
         const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
-        p->lds = value * values * ((size_t)p->block * (p->mixed ? p->vec : 1) + p->groups);
+        p->lds = value * values * ((size_t)(p->block + p->TX) * (p->mixed ? p->vec : 1) + p->groups);
         const size_t cols = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4;
         if (backward && p->lds < cols) p->lds = cols;
     }

@@ -45,7 +45,8 @@ struct NormPlan {
     int32_t groups;          // slab, split: most groups in a block
     int32_t parts;           // split: most blocks a group lies in
     int32_t regs;            // slab: rows per lane
-    int32_t L;               // slab, split: lanes that add up one group
+    int32_t P, L;            // slab, split: lanes that add up one column's rows, one group's columns
+    bool fused;              // split: the second pass adds the first's sums itself
     int32_t block;           // threads per workgroup
     int64_t blocks;          // workgroups
     int64_t chunks, chunk_rows;  // split: row chunks per sample; slab backward: chunks of samples

@@ -125,6 +125,24 @@ template <int V> struct Pack {
     }
 };
 
+// n <= V fp32 parameters at p (absent pointers give `none`), the rest zeros.
+template <int V> __device__ static inline void load_params(const float *p, int n, float none, float (&f)[V]) {
+    typedef float fvec __attribute__((ext_vector_type(V)));
+    typedef fvec any __attribute__((aligned(4)));
+    if (p && n == V) {
+        if constexpr (V > 1) {
+            const fvec v = *reinterpret_cast<const any *>(p);
+#pragma unroll
+            for (int e = 0; e < V; ++e) f[e] = v[e];
+        } else {
+            f[0] = p[0];
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = e < n ? (p ? p[e] : none) : 0.0f;
+}
+
 // A lane's columns: weight, bias and (rational) the coefficients of their one
 // activation group.  Absent columns get weight 0.
 template <int V, bool RAT> struct Cols {
@@ -135,12 +153,8 @@ template <int V, bool RAT> struct Cols {
     __device__ inline void init(const NormArgs &a, int col_, int nv_) {
         col = col_;
         nv = nv_;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const bool in = e < nv;
-            w[e] = in ? (a.w ? a.w[col + e] : 1.0f) : 0.0f;
-            b[e] = in && a.b ? a.b[col + e] : 0.0f;
-        }
+        load_params<V>(a.w ? a.w + col : nullptr, nv, 1.0f, w);
+        load_params<V>(a.b ? a.b + col : nullptr, nv, 0.0f, b);
         if constexpr (RAT) c = load_coefs<5, 4>(a.A, a.B, nv > 0 ? col / a.dga : 0);
     }
 };
@@ -188,13 +202,16 @@ __device__ static inline float slope(float xh, float dy, const Cols<V, RAT> &k, 
 }
 
 // A token lane's K accesses: columns, weights, biases and the rational's
-// coefficients.  Without coefficients the accesses of a group's lanes
-// interleave (access l + i T), which coalesces best; with them a lane takes a
-// run of K V consecutive columns, so that one set of coefficients (RAT 1), or
-// two where runs straddle activation groups (RAT 2: the second from element
-// `split` of the run on), serves them all.
-template <int V, int RAT, int K> struct TokenCols {
-    static constexpr int kSets = RAT == 2 ? 2 : 1;
+// coefficients.  The accesses of a group's lanes interleave (access l + i T),
+// which coalesces, and each has a set of coefficients (RAT 1).  RUN: a lane
+// takes K V consecutive columns instead, so that one set, or two where runs
+// straddle activation groups (RAT 2: the second from element `split` of the run
+// on), serves them all.  The backward of the rational, which also sums per
+// set, is bound by its arithmetic and takes runs (at 48 bytes a lane the forward
+// spent its time in the address units instead: 65 us against 50 at 50,432 x
+// 768).
+template <int V, int RAT, int K, bool RUN> struct TokenCols {
+    static constexpr int kSets = RAT == 0 ? 1 : (RUN ? RAT : K);
     int col[K], nv[K], split;
     float w[K][V], b[K][V];
     Coefs<5, 4> c[kSets];
@@ -202,18 +219,17 @@ template <int V, int RAT, int K> struct TokenCols {
     __device__ inline void init(const NormArgs &a, int g, int l) {
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            const int first = (RAT ? l * K + i : l + i * a.p.T) * V;
+            const int first = (RUN ? l * K + i : l + i * a.p.T) * V;
             nv[i] = min(max(a.D - first, 0), V);
             col[i] = g * a.D + (nv[i] > 0 ? first : 0);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const bool in = e < nv[i];
-                w[i][e] = in ? (a.w ? a.w[col[i] + e] : 1.0f) : 0.0f;
-                b[i][e] = in && a.b ? a.b[col[i] + e] : 0.0f;
-            }
+            load_params<V>(a.w ? a.w + col[i] : nullptr, nv[i], 1.0f, w[i]);
+            load_params<V>(a.b ? a.b + col[i] : nullptr, nv[i], 0.0f, b[i]);
         }
         split = K * V;
-        if constexpr (RAT != 0) {
+        if constexpr (RAT != 0 && !RUN) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) c[i] = load_coefs<5, 4>(a.A, a.B, col[i] / a.dga);
+        } else if constexpr (RAT != 0) {
             const int group = col[0] / a.dga;
             c[0] = load_coefs<5, 4>(a.A, a.B, group);
             if constexpr (RAT == 2) {
@@ -222,9 +238,11 @@ template <int V, int RAT, int K> struct TokenCols {
             }
         }
     }
-    // the coefficients of element j of the run
+    // the coefficients of element j = i V + e
     __device__ inline Coefs<5, 4> coefs(int j) const {
-        if constexpr (RAT == 2) {
+        if constexpr (!RUN) {
+            return c[RAT ? j / V : 0];
+        } else if constexpr (RAT == 2) {
             Coefs<5, 4> k;
 #pragma unroll
             for (int i = 0; i < 6; ++i) k.a[i] = j < split ? c[0].a[i] : c[1].a[i];
@@ -238,6 +256,8 @@ template <int V, int RAT, int K> struct TokenCols {
 };
 
 // ------------------------------------------------------------ reductions
+
+__device__ static inline float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
 // v of the lane that the DPP control names (all lanes are named by some lane).
 template <int CTRL> __device__ static inline float dpp(float v) {
@@ -293,6 +313,7 @@ struct Place {
     int c0, width;           // the block's columns
     int g0, ngroups;         // its groups (the first and last may reach outside it)
     int col, nv, tx, ty;
+    int first, edge;         // the lane's first element's group, counted from g0, and where the next begins
     __device__ inline Place(const NormArgs &a, int cb) {
         const NormPlan &p = a.p;
         const int t = (int)threadIdx.x;
@@ -304,47 +325,68 @@ struct Place {
         ngroups = (c0 + width - 1) / a.D - g0 + 1;
         col = c0 + tx * p.vec;
         nv = ty < p.TY ? min(max(width - tx * p.vec, 0), p.vec) : 0;
+        const int g = min(col, c0 + width - 1) / a.D;
+        first = g - g0;
+        edge = (g + 1) * a.D - col;
     }
-    // group of element e, counted from g0 (clamped for absent elements)
+    // group of element e, counted from g0 (clamped for absent elements); an
+    // access lies in at most two groups unless groups are shorter than it
     __device__ inline int group(const NormArgs &a, int e) const {
+        if (a.D >= a.p.vec) return min(first + (e < edge ? 0 : 1), ngroups - 1);
         return min(col + e, c0 + width - 1) / a.D - g0;
     }
 };
 
 // Sums over each group of a column block: v[i][e] is value i of element e (of
 // the whole access unless MIXED) in this lane; afterwards the sum over the
-// element's group, of its columns in this block.  `lds` holds NV * (E *
-// threads + groups) values, E = V if MIXED else 1.
+// element's group, of its columns in this block.  First over the row lanes of
+// each column (p.P lanes a column), then over the columns of each group (p.L
+// lanes a group).  `lds` holds NV * (E * (threads + TX) + groups) values, E = V
+// if MIXED else 1.
 template <class R, int NV, int V, bool MIXED>
 __device__ static inline void group_sum(R (&v)[NV][MIXED ? V : 1], const NormArgs &a, const Place &q, char *ldsb) {
     constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
     R *red = reinterpret_cast<R *>(ldsb);
-    R *res = red + NV * E * p.block;
-    const int t = (int)threadIdx.x, l = t & (p.L - 1);
+    R *sums = red + NV * E * p.block;
+    R *res = sums + NV * E * p.TX;
+    const int t = (int)threadIdx.x, ncols = E * p.TX;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) red[(i * E + e) * p.block + t] = v[i][e];
     __syncthreads();
+    for (int c = t / p.P; c < ncols; c += p.block / p.P) {
+        const int l = t & (p.P - 1), at = (c % E) * p.block + c / E;
+        R s[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = 0;
+        for (int r = l; r < p.TY; r += p.P)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] += red[i * E * p.block + at + r * p.TX];
+        for (int o = p.P >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] += __shfl_xor(s[i], o, 64);
+        if (l == 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sums[i * ncols + c] = s[i];
+        }
+    }
+    __syncthreads();
     for (int j = t / p.L; j < q.ngroups; j += p.block / p.L) {
         // the group's columns in this block; accesses unless MIXED
         int lo = max((q.g0 + j) * a.D - q.c0, 0), hi = min((q.g0 + j + 1) * a.D - q.c0, q.width);
         if constexpr (!MIXED) lo /= V, hi /= V;
-        const int n = hi - lo, count = n * p.TY;
         R s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) s[i] = 0;
-        for (int u = l; u < count; u += p.L) {
-            const int row = u / n, c = lo + (u - row * n);
-            const int at = MIXED ? (c % V) * p.block + row * p.TX + c / V : row * p.TX + c;
+        for (int c = lo + (t & (p.L - 1)); c < hi; c += p.L)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] += red[i * E * p.block + at];
-        }
+            for (int i = 0; i < NV; ++i) s[i] += sums[i * ncols + c];
         for (int o = p.L >> 1; o > 0; o >>= 1)
 #pragma unroll
             for (int i = 0; i < NV; ++i) s[i] += __shfl_xor(s[i], o, 64);
-        if (l == 0) {
+        if ((t & (p.L - 1)) == 0) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) res[i * p.groups + j] = s[i];
         }
@@ -358,19 +400,16 @@ __device__ static inline void group_sum(R (&v)[NV][MIXED ? V : 1], const NormArg
     }
 }
 
-// The groups' sums of a block as group_sum left them in LDS, by the first
-// threads: split plans store them as one part of the group's.
+// The groups' sums of a block as group_sum left them in LDS.
 template <class R, int NV, int E>
 __device__ static inline const R *group_results(const NormPlan &p, const char *ldsb) {
-    return reinterpret_cast<const R *>(ldsb) + NV * E * p.block;
+    return reinterpret_cast<const R *>(ldsb) + NV * E * (p.block + p.TX);
 }
 
 __device__ static inline const char *at(const void *base, int64_t e) {
     return static_cast<const char *>(base) + e * ES;
 }
 __device__ static inline char *at(void *base, int64_t e) { return static_cast<char *>(base) + e * ES; }
-
-__device__ static inline float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
 // Sample of a (workgroup, column block): with 8 samples or more the column
 // blocks of a sample go to one XCD (workgroups are dealt to the 8 XCDs in
@@ -401,12 +440,28 @@ __device__ static inline void store_parts(const NormArgs &a, const Place &q, int
     }
 }
 
+// Blocks that group g lies in.
+__device__ static inline int group_parts(const NormArgs &a, int g) {
+    return ((g + 1) * a.D - 1) / a.p.width - g * a.D / a.p.width + 1;
+}
+
+// A group's statistics from the sums of x and x^2 (forward), or <t> and <t xh>
+// from theirs (backward).
+__device__ static inline float2 of_sums(const NormArgs &a, double s0, double s1) {
+    const double m = (double)a.D * (double)a.S;
+#if GRKAN_NORM_BACKWARD
+    return float2{(float)(s0 / m), (float)(s1 / m)};
+#else
+    const double mean = s0 / m;
+    return float2{(float)mean, rstd_of((float)(s1 / m - mean * mean), a.eps)};
+#endif
+}
+
 // Split: the sum of a group's parts, by a workgroup of 256; in thread 0.
 __device__ static inline void add_parts(const NormArgs &a, int64_t ng, double &s0, double &s1) {
     __shared__ double red[2][4];
     const NormPlan &p = a.p;
-    const int g = (int)(ng % a.G), t = (int)threadIdx.x;
-    const int parts = ((g + 1) * a.D - 1) / p.width - g * a.D / p.width + 1;  // blocks the group lies in
+    const int g = (int)(ng % a.G), t = (int)threadIdx.x, parts = group_parts(a, g);
     const int64_t count = p.chunks * p.parts;
     s0 = s1 = 0.0;
 #pragma unroll 4
@@ -428,6 +483,45 @@ __device__ static inline void add_parts(const NormArgs &a, int64_t ng, double &s
     }
 }
 
+// Split, few parts: each workgroup of the second pass adds the parts of its
+// groups itself (p.L lanes a group, the same order in every workgroup) and
+// leaves the statistics in LDS.
+__device__ static inline void own_parts(const NormArgs &a, const Place &q, int64_t n, float2 *stats) {
+    const NormPlan &p = a.p;
+    const int t = (int)threadIdx.x, l = t & (p.L - 1);
+    const int count = (int)(p.chunks * p.parts);
+    for (int j = t / p.L; j < q.ngroups; j += p.block / p.L) {
+        const int parts = group_parts(a, q.g0 + j);
+        const double *o = a.stats + 2 * (n * a.G + q.g0 + j) * (int64_t)count;
+        double s0 = 0.0, s1 = 0.0;
+#pragma unroll 4
+        for (int i = l; i < count; i += p.L) {
+            if (p.parts > 1 && i % p.parts >= parts) continue;
+            s0 += o[2 * i];
+            s1 += o[2 * i + 1];
+        }
+        for (int u = p.L >> 1; u > 0; u >>= 1) {
+            s0 += __shfl_xor(s0, u, 64);
+            s1 += __shfl_xor(s1, u, 64);
+        }
+        if (l == 0) stats[j] = of_sums(a, s0, s1);
+    }
+    __syncthreads();
+}
+
+// Launches KERN with `lds` bytes of dynamic LDS, which may pass the 64 KB a kernel
+// has without asking.
+template <auto KERN>
+hipError_t start(const NormArgs &a, dim3 grid, dim3 block, size_t lds, hipStream_t s) {
+    if (lds > (64u << 10)) {
+        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(KERN),
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(KERN, grid, block, lds, s, a);
+    return hipGetLastError();
+}
+
 #if !GRKAN_NORM_BACKWARD
 // ============================================================ forward
 
@@ -441,7 +535,7 @@ __global__ __launch_bounds__(K * V == 1 ? 1024 : 256) void grkan_norm_token_fwd_
     const int64_t step = p.blocks * p.spw / a.G;
     const float inv = 1.0f / (float)a.D;
     int phase = 0;
-    TokenCols<V, RAT, K> k;
+    TokenCols<V, RAT, K, RAT == 2> k;
     k.init(a, g, l);
     // T <= 64: a slot ends when its samples do; larger T: the slot is the
     // workgroup, and n is the same in all its lanes.  The next sample's values
@@ -563,11 +657,11 @@ __global__ __launch_bounds__(1024) void grkan_norm_slab_fwd_kernel(NormArgs a) {
 
 // Split, first pass: sums of x and x^2 of a row chunk of a column block.  A
 // lane sums the differences from its first row (and their squares) in fp32,
-// column by column, over at most ~64 rows, and turns them into fp64 sums of x
+// column by column, over at most 32 rows, and turns them into fp64 sums of x
 // and x^2 about zero at the end: three fp32 operations an element, with the
 // digits of a mean far from zero kept out of them.
 template <int V, bool MIXED>
-__global__ __launch_bounds__(256) void grkan_norm_sums_kernel(NormArgs a) {
+__global__ __launch_bounds__(1024) void grkan_norm_sums_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
@@ -605,42 +699,54 @@ __global__ __launch_bounds__(256) void grkan_norm_sums_kernel(NormArgs a) {
     }
 }
 
-// Split, second step: a workgroup per (sample, group) adds the parts.
+// Split, many parts: a workgroup per (sample, group) adds them.
 __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
     const int64_t ng = blockIdx.x;
     double s0, s1;
     add_parts(a, ng, s0, s1);
     if (threadIdx.x == 0) {
-        const double m = (double)a.D * (double)a.S, mean = s0 / m;
-        a.mean[ng] = (float)mean;
-        a.rstd[ng] = rstd_of((float)(s1 / m - mean * mean), a.eps);
+        const float2 st = of_sums(a, s0, s1);
+        a.mean[ng] = st.x;
+        a.rstd[ng] = st.y;
     }
 }
 
-// Split, third step: y over a row chunk of a column block.
+// Split, second pass: y over a row chunk of a column block.
 template <int V, bool RAT, bool MIXED>
-__global__ __launch_bounds__(256) void grkan_norm_apply_fwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(1024) void grkan_norm_apply_fwd_kernel(NormArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    float2 *stats = reinterpret_cast<float2 *>(lds);
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int cb = (int)(b % p.ncb);
         const int64_t nc = b / p.ncb, n = nc / p.chunks, c = nc % p.chunks;
         const Place q(a, cb);
-        if (q.nv == 0) continue;
+        if (p.fused) own_parts(a, q, n, stats);
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
         Stats<V, MIXED> st;
 #pragma unroll
         for (int e = 0; e < Stats<V, MIXED>::N; ++e) {
-            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
-            st.mean[e] = a.mean[ng];
-            st.rstd[e] = a.rstd[ng];
+            const int j = q.group(a, e);
+            const int64_t ng = n * a.G + q.g0 + j;
+            st.mean[e] = p.fused ? stats[j].x : a.mean[ng];
+            st.rstd[e] = p.fused ? stats[j].y : a.rstd[ng];
         }
+        if (p.fused && c == 0)  // the first chunk's workgroups store the statistics of groups that begin in them
+            for (int j = (int)threadIdx.x; j < q.ngroups; j += p.block)
+                if ((q.g0 + j) * a.D >= q.c0) {
+                    a.mean[n * a.G + q.g0 + j] = stats[j].x;
+                    a.rstd[n * a.G + q.g0 + j] = stats[j].y;
+                }
         const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
+        if (q.nv > 0) {
 #pragma unroll 4
-        for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY)
-            apply_forward<V, RAT, MIXED>(Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv), st, k, a.act)
-                .store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
+            for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY)
+                apply_forward<V, RAT, MIXED>(Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv), st, k, a.act)
+                    .store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
+        }
+        __syncthreads();  // the statistics in LDS have been read
     }
 }
 
@@ -648,9 +754,8 @@ template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hi
     if constexpr (RAT == 2 && K * V < 4) {  // the plan straddles with runs of 4 or more only
         return hipErrorInvalidValue;
     } else {
-        hipLaunchKernelGGL((grkan_norm_token_fwd_kernel<V, RAT, K>), dim3((unsigned)a.p.blocks), dim3((unsigned)a.p.block),
-                           0, s, a);
-        return hipGetLastError();
+        return start<&grkan_norm_token_fwd_kernel<V, RAT, K>>(a, dim3((unsigned)a.p.blocks), dim3((unsigned)a.p.block), 0,
+                                                              s);
     }
 }
 
@@ -668,22 +773,15 @@ hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
     const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20))), block((unsigned)p.block);
     if (p.kind == kNormSlab) {
-        if (p.regs <= 4)
-            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 4>), grid, block, p.lds, s, a);
-        else if (p.regs <= 8)
-            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 8>), grid, block, p.lds, s, a);
-        else
-            hipLaunchKernelGGL((grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 16>), grid, block, p.lds, s, a);
-        return hipGetLastError();
+        if (p.regs <= 4) return start<&grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 4>>(a, grid, block, p.lds, s);
+        if (p.regs <= 8) return start<&grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 8>>(a, grid, block, p.lds, s);
+        return start<&grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 16>>(a, grid, block, p.lds, s);
     }
-    hipLaunchKernelGGL((grkan_norm_sums_kernel<V, MIXED>), grid, block, p.lds, s, a);
-    hipError_t e = hipGetLastError();
+    hipError_t e = start<&grkan_norm_sums_kernel<V, MIXED>>(a, grid, block, p.lds, s);
+    if (e == hipSuccess && !p.fused)
+        e = start<&grkan_norm_stats_kernel>(a, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grkan_norm_stats_kernel, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s, a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((grkan_norm_apply_fwd_kernel<V, RAT, MIXED>), grid, block, 0, s, a);
-    return hipGetLastError();
+    return start<&grkan_norm_apply_fwd_kernel<V, RAT, MIXED>>(a, grid, block, p.groups * sizeof(float2), s);
 }
 
 #else
@@ -743,7 +841,7 @@ grkan_norm_token_bwd_kernel(NormArgs a) {
     const int64_t step = p.blocks * p.spw / a.G;
     const float inv = 1.0f / (float)a.D;
     int phase = 0;
-    TokenCols<V, RAT, K> k;
+    TokenCols<V, RAT, K, RAT != 0> k;
     k.init(a, g, l);
     SlopeCoefs sc;
     if constexpr (RAT == 1) sc.init(k.c[0]);
@@ -912,7 +1010,7 @@ __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
 
 // Split, first pass: sums of t and t xh and the column sums of a row chunk.
 template <int V, bool RAT, bool MIXED>
-__global__ __launch_bounds__(256) void grkan_norm_sums_bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(512) void grkan_norm_sums_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int E = MIXED ? V : 1;
     const NormPlan &p = a.p;
@@ -936,7 +1034,7 @@ __global__ __launch_bounds__(256) void grkan_norm_sums_bwd_kernel(NormArgs a) {
                 st.mean[e] = a.mean[ng];
                 st.rstd[e] = a.rstd[ng];
             }
-#pragma unroll(RAT ? 1 : 2)
+#pragma unroll RAT ? 1 : 2
             for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
                 const Pack<V> x = Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv);
                 const Pack<V> dy = Pack<V>::load(at(a.dy, n * a.ds + r * a.dr + k.col), k.nv);
@@ -962,29 +1060,27 @@ __global__ __launch_bounds__(256) void grkan_norm_sums_bwd_kernel(NormArgs a) {
     }
 }
 
-// Split, second step: <t> and <t xh>, a workgroup per (sample, group).
+// Split, many parts: <t> and <t xh>, a workgroup per (sample, group).
 __global__ __launch_bounds__(256) void grkan_norm_means_kernel(NormArgs a) {
     const int64_t ng = blockIdx.x;
     double s0, s1;
     add_parts(a, ng, s0, s1);
-    if (threadIdx.x == 0) {
-        const double m = (double)a.D * (double)a.S;
-        a.means[2 * ng] = (float)(s0 / m);
-        a.means[2 * ng + 1] = (float)(s1 / m);
-    }
+    if (threadIdx.x == 0) reinterpret_cast<float2 *>(a.means)[ng] = of_sums(a, s0, s1);
 }
 
-// Split, third step: dx over a row chunk.  The slope is formed again: keeping
+// Split, second pass: dx over a row chunk.  The slope is formed again: keeping
 // it would cost a write and a read of a tensor.
 template <int V, bool RAT, bool MIXED>
-__global__ __launch_bounds__(256) void grkan_norm_apply_bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(512) void grkan_norm_apply_bwd_kernel(NormArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    float2 *means = reinterpret_cast<float2 *>(lds);
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int cb = (int)(b % p.ncb);
         const int64_t nc = b / p.ncb, n = nc / p.chunks, c = nc % p.chunks;
         const Place q(a, cb);
-        if (q.nv == 0) continue;
+        if (p.fused) own_parts(a, q, n, means);
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
         SlopeCoefs sc;
@@ -992,27 +1088,32 @@ __global__ __launch_bounds__(256) void grkan_norm_apply_bwd_kernel(NormArgs a) {
         Stats<V, MIXED> st, mm;  // mm: <t> and <t xh>
 #pragma unroll
         for (int e = 0; e < Stats<V, MIXED>::N; ++e) {
-            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+            const int j = q.group(a, e);
+            const int64_t ng = n * a.G + q.g0 + j;
+            const float2 m = p.fused ? means[j] : reinterpret_cast<const float2 *>(a.means)[ng];
             st.mean[e] = a.mean[ng];
             st.rstd[e] = a.rstd[ng];
-            mm.mean[e] = a.means[2 * ng];
-            mm.rstd[e] = a.means[2 * ng + 1];
+            mm.mean[e] = m.x;
+            mm.rstd[e] = m.y;
         }
         const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
         float unused[10] = {};
-#pragma unroll(RAT ? 1 : 2)
-        for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
-            const Pack<V> x = Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv);
-            const Pack<V> dy = Pack<V>::load(at(a.dy, n * a.ds + r * a.dr + k.col), k.nv);
-            float f[V];
+        if (q.nv > 0) {
+#pragma unroll RAT ? 1 : 2
+            for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY) {
+                const Pack<V> x = Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv);
+                const Pack<V> dy = Pack<V>::load(at(a.dy, n * a.ds + r * a.dr + k.col), k.nv);
+                float f[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float xh = (x.get(e) - st.m(e)) * st.r(e);
-                const float dh = slope<V, RAT>(xh, dy.get(e), k, sc, e, a.act, unused);
-                f[e] = st.r(e) * (dh * k.w[e] - fmaf(xh, mm.r(e), mm.m(e)));
+                for (int e = 0; e < V; ++e) {
+                    const float xh = (x.get(e) - st.m(e)) * st.r(e);
+                    const float dh = slope<V, RAT>(xh, dy.get(e), k, sc, e, a.act, unused);
+                    f[e] = st.r(e) * (dh * k.w[e] - fmaf(xh, mm.r(e), mm.m(e)));
+                }
+                Pack<V>::from(f).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
             }
-            Pack<V>::from(f).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
         }
+        __syncthreads();  // the means in LDS have been read
     }
 }
 
@@ -1085,8 +1186,7 @@ __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
 template <bool RAT> hipError_t launch_columns(const NormArgs &a, hipStream_t s) {
     if (!a.dw && !a.db && !RAT) return hipSuccess;
     const dim3 grid((unsigned)((2 * (int64_t)a.C + 63) / 64 + (RAT ? (int64_t)a.ng * 10 : 0)));
-    hipLaunchKernelGGL((grkan_norm_columns_kernel<RAT>), grid, dim3(1024), 0, s, a);
-    return hipGetLastError();
+    return start<&grkan_norm_columns_kernel<RAT>>(a, grid, dim3(1024), 0, s);
 }
 
 template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hipStream_t s) {
@@ -1094,9 +1194,8 @@ template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hi
     if constexpr ((K > 1 && K * V > 16) || (RAT == 2 && K * V < 4)) {
         return hipErrorInvalidValue;
     } else {
-        hipLaunchKernelGGL((grkan_norm_token_bwd_kernel<V, RAT, K>), dim3((unsigned)a.p.blocks), dim3((unsigned)a.p.block),
-                           a.p.lds, s, a);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = start<&grkan_norm_token_bwd_kernel<V, RAT, K>>(a, dim3((unsigned)a.p.blocks),
+                                                                            dim3((unsigned)a.p.block), a.p.lds, s);
         return e != hipSuccess ? e : launch_columns<RAT != 0>(a, s);
     }
 }
@@ -1113,25 +1212,22 @@ template <int V, int RAT> hipError_t launch_token(const NormArgs &a, hipStream_t
 template <int V, bool RAT, bool MIXED>
 hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
-    const dim3 block((unsigned)p.block);
+    const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20))), block((unsigned)p.block);
     hipError_t e;
     if (p.kind == kNormSlab) {
-        const dim3 grid((unsigned)p.blocks);
         if (p.regs <= 3)
-            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 3>), grid, block, p.lds, s, a);
+            e = start<&grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 3>>(a, dim3((unsigned)p.blocks), block, p.lds, s);
         else if (p.regs <= 5)
-            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 5>), grid, block, p.lds, s, a);
+            e = start<&grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 5>>(a, dim3((unsigned)p.blocks), block, p.lds, s);
         else
-            hipLaunchKernelGGL((grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 8>), grid, block, p.lds, s, a);
+            e = start<&grkan_norm_slab_bwd_kernel<V, RAT, MIXED, 8>>(a, dim3((unsigned)p.blocks), block, p.lds, s);
     } else {
-        const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20)));
-        hipLaunchKernelGGL((grkan_norm_sums_bwd_kernel<V, RAT, MIXED>), grid, block, p.lds, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(grkan_norm_means_kernel, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL((grkan_norm_apply_bwd_kernel<V, RAT, MIXED>), grid, block, 0, s, a);
+        e = start<&grkan_norm_sums_bwd_kernel<V, RAT, MIXED>>(a, grid, block, p.lds, s);
+        if (e == hipSuccess && !p.fused)
+            e = start<&grkan_norm_means_kernel>(a, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s);
+        if (e == hipSuccess)
+            e = start<&grkan_norm_apply_bwd_kernel<V, RAT, MIXED>>(a, grid, block, p.groups * sizeof(float2), s);
     }
-    e = hipGetLastError();
     return e != hipSuccess ? e : launch_columns<RAT>(a, s);
 }
 #endif
