@@ -189,27 +189,38 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
             p->kind = kNormSplit;
             p->vec = rational ? rational_vec(vmax, dga, 0) : vmax;
             const int64_t accesses = ceil_div(C, p->vec);
-            // Large workgroups, about one (forward) or two a CU, so that few sums
-            // are left to add.  At most 256 accesses across (128 where every column
-            // is a group, for the groups' sums in LDS).
-            const int64_t lanes = backward ? 512 : 1024, wanted = backward ? 512 : 256;
+            // At most 256 accesses across (128 where every column is a group, for the
+            // groups' sums in LDS).
             p->ncb = (int32_t)ceil_div(accesses, D == 1 ? 128 : 256);
             p->TX = (int32_t)ceil_div(accesses, p->ncb);
             p->width = p->TX * p->vec;
             p->ncb = (int32_t)ceil_div(C, p->width);
             p->groups = (int32_t)(p->width / D + 2 < G ? p->width / D + 2 : G);
             p->parts = (int32_t)(D / p->width + 2 < p->ncb ? D / p->width + 2 : p->ncb);
-            int64_t ty = lanes / p->TX;
-            if (ty > S) ty = S;
-            p->TY = (int32_t)ty;
-            p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
-            // chunks of 4 to 32 rows a lane
-            int64_t chunks = ceil_div(wanted, N * p->ncb);
-            const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 32 * ty);
-            if (chunks > most) chunks = most;
-            if (chunks < least) chunks = least;
-            p->chunk_rows = ceil_div(S, chunks);
-            p->chunks = ceil_div(S, p->chunk_rows);
+            // Chunks of 4 to 32 rows a lane, about a workgroup a CU; where those
+            // leave a lane of the second pass more than 2 sums to add (few
+            // samples), smaller workgroups, more of them, and a step between that
+            // adds (65,536 x 128 in 32 groups: 26 us against 29).
+            auto chunks_of = [&](int64_t lanes, int64_t wanted) {
+                int64_t ty = lanes / p->TX;
+                if (ty > S) ty = S;
+                p->TY = (int32_t)ty;
+                p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
+                int64_t chunks = ceil_div(wanted, N * p->ncb);
+                const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 32 * ty);
+                if (chunks > most) chunks = most;
+                if (chunks < least) chunks = least;
+                p->chunk_rows = ceil_div(S, chunks);
+                p->chunks = ceil_div(S, p->chunk_rows);
+                p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
+                p->fused = ceil_div(p->chunks * p->parts, p->L) <= 2;
+            };
+            if (backward) {
+                chunks_of(512, 512);
+            } else {
+                chunks_of(1024, 256);
+                if (!p->fused) chunks_of(256, 1024);
+            }
             p->blocks = N * p->chunks * p->ncb;
             p->prows = N * p->chunks;
         }
@@ -218,8 +229,6 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
         p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
         const int64_t cols_across = (int64_t)p->TX * (p->mixed ? p->vec : 1);
         p->P = pow2_at_most(p->block / cols_across < 1 ? 1 : (p->block / cols_across < 64 ? p->block / cols_across : 64));
-        // (up to 16 sums a lane: 8 us for the pass that adds them alone, with its launch)
-        p->fused = p->kind == kNormSplit && ceil_div(p->chunks * p->parts, p->L) <= 16;
         const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
         const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
         p->lds = value * values * ((size_t)(p->block + p->TX) * (p->mixed ? p->vec : 1) + p->groups);

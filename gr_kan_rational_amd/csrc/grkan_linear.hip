@@ -43,6 +43,8 @@
 //                  16 side by side eight different ones
 #include "grkan_linear.h"
 
+#include <type_traits>
+
 #include "grkan_act.h"
 
 namespace grkan {
@@ -151,8 +153,9 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
     int64_t ld;
     uint32_t off[kChunks];   // byte offset of the chunk from base, or kNowhere
     int k0;              // K contiguous: k of the chunks; strided: k of chunk 0
-    int valid;           // unaligned: elements of a chunk inside the operand's own range (strided)
-    u32x4 r[kAligned ? 1 : kChunks];
+    int valid;           // strided: elements of a chunk inside the operand's own range
+    bool inside;         // the tile lies inside the operand: unaligned chunks of a whole step need no checks
+    u32x4 r[2][kAligned ? 1 : kChunks];  // unaligned: chunks on their way, of two steps
 
     __device__ static inline int f(int row) { return ((BK == 64 ? row : row >> 1) & (BK / 8 - 1)) ^ ((row >> 3) & 1); }
     __device__ static inline int s(int k) { return ROWS >= 128 ? 2 * ((k & 3) + 4 * (k & 1)) : 2 * (k & 3); }
@@ -169,6 +172,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
             static_assert(kThreads / kPerRow % 4 == 0, "one swizzle per thread");
             const int c = slot ^ s(r0);
             valid = min(max(rows - row0 - c * 8, 0), 8);
+            inside = row0 + ROWS <= rows;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i)
                 off[i] = valid > 0 ? (uint32_t)((r0 + i * (kThreads / kPerRow)) * ld * 2 + c * 16) : kNowhere;
@@ -179,17 +183,21 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
             const int c = slot ^ f(r0);
             k0 = c * 8;
             valid = 8;
+            inside = true;
+            // rows past the end: zeros, or (unaligned) the last row once more; what
+            // they form is not stored
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int row = r0 + i * (kThreads / kPerRow);
+                int row = r0 + i * (kThreads / kPerRow);
+                if (!kAligned) row = min(row, rows - 1 - row0);
                 off[i] = row0 + row < rows ? (uint32_t)(row * ld * 2 + c * 16) : kNowhere;
             }
         }
     }
 
-    // Chunks of step t (k from kt on, `left` of them in this split) into the
-    // stage at LDS byte offset `stage`; past the end zeros.
-    __device__ inline void fetch(char *lds, int stage, int t, int left) {
+    // Chunks of step t, `left` values of k before its end: aligned into the stage
+    // at LDS byte offset `stage`, else into register set SET; past the end zeros.
+    template <int SET> __device__ inline void fetch(char *lds, int stage, int t, int left) {
         const char *src = base + t * step;
         if constexpr (kAligned) {
             __amdgpu_buffer_rsrc_t rsrc =
@@ -203,22 +211,24 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
                     rsrc, (__attribute__((address_space(3))) void *)(lds + stage + (i * kThreads + wave * 64) * 16), 16, o,
                     0, 0, 0);
             }
+        } else if (left >= BK && inside) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) r[SET][i] = *reinterpret_cast<const u32x4_any *>(src + off[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
-                int nv = STRIDED ? (k < left ? valid : 0) : min(max(left - k, 0), 8);
-                if (off[i] == kNowhere) nv = 0;
-                r[i] = load8(reinterpret_cast<const uint16_t *>(src + (nv ? off[i] : 0)), nv);
+                const int nv = STRIDED ? (k < left ? valid : 0) : min(max(left - k, 0), 8);
+                r[SET][i] = load8(reinterpret_cast<const uint16_t *>(src + (nv ? off[i] : 0)), nv);
             }
         }
     }
-    // Unaligned: the fetched chunks into their stage.
-    __device__ inline void put(char *lds, int stage) {
+    // Unaligned: the chunks of a register set into their stage.
+    template <int SET> __device__ inline void put(char *lds, int stage) {
         if constexpr (!kAligned) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i)
-                *reinterpret_cast<u32x4 *>(lds + stage + (i * kThreads + (int)threadIdx.x) * 16) = r[i];
+                *reinterpret_cast<u32x4 *>(lds + stage + (i * kThreads + (int)threadIdx.x) * 16) = r[SET][i];
         }
     }
 };
@@ -361,7 +371,6 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
     rq.init(mrow);
     rp.init(ncol);
     constexpr int kInFlight = Stager<BM, BK, QS>::kChunks + Stager<BN, BK, PS>::kChunks;
-    constexpr int kAhead = kAligned ? 2 : 1;  // steps between a fetch and its use
 
     f32x16 acc[NN][NM];
     bf16x8 fq[2][NM], fp[2][NN];
@@ -373,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                 acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[set][j], fq[set][i], acc[j][i], 0, 0, 0);
     };
 
-    // The fetches run kAhead steps ahead of the products, on through the tiles
+    // The fetches run two steps ahead of the products, on through the tiles
     // of this workgroup: fetch_tile, fetch_step say what comes next.  Past
     // the last tile they read zeros, so the count in flight is fixed.
     int fetch_tile = next((int)blockIdx.x), fetch_step = 0, fetch_len = 0;
@@ -389,31 +398,42 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
         }
         fetch_step = 0;
     };
-    auto fetch = [&](int stage) {
+    auto fetch = [&](int stage, auto set) {
         const int left = fetch_len - fetch_step * BK;
-        sq.fetch(lds, stage, fetch_step, left);
-        sp.fetch(lds, stage + kQ, fetch_step, left);
+        sq.template fetch<set()>(lds, stage, fetch_step, left);
+        sp.template fetch<set()>(lds, stage + kQ, fetch_step, left);
         ++fetch_step;
         if (fetch_step * BK >= fetch_len && fetch_tile < count) {
             fetch_tile = next(fetch_tile + (int)gridDim.x);
             start_tile();
         }
     };
-    auto put = [&](int stage) {
-        sq.put(lds, stage);
-        sp.put(lds, stage + kQ);
+    auto put = [&](int stage, auto set) {
+        sq.template put<set()>(lds, stage);
+        sp.template put<set()>(lds, stage + kQ);
     };
+    // The step whose chunks put has stored, or that was fetched into LDS before
+    // the last kInFlight fetches (and `later` operations after it), has arrived.
+    auto arrived = [&](auto later) {
+        if constexpr (kAligned)
+            wait_loads<kInFlight + later()>();
+        else
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    };
+    constexpr std::integral_constant<int, 0> zero;
+    constexpr std::integral_constant<int, 1> one;
 
     // Stages of steps t, t + 1, t + 2.
     int s0 = 0, s1 = kStage, s2 = 2 * kStage;
     int tile = fetch_tile;
     bool whole = false;  // the last tile stored by this workgroup had no edge
+    bool odd = true;     // the register set of the next step
     constexpr int kStores = WM * WN / 512;
     start_tile();
-    fetch(s0);
-    put(s0);
-    if constexpr (kAligned) fetch(s1);
-    wait_loads<kAligned ? kInFlight : 0>();
+    fetch(s0, zero);
+    put(s0, zero);
+    fetch(s1, one);
+    arrived(zero);
     barrier();
     rq.read(lds + s0, 0, fq[0]);
     rp.read(lds + s0 + kQ, 0, fp[0]);
@@ -427,8 +447,9 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
         for (int j = 0; j < NN; ++j)
 #pragma unroll
             for (int i = 0; i < NM; ++i) acc[j][i] = f32x16{};
-        for (int t = 0; t < steps; ++t) {
-            fetch(kAhead == 2 ? s2 : s1);
+        // SET: the register set that holds (unaligned) step t + 1
+        auto step = [&](int t, auto SET) {
+            fetch(s2, std::integral_constant<int, 1 - SET()>{});
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int set = ks & 1;
@@ -438,14 +459,14 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                 } else {
                     // step t + 1 has arrived, and every wave holds its last
                     // fragments of step t in registers
-                    put(s1);
+                    put(s1, SET);
                     // memory operations end in the order of their issue: after a
                     // whole tile its kStores stores stand between step 1's fetch
                     // and step 2's, and need not be waited for
-                    if (kAligned && !PARTIAL && t == 0 && whole)
-                        wait_loads<kInFlight + kStores>();
+                    if (!PARTIAL && t == 0 && whole)
+                        arrived(std::integral_constant<int, kStores>{});
                     else
-                        wait_loads<kAligned ? kInFlight : 0>();
+                        arrived(zero);
                     barrier();
                     rq.read(lds + s1, 0, fq[set ^ 1]);
                     rp.read(lds + s1 + kQ, 0, fp[set ^ 1]);
@@ -456,6 +477,16 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
             s0 = s1;
             s1 = s2;
             s2 = s;
+        };
+        if constexpr (kAligned) {
+            for (int t = 0; t < steps; ++t) step(t, one);
+        } else {
+            for (int t = 0; t < steps; ++t, odd = !odd) {
+                if (odd)
+                    step(t, one);
+                else
+                    step(t, zero);
+            }
         }
         // Here s0 holds the next tile's first step (its first fragments are in
         // registers), s1 receives its second, and s2 is free.
@@ -585,36 +616,58 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
 // reading 32 consecutive bytes of a row of W (a line per row and turn) and of
 // x, straight into the operand registers of v_mfma_f32_16x16x32_bf16: the
 // order of k inside a turn is the lanes' own, the same for both operands.  The
-// waves' sums meet in LDS, where one thread finishes 8 columns of a row.
+// loads of up to kTurns turns are on their way at once.  The waves' sums meet in LDS,
+// where one thread finishes 8 columns of a row.
 constexpr int kSkinnyWaves = 8;
 
 template <int MT, int RAT>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void grkan_linear_skinny_kernel(ProductArgs a) {
+    constexpr int kTurns = MT == 1 ? 4 : 2;
     __shared__ float red[kSkinnyWaves][MT * 16][17];
     const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
     const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16 * MT;
-    const uint16_t *W = static_cast<const uint16_t *>(a.p.p) + (int64_t)min(n0 + (lane & 15), a.N - 1) * a.p.ld;
+    // rows past the end are clamped (their results are not stored)
+    const int kl = (lane >> 4) * 16;
+    const uint16_t *W = static_cast<const uint16_t *>(a.p.p) + (int64_t)min(n0 + (lane & 15), a.N - 1) * a.p.ld + kl;
     const uint16_t *x[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        x[i] = static_cast<const uint16_t *>(a.q.p) + (int64_t)min(m0 + 16 * i + (lane & 15), a.M - 1) * a.q.ld;
+        x[i] = static_cast<const uint16_t *>(a.q.p) + (int64_t)min(m0 + 16 * i + (lane & 15), a.M - 1) * a.q.ld + kl;
     f32x4 acc[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
-    const int kl = (lane >> 4) * 16;
-    for (int k0 = wave * 64; k0 < a.K; k0 += kSkinnyWaves * 64) {
+    // k0 of this wave's turns: 64 wave, then every 64 kSkinnyWaves
+    constexpr int kNext = 64 * kSkinnyWaves;
+    int k0 = wave * 64;
+    auto turns = [&](auto count, auto whole) {
+        constexpr int U = count();
+        u32x4 w[U][2], q[U][MT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = k0 + kl + 8 * h, nv = min(max(a.K - k, 0), 8);
-            // rows past the end are clamped (their results are not stored); past K both operands are zeros
-            const bf16x8 w = __builtin_bit_cast(bf16x8, load8(W + (nv ? k : 0), nv));
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const bf16x8 q = __builtin_bit_cast(bf16x8, load8(x[i] + (nv ? k : 0), nv));
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, q, acc[i], 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+                // whole: every chunk of these turns lies before K; else each lane
+                // takes what does, and zeros past it for both operands
+                const int k = k0 + u * kNext + 8 * h;
+                const int nv = whole() ? 8 : min(max(a.K - k - kl, 0), 8);
+                w[u][h] = load8(W + (nv ? k : 0), nv);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) q[u][i][h] = load8(x[i] + (nv ? k : 0), nv);
             }
-        }
-    }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[u][h]),
+                                                                     __builtin_bit_cast(bf16x8, q[u][i][h]), acc[i], 0, 0, 0);
+        k0 += U * kNext;
+    };
+    while (k0 + (kTurns - 1) * kNext + 64 <= a.K) turns(std::integral_constant<int, kTurns>{}, std::true_type{});
+    if (kTurns > 2 && k0 + kNext + 64 <= a.K) turns(std::integral_constant<int, 2>{}, std::true_type{});
+    if (k0 + 64 <= a.K) turns(std::integral_constant<int, 1>{}, std::true_type{});
+    if (k0 < a.K) turns(std::integral_constant<int, 1>{}, std::false_type{});
     // lane: row lane mod 16, columns 4 (lane / 16) + v
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -640,36 +693,51 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void grkan_linear_skinny_kernel(
 
 // ------------------------------------------------------------ second step
 
-// The splits' sums added in order, then the epilogue; a thread keeps its 8
-// columns over its rows.
-template <int RAT>
+// The splits' sums added, then the epilogue.  SL lanes share the splits of 8
+// columns (each adds every SL-th in order, the lanes' sums then in order through
+// LDS), so that a small result with many splits still fills the GPU: 768 x 192
+// from 42 splits is 18,432 columns of 8.
+template <int RAT, int SL>
 __global__ __launch_bounds__(256) void grkan_linear_finish_kernel(ProductArgs a) {
-    const int chunks = (a.N + 7) / 8;
+    constexpr int kItems = 256 / SL;
+    __shared__ f32x4 red[SL > 1 ? SL : 1][SL > 1 ? 2 * kItems : 1];
+    const int chunks = (a.N + 7) / 8, t = (int)threadIdx.x, x = t % kItems, sl = t / kItems;
     const int64_t total = (int64_t)chunks * a.M, plane = (int64_t)a.M * a.N;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int64_t m = i / chunks;
-    const int n = (int)(i - m * chunks) * 8;
-    ChunkParams<RAT> k;
-    k.init(a.e, n, a.N);
-    const float *p = a.partials + m * a.N + n;
-    float h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
-    for (int s = 0; s < a.splits; ++s, p += plane) {
-        if (k.nv == 8) {
-            const f32x4 u = *reinterpret_cast<const f32x4_any *>(p), v = *reinterpret_cast<const f32x4_any *>(p + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                h[e] += u[e];
-                h[4 + e] += v[e];
-            }
+    const int64_t i = (int64_t)blockIdx.x * kItems + x;
+    const bool on = i < total;
+    const int64_t m = on ? i / chunks : 0;
+    const int n = on ? (int)(i - m * chunks) * 8 : 0;
+    const int nv = min(a.N - n, 8);
+    const float *p = a.partials + m * a.N + n + sl * plane;
+    f32x4 u = {}, v = {};
+#pragma unroll 4
+    for (int s = sl; s < a.splits; s += SL, p += SL * plane) {
+        if (nv == 8) {
+            u += *reinterpret_cast<const f32x4_any *>(p);
+            v += *reinterpret_cast<const f32x4_any *>(p + 4);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < k.nv) h[e] += p[e];
+            for (int e = 0; e < 4; ++e) {
+                if (e < nv) u[e] += p[e];
+                if (4 + e < nv) v[e] += p[4 + e];
+            }
         }
     }
+    if constexpr (SL > 1) {
+        red[sl][2 * x] = u;
+        red[sl][2 * x + 1] = v;
+        __syncthreads();
+        if (sl > 0) return;
+#pragma unroll
+        for (int q = 1; q < SL; ++q) {
+            u += red[q][2 * x];
+            v += red[q][2 * x + 1];
+        }
+    }
+    if (!on) return;
+    ChunkParams<RAT> k;
+    k.init(a.e, n, a.N);
+    float h[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
     finish8<RAT>(h, a.e, k, m, a.N);
 }
 
@@ -712,7 +780,13 @@ hipError_t launch_shape(int form, bool partial, bool rational, const ProductArgs
 #endif
 hipError_t GRKAN_LAUNCH_TILES(int tile, int form, bool partial, bool rational, const ProductArgs &a, hipStream_t s) {
     switch (tile) {
+#if GRKAN_LINEAR_ALIGNED
         case 0: return launch_shape<256, 128, 32>(form, partial, rational, a, s);
+#else
+        // (the chunks on their way take registers here; with 256 rows they spilled,
+        // 574 us against 75 at 8,003 x 1,501 from 777)
+        case 0: return launch_shape<128, 128, 32>(form, partial, rational, a, s);
+#endif
         case 1: return launch_shape<128, 128, 32>(form, partial, rational, a, s);
         case 2: return launch_shape<64, 64, 64>(form, partial, rational, a, s);
         default: return hipErrorInvalidValue;
@@ -734,41 +808,69 @@ template <int RAT> hipError_t launch_skinny(int mt, const ProductArgs &a, hipStr
 }
 }  // namespace
 
+namespace {
+template <int RAT> hipError_t launch_finish(const ProductArgs &a, hipStream_t s) {
+    const int64_t work = (int64_t)((a.N + 7) / 8) * a.M;
+    // lanes that share the splits, while a thread per 8 columns leaves CUs idle
+    if (a.splits >= 8 && work < 64 * 1024)
+        hipLaunchKernelGGL((grkan_linear_finish_kernel<RAT, 8>), dim3((unsigned)((work + 31) / 32)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((grkan_linear_finish_kernel<RAT, 1>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+}  // namespace
+
+// Rows up to which the skinny kernel is taken (128 x 3,072 from 768: 9.4 us against
+// 8.9 with tiles; 64: 6.9 against 8.7).
+constexpr int64_t kSkinnyRows = 64;
+
 constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {128, 128, 64}, kTileK[] = {32, 32, 64};
-constexpr int64_t kSlots = 512;  // workgroups resident at once, two a CU
 
 ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga) {
     ProductPlan p{};
     p.aligned = aligned;
     p.splits = 1;
+    p.k_split = (int32_t)(K > 0 ? K : 1);
     const bool any_groups = act == GRKAN_ACT_RATIONAL && dga % 8 != 0;
-    if (form == kFormForward && M <= 64) {
+    if (form == kFormForward && M <= kSkinnyRows) {
         p.kind = kSkinny;
+        // as many rows a workgroup as there are, while 192 workgroups remain (64 x
+        // 768 from 3,072: 9.1, 10.6, 15.9 us with 1, 2, 4 blocks of 16 rows; 64 x 3,072
+        // from 768: 8.6, 6.9, 6.9)
         p.mt = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        p.k_split = (int32_t)K;
+        while (p.mt > 1 && (N + 15) / 16 * ((M + 16 * p.mt - 1) / (16 * p.mt)) < 192) p.mt /= 2;
         return p;
     }
+    // The tile and the number of k splits with the least estimated time.  A
+    // step takes a workgroup `alone` us while the GPU is nearly empty, up to
+    // `full` with every place taken (768 x 768 products of 1,003 to 50,432 rows:
+    // 2,048 rows 8.2 / 13.0 / 20.0 us with 384, 96, 48 tiles of 64, 128, 256 rows;
+    // 12,608 rows from 3,072: 102 / 90 / 90 us).  Splits add a launch, a write
+    // and a read of their fp32 sums (197 x 768 from 3,072: 16.4, 12.6, 11.1, 11.3 us
+    // with 1, 2, 4, 8; 2,048 x 768 from 768: 8.2 and 18.2 us with 1 and 2).  No
+    // sum runs over more than 16,384 values of k in fp32.
+    static const double kAlone[] = {0.7, 0.4, 0.3}, kFull[] = {1.25, 1.3, 0.75};
+    static const int64_t kPlaces[] = {512, 768, 768};
+    double best = 1e30;
     p.kind = kTile;
-    // the largest tile that still gives every CU two workgroups, else the smallest
-    p.tile = 2;
-    for (int i = 0; i < 2; ++i)
-        if (((M + kTileM[i] - 1) / kTileM[i]) * ((N + kTileN[i] - 1) / kTileN[i]) >= kSlots) {
-            p.tile = i;
-            break;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = ((M + kTileM[i] - 1) / kTileM[i]) * ((N + kTileN[i] - 1) / kTileN[i]);
+        const int64_t steps = (K + kTileK[i] - 1) / kTileK[i], least = (K + 16383) / 16384;
+        for (int64_t s = least < 1 ? 1 : least; s <= 64 || s == least; ++s) {
+            if (s > 1 && s > least && (steps < 4 * s || (double)s * M * N * 4 > 256e6)) break;
+            const int64_t per = (steps + s - 1) / s, wgs = tiles * s, rounds = (wgs + kPlaces[i] - 1) / kPlaces[i];
+            const int64_t here = wgs < kPlaces[i] ? wgs : kPlaces[i];
+            const double load = (double)((here + 255) / 256 * 256) / (double)kPlaces[i];  // of the busiest CU
+            const double step = kFull[i] * load > kAlone[i] ? kFull[i] * load : kAlone[i];
+            double us = 3.0 + (double)rounds * per * step;
+            if (s > 1) us += 4.0 + 2.0 * (double)s * M * N * 4 / 4e6;
+            if (us < best) {
+                best = us;
+                p.tile = i;
+                p.k_split = (int32_t)(per * kTileK[i] < K ? per * kTileK[i] : (K > 0 ? K : 1));
+            }
         }
-    if (p.tile == 2 && K >= 4096) p.tile = (M >= 256 && N >= 128) ? 0 : 2;  // a long k range: split it
-    const int64_t tiles = ((M + kTileM[p.tile] - 1) / kTileM[p.tile]) * ((N + kTileN[p.tile] - 1) / kTileN[p.tile]);
-    const int bk = kTileK[p.tile];
-    const int64_t steps = (K + bk - 1) / bk;
-    int64_t splits = tiles >= kSlots ? 1 : kSlots / tiles;
-    const int64_t most = steps / 8;  // at least 8 steps a split
-    if (splits > most) splits = most;
-    if (splits < 1) splits = 1;
-    // fp32 sums of one split run over at most 16384 k
-    const int64_t least = (K + 16383) / 16384;
-    if (splits < least) splits = least;
-    const int64_t per = (steps + splits - 1) / splits;
-    p.k_split = (int32_t)(per * bk < K ? per * bk : (K > 0 ? K : 1));
+    }
     p.splits = (int32_t)((K + p.k_split - 1) / p.k_split);
     if (p.splits < 1) p.splits = 1;
     p.two_steps = p.splits > 1 || any_groups;
@@ -786,12 +888,7 @@ hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &arg
     hipError_t e = p.aligned ? launch_tiles_aligned(p.tile, form, p.two_steps, rat == 1, a, s)
                              : launch_tiles_any(p.tile, form, p.two_steps, rat == 1, a, s);
     if (e != hipSuccess || !p.two_steps) return e;
-    const int64_t work = (int64_t)((a.N + 7) / 8) * a.M;
-    const dim3 grid((unsigned)((work + 255) / 256));
-    if (rat == 0) hipLaunchKernelGGL((grkan_linear_finish_kernel<0>), grid, dim3(256), 0, s, a);
-    if (rat == 1) hipLaunchKernelGGL((grkan_linear_finish_kernel<1>), grid, dim3(256), 0, s, a);
-    if (rat == 2) hipLaunchKernelGGL((grkan_linear_finish_kernel<2>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    return rat == 0 ? launch_finish<0>(a, s) : (rat == 1 ? launch_finish<1>(a, s) : launch_finish<2>(a, s));
 }
 
 // ------------------------------------------------------------ dpre, dbias

@@ -716,12 +716,24 @@ template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(1024) void grkan_norm_apply_fwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     float2 *stats = reinterpret_cast<float2 *>(lds);
+    constexpr int B = 4;  // rows on their way at a time
     const NormPlan &p = a.p;
     const int64_t total = a.N * p.chunks * p.ncb;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
         const int cb = (int)(b % p.ncb);
         const int64_t nc = b / p.ncb, n = nc / p.chunks, c = nc % p.chunks;
         const Place q(a, cb);
+        // the first rows are on their way while the statistics are formed
+        const int64_t r0 = c * p.chunk_rows + q.ty, r1 = min(a.S, (c + 1) * p.chunk_rows);
+        Pack<V> next[B];
+        auto fetch = [&](int64_t r) {
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const int64_t row = r + i * p.TY;
+                next[i] = Pack<V>::load(at(a.x, n * a.xs + (row < r1 ? row : 0) * a.xr + q.col), row < r1 ? q.nv : 0);
+            }
+        };
+        fetch(r0);
         if (p.fused) own_parts(a, q, n, stats);
         Cols<V, RAT> k;
         k.init(a, q.col, q.nv);
@@ -739,12 +751,16 @@ __global__ __launch_bounds__(1024) void grkan_norm_apply_fwd_kernel(NormArgs a) 
                     a.mean[n * a.G + q.g0 + j] = stats[j].x;
                     a.rstd[n * a.G + q.g0 + j] = stats[j].y;
                 }
-        const int64_t r1 = min(a.S, (c + 1) * p.chunk_rows);
-        if (q.nv > 0) {
-#pragma unroll 4
-            for (int64_t r = c * p.chunk_rows + q.ty; r < r1; r += p.TY)
-                apply_forward<V, RAT, MIXED>(Pack<V>::load(at(a.x, n * a.xs + r * a.xr + k.col), k.nv), st, k, a.act)
-                    .store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
+        for (int64_t r = r0; r < r1; r += B * p.TY) {
+            Pack<V> x[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) x[i] = next[i];
+            fetch(r + B * p.TY);
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                if (r + i * p.TY < r1 && k.nv > 0)
+                    apply_forward<V, RAT, MIXED>(x[i], st, k, a.act)
+                        .store(at(a.y, (n * a.S + r + i * p.TY) * a.C + k.col), k.nv);
         }
         __syncthreads();  // the statistics in LDS have been read
     }
