@@ -85,18 +85,27 @@ __device__ static inline float act_slope(float h, int act) {
 // deciding the sign of Q more exactly than h is known would mean nothing --
 // with sign(0) = 0.  The powers of h serve the polynomials and the sums (46
 // instructions; Horner's rule with running products for the sums takes 51).
+// EXACT: h is an exact input (a kept bf16 product), and the sign of Q is
+// decided for it: the fp32 Q is within 8 u sum |b_j| |h|^j <= 8 u (1 + h^4) sum
+// |b_j| of Q (u = 2^-24; four products and sums over exact b), so beyond twice that its
+// sign is Q's; the rare element within it (h = 0 among them) takes the
+// compensated decision of the activation's own backward.  (That backward also
+// evaluates Q itself in fp64, 70 instructions an element against 42.)
 struct SlopeCoefs {
     Coefs<5, 4> c;
     float da[4], db[3];  // 2 a_2 .. 5 a_5, 2 b_2 .. 4 b_4
+    float guard;         // 16 u sum |b_j|, at least the smallest normal number
     __device__ inline void init(const Coefs<5, 4> &k) {
         c = k;
 #pragma unroll
         for (int i = 2; i <= 5; ++i) da[i - 2] = (float)i * k.a[i];
 #pragma unroll
         for (int j = 2; j <= 4; ++j) db[j - 2] = (float)j * k.b[j - 1];
+        guard = fmaxf((fabsf(k.b[0]) + fabsf(k.b[1]) + fabsf(k.b[2]) + fabsf(k.b[3])) * 0x1p-20f, kGuardFloor);
     }
 };
 
+template <bool EXACT = false>
 __device__ static inline float rational_slope(float h, float dy, const SlopeCoefs &k, float (&acc)[10]) {
     // One element after another (the asm ties h to every sum so far): left
     // alone, the compiler puts the sums off and holds the powers of all of a
@@ -112,7 +121,14 @@ __device__ static inline float rational_slope(float h, float dy, const SlopeCoef
     const float r = __builtin_amdgcn_rcpf(1.0f + fabsf(Q));
     const float w = dy * r;
     const float v = w * (P * r);
-    const float sv = Q == 0.0f ? 0.0f : __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(Q) & 0x80000000u));
+    float sv = __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(Q) & 0x80000000u));
+    if constexpr (!EXACT) {
+        sv = Q == 0.0f ? 0.0f : sv;
+    } else if (!(fabsf(Q) > fmaf(h4, k.guard, k.guard))) {
+        const bool zero = h == 0.0f || (b[0] == 0.0f && b[1] == 0.0f && b[2] == 0.0f && b[3] == 0.0f);
+        const int s = zero ? 0 : qsign_compensated<4>(h, k.c.b) * (h > 0.0f ? 1 : -1);
+        sv = s == 0 ? 0.0f * v : (s > 0 ? v : -v);
+    }
     acc[0] += w;
     acc[1] = fmaf(w, h, acc[1]);
     acc[2] = fmaf(w, h2, acc[2]);

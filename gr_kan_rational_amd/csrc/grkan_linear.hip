@@ -140,6 +140,22 @@ __device__ static inline void finish8(float (&h)[8], const Epilogue &e, const Ch
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer: reads zeros
 constexpr int kThreads = 256;
 
+// 16 bytes per lane from offset `off` of the buffer to LDS, lane after lane
+// from `to` (the same in all lanes; the instruction takes it from M0).  Written
+// as an instruction because it has no result: the compiler, which cannot tell
+// the stages apart, would wait for every such load before each transposing LDS
+// read (the products with a strided operand took 1.5 times as long); arrival is
+// waited for by count (wait_loads).  Loads that the compiler does know of only
+// wait longer for the ones it does not.  M0 is the compiler's to use nowhere
+// else in these kernels.
+__device__ static inline void fetch_chunk(u32x4 rsrc, uint32_t off, const char *to) {
+    const uint32_t lds = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)to);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(rsrc)
+                 : "memory");
+}
+
 // One operand's tile of ROWS x BK, as this thread's chunks: chunk id i * 256 +
 // thread, at byte 16 id of its stage.
 template <int ROWS, int BK, bool STRIDED> struct Stager {
@@ -200,16 +216,13 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
     template <int SET> __device__ inline void fetch(char *lds, int stage, int t, int left) {
         const char *src = base + t * step;
         if constexpr (kAligned) {
-            __amdgpu_buffer_rsrc_t rsrc =
-                __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, 0x7ffffff0, 0x00020000);
+            const uint64_t addr = reinterpret_cast<uint64_t>(src);
+            const u32x4 rsrc = {(uint32_t)addr, (uint32_t)(addr >> 32) & 0xffffu, 0x7ffffff0u, 0x00020000u};
             const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
-                const uint32_t o = k < left ? off[i] : kNowhere;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (__attribute__((address_space(3))) void *)(lds + stage + (i * kThreads + wave * 64) * 16), 16, o,
-                    0, 0, 0);
+                fetch_chunk(rsrc, k < left ? off[i] : kNowhere, lds + stage + (i * kThreads + wave * 64) * 16);
             }
         } else if (left >= BK && inside) {
 #pragma unroll
@@ -337,27 +350,47 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
     constexpr int WM = BM / 2, WN = BN / 2;
     const int mrow = (wave >> 1) * WM, ncol = (wave & 1) * WN;
 
-    // Tile b of the launch.  Workgroups go to the 8 XCDs in turn.  Without
-    // splits each XCD takes whole panels of BM rows, column tiles of a panel one
-    // after another, so that a panel of Q stays in one L2; with splits, tiles
-    // of one k range come one after another.
+    // Tile b of the launch.  Workgroups go to the 8 XCDs in turn, and what an
+    // XCD's workgroups share should stay in its L2.  Without splits each XCD
+    // takes whole panels of BM rows, column tiles of a panel one after another.
+    // With splits in eighths each XCD takes whole k ranges; with others, an
+    // eighth of the row or column tiles of all of them if those come in eighths
+    // (768 x 3,072 from 50,432 rows in 7 splits: 271 us with all of both operands
+    // going to every XCD, 257 us so), else tiles in their order.
+    enum { kByTile, kBySplit, kByN, kByM };
+    const int order = a.splits % 8 == 0 ? kBySplit : (nb % 8 == 0 ? kByN : (mb % 8 == 0 ? kByM : kByTile));
     const int count = PARTIAL ? tiles * a.splits : (mb + 7) / 8 * 8 * nb;
     int m0, n0, split = 0, kb = 0, len = a.K;
     auto place = [&](int b) {
+        const int xcd = b & 7, idx = b >> 3;
         if constexpr (PARTIAL) {
-            split = b / tiles;
-            const int tile = b - split * tiles;
-            m0 = tile / nb * BM;
-            n0 = tile % nb * BN;
+            int mt, nt;
+            if (order == kByN) {
+                const int w = nb / 8;
+                nt = idx % w * 8 + xcd;
+                mt = idx / w % mb;
+                split = idx / w / mb;
+            } else if (order == kByM) {
+                const int w = mb / 8;
+                mt = idx % w * 8 + xcd;
+                nt = idx / w % nb;
+                split = idx / w / nb;
+            } else {
+                const int i = order == kBySplit ? idx : b;
+                split = order == kBySplit ? i / tiles * 8 + xcd : i / tiles;
+                mt = i % tiles / nb;
+                nt = i % tiles % nb;
+            }
+            m0 = mt * BM;
+            n0 = nt * BN;
             kb = split * a.k_split;
             len = min(a.K - kb, a.k_split);
         } else {
-            const int idx = b >> 3;
-            m0 = (idx / nb * 8 + (b & 7)) * BM;
+            m0 = (idx / nb * 8 + xcd) * BM;
             n0 = idx % nb * BN;
         }
     };
-    // The next tile of this workgroup from b on, or `count`.
+    // The next tile of this workgroup from b on, or `count` or more.
     auto next = [&](int b) {
         if constexpr (!PARTIAL)
             while (b < count && ((b >> 3) / nb * 8 + (b & 7)) * BM >= a.M) b += (int)gridDim.x;
@@ -696,7 +729,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void grkan_linear_skinny_kernel(
 // The splits' sums added, then the epilogue.  SL lanes share the splits of 8
 // columns (each adds every SL-th in order, the lanes' sums then in order through
 // LDS), so that a small result with many splits still fills the GPU: 768 x 192
-// from 42 splits is 18,432 columns of 8.
+// is 18,432 columns of 8.
 template <int RAT, int SL>
 __global__ __launch_bounds__(256) void grkan_linear_finish_kernel(ProductArgs a) {
     constexpr int kItems = 256 / SL;
@@ -812,8 +845,8 @@ namespace {
 template <int RAT> hipError_t launch_finish(const ProductArgs &a, hipStream_t s) {
     const int64_t work = (int64_t)((a.N + 7) / 8) * a.M;
     // lanes that share the splits, while a thread per 8 columns leaves CUs idle
-    if (a.splits >= 8 && work < 64 * 1024)
-        hipLaunchKernelGGL((grkan_linear_finish_kernel<RAT, 8>), dim3((unsigned)((work + 31) / 32)), dim3(256), 0, s, a);
+    if (a.splits >= 4 && work < 64 * 1024)
+        hipLaunchKernelGGL((grkan_linear_finish_kernel<RAT, 4>), dim3((unsigned)((work + 63) / 64)), dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((grkan_linear_finish_kernel<RAT, 1>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -847,9 +880,12 @@ ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned
     // 2,048 rows 8.2 / 13.0 / 20.0 us with 384, 96, 48 tiles of 64, 128, 256 rows;
     // 12,608 rows from 3,072: 102 / 90 / 90 us).  Splits add a launch, a write
     // and a read of their fp32 sums (197 x 768 from 3,072: 16.4, 12.6, 11.1, 11.3 us
-    // with 1, 2, 4, 8; 2,048 x 768 from 768: 8.2 and 18.2 us with 1 and 2).  No
-    // sum runs over more than 16,384 values of k in fp32.
-    static const double kAlone[] = {0.7, 0.4, 0.3}, kFull[] = {1.25, 1.3, 0.75};
+    // with 1, 2, 4, 8; 2,048 x 768 from 768: 8.2 and 18.2 us with 1 and 2).  The
+    // operands reach the XCDs at about 10 TB/s, once or to each of the 8 as the
+    // tiles' order has it (768 x 192 from 25,216 rows: 43-49 us in 7 splits, all of
+    // both to each; 25 us in 16, each k range to one).  No sum runs over more
+    // than 16,384 values of k in fp32.
+    static const double kAlone[] = {0.85, 0.4, 0.33}, kFull[] = {1.25, 1.3, 0.75};
     static const int64_t kPlaces[] = {512, 768, 768};
     double best = 1e30;
     p.kind = kTile;
@@ -857,12 +893,17 @@ ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned
         const int64_t tiles = ((M + kTileM[i] - 1) / kTileM[i]) * ((N + kTileN[i] - 1) / kTileN[i]);
         const int64_t steps = (K + kTileK[i] - 1) / kTileK[i], least = (K + 16383) / 16384;
         for (int64_t s = least < 1 ? 1 : least; s <= 64 || s == least; ++s) {
+            if (s > 8 && s % 8 != 0 && s != least) continue;  // eighths: a k range to an XCD
             if (s > 1 && s > least && (steps < 4 * s || (double)s * M * N * 4 > 256e6)) break;
             const int64_t per = (steps + s - 1) / s, wgs = tiles * s, rounds = (wgs + kPlaces[i] - 1) / kPlaces[i];
             const int64_t here = wgs < kPlaces[i] ? wgs : kPlaces[i];
             const double load = (double)((here + 255) / 256 * 256) / (double)kPlaces[i];  // of the busiest CU
             const double step = kFull[i] * load > kAlone[i] ? kFull[i] * load : kAlone[i];
-            double us = 3.0 + (double)rounds * per * step;
+            const int64_t mt = (M + kTileM[i] - 1) / kTileM[i], nt = (N + kTileN[i] - 1) / kTileN[i];
+            const bool once = s > 1 && s % 8 == 0;
+            const double qx = once || s == 1 || (nt % 8 != 0 && mt % 8 == 0) ? 1 : 8, px = once || (s > 1 && nt % 8 == 0) ? 1 : 8;
+            const double fetch = 2.0 * (double)K * (qx * (double)M + px * (double)N) / 10e6, work = (double)rounds * per * step;
+            double us = 3.0 + (work > fetch ? work : fetch);
             if (s > 1) us += 4.0 + 2.0 * (double)s * M * N * 4 / 4e6;
             if (us < best) {
                 best = us;
@@ -909,13 +950,8 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
     float sum[V], coef[RAT ? 10 : 1] = {};
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-    BwdCoefs<5, 4> kc;
-    QWide<4> kw;
-    if constexpr (RAT) {
-        const Coefs<5, 4> c = load_coefs<5, 4>(a.A, a.B, nv > 0 ? n / a.dga : 0);
-        kc = derive<5, 4>(c);
-        kw = widen<5, 4, false>(c);
-    }
+    SlopeCoefs sc;
+    if constexpr (RAT) sc.init(load_coefs<5, 4>(a.A, a.B, nv > 0 ? n / a.dga : 0));
     auto value = [](u32x4 v, int e) { return __uint_as_float((e & 1) ? (v[e / 2] & 0xffff0000u) : (v[e / 2] << 16)); };
     if (nv > 0) {
         for (int64_t r = r0 + ty; r < r1; r += kSlopeTy) {
@@ -931,12 +967,9 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
             for (int e = 0; e < V; ++e) {
                 const float he = value(h, e), ge = value(g, e);
                 if constexpr (RAT) {
-                    // pre is what the forward kept, an exact input: the sign of Q is decided as by the
-                    // activation's own backward
-                    const Pow<5> X(he);
-                    const ElemBwd el = sign_fixed_element<5, 4, 5>(X, ge, kc, kw);
-                    accumulate<5, 4, 5>(el.w, el.sv, X, coef);
-                    d[e] = el.dx;
+                    // pre is what the forward kept, an exact input: the sign of Q is decided
+                    // as by the activation's own backward
+                    d[e] = rational_slope<true>(he, ge, sc, *reinterpret_cast<float (*)[10]>(coef));
                 } else {
                     d[e] = ge * act_slope(he, a.act);
                 }
