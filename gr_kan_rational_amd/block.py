@@ -10,6 +10,7 @@ call runs on.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -47,6 +48,12 @@ def _library() -> ctypes.CDLL:
         size.restype = sz
     _lib = lib
     return lib
+
+
+@functools.lru_cache(maxsize=256)
+def _need(name: str, *shape) -> int:
+    """Workspace bytes of an operator, a function of its shape alone."""
+    return getattr(_library(), f"grkan_{name}_workspace_size")(*shape)
 
 
 def _act(act: str) -> int:
@@ -179,7 +186,7 @@ def grkan_group_norm_forward(x: torch.Tensor, norm_groups: int, weight=None, bia
     if out is not None and out.shape != x.shape:
         raise ValueError("out must match x")
     lib = _library()
-    need = lib.grkan_group_norm_forward_workspace_size(n, s, c, norm_groups, ng, code, io)
+    need = _need("group_norm_forward", n, s, c, norm_groups, ng, code, io)
 
     def launch(handle):
         y = _given(out, "out", x.shape, x.dtype, dev)
@@ -220,7 +227,7 @@ def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Ten
     if dx is not None and dx.shape != x.shape:
         raise ValueError("dx must match x")
     lib = _library()
-    need = lib.grkan_group_norm_backward_workspace_size(n, s, c, norm_groups, ng, code, io)
+    need = _need("group_norm_backward", n, s, c, norm_groups, ng, code, io)
 
     def launch(handle):
         gx = _given(dx, "dx", x.shape, x.dtype, dev)
@@ -307,7 +314,7 @@ def grkan_linear_act_forward(x: torch.Tensor, W: torch.Tensor, bias=None, act: s
             raise ValueError(f"residual must be {list(shape)}")
         ldr = _rows(residual, "residual", dev)[2]
     lib = _library()
-    need = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, ng, code)
+    need = _need("linear_act_forward", rows, d_in, d_out, ng, code)
 
     def launch(handle):
         z = _given(out, "out", shape, torch.bfloat16, dev)
@@ -342,7 +349,7 @@ def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor
         _check_out(pre, "pre", torch.bfloat16, rows * d_out, dev)
     A, B, ng = _act_coefs(code, A, B, n_groups, d_out, dev)
     lib = _library()
-    need = lib.grkan_linear_act_backward_workspace_size(rows, d_in, d_out, ng, code)
+    need = _need("linear_act_backward", rows, d_in, d_out, ng, code)
 
     def launch(handle):
         gx = _given(dx, "dx", x.shape, torch.bfloat16, dev)

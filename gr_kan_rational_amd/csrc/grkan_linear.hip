@@ -937,6 +937,7 @@ hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &arg
 namespace {
 
 constexpr int kSlopeTx = 32, kSlopeTy = 8;
+constexpr int64_t kSlopeBlocks = 1536;  // workgroups, 6 a CU
 
 template <int V, bool RAT>
 __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel(SlopeArgs a) {
@@ -953,16 +954,27 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
     SlopeCoefs sc;
     if constexpr (RAT) sc.init(load_coefs<5, 4>(a.A, a.B, nv > 0 ? n / a.dga : 0));
     auto value = [](u32x4 v, int e) { return __uint_as_float((e & 1) ? (v[e / 2] & 0xffff0000u) : (v[e / 2] << 16)); };
+    // the next row's values are on their way while this one's are worked on
+    auto fetch = [&](int64_t r, u32x4 &g, u32x4 &h) {
+        if (r >= r1) return;
+        g = V == 8 ? load8(dz + r * a.lddz, nv) : u32x4{dz[r * a.lddz], 0u, 0u, 0u};
+        if (a.act != GRKAN_ACT_NONE) h = V == 8 ? load8(pre + r * a.N, nv) : u32x4{pre[r * a.N], 0u, 0u, 0u};
+    };
     if (nv > 0) {
+        u32x4 ng[2] = {}, nh[2] = {};
+        fetch(r0 + ty, ng[0], nh[0]);
+        fetch(r0 + ty + kSlopeTy, ng[1], nh[1]);
         for (int64_t r = r0 + ty; r < r1; r += kSlopeTy) {
-            const u32x4 g = V == 8 ? load8(dz + r * a.lddz, nv) : u32x4{dz[r * a.lddz], 0u, 0u, 0u};
+            const u32x4 g = ng[0], h = nh[0];
+            ng[0] = ng[1];
+            nh[0] = nh[1];
+            fetch(r + 2 * kSlopeTy, ng[1], nh[1]);
             float d[8] = {};
             if (a.act == GRKAN_ACT_NONE) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) sum[e] += value(g, e);
                 continue;
             }
-            const u32x4 h = V == 8 ? load8(pre + r * a.N, nv) : u32x4{pre[r * a.N], 0u, 0u, 0u};
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float he = value(h, e), ge = value(g, e);
@@ -1061,7 +1073,7 @@ SlopePlan plan_slope(int64_t rows, int64_t N, int32_t act, int64_t dga) {
     p.vec = rational && dga % 8 != 0 ? 1 : 8;
     p.vpr = (int32_t)((N + p.vec - 1) / p.vec);
     const int64_t blocks = (p.vpr + kSlopeTx - 1) / kSlopeTx;
-    int64_t chunks = (2048 + blocks - 1) / blocks;
+    int64_t chunks = (kSlopeBlocks + blocks - 1) / blocks;
     const int64_t most = (rows + 4 * kSlopeTy - 1) / (4 * kSlopeTy);
     if (chunks > most) chunks = most;
     if (chunks < 1) chunks = 1;
