@@ -49,6 +49,8 @@ enum ProductKind : int32_t { kTile = 0, kSkinny = 1 };
 struct ProductPlan {
     int32_t kind;
     int32_t tile;            // kTile: index of the tile shape
+    int32_t rest_tile;       // kTile: shape of the rows from `rows` on, when rows > 0
+    int64_t rows;
     int32_t mt;              // kSkinny: 16-row blocks per workgroup
     int32_t splits, k_split;
     bool two_steps;          // partials, then grkan_linear_finish

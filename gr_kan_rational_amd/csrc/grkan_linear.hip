@@ -6,28 +6,33 @@
 //
 // Bound: many rows, the matrix cores; few rows, the bytes of W.
 //
-// The tile kernel.  A workgroup of 4 waves (2 x 2) forms a BM x BN tile of
-// the result; a wave BM/2 x BN/2 of it in 32 x 32 blocks of
-// v_mfma_f32_32x32x16_bf16.  The instruction's row operand is P (columns of
-// the result) and its column operand Q (rows of the result), so a lane's
-// accumulators run along n within one row of the result, and exchanging them
-// with the lane 32 away leaves 8 consecutive columns in a lane, which take bias,
-// activation and residual together and leave through LDS as whole rows.
-// k advances BK at a time through three LDS stages.  While step t is
-// multiplied, the chunks of step t + 2 travel from memory straight into LDS
-// (no registers); one barrier a step, before the step's last group of matrix
-// instructions, whose fragments are already in registers, covers both the
-// arrival of step t + 1 and the release of step t's stage.  The launch has as
-// many workgroups as the CUs hold at once (two or three a CU, so that one's
-// epilogue and barriers overlap another's products); each walks over its
-// tiles, and the fetches run on into the next tile while a result leaves.
+// The tile kernel.  A workgroup of 4 waves (2 x 2; 8 waves, 2 x 4, for the
+// 256 x 256 tile) forms a BM x BN tile of the result; a wave a part of it in
+// 32 x 32 blocks of v_mfma_f32_32x32x16_bf16.  The instruction's row operand is
+// P (columns of the result) and its column operand Q (rows of the result), so a
+// lane's accumulators run along n within one row of the result, and exchanging
+// them with the lane 32 away leaves 8 consecutive columns in a lane, which take
+// bias, activation and residual together and leave through LDS as whole rows.
+// k advances BK at a time through two or three LDS stages.  While step t is
+// multiplied, the chunks of the step after (or two after) travel from memory
+// straight into LDS (no registers); one barrier a step, before the step's last
+// group of matrix instructions, whose fragments are already in registers,
+// covers both the arrival of step t + 1 and the release of step t's stage.  The
+// launch has as many workgroups as the CUs hold at once (one of 8 waves, three
+// of 4); each walks over its tiles, and the fetches run on into the next tile
+// while a result leaves.
 //
-// Measured on MI355X at 50,432 rows (238 GFLOP a product): 293-302 us for d =
-// 768 -> 3,072 and 267-280 us for 3,072 -> 768 (790-890 TFLOP/s; the library's
-// product on the first takes 297 us).  LDS bounds the products: without the
-// fetches (64 bytes a cycle into LDS beside the fragments' 128 out of it) the
-// same loop runs 1.5 times as fast.  A 256 x 256 tile of 4 waves, which reads a
-// third less, needs 352 registers and ran at 376 TFLOP/s with one wave a SIMD.
+// Measured on MI355X, products alone: 1,180-1,240 TFLOP/s at 8,192 x 8,192 from
+// 8,192 (the library's 1,358), 286-324 us at 50,432 x 3,072 from 768 and 280 us at
+// 50,432 x 768 from 3,072 (238 GFLOP; the library's 230-300 us).  What bounds them
+// is the way into LDS and the power it takes: with every fetch left out the
+// same loop ran at 1,700-1,800 TFLOP/s, with all fetches from one place in L2
+// as fast as without the change, and more steps in flight, wave priorities and
+// fixed orders of reads and products changed 0-3%.  So the largest tile counts, since it
+// fetches least: 256 x 256 in 8 waves and two stages of 64 against 256 x 128
+// in 4 waves, two workgroups a CU, three stages of 32 (the products above 1.1 to
+// 1.3 times as long) and against three or four stages of 32 (1.05 to 1.1 times).
+// 256 x 256 in 4 waves needs 352 registers: 376 TFLOP/s with one wave a SIMD.
 //
 // LDS layouts.  Chunks are 16 bytes and land in the order of the lanes, so
 // bank conflicts are avoided by choosing which chunk a lane fetches:
@@ -78,7 +83,7 @@ __device__ static inline void store8(uint16_t *p, int nv, u32x4 v) {
 }
 
 // store8 for results larger than the caches: non-temporal, so that they do not
-// drive the operands out (50,432 x 768 -> 3,072: 355 us with ordinary stores,
+// drive the operands out (50,432 x 3,072 from 768: 355 us with ordinary stores,
 // 323 with these).
 __device__ static inline void stream8(uint16_t *p, int nv, u32x4 v) {
     if (nv >= 8)
@@ -138,7 +143,6 @@ __device__ static inline void finish8(float (&h)[8], const Epilogue &e, const Ch
 // ------------------------------------------------------------ staging
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer: reads zeros
-constexpr int kThreads = 256;
 
 // 16 bytes per lane from offset `off` of the buffer to LDS, lane after lane
 // from `to` (the same in all lanes; the instruction takes it from M0).  Written
@@ -156,13 +160,21 @@ __device__ static inline void fetch_chunk(u32x4 rsrc, uint32_t off, const char *
                  : "memory");
 }
 
-// One operand's tile of ROWS x BK, as this thread's chunks: chunk id i * 256 +
+// The swizzles f and s of the LDS layouts above.
+template <int BK> __device__ static inline int chunk_of_row(int row) {
+    return ((BK == 64 ? row : row >> 1) & (BK / 8 - 1)) ^ ((row >> 3) & 1);
+}
+template <int ROWS> __device__ static inline int chunk_of_k(int k) {
+    return ROWS >= 128 ? 2 * ((k & 3) + 4 * (k & 1)) : 2 * (k & 3);
+}
+
+// One operand's tile of ROWS x BK, as this thread's chunks: chunk id i * T +
 // thread, at byte 16 id of its stage.
-template <int ROWS, int BK, bool STRIDED> struct Stager {
-    static constexpr int kChunks = ROWS * BK / 8 / kThreads;
+template <int ROWS, int BK, bool STRIDED, int T> struct Stager {
+    static constexpr int kChunks = ROWS * BK / 8 / T;
     static constexpr int kBytes = ROWS * BK * 2;
     static constexpr int kPerRow = STRIDED ? ROWS / 8 : BK / 8;  // chunks per LDS row
-    static_assert(ROWS * BK / 8 % kThreads == 0 && kThreads % kPerRow == 0, "whole chunks");
+    static_assert(ROWS * BK / 8 % T == 0 && T % kPerRow == 0, "whole chunks");
 
     const char *base;    // first row of the tile at its first k
     int64_t step;        // bytes from one k step to the next
@@ -173,9 +185,6 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
     bool inside;         // the tile lies inside the operand: unaligned chunks of a whole step need no checks
     u32x4 r[2][kAligned ? 1 : kChunks];  // unaligned: chunks on their way, of two steps
 
-    __device__ static inline int f(int row) { return ((BK == 64 ? row : row >> 1) & (BK / 8 - 1)) ^ ((row >> 3) & 1); }
-    __device__ static inline int s(int k) { return ROWS >= 128 ? 2 * ((k & 3) + 4 * (k & 1)) : 2 * (k & 3); }
-
     __device__ inline void init(const Operand &o, int row0, int rows, int kstart) {
         const int t = (int)threadIdx.x;
         ld = o.ld;
@@ -184,19 +193,19 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
             base = static_cast<const char *>(o.p) + ((int64_t)kstart * ld + row0) * 2;
             step = (int64_t)BK * ld * 2;
             k0 = r0;
-            // the rows of a thread's chunks are a multiple of 4 apart, so s() is one value
-            static_assert(kThreads / kPerRow % 4 == 0, "one swizzle per thread");
-            const int c = slot ^ s(r0);
+            // the rows of a thread's chunks are a multiple of 4 apart, so chunk_of_k is one value
+            static_assert(T / kPerRow % 4 == 0, "one swizzle per thread");
+            const int c = slot ^ chunk_of_k<ROWS>(r0);
             valid = min(max(rows - row0 - c * 8, 0), 8);
             inside = row0 + ROWS <= rows;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i)
-                off[i] = valid > 0 ? (uint32_t)((r0 + i * (kThreads / kPerRow)) * ld * 2 + c * 16) : kNowhere;
+                off[i] = valid > 0 ? (uint32_t)((r0 + i * (T / kPerRow)) * ld * 2 + c * 16) : kNowhere;
         } else {
             base = static_cast<const char *>(o.p) + ((int64_t)row0 * ld + kstart) * 2;
             step = BK * 2;
-            static_assert(kThreads / kPerRow % 16 == 0, "one swizzle per thread");
-            const int c = slot ^ f(r0);
+            static_assert(T / kPerRow % 16 == 0, "one swizzle per thread");
+            const int c = slot ^ chunk_of_row<BK>(r0);
             k0 = c * 8;
             valid = 8;
             inside = true;
@@ -204,7 +213,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
             // they form is not stored
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                int row = r0 + i * (kThreads / kPerRow);
+                int row = r0 + i * (T / kPerRow);
                 if (!kAligned) row = min(row, rows - 1 - row0);
                 off[i] = row0 + row < rows ? (uint32_t)(row * ld * 2 + c * 16) : kNowhere;
             }
@@ -217,12 +226,13 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
         const char *src = base + t * step;
         if constexpr (kAligned) {
             const uint64_t addr = reinterpret_cast<uint64_t>(src);
-            const u32x4 rsrc = {(uint32_t)addr, (uint32_t)(addr >> 32) & 0xffffu, 0x7ffffff0u, 0x00020000u};
+            const u32x4 rsrc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)addr), (uint32_t)__builtin_amdgcn_readfirstlane((int)(addr >> 32)) & 0xffffu,
+                                0x7ffffff0u, 0x00020000u};
             const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
-                fetch_chunk(rsrc, k < left ? off[i] : kNowhere, lds + stage + (i * kThreads + wave * 64) * 16);
+                const int k = STRIDED ? k0 + i * (T / kPerRow) : k0;
+                fetch_chunk(rsrc, k < left ? off[i] : kNowhere, lds + stage + (i * T + wave * 64) * 16);
             }
         } else if (left >= BK && inside) {
 #pragma unroll
@@ -230,7 +240,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
         } else {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int k = STRIDED ? k0 + i * (kThreads / kPerRow) : k0;
+                const int k = STRIDED ? k0 + i * (T / kPerRow) : k0;
                 const int nv = STRIDED ? (k < left ? valid : 0) : min(max(left - k, 0), 8);
                 r[SET][i] = load8(reinterpret_cast<const uint16_t *>(src + (nv ? off[i] : 0)), nv);
             }
@@ -241,7 +251,7 @@ template <int ROWS, int BK, bool STRIDED> struct Stager {
         if constexpr (!kAligned) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i)
-                *reinterpret_cast<u32x4 *>(lds + stage + (i * kThreads + (int)threadIdx.x) * 16) = r[SET][i];
+                *reinterpret_cast<u32x4 *>(lds + stage + (i * T + (int)threadIdx.x) * 16) = r[SET][i];
         }
     }
 };
@@ -259,13 +269,13 @@ template <int ROWS, int BK, bool STRIDED, int NB> struct Reader {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int c = (col + 32 * i) >> 3;
-                at[i] = k * ROWS * 2 + ((c ^ Stager<ROWS, BK, true>::s(k)) << 4) + (col & 4) * 2;
+                at[i] = k * ROWS * 2 + ((c ^ chunk_of_k<ROWS>(k)) << 4) + (col & 4) * 2;
             }
         } else {
             const int row = row0 + (lane & 31);
 #pragma unroll
             for (int ks = 0; ks < BK / 16; ++ks)
-                at[ks] = row * BK * 2 + (((2 * ks + (lane >> 5)) ^ Stager<ROWS, BK, false>::f(row)) << 4);
+                at[ks] = row * BK * 2 + (((2 * ks + (lane >> 5)) ^ chunk_of_row<BK>(row)) << 4);
         }
     }
     __device__ inline void read(const char *stage, int ks, bf16x8 (&f)[NB]) const {
@@ -297,18 +307,20 @@ __device__ static inline void barrier() {
 // ------------------------------------------------------------ tile kernel
 
 template <int BM, int BN, int BK> struct TileShape {
+    static constexpr int kWavesN = BN == 256 ? 4 : 2, kThreads = 2 * kWavesN * 64;
+    static constexpr int kStages = BN == 256 ? 2 : 3;
     static constexpr int kStage = (BM + BN) * BK * 2;
-    static constexpr size_t kLds = 3 * (size_t)kStage + BN * 4 + BN / 8 * 12 * 4;
+    static constexpr size_t kLds = kStages * (size_t)kStage + BN * 4 + BN / 8 * 12 * 4;
 };
 
 // The epilogue's parameters of a tile's BN columns in LDS: bias, then for each
 // 8-column chunk the rational's coefficients (a_0..a_5, b_1..b_4, two unused).
-template <int RAT, int BN>
+template <int RAT, int BN, int T>
 __device__ static inline void load_params(float *params, const Epilogue &e, int n0, int N) {
     const int t = (int)threadIdx.x;
     if (t < BN) params[t] = e.bias && n0 + t < N ? e.bias[n0 + t] : 0.0f;
     if constexpr (RAT == 1) {
-        for (int i = t; i < BN / 8 * 12; i += kThreads) {
+        for (int i = t; i < BN / 8 * 12; i += T) {
             const int c = i / 12, k = i - 12 * c, n = n0 + 8 * c, g = n < N ? n / e.dga : 0;
             params[BN + i] = k < 6 ? e.A[g * 6 + k] : (k < 10 ? e.B[g * 4 + k - 6] : 0.0f);
         }
@@ -337,73 +349,49 @@ __device__ static inline void activate_tile(float (&h)[8], const float *params, 
 
 // FORM as in ProductForm; PARTIAL: fp32 sums of a split to memory.
 template <int BM, int BN, int BK, int FORM, bool PARTIAL, int RAT>
-__global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductArgs a) {
+__global__ __launch_bounds__((TileShape<BM, BN, BK>::kThreads), 2) void grkan_linear_tile_kernel(ProductArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    float *params = reinterpret_cast<float *>(lds + 3 * TileShape<BM, BN, BK>::kStage);
+    using Shape = TileShape<BM, BN, BK>;
+    constexpr int T = Shape::kThreads, S = Shape::kStages;
+    float *params = reinterpret_cast<float *>(lds + S * Shape::kStage);
     constexpr bool QS = FORM == kFormDw, PS = FORM != kFormForward;
-    constexpr int NM = BM / 64, NN = BN / 64;  // 32 x 32 blocks of a wave
-    constexpr int kStage = TileShape<BM, BN, BK>::kStage, kQ = BM * BK * 2;
+    constexpr int WM = BM / 2, WN = BN / Shape::kWavesN, NM = WM / 32, NN = WN / 32;  // 32 x 32 blocks of a wave
+    constexpr int kStage = Shape::kStage, kQ = BM * BK * 2;
     constexpr int KS = BK / 16;
 
     const int nb = (a.N + BN - 1) / BN, mb = (a.M + BM - 1) / BM, tiles = mb * nb;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    constexpr int WM = BM / 2, WN = BN / 2;
-    const int mrow = (wave >> 1) * WM, ncol = (wave & 1) * WN;
+    const int mrow = wave / Shape::kWavesN * WM, ncol = wave % Shape::kWavesN * WN;
 
     // Tile b of the launch.  Workgroups go to the 8 XCDs in turn, and what an
-    // XCD's workgroups share should stay in its L2.  Without splits each XCD
-    // takes whole panels of BM rows, column tiles of a panel one after another.
-    // With splits in eighths each XCD takes whole k ranges; with others, an
-    // eighth of the row or column tiles of all of them if those come in eighths
-    // (768 x 3,072 from 50,432 rows in 7 splits: 271 us with all of both operands
-    // going to every XCD, 257 us so), else tiles in their order.
-    enum { kByTile, kBySplit, kByN, kByM };
-    const int order = a.splits % 8 == 0 ? kBySplit : (nb % 8 == 0 ? kByN : (mb % 8 == 0 ? kByM : kByTile));
-    const int count = PARTIAL ? tiles * a.splits : (mb + 7) / 8 * 8 * nb;
+    // XCD's workgroups share should stay in its L2, so each XCD takes an eighth
+    // of the tiles: of all splits, those of a split together, its column tiles of a panel of
+    // BM rows one after another.
+    const int all = tiles * (PARTIAL ? a.splits : 1), per = (all + 7) / 8, count = per * 8;
     int m0, n0, split = 0, kb = 0, len = a.K;
     auto place = [&](int b) {
-        const int xcd = b & 7, idx = b >> 3;
+        const int t = (b & 7) * per + (b >> 3), i = PARTIAL ? t % tiles : t;
         if constexpr (PARTIAL) {
-            int mt, nt;
-            if (order == kByN) {
-                const int w = nb / 8;
-                nt = idx % w * 8 + xcd;
-                mt = idx / w % mb;
-                split = idx / w / mb;
-            } else if (order == kByM) {
-                const int w = mb / 8;
-                mt = idx % w * 8 + xcd;
-                nt = idx / w % nb;
-                split = idx / w / nb;
-            } else {
-                const int i = order == kBySplit ? idx : b;
-                split = order == kBySplit ? i / tiles * 8 + xcd : i / tiles;
-                mt = i % tiles / nb;
-                nt = i % tiles % nb;
-            }
-            m0 = mt * BM;
-            n0 = nt * BN;
+            split = t / tiles;
             kb = split * a.k_split;
             len = min(a.K - kb, a.k_split);
-        } else {
-            m0 = (idx / nb * 8 + xcd) * BM;
-            n0 = idx % nb * BN;
         }
+        m0 = i / nb * BM;
+        n0 = i % nb * BN;
     };
     // The next tile of this workgroup from b on, or `count` or more.
     auto next = [&](int b) {
-        if constexpr (!PARTIAL)
-            while (b < count && ((b >> 3) / nb * 8 + (b & 7)) * BM >= a.M) b += (int)gridDim.x;
+        while (b < count && (b & 7) * per + (b >> 3) >= all) b += (int)gridDim.x;
         return b;
     };
 
-    Stager<BM, BK, QS> sq;
-    Stager<BN, BK, PS> sp;
+    Stager<BM, BK, QS, T> sq;
+    Stager<BN, BK, PS, T> sp;
     Reader<BM, BK, QS, NM> rq;
     Reader<BN, BK, PS, NN> rp;
     rq.init(mrow);
     rp.init(ncol);
-    constexpr int kInFlight = Stager<BM, BK, QS>::kChunks + Stager<BN, BK, PS>::kChunks;
+    constexpr int kInFlight = Stager<BM, BK, QS, T>::kChunks + Stager<BN, BK, PS, T>::kChunks;
 
     f32x16 acc[NN][NM];
     bf16x8 fq[2][NM], fp[2][NN];
@@ -449,7 +437,7 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
     // the last kInFlight fetches (and `later` operations after it), has arrived.
     auto arrived = [&](auto later) {
         if constexpr (kAligned)
-            wait_loads<kInFlight + later()>();
+            wait_loads<(S - 2) * kInFlight + later()>();
         else
             __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
     };
@@ -457,59 +445,62 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
     constexpr std::integral_constant<int, 1> one;
 
     // Stages of steps t, t + 1, t + 2.
-    int s0 = 0, s1 = kStage, s2 = 2 * kStage;
+    int at[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) at[i] = i * kStage;
     int tile = fetch_tile;
     bool whole = false;  // the last tile stored by this workgroup had no edge
     bool odd = true;     // the register set of the next step
     constexpr int kStores = WM * WN / 512;
     start_tile();
-    fetch(s0, zero);
-    put(s0, zero);
-    fetch(s1, one);
+    fetch(at[0], zero);
+    put(at[0], zero);
+#pragma unroll
+    for (int i = 1; i < S - 1; ++i) fetch(at[i], one);
     arrived(zero);
     barrier();
-    rq.read(lds + s0, 0, fq[0]);
-    rp.read(lds + s0 + kQ, 0, fp[0]);
+    rq.read(lds + at[0], 0, fq[0]);
+    rp.read(lds + at[0] + kQ, 0, fp[0]);
     static_assert(KS % 2 == 0, "the first fragments of a step are always set 0");
     for (; tile < count; tile = next(tile + (int)gridDim.x)) {
         place(tile);
         const int steps = (len + BK - 1) / BK;
         const int tm0 = m0, tn0 = n0, tsplit = split;
-        if constexpr (!PARTIAL) load_params<RAT, BN>(params, a.e, tn0, a.N);
+        if constexpr (!PARTIAL) load_params<RAT, BN, T>(params, a.e, tn0, a.N);
 #pragma unroll
         for (int j = 0; j < NN; ++j)
 #pragma unroll
             for (int i = 0; i < NM; ++i) acc[j][i] = f32x16{};
         // SET: the register set that holds (unaligned) step t + 1
         auto step = [&](int t, auto SET) {
-            fetch(s2, std::integral_constant<int, 1 - SET()>{});
+            fetch(at[S - 1], std::integral_constant<int, 1 - SET()>{});
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int set = ks & 1;
                 if (ks + 1 < KS) {
-                    rq.read(lds + s0, ks + 1, fq[set ^ 1]);
-                    rp.read(lds + s0 + kQ, ks + 1, fp[set ^ 1]);
+                    rq.read(lds + at[0], ks + 1, fq[set ^ 1]);
+                    rp.read(lds + at[0] + kQ, ks + 1, fp[set ^ 1]);
                 } else {
                     // step t + 1 has arrived, and every wave holds its last
                     // fragments of step t in registers
-                    put(s1, SET);
+                    put(at[1], SET);
                     // memory operations end in the order of their issue: after a
                     // whole tile its kStores stores stand between step 1's fetch
                     // and step 2's, and need not be waited for
-                    if (!PARTIAL && t == 0 && whole)
+                    if (!PARTIAL && S > 2 && t == 0 && whole)
                         arrived(std::integral_constant<int, kStores>{});
                     else
                         arrived(zero);
                     barrier();
-                    rq.read(lds + s1, 0, fq[set ^ 1]);
-                    rp.read(lds + s1 + kQ, 0, fp[set ^ 1]);
+                    rq.read(lds + at[1], 0, fq[set ^ 1]);
+                    rp.read(lds + at[1] + kQ, 0, fp[set ^ 1]);
                 }
                 multiply(set);
             }
-            const int s = s0;
-            s0 = s1;
-            s1 = s2;
-            s2 = s;
+            const int first = at[0];
+#pragma unroll
+            for (int i = 0; i + 1 < S; ++i) at[i] = at[i + 1];
+            at[S - 1] = first;
         };
         if constexpr (kAligned) {
             for (int t = 0; t < steps; ++t) step(t, one);
@@ -521,8 +512,8 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                     step(t, zero);
             }
         }
-        // Here s0 holds the next tile's first step (its first fragments are in
-        // registers), s1 receives its second, and s2 is free.
+        // Here the first stage holds the next tile's first step (its first
+        // fragments are in registers) and the last stage is free.
 
         // A lane's 16 accumulators of a block: row of the result lane mod 32,
         // columns 8 (v / 4) + 4 (lane / 32) + v mod 4.  Swapping the upper lanes of
@@ -560,16 +551,16 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                         }
                     }
         } else {
-            // bf16 results pass through the wave's own corner of stage s2, 32 rows
+            // bf16 results pass through the wave's own corner of the free stage, 32 rows
             // of WN columns at a time, so that memory sees whole rows: from the
             // accumulators a lane holds 8 columns of 32 different rows (32-byte
-            // pieces; storing those took 110 us of 420 at 50,432 x 768 ->
-            // 3,072).  Chunk c of row r sits at c ^ g(r), conflict-free both
+            // pieces; storing those took 110 us of 420 at 50,432 x 3,072 from
+            // 768).  Chunk c of row r sits at c ^ g(r), conflict-free both
             // ways.  The residual comes the same way, into the slot its result
             // will take.
             constexpr int CP = WN / 8, RP = 64 / CP;
-            static_assert(4 * 32 * WN * 2 <= kStage, "staging fits");
-            char *own = lds + s2 + wave * (32 * WN * 2);
+            static_assert(T / 64 * 32 * WN * 2 <= kStage, "staging fits");
+            char *own = lds + at[S - 1] + wave * (32 * WN * 2);
             auto slot = [&](int r, int c) {
                 const int g = ((CP == 8 ? r : r >> 1) & (CP - 1)) ^ ((r >> 3) & 1);
                 return reinterpret_cast<u32x4 *>(own + r * (WN * 2) + ((c ^ g) << 4));
@@ -590,19 +581,20 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                     }
                     fence();
                 };
-                if (a.e.pre) {
+                // sums + bias, back in the accumulators in their new order
 #pragma unroll
-                    for (int j = 0; j < NN; ++j)
+                for (int j = 0; j < NN; ++j)
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const int c = 4 * j + 2 * p + (lane >> 5);
-                            float h[8];
-                            take8(j, p, i, h);
-                            add_bias<BN>(h, params, ncol / 8 + c);
-                            *slot(lane & 31, c) = Io<bf16io>::pack(h);
-                        }
-                    store_rows(a.e.pre);
-                }
+                    for (int p = 0; p < 2; ++p) {
+                        const int c = 4 * j + 2 * p + (lane >> 5);
+                        float h[8];
+                        take8(j, p, i, h);
+                        add_bias<BN>(h, params, ncol / 8 + c);
+                        if (a.e.pre) *slot(lane & 31, c) = Io<bf16io>::pack(h);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) acc[j][i][8 * p + v] = h[v];
+                    }
+                if (a.e.pre) store_rows(a.e.pre);
                 if (a.e.residual) {
 #pragma unroll
                     for (int it = 0; it < 32 / RP; ++it) {
@@ -619,8 +611,8 @@ __global__ __launch_bounds__(kThreads, 2) void grkan_linear_tile_kernel(ProductA
                     for (int p = 0; p < 2; ++p) {
                         const int c = 4 * j + 2 * p + (lane >> 5);
                         float h[8];
-                        take8(j, p, i, h);
-                        add_bias<BN>(h, params, ncol / 8 + c);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) h[v] = acc[j][i][8 * p + v];
                         activate_tile<RAT, BN>(h, params, ncol / 8 + c, a.e.act);
                         u32x4 *to = slot(lane & 31, c);
                         if (a.e.residual) {
@@ -784,11 +776,11 @@ hipError_t launch_tile(const ProductArgs &a, hipStream_t s) {
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (attr != hipSuccess) return attr;
     const int64_t mb = (a.M + BM - 1) / BM, nb = (a.N + BN - 1) / BN;
-    int64_t grid = PARTIAL ? mb * nb * a.splits : (mb + 7) / 8 * 8 * nb;
+    int64_t grid = (mb * nb * (PARTIAL ? a.splits : 1) + 7) / 8 * 8;
     // as many workgroups as fit on the 256 CUs at once; each walks over its tiles
-    constexpr int64_t resident = 256 * (BM * BN >= 256 * 128 ? 2 : 3);
+    constexpr int64_t resident = BN == 256 ? 256 : 768;
     if (grid > resident) grid = resident;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, s, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3((TileShape<BM, BN, BK>::kThreads)), lds, s, a);
     return hipGetLastError();
 }
 
@@ -814,10 +806,10 @@ hipError_t launch_shape(int form, bool partial, bool rational, const ProductArgs
 hipError_t GRKAN_LAUNCH_TILES(int tile, int form, bool partial, bool rational, const ProductArgs &a, hipStream_t s) {
     switch (tile) {
 #if GRKAN_LINEAR_ALIGNED
-        case 0: return launch_shape<256, 128, 32>(form, partial, rational, a, s);
+        case 0: return launch_shape<256, 256, 64>(form, partial, rational, a, s);
 #else
-        // (the chunks on their way take registers here; with 256 rows they spilled,
-        // 574 us against 75 at 8,003 x 1,501 from 777)
+        // (the chunks on their way take registers here; with 256 rows and 128 columns
+        // they spilled, 574 us against 75 at 8,003 x 1,501 from 777)
         case 0: return launch_shape<128, 128, 32>(form, partial, rational, a, s);
 #endif
         case 1: return launch_shape<128, 128, 32>(form, partial, rational, a, s);
@@ -857,7 +849,7 @@ template <int RAT> hipError_t launch_finish(const ProductArgs &a, hipStream_t s)
 // 8.9 with tiles; 64: 6.9 against 8.7).
 constexpr int64_t kSkinnyRows = 64;
 
-constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {128, 128, 64}, kTileK[] = {32, 32, 64};
+constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {256, 128, 64}, kTileK[] = {64, 32, 64};
 
 ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga) {
     ProductPlan p{};
@@ -874,41 +866,64 @@ ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned
         while (p.mt > 1 && (N + 15) / 16 * ((M + 16 * p.mt - 1) / (16 * p.mt)) < 192) p.mt /= 2;
         return p;
     }
-    // The tile and the number of k splits with the least estimated time.  A
-    // step takes a workgroup `alone` us while the GPU is nearly empty, up to
-    // `full` with every place taken (768 x 768 products of 1,003 to 50,432 rows:
-    // 2,048 rows 8.2 / 13.0 / 20.0 us with 384, 96, 48 tiles of 64, 128, 256 rows;
-    // 12,608 rows from 3,072: 102 / 90 / 90 us).  Splits add a launch, a write
-    // and a read of their fp32 sums (197 x 768 from 3,072: 16.4, 12.6, 11.1, 11.3 us
-    // with 1, 2, 4, 8; 2,048 x 768 from 768: 8.2 and 18.2 us with 1 and 2).  The
-    // operands reach the XCDs at about 10 TB/s, once or to each of the 8 as the
-    // tiles' order has it (768 x 192 from 25,216 rows: 43-49 us in 7 splits, all of
-    // both to each; 25 us in 16, each k range to one).  No sum runs over more
-    // than 16,384 values of k in fp32.
-    static const double kAlone[] = {0.85, 0.4, 0.33}, kFull[] = {1.25, 1.3, 0.75};
-    static const int64_t kPlaces[] = {512, 768, 768};
+    // The tile and the number of k splits with the least estimated time.  Places
+    // are the workgroups that the CUs hold at once; a step takes a workgroup
+    // `alone` us while few are taken, in proportion to those that are up to
+    // `full`, and a tile's result `tail` (M x N from K, rows of tiles 256 / 128 / 64,
+    // us: 1,003 x 768 from 768 25 / 14.8 / 7.8; 4,096 x 768 from 3,072 66 / 42 / 34;
+    // 4,096 x 3,072 from 768 29 / 32 / 40; 4,096 x 4,096 from 4,096 115 / 183 / 273;
+    // 50,432 x 3,072 from 768 324 / 365 / 470).  Splits add a launch, a write and a
+    // read of their fp32 sums (768 x 768 from 50,432 in tiles of 256 rows: 158, 88,
+    // 75 us with 7, 16, 24; of 1,003 rows from 768 in tiles of 64: 7.8, 15 us with 1
+    // and 2).  The operands reach the XCDs at about 10 TB/s, once or to each of
+    // the 8 as the tiles' order has it (768 x 192 from 25,216: 33 us in 7 splits,
+    // all of both to each; 25 us in 16, each k range to one).  No sum runs over
+    // more than 16,384 values of k in fp32.
+    static const double kAlone[] = {1.5, 0.4, 0.33}, kFull[] = {1.65, 1.2, 0.75}, kTail[] = {7.0, 2.0, 0.5};
+    static const int64_t kPlaces[] = {256, 768, 768};
+    auto tiles_us = [&](int i, int64_t wgs, int64_t steps) {
+        const int64_t rounds = wgs / kPlaces[i], rest = wgs % kPlaces[i];
+        const double part = kFull[i] * (double)rest / (double)kPlaces[i];
+        double us = (double)rounds * (steps * kFull[i] + kTail[i]);
+        if (rest) us += steps * (part > kAlone[i] ? part : kAlone[i]) + kTail[i];
+        return us;
+    };
+    const int first = aligned ? 0 : 1;  // the unaligned kernels have no tile of 256 rows
     double best = 1e30;
     p.kind = kTile;
-    for (int i = 0; i < 3; ++i) {
-        const int64_t tiles = ((M + kTileM[i] - 1) / kTileM[i]) * ((N + kTileN[i] - 1) / kTileN[i]);
+    for (int i = first; i < 3; ++i) {
+        const int64_t mt = (M + kTileM[i] - 1) / kTileM[i], nt = (N + kTileN[i] - 1) / kTileN[i], tiles = mt * nt;
         const int64_t steps = (K + kTileK[i] - 1) / kTileK[i], least = (K + 16383) / 16384;
         for (int64_t s = least < 1 ? 1 : least; s <= 64 || s == least; ++s) {
             if (s > 8 && s % 8 != 0 && s != least) continue;  // eighths: a k range to an XCD
             if (s > 1 && s > least && (steps < 4 * s || (double)s * M * N * 4 > 256e6)) break;
-            const int64_t per = (steps + s - 1) / s, wgs = tiles * s, rounds = (wgs + kPlaces[i] - 1) / kPlaces[i];
-            const int64_t here = wgs < kPlaces[i] ? wgs : kPlaces[i];
-            const double load = (double)((here + 255) / 256 * 256) / (double)kPlaces[i];  // of the busiest CU
-            const double step = kFull[i] * load > kAlone[i] ? kFull[i] * load : kAlone[i];
-            const int64_t mt = (M + kTileM[i] - 1) / kTileM[i], nt = (N + kTileN[i] - 1) / kTileN[i];
-            const bool once = s > 1 && s % 8 == 0;
-            const double qx = once || s == 1 || (nt % 8 != 0 && mt % 8 == 0) ? 1 : 8, px = once || (s > 1 && nt % 8 == 0) ? 1 : 8;
-            const double fetch = 2.0 * (double)K * (qx * (double)M + px * (double)N) / 10e6, work = (double)rounds * per * step;
+            const int64_t per = (steps + s - 1) / s;
+            const double times = s % 8 == 0 ? 1 : 8.0 / (double)(s < 8 ? s : 8);
+            const double fetch = 2.0 * (double)K * ((double)M + times * (double)N) / 10e6, work = tiles_us(i, tiles * s, per);
             double us = 3.0 + (work > fetch ? work : fetch);
-            if (s > 1) us += 4.0 + 2.0 * (double)s * M * N * 4 / 4e6;
+            if (s > 1) us += 3.0 + 2.0 * (double)s * M * N * 4 / 6e6;
             if (us < best) {
                 best = us;
                 p.tile = i;
+                p.rows = 0;
                 p.k_split = (int32_t)(per * kTileK[i] < K ? per * kTileK[i] : (K > 0 ? K : 1));
+            }
+            // Rows that fill whole rounds of 256-row tiles, the rest in smaller ones
+            // (50,432 x 768 from 3,072: 312 us whole, 198 + 57 us so)
+            if (i == 0 && s == 1 && form != kFormDw && !any_groups) {
+                const int64_t panels = tiles / kPlaces[0] * kPlaces[0] / nt, rows = panels * kTileM[0], left = M - rows;
+                if (rows <= 0 || left <= 0) continue;
+                for (int j = 1; j < 3; ++j) {
+                    const int64_t rest = ((left + kTileM[j] - 1) / kTileM[j]) * ((N + kTileN[j] - 1) / kTileN[j]);
+                    const double both = 6.0 + tiles_us(0, panels * nt, steps) + tiles_us(j, rest, (K + kTileK[j] - 1) / kTileK[j]);
+                    if (both < best) {
+                        best = both;
+                        p.tile = 0;
+                        p.k_split = (int32_t)K;
+                        p.rows = rows;
+                        p.rest_tile = j;
+                    }
+                }
             }
         }
     }
@@ -926,8 +941,20 @@ hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &arg
     const int rat = a.e.act != GRKAN_ACT_RATIONAL ? 0 : (a.e.dga % 8 == 0 ? 1 : 2);
     if (p.kind == kSkinny)
         return rat == 0 ? launch_skinny<0>(p.mt, a, s) : (rat == 1 ? launch_skinny<1>(p.mt, a, s) : launch_skinny<2>(p.mt, a, s));
-    hipError_t e = p.aligned ? launch_tiles_aligned(p.tile, form, p.two_steps, rat == 1, a, s)
-                             : launch_tiles_any(p.tile, form, p.two_steps, rat == 1, a, s);
+    hipError_t e;
+    if (p.rows > 0) {
+        ProductArgs top = a, rest = a;
+        top.M = (int32_t)p.rows;
+        rest.M = a.M - top.M;
+        rest.q.p = static_cast<const uint16_t *>(a.q.p) + p.rows * a.q.ld;
+        if (a.e.residual) rest.e.residual = static_cast<const uint16_t *>(a.e.residual) + p.rows * a.e.ldr;
+        if (a.e.pre) rest.e.pre = static_cast<uint16_t *>(a.e.pre) + p.rows * a.N;
+        rest.e.z = static_cast<uint16_t *>(a.e.z) + p.rows * a.N;
+        e = launch_tiles_aligned(p.tile, form, false, rat == 1, top, s);
+        return e != hipSuccess ? e : launch_tiles_aligned(p.rest_tile, form, false, rat == 1, rest, s);
+    }
+    e = p.aligned ? launch_tiles_aligned(p.tile, form, p.two_steps, rat == 1, a, s)
+                  : launch_tiles_any(p.tile, form, p.two_steps, rat == 1, a, s);
     if (e != hipSuccess || !p.two_steps) return e;
     return rat == 0 ? launch_finish<0>(a, s) : (rat == 1 ? launch_finish<1>(a, s) : launch_finish<2>(a, s));
 }

@@ -89,6 +89,13 @@ def test_larger_tiles(gk, shape, act):
     both_ways(gk, shape, act, 300 + sum(shape))
 
 
+# 256-row tiles: one round, and whole rounds with the other rows in smaller tiles (forward; dx); dW in splits
+@pytest.mark.parametrize("act", ("silu", "rational"))
+@pytest.mark.parametrize("shape", [(4095, 2056, 3944, 8), (8449, 1032, 2040, 8), (8450, 2040, 1032, 8)], ids=name)
+def test_largest_tiles(gk, shape, act):
+    both_ways(gk, shape, act, 400 + sum(shape))
+
+
 @pytest.mark.parametrize("shape", [(1, 96, 80, 8), (70, 96, 80, 8), (40, 33, 27, 1)], ids=name)
 def test_optional_arguments(gk, shape):
     """No bias, no residual, no pre: each alone and all together."""
