@@ -166,8 +166,14 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
             p->groups = (int32_t)gpb;
             p->TX = (int32_t)ceil_div(p->width, p->vec);
             // Row lanes: 256 threads if many workgroups share a CU, all there are
-            // if not; at least what the registers need.
-            const int64_t want = N * p->ncb >= 1024 ? 256 : threads;
+            // if not; at least what the registers need.  The backward walks over the
+            // samples, the next one's values on their way: two workgroups of 256
+            // threads a CU (128 x 197 x 192 in 8 groups, fp32: 28.5 us; one of 512: 30.7;
+            // 64 x 256 x 512 in 32: 38.7, 46.4), one of 512 for 8 rounds or more of
+            // wide rows (1,024 x 197 x 192: 132 us against 183; 256 x 197 x 768, bf16: 116
+            // against 200).
+            const bool long_walk = backward && N * p->ncb >= 2048 && gpb * D * es >= 96;
+            const int64_t want = N * p->ncb >= 1024 && !long_walk ? 256 : threads;
             int64_t ty = want / p->TX;
             if (ty < ceil_div(S, regs)) ty = ceil_div(S, regs);
             if (ty > S) ty = S;
@@ -177,7 +183,7 @@ grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng,
             if (!backward) {
                 p->blocks = (N >= 8 ? ceil_div(N, 8) * 8 : N) * p->ncb;
             } else {
-                int64_t chunks = kNormWorkgroups / p->ncb;
+                int64_t chunks = (long_walk ? 256 : 512) / p->ncb;
                 if (chunks < 1) chunks = 1;
                 if (chunks > N) chunks = N;
                 if (chunks >= 8) chunks = chunks / 8 * 8;

@@ -645,9 +645,13 @@ __global__ __launch_bounds__(1024) void grkan_norm_slab_fwd_kernel(NormArgs a) {
                 a.rstd[ng] = st.rstd[e];
             }
         }
+        // (the asm keeps the stores' rows and addresses from being formed, and held
+        // in registers, before the sums)
+        int row = q.ty;
+        asm volatile("" : "+v"(row));
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int r = q.ty + i * p.TY;
+            const int r = row + i * p.TY;
             x[i].repack();
             if (r < S && k.nv > 0)
                 apply_forward<V, RAT, MIXED>(x[i], st, k, a.act).store(at(a.y, (n * a.S + r) * a.C + k.col), k.nv);
@@ -967,22 +971,43 @@ __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
     ColSums<V, RAT> cs;
     cs.clear();
     const int S = (int)a.S;
-    for (int64_t n = n0; n < a.N; n += p.chunks) {
-        Pack<V> x[R], dy[R];
+    // A sample's values; AHEAD: while one is worked on, the next one's are on
+    // their way.
+    constexpr bool AHEAD = R * V <= 24;
+    Pack<V> nx[R], ndy[R];
+    Stats<V, MIXED> nst;
+    auto fetch = [&](int64_t n, Pack<V>(&x)[R], Pack<V>(&dy)[R], Stats<V, MIXED> &st) {
+        const bool any = n < a.N;
+        const int64_t m = any ? n : 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int r = q.ty + i * p.TY;
-            const int nv = r < S ? k.nv : 0;
+            const int nv = any && r < S ? k.nv : 0;
             const int64_t rr = r < S ? r : 0;
-            x[i] = Pack<V>::load(at(a.x, n * a.xs + rr * a.xr + k.col), nv);
-            dy[i] = Pack<V>::load(at(a.dy, n * a.ds + rr * a.dr + k.col), nv);
+            x[i] = Pack<V>::load(at(a.x, m * a.xs + rr * a.xr + k.col), nv);
+            dy[i] = Pack<V>::load(at(a.dy, m * a.ds + rr * a.dr + k.col), nv);
         }
-        Stats<V, MIXED> st;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int64_t ng = n * a.G + q.g0 + q.group(a, e);
+            const int64_t ng = m * a.G + q.g0 + q.group(a, e);
             st.mean[e] = a.mean[ng];
             st.rstd[e] = a.rstd[ng];
+        }
+    };
+    if constexpr (AHEAD) fetch(n0, nx, ndy, nst);
+    for (int64_t n = n0; n < a.N; n += p.chunks) {
+        Pack<V> x[R], dy[R];
+        Stats<V, MIXED> st;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                x[i] = nx[i];
+                dy[i] = ndy[i];
+            }
+            st = nst;
+            fetch(n + p.chunks, nx, ndy, nst);
+        } else {
+            fetch(n, x, dy, st);
         }
         float dh[R][V], sdh[V] = {}, sdx[V] = {};
 #pragma unroll
