@@ -208,7 +208,7 @@ __device__ static inline float slope(float xh, float dy, const Cols<V, RAT> &k, 
 // straddle activation groups (RAT 2: the second from element `split` of the run
 // on), serves them all.  The backward of the rational, which also sums per
 // set, is bound by its arithmetic and takes runs (at 48 bytes a lane the forward
-// spent its time in the address units instead: 65 us against 50 at 50,432 x
+// spent its time in the address units instead: 65 us against 44 at 50,432 x
 // 768).
 template <int V, int RAT, int K, bool RUN> struct TokenCols {
     static constexpr int kSets = RAT == 0 ? 1 : (RUN ? RAT : K);
@@ -525,6 +525,11 @@ hipError_t start(const NormArgs &a, dim3 grid, dim3 block, size_t lds, hipStream
 #if !GRKAN_NORM_BACKWARD
 // ============================================================ forward
 
+// Token: a group of one position lies in T lanes' registers; sums by lane
+// exchanges (LDS beyond a wave), mean first, then the variance about it.  The
+// next sample's values are on their way while this one's are worked on.
+// 50,432 x 768, bf16, the rational: 44 us, 3.5 TB/s of 5.0; the vector units are
+// busy 0.93 of the CUs' time, which bounds it.  1 x 768: 5.3 us, latency.
 template <int V, int RAT, int K>
 __global__ __launch_bounds__(K * V == 1 ? 1024 : 256) void grkan_norm_token_fwd_kernel(NormArgs a) {
     __shared__ float lds[2 * 16];
@@ -591,6 +596,10 @@ __global__ __launch_bounds__(K * V == 1 ? 1024 : 256) void grkan_norm_token_fwd_
     }
 }
 
+// Slab: whole groups of a sample, all positions, in a workgroup's registers;
+// one read of x, the variance about the mean.  Rows are cut into pieces of 64
+// bytes or more: with 20- and 40-byte pieces (8 x 4,096 x 320, bf16, 32 groups,
+// held in registers all the same) it ran 58 and 42 us against the split's 28.
 template <int V, bool RAT, bool MIXED, int R>
 __global__ __launch_bounds__(1024) void grkan_norm_slab_fwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -663,7 +672,9 @@ __global__ __launch_bounds__(1024) void grkan_norm_slab_fwd_kernel(NormArgs a) {
 // lane sums the differences from its first row (and their squares) in fp32,
 // column by column, over at most 32 rows, and turns them into fp64 sums of x
 // and x^2 about zero at the end: three fp32 operations an element, with the
-// digits of a mean far from zero kept out of them.
+// digits of a mean far from zero kept out of them.  8 x 4,096 x 320, bf16: 12.9 us
+// for 21 MB, 1 x 65,536 x 128, fp32: 11.3 us for 34 MB: ramp and latency, a
+// workgroup or four a CU with 4 to 32 rows a lane.
 template <int V, bool MIXED>
 __global__ __launch_bounds__(1024) void grkan_norm_sums_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -703,7 +714,8 @@ __global__ __launch_bounds__(1024) void grkan_norm_sums_kernel(NormArgs a) {
     }
 }
 
-// Split, many parts: a workgroup per (sample, group) adds them.
+// Split, many parts: a workgroup per (sample, group) adds them (4.1 us for 32
+// groups of 1,024 parts; latency).
 __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
     const int64_t ng = blockIdx.x;
     double s0, s1;
@@ -715,7 +727,10 @@ __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
     }
 }
 
-// Split, second pass: y over a row chunk of a column block.
+// Split, second pass: y over a row chunk of a column block, x most likely from
+// the Infinity Cache.  8 x 4,096 x 320, bf16, silu: 17.5 us; 1 x 65,536 x 128,
+// fp32: 13.4 us for 67 MB, 5.0 TB/s.  Reading four rows ahead moved the one by
+// +2% and the other by -5%.
 template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(1024) void grkan_norm_apply_fwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -846,6 +861,11 @@ __device__ static inline void store_col_sums(const NormArgs &a, const ColSums<V,
                        p.cv, lds);
 }
 
+// Token backward: dh and xh of a lane's run in registers, two sums over the
+// group, dx; column and coefficient sums stay in registers over all the
+// samples a workgroup walks over.  201,728 x 768, bf16, the rational: 296 us and
+// 10 for the columns, 3.0 TB/s of 5.0; its 64 instructions an element keep the
+// vector units busy 0.94 of the time, which bounds it.
 // The second bound keeps two or three waves on a SIMD: left alone, the compiler
 // evaluates all of a lane's elements side by side, in 270 registers for 12.
 template <int V, int RAT, int K>
@@ -953,6 +973,10 @@ grkan_norm_token_bwd_kernel(NormArgs a) {
     }
 }
 
+// Slab backward: x, dy and dh of a sample's groups in registers, so that x and
+// dy are read once.  128 x 197 x 192 in 8 groups, fp32, gelu: 22 us for 58 MB (2.6
+// TB/s; two samples a workgroup, the loads and the sums of the first exposed);
+// 1,024 samples: 132 us, 3.5 TB/s.
 template <int V, bool RAT, bool MIXED, int R>
 __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -1049,7 +1073,8 @@ __global__ __launch_bounds__(512) void grkan_norm_slab_bwd_kernel(NormArgs a) {
     store_col_sums<V, RAT>(a, cs, q, cb, n0, lds);
 }
 
-// Split, first pass: sums of t and t xh and the column sums of a row chunk.
+// Split, first pass: sums of t and t xh and the column sums of a row chunk (one
+// read of x and dy; for groups too long for registers).
 template <int V, bool RAT, bool MIXED>
 __global__ __launch_bounds__(512) void grkan_norm_sums_bwd_kernel(NormArgs a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -1160,7 +1185,8 @@ __global__ __launch_bounds__(512) void grkan_norm_apply_bwd_kernel(NormArgs a) {
 
 // The column partials added over their rows in fp64: workgroups of 64 columns
 // x 16 row lanes for dw and db, then one workgroup per (activation group,
-// coefficient), whose accesses are a contiguous range.
+// coefficient), whose accesses are a contiguous range.  3.9 us for 64 rows of 384
+// columns, 10.5 us for 1,009 rows of 1,536 and 8 x 10 coefficients: latency.
 template <bool RAT>
 __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
     __shared__ double red[1024];
