@@ -79,34 +79,52 @@ __device__ static inline float act_slope(float h, int act) {
     return 1.0f;
 }
 
-// The rational's backward at an h that is itself the result of fp32
-// arithmetic (a normalised value): dy dF/dh, the ten coefficient terms added
-// to acc.  Q and its sign are taken in fp32 -- h carries its own rounding, so
-// deciding the sign of Q more exactly than h is known would mean nothing --
-// with sign(0) = 0.  The powers of h serve the polynomials and the sums (46
-// instructions; Horner's rule with running products for the sums takes 51).
-// EXACT: h is an exact input (a kept bf16 product), and the sign of Q is
-// decided for it: the fp32 Q is within 8 u sum |b_j| |h|^j <= 8 u (1 + h^4) sum
-// |b_j| of Q (u = 2^-24; four products and sums over exact b), so beyond twice that its
-// sign is Q's; the rare element within it (h = 0 among them) takes the
-// compensated decision of the activation's own backward.  (That backward also
-// evaluates Q itself in fp64, 70 instructions an element against 42.)
+// The rational's backward: dy dF/dh, the ten coefficient terms added to acc.
+// The powers of h serve the polynomials and the sums (46 instructions; Horner's
+// rule with running products for the sums takes 51).  Two forms of Q, by the
+// coefficients' type:
+//
+// SlopeCoefs: h is itself the result of fp32 arithmetic (a normalised value).
+// Q and its sign are taken in fp32, with sign(0) = 0: h's own rounding moves Q
+// by up to sum j |b_j h^j| 2^-24, as much as the evaluation does, so a better Q
+// at a rounded h gains nothing (over six sets of coefficients with real roots of
+// Q, dB was off by 1e-7 .. 3e-5 either way, by less with Q in fp64 in two sets
+// and by more in four).
+//
+// ExactSlopeCoefs: h is an exact input (a kept bf16 product).  Then Q's rounding
+// is the whole error of D next to a root of Q, and since bf16 values recur it
+// does not average out over the rows: with Q in fp32 dB was 1.6 to 34 times
+// farther from its fp64 value than with Q as here, by Horner's rule in fp64
+// from exact copies, rounded once, as in the activation's own backward (six sets
+// as above; four fp64 instructions and two conversions in place of four in
+// fp32, at the same rate).  The sign of Q is proven by that backward's guard
+// (BwdCoefs), |Q| > 2^-46 (sum |b_j|) (1 + h^4); the rare element within it (h =
+// 0 among them) takes the compensated decision.
 struct SlopeCoefs {
+    static constexpr bool kExact = false;
     Coefs<5, 4> c;
     float da[4], db[3];  // 2 a_2 .. 5 a_5, 2 b_2 .. 4 b_4
-    float guard;         // 16 u sum |b_j|, at least the smallest normal number
     __device__ inline void init(const Coefs<5, 4> &k) {
         c = k;
 #pragma unroll
         for (int i = 2; i <= 5; ++i) da[i - 2] = (float)i * k.a[i];
 #pragma unroll
         for (int j = 2; j <= 4; ++j) db[j - 2] = (float)j * k.b[j - 1];
-        guard = fmaxf((fabsf(k.b[0]) + fabsf(k.b[1]) + fabsf(k.b[2]) + fabsf(k.b[3])) * 0x1p-20f, kGuardFloor);
+    }
+};
+struct ExactSlopeCoefs : SlopeCoefs {
+    static constexpr bool kExact = true;
+    QWide<4> wide;
+    float guard;
+    __device__ inline void init(const Coefs<5, 4> &k) {
+        SlopeCoefs::init(k);
+        wide = widen<5, 4, false>(k);  // the columns, and with them the group, differ between lanes
+        guard = fmaxf((fabsf(k.b[0]) + fabsf(k.b[1]) + fabsf(k.b[2]) + fabsf(k.b[3])) * sign_guard_scale<4>(), kGuardFloor);
     }
 };
 
-template <bool EXACT = false>
-__device__ static inline float rational_slope(float h, float dy, const SlopeCoefs &k, float (&acc)[10]) {
+template <class K>
+__device__ static inline float rational_slope(float h, float dy, const K &k, float (&acc)[10]) {
     // One element after another (the asm ties h to every sum so far): left
     // alone, the compiler puts the sums off and holds the powers of all of a
     // lane's elements (270 registers for 12 of them).
@@ -116,13 +134,19 @@ __device__ static inline float rational_slope(float h, float dy, const SlopeCoef
     const float h2 = h * h, h3 = h2 * h, h4 = h2 * h2, h5 = h4 * h;
     const float P = fmaf(a[5], h5, fmaf(a[4], h4, fmaf(a[3], h3, fmaf(a[2], h2, fmaf(a[1], h, a[0])))));
     const float dP = fmaf(k.da[3], h4, fmaf(k.da[2], h3, fmaf(k.da[1], h2, fmaf(k.da[0], h, a[1]))));
-    const float Q = fmaf(b[3], h4, fmaf(b[2], h3, fmaf(b[1], h2, b[0] * h)));
+    float Q;
+    if constexpr (K::kExact) {
+        const double hd = (double)h;
+        Q = (float)(hd * fma(fma(fma(k.wide.b[3], hd, k.wide.b[2]), hd, k.wide.b[1]), hd, k.wide.b[0]));
+    } else {
+        Q = fmaf(b[3], h4, fmaf(b[2], h3, fmaf(b[1], h2, b[0] * h)));
+    }
     const float dQ = fmaf(k.db[2], h3, fmaf(k.db[1], h2, fmaf(k.db[0], h, b[0])));
     const float r = __builtin_amdgcn_rcpf(1.0f + fabsf(Q));
     const float w = dy * r;
     const float v = w * (P * r);
     float sv = __uint_as_float(__float_as_uint(v) ^ (__float_as_uint(Q) & 0x80000000u));
-    if constexpr (!EXACT) {
+    if constexpr (!K::kExact) {
         sv = Q == 0.0f ? 0.0f : sv;
     } else if (!(fabsf(Q) > fmaf(h4, k.guard, k.guard))) {
         const bool zero = h == 0.0f || (b[0] == 0.0f && b[1] == 0.0f && b[2] == 0.0f && b[3] == 0.0f);

@@ -985,7 +985,7 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
     float sum[V], coef[RAT ? 10 : 1] = {};
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-    SlopeCoefs sc;
+    ExactSlopeCoefs sc;
     if constexpr (RAT) sc.init(load_coefs<5, 4>(a.A, a.B, nv > 0 ? n / a.dga : 0));
     auto value = [](u32x4 v, int e) { return __uint_as_float((e & 1) ? (v[e / 2] & 0xffff0000u) : (v[e / 2] << 16)); };
     // the next row's values are on their way while this one's are worked on
@@ -1013,9 +1013,9 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
             for (int e = 0; e < V; ++e) {
                 const float he = value(h, e), ge = value(g, e);
                 if constexpr (RAT) {
-                    // pre is what the forward kept, an exact input: the sign of Q is decided
-                    // as by the activation's own backward
-                    d[e] = rational_slope<true>(he, ge, sc, *reinterpret_cast<float (*)[10]>(coef));
+                    // pre is what the forward kept, an exact input: Q and its sign are
+                    // formed as by the activation's own backward
+                    d[e] = rational_slope(he, ge, sc, *reinterpret_cast<float (*)[10]>(coef));
                 } else {
                     d[e] = ge * act_slope(he, a.act);
                 }
