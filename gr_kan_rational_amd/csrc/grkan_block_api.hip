@@ -40,8 +40,6 @@ bool outputs_overlap(const Range *outs, int no, const Range *ins, int ni) {
 
 grkan_status_t from_hip(hipError_t e) { return e == hipSuccess ? GRKAN_OK : GRKAN_ERR_HIP; }
 
-size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-
 __global__ __launch_bounds__(256) void grkan_norm_empty_kernel(float *mean, float *rstd, int64_t n, float value) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
@@ -55,204 +53,6 @@ hipError_t launch_norm_empty(const NormArgs &a, hipStream_t s) {
     hipLaunchKernelGGL(grkan_norm_empty_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.mean, a.rstd, n,
                        1.0f / sqrtf(a.eps));
     return hipGetLastError();
-}
-
-int io_bytes(grkan_dtype_t io) { return io == GRKAN_BF16 ? 2 : 4; }
-
-bool act_valid(grkan_act_t act) {
-    return act == GRKAN_ACT_NONE || act == GRKAN_ACT_SILU || act == GRKAN_ACT_GELU || act == GRKAN_ACT_RATIONAL;
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int pow2_at_most(int64_t v) {
-    int p = 1;
-    while (2 * (int64_t)p <= v) p *= 2;
-    return p;
-}
-
-// ------------------------------------------------------------ norm plans
-
-constexpr int kTokenMaxLanes = 256, kTokenMaxAccesses = 4;
-constexpr int64_t kNormWorkgroups = 2048;  // target of the looping kernels: 8 workgroups a CU
-
-// Largest power of two <= v elements per access such that accesses that start
-// at multiples of `start` columns (and then every v) lie in one activation
-// group each.
-int rational_vec(int v, int64_t dga, int64_t start) {
-    while (v > 1 && (dga % v != 0 || start % v != 0)) v /= 2;
-    return v;
-}
-
-grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int32_t ng, grkan_act_t act, grkan_dtype_t io,
-                         bool backward, NormPlan *p) {
-    if (io != GRKAN_F32 && io != GRKAN_BF16) return GRKAN_ERR_INVALID_ARG;
-    if (!act_valid(act)) return GRKAN_ERR_INVALID_ARG;
-    const bool rational = act == GRKAN_ACT_RATIONAL;
-    if (N < 0 || S < 0 || C < 1 || G < 1 || C % G != 0) return GRKAN_ERR_INVALID_ARG;
-    if (rational && (ng < 1 || C % ng != 0)) return GRKAN_ERR_INVALID_ARG;
-    if (C >= (1 << 24) || S > INT32_MAX) return GRKAN_ERR_UNSUPPORTED;
-    if (N > INT32_MAX / G) return GRKAN_ERR_UNSUPPORTED;
-    const int es = io_bytes(io), vmax = 16 / es;
-    const int64_t D = C / G, dga = rational ? C / ng : 0;
-    *p = NormPlan{};
-    if (N == 0 || S == 0) return GRKAN_OK;
-
-    // Token: T lanes of K accesses of v elements with the fewest idle places for
-    // a group, then the widest accesses (16 bytes or 8), then the fewest.  The
-    // backward keeps two sums, a weight and a bias per element of a lane, so it
-    // takes at most 16 (768 channels in bf16: 64 lanes x 3 x 4).  A rational's
-    // lanes prefer runs inside one activation group; else a run may lie in two,
-    // and has to be no longer than a group for that.
-    int64_t best = INT64_MAX;
-    if (S == 1) {
-        for (int straddle = 0; straddle <= (rational ? 1 : 0) && best == INT64_MAX; ++straddle)
-            for (int v = vmax; v >= 1; v /= 2) {
-                if (!rational && v < vmax / 2) break;
-                for (int K = 1; K <= kTokenMaxAccesses; ++K) {
-                    const int run = K * v;
-                    if (backward && run > 16) break;
-                    // (the forward has coefficients per access, the backward per run)
-                    const int unit = backward ? run : v;
-                    if (rational && !straddle && dga % D != 0 && (dga % unit != 0 || D % unit != 0)) continue;
-                    if (straddle && (run > dga || run < 4)) continue;
-                    int T = 1;
-                    while ((int64_t)T * run < D) T *= 2;
-                    if (T > (run == 1 ? 1024 : kTokenMaxLanes) || (int64_t)T * run >= best) continue;
-                    best = (int64_t)T * run;
-                    p->vec = v;
-                    p->T = T;
-                    p->K = K;
-                    p->straddle = straddle != 0;
-                }
-            }
-    }
-    if (best != INT64_MAX) {
-        p->kind = kNormToken;
-        p->vpg = (int32_t)ceil_div(D, p->K * p->vec);  // (read for a rational only)
-        p->cv = (int64_t)G * p->vpg;
-        int spw = p->T <= 64 ? 256 / p->T : 1;
-        while (spw % G != 0 && G % spw != 0) --spw;
-        p->spw = spw;
-        p->block = spw * p->T;
-        // Enough workgroups to fill the GPU, walking over the samples in as
-        // many rounds each as the last of them needs.
-        const int64_t unit = spw < G ? G / spw : 1;  // workgroups that cover one sample
-        const int64_t wanted = ceil_div(N * G, spw), cap = backward ? kNormWorkgroups / 2 : kNormWorkgroups;
-        const int64_t rounds = ceil_div(wanted, cap);
-        p->blocks = ceil_div(ceil_div(wanted, rounds), unit) * unit;
-        p->prows = spw > G ? p->blocks : p->blocks * spw / G;
-        p->lds = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4 + 256;
-    } else {
-        // A slab: whole groups side by side until they make 64 bytes or more of
-        // every row, if a workgroup's registers hold all rows of that.
-        const int threads = backward ? 512 : 1024, regs = backward ? 8 : 16;
-        int64_t gpb = ceil_div(64, D * es);
-        if (gpb > G) gpb = G;
-        auto vec_of = [&](int64_t groups) { return rational ? rational_vec(vmax, dga, groups * D) : vmax; };
-        auto rows_of = [&](int64_t groups) {  // rows a workgroup can hold
-            const int64_t tx = ceil_div(groups * D, vec_of(groups));
-            return tx <= threads ? threads / tx * regs : 0;
-        };
-        if (S > 1 && S <= rows_of(gpb)) {
-            p->kind = kNormSlab;
-            // wider blocks while many workgroups remain and rows are short
-            while (gpb * 2 <= G && gpb * D * es < 256 && S <= rows_of(gpb * 2) && vec_of(gpb * 2) >= vec_of(gpb) &&
-                   N * ceil_div(G, gpb * 2) >= kNormWorkgroups)
-                gpb *= 2;
-            p->vec = vec_of(gpb);
-            p->width = (int32_t)(gpb * D);
-            p->ncb = (int32_t)ceil_div(G, gpb);
-            p->groups = (int32_t)gpb;
-            p->TX = (int32_t)ceil_div(p->width, p->vec);
-            // Row lanes: 256 threads if many workgroups share a CU, all there are
-            // if not; at least what the registers need.  The backward walks over the
-            // samples, the next one's values on their way: two workgroups of 256
-            // threads a CU (128 x 197 x 192 in 8 groups, fp32: 28.5 us; one of 512: 30.7;
-            // 64 x 256 x 512 in 32: 38.7, 46.4), one of 512 for 8 rounds or more of
-            // wide rows (1,024 x 197 x 192: 132 us against 183; 256 x 197 x 768, bf16: 116
-            // against 200).
-            const bool long_walk = backward && N * p->ncb >= 2048 && gpb * D * es >= 96;
-            const int64_t want = N * p->ncb >= 1024 && !long_walk ? 256 : threads;
-            int64_t ty = want / p->TX;
-            if (ty < ceil_div(S, regs)) ty = ceil_div(S, regs);
-            if (ty > S) ty = S;
-            p->regs = (int32_t)ceil_div(S, ty);
-            p->TY = (int32_t)ceil_div(S, p->regs);
-            p->block = (int32_t)(ceil_div((int64_t)p->TX * p->TY, 64) * 64);
-            if (!backward) {
-                p->blocks = (N >= 8 ? ceil_div(N, 8) * 8 : N) * p->ncb;
-            } else {
-                int64_t chunks = (long_walk ? 256 : 512) / p->ncb;
-                if (chunks < 1) chunks = 1;
-                if (chunks > N) chunks = N;
-                if (chunks >= 8) chunks = chunks / 8 * 8;
-                p->chunks = chunks;
-                p->blocks = chunks * p->ncb;
-                p->prows = chunks;
-            }
-        } else {
-            p->kind = kNormSplit;
-            p->vec = rational ? rational_vec(vmax, dga, 0) : vmax;
-            const int64_t accesses = ceil_div(C, p->vec);
-            // At most 256 accesses across (128 where every column is a group, for the
-            // groups' sums in LDS).
-            p->ncb = (int32_t)ceil_div(accesses, D == 1 ? 128 : 256);
-            p->TX = (int32_t)ceil_div(accesses, p->ncb);
-            p->width = p->TX * p->vec;
-            p->ncb = (int32_t)ceil_div(C, p->width);
-            p->groups = (int32_t)(p->width / D + 2 < G ? p->width / D + 2 : G);
-            p->parts = (int32_t)(D / p->width + 2 < p->ncb ? D / p->width + 2 : p->ncb);
-            // Chunks of 4 to 32 rows a lane, about a workgroup a CU; where those
-            // leave a lane of the second pass more than 2 sums to add (few
-            // samples), smaller workgroups, more of them, and a step between that
-            // adds (65,536 x 128 in 32 groups: 26 us against 29).
-            auto chunks_of = [&](int64_t lanes, int64_t wanted) {
-                int64_t ty = lanes / p->TX;
-                if (ty > S) ty = S;
-                p->TY = (int32_t)ty;
-                p->block = (int32_t)(ceil_div((int64_t)p->TX * ty, 64) * 64);
-                int64_t chunks = ceil_div(wanted, N * p->ncb);
-                const int64_t most = ceil_div(S, 4 * ty), least = ceil_div(S, 32 * ty);
-                if (chunks > most) chunks = most;
-                if (chunks < least) chunks = least;
-                p->chunk_rows = ceil_div(S, chunks);
-                p->chunks = ceil_div(S, p->chunk_rows);
-                p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
-                p->fused = ceil_div(p->chunks * p->parts, p->L) <= 2;
-            };
-            if (backward) {
-                chunks_of(512, 512);
-            } else {
-                chunks_of(1024, 256);
-                if (!p->fused) chunks_of(256, 1024);
-            }
-            p->blocks = N * p->chunks * p->ncb;
-            p->prows = N * p->chunks;
-        }
-        p->cv = (int64_t)p->ncb * p->TX;
-        p->mixed = D % p->vec != 0;
-        p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
-        const int64_t cols_across = (int64_t)p->TX * (p->mixed ? p->vec : 1);
-        p->P = pow2_at_most(p->block / cols_across < 1 ? 1 : (p->block / cols_across < 64 ? p->block / cols_across : 64));
-        const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
-        const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
-        p->lds = value * values * ((size_t)(p->block + p->TX) * (p->mixed ? p->vec : 1) + p->groups);
-        const size_t cols = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4;
-        if (backward && p->lds < cols) p->lds = cols;
-    }
-    p->row = 2 * C + (rational ? (p->straddle ? 20 : 10) * p->cv : 0);
-    size_t at = 0;
-    if (p->kind == kNormSplit) {
-        p->off_stats = at;
-        at += align256((size_t)N * G * p->chunks * p->parts * 16);
-        p->off_means = at;
-        if (backward) at += align256((size_t)N * G * 8);
-    }
-    p->off_partials = at;
-    if (backward) at += align256((size_t)p->prows * p->row * 4);
-    p->total = at;
-    return GRKAN_OK;
 }
 
 // Elements from the first to the last of a strided [N][S][C] tensor, or -1 if
@@ -434,42 +234,8 @@ extern "C" grkan_status_t grkan_group_norm_backward(
 
 namespace {
 
-constexpr int64_t kMaxWidth = int64_t(1) << 22;
-
-grkan_status_t linear_shape(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act) {
-    if (!act_valid(act) || rows < 0 || d_in < 1 || d_out < 1) return GRKAN_ERR_INVALID_ARG;
-    if (act == GRKAN_ACT_RATIONAL && (n_groups < 1 || d_out % n_groups != 0)) return GRKAN_ERR_INVALID_ARG;
-    if (rows > INT32_MAX || d_in > kMaxWidth || d_out > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
-    // one thread per 8 elements of a result, one launch
-    if (rows * ceil_div(d_out, 8) >= (int64_t(1) << 32) || rows * ceil_div(d_in, 8) >= (int64_t(1) << 32) ||
-        d_in * ceil_div(d_out, 8) >= (int64_t(1) << 32))
-        return GRKAN_ERR_UNSUPPORTED;
-    return GRKAN_OK;
-}
-
 bool chunks_aligned(const void *p, int64_t ld, int64_t width) {
     return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0;
-}
-
-int64_t act_group(int64_t d_out, int32_t n_groups, grkan_act_t act) {
-    return act == GRKAN_ACT_RATIONAL ? d_out / n_groups : 8;
-}
-
-// Plans and workspace do not depend on alignment.
-struct LinearBwdPlan {
-    SlopePlan slope;
-    ProductPlan dx, dw;
-    size_t off_slope, off_sums, total;
-};
-
-void linear_bwd_plan(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act, LinearBwdPlan *p) {
-    p->slope = plan_slope(rows, d_out, act, act_group(d_out, n_groups, act));
-    p->dx = plan_product(kFormDx, rows, d_in, d_out, true, GRKAN_ACT_NONE, 8);
-    p->dw = plan_product(kFormDw, d_out, d_in, rows, true, GRKAN_ACT_NONE, 8);
-    p->off_slope = act == GRKAN_ACT_NONE ? 0 : align256((size_t)rows * d_out * 2);
-    p->off_sums = p->off_slope + align256(p->slope.partials_bytes);
-    const size_t sums = p->dx.partials_bytes > p->dw.partials_bytes ? p->dx.partials_bytes : p->dw.partials_bytes;
-    p->total = p->off_sums + align256(sums);
 }
 
 __global__ __launch_bounds__(256) void grkan_zero16_kernel(uint16_t *p, int64_t n) {

@@ -1,11 +1,11 @@
-// grkan_linear.h -- plans and kernel arguments of the linear map with bias,
+// grkan_linear.h -- kernel arguments of the linear map with bias,
 // activation and residual in its epilogue (grkan_linear.hip); internal.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "grkan_block.h"
+#include "grkan_plan.h"
 
 namespace grkan {
 
@@ -38,34 +38,6 @@ struct ProductArgs {
     Epilogue e;
 };
 
-// Ways to multiply.
-//   kTile     tiles of the result in registers, operands through LDS; with
-//             splits > 1 (or an epilogue the tile kernel lacks) fp32 sums go
-//             to memory and a second kernel adds them and applies the epilogue
-//   kSkinny   few rows: 16 columns of the result a workgroup, its waves share
-//             the k range, the weights go from memory straight to registers
-enum ProductKind : int32_t { kTile = 0, kSkinny = 1 };
-
-struct ProductPlan {
-    int32_t kind;
-    int32_t tile;            // kTile: index of the tile shape
-    int32_t rest_tile;       // kTile: shape of the rows from `rows` on, when rows > 0
-    int64_t rows;
-    int32_t mt;              // kSkinny: 16-row blocks per workgroup
-    int32_t splits, k_split;
-    bool two_steps;          // partials, then grkan_linear_finish
-    bool aligned;            // 16-byte chunks of both operands are aligned and whole
-    size_t partials_bytes;
-};
-
-// The layouts of the three products.
-enum ProductForm : int32_t {
-    kFormForward = 0,   // Q = x [M][K], P = W [N][K]
-    kFormDx = 1,        // Q = dpre [M][K], P = W [K][N]
-    kFormDw = 2         // Q = dpre [K][M], P = x [K][N]
-};
-
-ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga);
 hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &a, hipStream_t s);
 
 // dpre = dz act'(pre) (bf16 [rows][ldp]) with the column sums of dpre in fp32
@@ -82,12 +54,6 @@ struct SlopeArgs {
     int32_t chunks;
     int64_t chunk_rows;
 };
-struct SlopePlan {
-    int32_t vec, vpr, chunks;
-    int64_t chunk_rows;
-    size_t partials_bytes;
-};
-SlopePlan plan_slope(int64_t rows, int64_t N, int32_t act, int64_t dga);
 hipError_t launch_slope(const SlopeArgs &a, hipStream_t s);
 
 }  // namespace grkan

@@ -843,97 +843,6 @@ template <int RAT> hipError_t launch_finish(const ProductArgs &a, hipStream_t s)
 }
 }  // namespace
 
-// Rows up to which the skinny kernel is taken (128 x 3,072 from 768: 9.4 us against
-// 8.9 with tiles; 64: 6.9 against 8.7).
-constexpr int64_t kSkinnyRows = 64;
-
-constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {256, 128, 64}, kTileK[] = {64, 32, 64};
-
-ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga) {
-    ProductPlan p{};
-    p.aligned = aligned;
-    p.splits = 1;
-    p.k_split = (int32_t)(K > 0 ? K : 1);
-    const bool any_groups = act == GRKAN_ACT_RATIONAL && dga % 8 != 0;
-    if (form == kFormForward && M <= kSkinnyRows) {
-        p.kind = kSkinny;
-        // as many rows a workgroup as there are, while 192 workgroups remain (64 x
-        // 768 from 3,072: 9.1, 10.6, 15.9 us with 1, 2, 4 blocks of 16 rows; 64 x 3,072
-        // from 768: 8.6, 6.9, 6.9)
-        p.mt = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-        while (p.mt > 1 && (N + 15) / 16 * ((M + 16 * p.mt - 1) / (16 * p.mt)) < 192) p.mt /= 2;
-        return p;
-    }
-    // The tile and the number of k splits with the least estimated time.  Places
-    // are the workgroups that the CUs hold at once; a step takes a workgroup
-    // `alone` us while few are taken, in proportion to those that are up to
-    // `full`, and a tile's result `tail` (M x N from K, rows of tiles 256 / 128 / 64,
-    // us: 1,003 x 768 from 768 25 / 14.8 / 7.8; 4,096 x 768 from 3,072 66 / 42 / 34;
-    // 4,096 x 3,072 from 768 29 / 32 / 40; 4,096 x 4,096 from 4,096 115 / 183 / 273;
-    // 50,432 x 3,072 from 768 324 / 365 / 470).  Splits add a launch, a write and a
-    // read of their fp32 sums (768 x 768 from 50,432 in tiles of 256 rows: 158, 88,
-    // 75 us with 7, 16, 24; of 1,003 rows from 768 in tiles of 64: 7.8, 15 us with 1
-    // and 2).  The operands reach the XCDs at about 10 TB/s, once or to each of
-    // the 8 as the tiles' order has it (768 x 192 from 25,216: 33 us in 7 splits,
-    // all of both to each; 25 us in 16, each k range to one).  No sum runs over
-    // more than 16,384 values of k in fp32.
-    static const double kAlone[] = {1.5, 0.4, 0.33}, kFull[] = {1.65, 1.2, 0.75}, kTail[] = {7.0, 2.0, 0.5};
-    static const int64_t kPlaces[] = {256, 768, 768};
-    auto tiles_us = [&](int i, int64_t wgs, int64_t steps) {
-        const int64_t rounds = wgs / kPlaces[i], rest = wgs % kPlaces[i];
-        const double part = kFull[i] * (double)rest / (double)kPlaces[i];
-        double us = (double)rounds * (steps * kFull[i] + kTail[i]);
-        if (rest) us += steps * (part > kAlone[i] ? part : kAlone[i]) + kTail[i];
-        return us;
-    };
-    // (unaligned chunks are on their way in registers: a tile of 256 x 128 spilled,
-    // 574 us against 75 with 128 x 128 at 8,003 x 1,501 from 777)
-    const int first = aligned ? 0 : 1;
-    double best = 1e30;
-    p.kind = kTile;
-    for (int i = first; i < 3; ++i) {
-        const int64_t mt = (M + kTileM[i] - 1) / kTileM[i], nt = (N + kTileN[i] - 1) / kTileN[i], tiles = mt * nt;
-        const int64_t steps = (K + kTileK[i] - 1) / kTileK[i], least = (K + 16383) / 16384;
-        for (int64_t s = least < 1 ? 1 : least; s <= 64 || s == least; ++s) {
-            if (s > 8 && s % 8 != 0 && s != least) continue;  // eighths: a k range to an XCD
-            if (s > 1 && s > least && (steps < 4 * s || (double)s * M * N * 4 > 256e6)) break;
-            const int64_t per = (steps + s - 1) / s;
-            const double times = s % 8 == 0 ? 1 : 8.0 / (double)(s < 8 ? s : 8);
-            const double fetch = 2.0 * (double)K * ((double)M + times * (double)N) / 10e6, work = tiles_us(i, tiles * s, per);
-            double us = 3.0 + (work > fetch ? work : fetch);
-            if (s > 1) us += 3.0 + 2.0 * (double)s * M * N * 4 / 6e6;
-            if (us < best) {
-                best = us;
-                p.tile = i;
-                p.rows = 0;
-                p.k_split = (int32_t)(per * kTileK[i] < K ? per * kTileK[i] : (K > 0 ? K : 1));
-            }
-            // Rows that fill whole rounds of 256-row tiles, the rest in smaller ones
-            // (50,432 x 768 from 3,072: 312 us whole, 198 + 57 us so)
-            if (i == 0 && s == 1 && form != kFormDw && !any_groups) {
-                const int64_t panels = tiles / kPlaces[0] * kPlaces[0] / nt, rows = panels * kTileM[0], left = M - rows;
-                if (rows <= 0 || left <= 0) continue;
-                for (int j = 1; j < 3; ++j) {
-                    const int64_t rest = ((left + kTileM[j] - 1) / kTileM[j]) * ((N + kTileN[j] - 1) / kTileN[j]);
-                    const double both = 6.0 + tiles_us(0, panels * nt, steps) + tiles_us(j, rest, (K + kTileK[j] - 1) / kTileK[j]);
-                    if (both < best) {
-                        best = both;
-                        p.tile = 0;
-                        p.k_split = (int32_t)K;
-                        p.rows = rows;
-                        p.rest_tile = j;
-                    }
-                }
-            }
-        }
-    }
-    p.splits = (int32_t)((K + p.k_split - 1) / p.k_split);
-    if (p.splits < 1) p.splits = 1;
-    p.two_steps = p.splits > 1 || any_groups;
-    if (p.two_steps) p.partials_bytes = (size_t)p.splits * (size_t)M * (size_t)N * 4;
-    return p;
-}
-
 hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &args, hipStream_t s) {
     ProductArgs a = args;
     a.splits = p.splits;
@@ -962,9 +871,6 @@ hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &arg
 // ------------------------------------------------------------ dpre, dbias
 
 namespace {
-
-constexpr int kSlopeTx = 32, kSlopeTy = 8;
-constexpr int64_t kSlopeBlocks = 1536;  // workgroups, 6 a CU
 
 // dpre = dz act'(pre) with its column sums (dbias) and the rational's coefficient
 // sums: one pass, two rows of a lane on their way while one is worked on; column
@@ -1101,23 +1007,6 @@ __global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a)
 }
 
 }  // namespace
-
-SlopePlan plan_slope(int64_t rows, int64_t N, int32_t act, int64_t dga) {
-    SlopePlan p{};
-    const bool rational = act == GRKAN_ACT_RATIONAL;
-    p.vec = rational && dga % 8 != 0 ? 1 : 8;
-    p.vpr = (int32_t)((N + p.vec - 1) / p.vec);
-    const int64_t blocks = (p.vpr + kSlopeTx - 1) / kSlopeTx;
-    int64_t chunks = (kSlopeBlocks + blocks - 1) / blocks;
-    const int64_t most = (rows + 4 * kSlopeTy - 1) / (4 * kSlopeTy);
-    if (chunks > most) chunks = most;
-    if (chunks < 1) chunks = 1;
-    p.chunk_rows = (rows + chunks - 1) / chunks;
-    if (p.chunk_rows < 1) p.chunk_rows = 1;
-    p.chunks = (int32_t)((rows + p.chunk_rows - 1) / p.chunk_rows);
-    p.partials_bytes = (size_t)p.chunks * (size_t)(N + (rational ? 10 * (int64_t)p.vpr : 0)) * 4;
-    return p;
-}
 
 hipError_t launch_slope(const SlopeArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)((a.vpr + kSlopeTx - 1) / kSlopeTx), (unsigned)a.chunks), block(kSlopeTx * kSlopeTy);
