@@ -298,9 +298,7 @@ extern "C" grkan_status_t grkan_linear_act_forward(const void *x, const void *W,
 extern "C" size_t grkan_linear_act_backward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
                                                            int32_t n_groups, grkan_act_t act) {
     if (linear_shape(rows, d_in, d_out, n_groups, act) != GRKAN_OK || rows == 0) return 0;
-    LinearBwdPlan p;
-    linear_bwd_plan(rows, d_in, d_out, n_groups, act, &p);
-    return p.total;
+    return linear_bwd_bytes(rows, d_in, d_out, n_groups, act);
 }
 
 extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W, const void *dz, const void *pre,
@@ -321,7 +319,10 @@ extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W
     LinearBwdPlan p{};
     if (rows > 0) {
         if (!x || !W || !dz || (act != GRKAN_ACT_NONE && !pre)) return GRKAN_ERR_INVALID_ARG;
-        linear_bwd_plan(rows, d_in, d_out, n_groups, act, &p);
+        // dpre: dz itself, or dense at the workspace's 256-byte aligned start
+        const bool q_ok = act == GRKAN_ACT_NONE ? chunks_aligned(dz, lddz, d_out) : d_out % 8 == 0;
+        linear_bwd_plan(rows, d_in, d_out, n_groups, act, q_ok && chunks_aligned(W, d_in, d_in),
+                        q_ok && chunks_aligned(x, ldx, d_in), &p);
     }
     const size_t ab = rational ? (size_t)n_groups * 24 : 0, bb = rational ? (size_t)n_groups * 16 : 0;
     const size_t wb = (size_t)d_out * d_in * 2;
@@ -374,12 +375,10 @@ extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W
         st = from_hip(launch_slope(s, stream));
         if (st != GRKAN_OK) return st;
     }
-    const bool q_ok = chunks_aligned(dpre, ldp, d_out);
     ProductArgs a{};
     a.partials = reinterpret_cast<float *>(ws + p.off_sums);
     a.q = Operand{dpre, ldp};
     if (dx) {
-        p.dx.aligned = q_ok && chunks_aligned(W, d_in, d_in);
         a.p = Operand{W, d_in};
         a.M = (int32_t)rows;
         a.N = (int32_t)d_in;
@@ -389,7 +388,6 @@ extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W
         if (st != GRKAN_OK) return st;
     }
     if (dW) {
-        p.dw.aligned = q_ok && chunks_aligned(x, ldx, d_in);
         a.p = Operand{x, ldx};
         a.M = (int32_t)d_out;
         a.N = (int32_t)d_in;

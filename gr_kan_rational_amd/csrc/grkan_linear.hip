@@ -844,6 +844,7 @@ template <int RAT> hipError_t launch_finish(const ProductArgs &a, hipStream_t s)
 }  // namespace
 
 hipError_t launch_product(int form, const ProductPlan &p, const ProductArgs &args, hipStream_t s) {
+    if (!plan_has_kernel(p)) return hipErrorInvalidValue;
     ProductArgs a = args;
     a.splits = p.splits;
     a.k_split = p.k_split;

@@ -292,6 +292,13 @@ constexpr int64_t kSkinnyRows = 64;
 
 constexpr int kTileM[] = {256, 128, 64}, kTileN[] = {256, 128, 64}, kTileK[] = {64, 32, 64};
 
+// Whether a kernel exists for the plan: the 256-row tile takes aligned operands
+// only, and what is cut into whole rounds of it and a rest runs the aligned
+// kernels throughout.
+inline bool plan_has_kernel(const ProductPlan &p) {
+    return p.kind == kSkinny || p.aligned || (p.tile != 0 && p.rows == 0);
+}
+
 inline ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool aligned, int32_t act, int64_t dga) {
     ProductPlan p{};
     p.aligned = aligned;
@@ -424,21 +431,35 @@ inline int64_t act_group(int64_t d_out, int32_t n_groups, grkan_act_t act) {
     return act == GRKAN_ACT_RATIONAL ? d_out / n_groups : 8;
 }
 
-// Plans and workspace do not depend on alignment.
+// The products are planned for the alignment that their operands have: the
+// 256-row tile, alone or with the other rows in smaller ones, exists for
+// aligned operands alone.
 struct LinearBwdPlan {
     SlopePlan slope;
     ProductPlan dx, dw;
     size_t off_slope, off_sums, total;
 };
 
-inline void linear_bwd_plan(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act, LinearBwdPlan *p) {
+inline void linear_bwd_plan(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act,
+                            bool dx_aligned, bool dw_aligned, LinearBwdPlan *p) {
     p->slope = plan_slope(rows, d_out, act, act_group(d_out, n_groups, act));
-    p->dx = plan_product(kFormDx, rows, d_in, d_out, true, GRKAN_ACT_NONE, 8);
-    p->dw = plan_product(kFormDw, d_out, d_in, rows, true, GRKAN_ACT_NONE, 8);
+    p->dx = plan_product(kFormDx, rows, d_in, d_out, dx_aligned, GRKAN_ACT_NONE, 8);
+    p->dw = plan_product(kFormDw, d_out, d_in, rows, dw_aligned, GRKAN_ACT_NONE, 8);
     p->off_slope = act == GRKAN_ACT_NONE ? 0 : align256((size_t)rows * d_out * 2);
     p->off_sums = p->off_slope + align256(p->slope.partials_bytes);
     const size_t sums = p->dx.partials_bytes > p->dw.partials_bytes ? p->dx.partials_bytes : p->dw.partials_bytes;
     p->total = p->off_sums + align256(sums);
+}
+
+// Workspace that is enough whatever the operands' alignment.
+inline size_t linear_bwd_bytes(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act) {
+    size_t most = 0;
+    for (int al = 0; al < 4; ++al) {
+        LinearBwdPlan p;
+        linear_bwd_plan(rows, d_in, d_out, n_groups, act, (al & 1) != 0, (al & 2) != 0, &p);
+        if (p.total > most) most = p.total;
+    }
+    return most;
 }
 
 }  // namespace grkan

@@ -1,0 +1,57 @@
+"""CPU checks of the block operators' plans (csrc/grkan_plan.h, host code without HIP): a g++-built harness
+asks for the plans of a grid of shapes and checks what the kernels and the callers rely on."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "gr_kan_rational_amd", "csrc")
+
+COMMON = r"""
+#include "grkan_plan.h"
+#include <cstdio>
+using namespace grkan;
+static long checked = 0, bad = 0;
+#define CHECK(ok, ...) do { ++checked; if (!(ok) && bad++ < 10) { printf(__VA_ARGS__); printf("\n"); } } while (0)
+"""
+TAIL = r"""
+    printf("checked %ld bad %ld\n", checked, bad);
+    return checked == 0 || bad != 0;
+}
+"""
+
+
+def run(tmp_path, body):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    src, exe = tmp_path / "plans.cpp", tmp_path / "plans"
+    src.write_text(COMMON + "int main() {" + body + TAIL)
+    subprocess.run([gxx, "-O2", "-std=c++17", "-D__HIP_PLATFORM_AMD__", "-I", CSRC, "-I", os.path.join(ROOT, "include"),
+                    "-I", "/opt/rocm/include", str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_linear_backward_plans_have_kernels_and_workspace(tmp_path):
+    """Whatever the alignment of its operands, each product of the backward is planned for a kernel that
+    exists, and the workspace asked of the caller, who states none of it, is enough."""
+    run(tmp_path, r"""
+    const int rows[] = {1, 65, 197, 1003, 4099, 5297, 8449, 12801, 50432, 201728};
+    const int act[] = {GRKAN_ACT_NONE, GRKAN_ACT_RATIONAL};
+    for (int r : rows)
+        for (int i = 49; i < 4100; i += 97)
+            for (int o = 51; o < 4100; o += 97)
+                for (int a : act) {
+                    const size_t most = linear_bwd_bytes(r, i, o, 1, (grkan_act_t)a);
+                    for (int al = 0; al < 4; ++al) {
+                        LinearBwdPlan p;
+                        linear_bwd_plan(r, i, o, 1, (grkan_act_t)a, al & 1, al & 2, &p);
+                        CHECK(p.dx.aligned == ((al & 1) != 0) && p.dw.aligned == ((al & 2) != 0), "alignment");
+                        CHECK(plan_has_kernel(p.dx) && plan_has_kernel(p.dw), "%d %d %d: no kernel", r, i, o);
+                        CHECK(p.total <= most, "%d %d %d: %zu of %zu", r, i, o, p.total, most);
+                    }
+                }
+""")

@@ -83,3 +83,64 @@ def test_coefficient_gradients_at_full_size(gk, seed):
         want, norm = t.sum((0, 2)), t.square().sum((0, 2)).sqrt()
         got = dA[:, k] if k < 6 else dB[:, k - 6]
         ref.check(f"coefficient {k}", got, want, 1e-4 * torch.maximum(want.abs(), 1e-2 * norm) + 1e-6)
+
+
+def inputs(rows, d_in, d_out, act, groups, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(size, std):
+        return torch.randn(size, generator=gen, device=DEV) * std
+
+    x, W = normal((rows, d_in), 1.0).to(BF), normal((d_out, d_in), d_in ** -0.5).to(BF)
+    dz, pre = normal((rows, d_out), 0.1).to(BF), normal((rows, d_out), 1.2).to(BF)
+    A, B = (normal((groups, 6), 0.5), normal((groups, 4), 0.5)) if act == "rational" else (None, None)
+    return x, W, dz, pre, A, B
+
+
+def check_backward(gk, x, W, dz, pre, act, A, B, groups):
+    got = gk.grkan_linear_act_backward(x, W, dz, pre, act, A, B, groups)
+    want = ref.linear_backward(x, W, dz, pre, act, A, B)
+    for k, g in zip(("dx", "dW", "dbias", "dA", "dB"), got):
+        if k in want:
+            ref.check(k, g, *want[k])
+
+
+# 256-row tiles, or whole rounds of them with the other rows in smaller tiles, where aligned operands would
+# be; for the third of these dx alone
+@pytest.mark.parametrize("shape, act, groups", [((8449, 1033, 2041), "silu", 1), ((8450, 2041, 1033), "silu", 1),
+                                                ((5297, 3839, 407), "silu", 1), ((50432, 777, 1501), "rational", 19),
+                                                ((50432, 770, 1500), "none", 1)], ids=str)
+def test_unaligned_widths_of_large_products(gk, shape, act, groups):
+    """Odd widths: no row but the first of an operand begins on a 16-byte boundary."""
+    print(f"[linear backward, unaligned] {shape} {act}", flush=True)
+    x, W, dz, pre, A, B = inputs(*shape, act, groups, 60)
+    check_backward(gk, x, W, dz, pre, act, A, B, groups)
+
+
+def off_boundary(t, left, right):
+    """The values of t in the columns of a wider tensor of NaN, `left` elements off its rows' starts."""
+    wide = torch.full((t.shape[0], left + t.shape[1] + right), float("nan"), dtype=t.dtype, device=DEV)
+    view = wide[:, left:left + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("which", ("x", "W", "dz", "dz-stride"))
+@pytest.mark.parametrize("shape", [(8449, 1032, 2040), (8450, 2040, 1032)], ids=str)
+def test_unaligned_operands_of_aligned_widths(gk, shape, which):
+    """One operand at an odd address or with an odd row stride, its neighbours in memory NaN."""
+    print(f"[linear backward, unaligned {which}] {shape}", flush=True)
+    rows, d_in, d_out = shape
+    x, W, dz, _, _, _ = inputs(*shape, "none", 1, 61)
+    if which == "W":
+        buf = torch.full((d_out * d_in + 16,), float("nan"), dtype=BF, device=DEV)
+        w2 = buf[7:7 + d_out * d_in].view(d_out, d_in)
+        w2.copy_(W)
+        W = w2
+    elif which == "x":
+        x = off_boundary(x, 3, 5)
+    elif which == "dz":
+        dz = off_boundary(dz, 1, 7)
+    else:
+        dz = off_boundary(dz, 0, 3)
+    check_backward(gk, x, W, dz, None, "none", None, None, 1)
