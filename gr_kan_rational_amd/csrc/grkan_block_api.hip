@@ -1,6 +1,7 @@
 // grkan_block_api.hip -- the C ABI of include/grkan_block.h: argument
-// validation, plans and dispatch.  Plans depend on shapes, types and the
-// activation alone, so results have the same bits on every device.
+// validation and dispatch.  Plans depend on shapes, types, the activation and,
+// for the products, on whether the operands' 16-byte chunks are aligned and whole,
+// so results have the same bits on every device.
 #include <limits.h>
 #include <stdint.h>
 
@@ -248,8 +249,7 @@ __global__ __launch_bounds__(256) void grkan_zero16_kernel(uint16_t *p, int64_t 
 extern "C" size_t grkan_linear_act_forward_workspace_size(int64_t rows, int64_t d_in, int64_t d_out,
                                                           int32_t n_groups, grkan_act_t act) {
     if (linear_shape(rows, d_in, d_out, n_groups, act) != GRKAN_OK || rows == 0) return 0;
-    return align256(
-        plan_product(kFormForward, rows, d_out, d_in, true, act, act_group(d_out, n_groups, act)).partials_bytes);
+    return linear_fwd_bytes(rows, d_in, d_out, n_groups, act);
 }
 
 extern "C" grkan_status_t grkan_linear_act_forward(const void *x, const void *W, const float *bias,

@@ -431,6 +431,17 @@ inline int64_t act_group(int64_t d_out, int32_t n_groups, grkan_act_t act) {
     return act == GRKAN_ACT_RATIONAL ? d_out / n_groups : 8;
 }
 
+// Workspace of the forward that is enough whatever its operands' alignment (the
+// unaligned plan may have more k splits).
+inline size_t linear_fwd_bytes(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act) {
+    size_t most = 0;
+    for (int al = 0; al < 2; ++al) {
+        const ProductPlan p = plan_product(kFormForward, rows, d_out, d_in, al != 0, act, act_group(d_out, n_groups, act));
+        if (p.partials_bytes > most) most = p.partials_bytes;
+    }
+    return align256(most);
+}
+
 // The products are planned for the alignment that their operands have: the
 // 256-row tile, alone or with the other rows in smaller ones, exists for
 // aligned operands alone.

@@ -22,7 +22,8 @@
  * `stream` and the call returns without waiting; arguments are validated
  * before any HIP call; no C++ exception crosses the interface.  Results are
  * bitwise reproducible: every sum is taken in an order that depends on the
- * shape alone.
+ * shape and, in the linear map's products, on whether the operands are whole
+ * 16-byte vectors at aligned addresses.
  */
 #ifndef GRKAN_BLOCK_H
 #define GRKAN_BLOCK_H
@@ -140,7 +141,7 @@ GRKAN_API size_t grkan_group_norm_backward_workspace_size(
  *   rows >= 0 (0 is a no-op), d_in, d_out >= 1; any sizes, strides and element
  *   alignment are served, whole 16-byte vectors in both widths fastest.
  *   workspace grkan_linear_act_forward_workspace_size() bytes (may be 0),
- *             256-byte aligned.
+ *             256-byte aligned; enough for any strides and alignment.
  * GRKAN_ERR_UNSUPPORTED: rows >= 2^31, a width or stride above 2^22, rows x
  * d_out past the launch limits, a misaligned pointer.
  */

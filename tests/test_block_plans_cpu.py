@@ -55,3 +55,37 @@ def test_linear_backward_plans_have_kernels_and_workspace(tmp_path):
                     }
                 }
 """)
+
+
+def test_linear_forward_workspace_is_enough_for_any_alignment(tmp_path):
+    """The bytes that the caller is told, who states no alignment, against those of either plan."""
+    run(tmp_path, r"""
+    const int rows[] = {1, 65, 130, 241, 700, 1003, 1500, 3000, 6789, 9366, 20000, 50432};
+    const int act[] = {GRKAN_ACT_NONE, GRKAN_ACT_RATIONAL};
+    for (int r : rows)
+        for (int i = 48; i < 10000; i += 123)
+            for (int o = 60; o < 30000; o += 317)
+                for (int a : act) {
+                    const size_t said = linear_fwd_bytes(r, i, o, 1, (grkan_act_t)a);
+                    for (int al = 0; al < 2; ++al) {
+                        const ProductPlan p = plan_product(kFormForward, r, o, i, al, a, act_group(o, 1, (grkan_act_t)a));
+                        CHECK(plan_has_kernel(p), "%d %d %d: no kernel", r, i, o);
+                        CHECK(p.partials_bytes <= said, "%d %d %d: %zu of %zu", r, i, o, p.partials_bytes, said);
+                    }
+                }
+""")
+
+
+def test_workspace_queries_follow_the_plans(tmp_path):
+    """The library's queries at shapes whose aligned and unaligned plans differ: rows, widths, bytes of the
+    plan with more of them."""
+    from gr_kan_rational_amd import binding, block
+
+    if not os.path.exists(binding.LIB_PATH):
+        import __graft_entry__
+
+        __graft_entry__.build()
+    lib = block._library()
+    for rows, d_in, d_out, splits in ((130, 2265, 24786, 3), (1003, 6203, 12387, 2), (130, 1688, 24608, 3)):
+        got = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, 1, block.GRKAN_ACT_SILU)
+        assert got == (splits * rows * d_out * 4 + 255) // 256 * 256
