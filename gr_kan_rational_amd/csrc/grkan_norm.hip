@@ -515,7 +515,7 @@ template <auto KERN>
 hipError_t start(const NormArgs &a, dim3 grid, dim3 block, size_t lds, hipStream_t s) {
     if (lds > (64u << 10)) {
         static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(KERN),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxLds);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(KERN, grid, block, lds, s, a);

@@ -75,6 +75,7 @@ struct NormPlan {
     size_t off_stats, off_means, off_partials, total;  // workspace
 };
 
+constexpr size_t kMaxLds = 160 << 10;  // of a CU
 constexpr int kTokenMaxLanes = 256, kTokenMaxAccesses = 4;
 constexpr int64_t kNormWorkgroups = 2048;  // target of the looping kernels: 8 workgroups a CU
 
@@ -156,6 +157,12 @@ inline grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int3
             const int64_t tx = ceil_div(groups * D, vec_of(groups));
             return tx <= threads ? threads / tx * regs : 0;
         };
+        // LDS of the groups' sums (group_sum): every lane's and column's, and the groups'
+        auto lds_of = [&](bool mixed) {
+            const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
+            const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
+            return value * values * ((size_t)(p->block + p->TX) * (mixed ? p->vec : 1) + p->groups);
+        };
         if (S > 1 && S <= rows_of(gpb)) {
             p->kind = kNormSlab;
             // wider blocks while many workgroups remain and rows are short
@@ -227,6 +234,11 @@ inline grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int3
                 chunks_of(512, 512);
             } else {
                 chunks_of(1024, 256);
+                // (1,024 lanes' fp64 sums of 8 elements each, where accesses straddle
+                // groups, may pass what a CU has: half the lanes then.  2 x 1,024 x
+                // 2,044 in 4 groups 23.7 us, with 256 lanes and the step between 26.6;
+                // 64 x 197 x 2,046 in one 86, 82)
+                if (p->fused && lds_of(D % p->vec != 0) > kMaxLds) chunks_of(512, 256);
                 if (!p->fused) chunks_of(256, 1024);
             }
             p->blocks = N * p->chunks * p->ncb;
@@ -237,9 +249,7 @@ inline grkan_status_t norm_plan(int64_t N, int64_t S, int64_t C, int32_t G, int3
         p->L = pow2_at_most(p->block / p->groups < 64 ? (p->block > p->groups ? p->block / p->groups : 1) : 64);
         const int64_t cols_across = (int64_t)p->TX * (p->mixed ? p->vec : 1);
         p->P = pow2_at_most(p->block / cols_across < 1 ? 1 : (p->block / cols_across < 64 ? p->block / cols_across : 64));
-        const size_t value = p->kind == kNormSplit ? sizeof(double) : sizeof(float);
-        const size_t values = p->kind == kNormSlab && !backward ? 1 : 2;
-        p->lds = value * values * ((size_t)(p->block + p->TX) * (p->mixed ? p->vec : 1) + p->groups);
+        p->lds = lds_of(p->mixed);
         const size_t cols = (size_t)p->block * ((rational ? 10 : p->vec) + 3) * 4;
         if (backward && p->lds < cols) p->lds = cols;
     }

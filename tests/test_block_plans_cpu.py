@@ -89,3 +89,27 @@ def test_workspace_queries_follow_the_plans(tmp_path):
     for rows, d_in, d_out, splits in ((130, 2265, 24786, 3), (1003, 6203, 12387, 2), (130, 1688, 24608, 3)):
         got = lib.grkan_linear_act_forward_workspace_size(rows, d_in, d_out, 1, block.GRKAN_ACT_SILU)
         assert got == (splits * rows * d_out * 4 + 255) // 256 * 256
+
+
+def test_group_norm_plans_fit_a_cus_lds(tmp_path):
+    """1 to 8,192 channels with every divisor as groups: no plan asks for more LDS than a CU has, in a launch
+    of at most 1,024 threads, and the forward's second pass has room for its statistics."""
+    run(tmp_path, r"""
+    const int ns[] = {1, 2, 8, 64, 128}, ss[] = {1, 2, 197, 1024, 4097};
+    for (int C = 1; C <= 8192; ++C)
+        for (int G = 1; G <= C; ++G) {
+            if (C % G) continue;
+            for (int n : ns)
+                for (int s : ss)
+                    for (int k = 0; k < 8; ++k) {
+                        const int act = k & 1 ? GRKAN_ACT_RATIONAL : GRKAN_ACT_SILU;
+                        const int ng = C % 8 ? (C % 3 ? 1 : 3) : 8;
+                        NormPlan p;
+                        const int st = norm_plan(n, s, C, G, ng, (grkan_act_t)act, k & 2 ? GRKAN_F32 : GRKAN_BF16, k & 4, &p);
+                        CHECK(st == GRKAN_OK, "%d x %d x %d / %d: status %d", n, s, C, G, st);
+                        CHECK(p.lds <= (160 << 10), "%d x %d x %d / %d: %zu of LDS", n, s, C, G, p.lds);
+                        CHECK(p.block >= 1 && p.block <= 1024, "%d x %d x %d / %d: %d threads", n, s, C, G, p.block);
+                        CHECK(p.kind != kNormSplit || (size_t)p.groups * 8 <= (160 << 10), "%d groups", p.groups);
+                    }
+        }
+""")
