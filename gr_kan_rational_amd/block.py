@@ -389,11 +389,22 @@ class GRKANGroupNorm(torch.autograd.Function):
 
 
 class GRKANLinearAct(torch.autograd.Function):
-    """Autograd wrapper: z = act(x W^T + bias) + residual, ``apply(x, W, bias, act, A, B, n_groups, residual)``."""
+    """Autograd wrapper: z = act(x W^T + bias) + residual, ``apply(x, W, bias, act, A, B, n_groups, residual)``.
+
+    The product before the activation is written and kept only for a backward that reads it: not without
+    gradients (``torch.no_grad``, or no input that asks for one), for act "none" or for the residual's alone."""
+
+    @classmethod
+    def apply(cls, x, W, bias=None, act="none", A=None, B=None, n_groups=8, residual=None):
+        # (inside forward the grad mode is off and needs_input_grad does not know of it)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, W, bias, A, B, residual)):
+            return super().apply(x, W, bias, act, A, B, n_groups, residual)
+        return grkan_linear_act_forward(x, W, bias, act, A, B, n_groups, residual)[0]
 
     @staticmethod
     def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, residual=None):
-        z, pre = grkan_linear_act_forward(x, W, bias, act, A, B, n_groups, residual, keep=act != "none")
+        keep = act != "none" and any(ctx.needs_input_grad[:-1])
+        z, pre = grkan_linear_act_forward(x, W, bias, act, A, B, n_groups, residual, keep=keep)
         ctx.save_for_backward(x, W, bias, A, B, pre)
         ctx.args = act, n_groups, residual is not None
         return z
@@ -402,6 +413,8 @@ class GRKANLinearAct(torch.autograd.Function):
     def backward(ctx, dz):
         x, W, bias, A, B, pre = ctx.saved_tensors
         act, n_groups, residual = ctx.args
+        if not any(ctx.needs_input_grad[:-1]):
+            return (None,) * 7 + (dz,)
         dz = dz.contiguous()
         dx, dW, db, dA, dB = grkan_linear_act_backward(x, W, dz, pre, act, A, B, n_groups)
         return (dx, dW, None if bias is None else db.view_as(bias), None, None if dA is None else dA.view_as(A),

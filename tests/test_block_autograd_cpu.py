@@ -1,0 +1,76 @@
+"""CPU checks of the block operators' autograd functions: what they ask of the operators, which a recorder
+stands in for here."""
+import pytest
+import torch
+
+from gr_kan_rational_amd import block
+
+BF = torch.bfloat16
+
+
+@pytest.fixture
+def linear(monkeypatch):
+    """Calls of the linear map, as dicts; its values by torch."""
+    calls = []
+
+    def forward(x, W, bias=None, act="none", A=None, B=None, n_groups=8, residual=None, keep=False):
+        calls.append({"way": "forward", "keep": keep})
+        pre = torch.nn.functional.linear(x, W)
+        z = pre if residual is None else pre + residual
+        return z.clone(), pre.clone() if keep else None
+
+    def backward(x, W, dz, pre=None, act="none", A=None, B=None, n_groups=8, **kw):
+        assert act == "none" or pre is not None
+        calls.append({"way": "backward", **kw})
+        skip = kw.get("skip", ())
+        out = [t if n not in skip else None for n, t in (("dx", dz @ W), ("dW", dz.t() @ x), ("dbias", dz.float().sum(0)))]
+        return (*out, torch.zeros_like(A), torch.zeros_like(B)) if act == "rational" else (*out, None, None)
+
+    monkeypatch.setattr(block, "grkan_linear_act_forward", forward)
+    monkeypatch.setattr(block, "grkan_linear_act_backward", backward)
+    return calls
+
+
+def linear_inputs(**grads):
+    shapes = {"x": (5, 16), "W": (24, 16), "bias": (24,), "A": (8, 6), "B": (8, 4), "residual": (5, 24)}
+    out = {}
+    for k, s in shapes.items():
+        t = torch.randn(s, generator=torch.Generator().manual_seed(len(out)))
+        out[k] = (t if k in ("bias", "A", "B") else t.to(BF)).requires_grad_(grads.get(k, False))
+    return out
+
+
+def apply(t, act):
+    rational = act == "rational"
+    return block.GRKANLinearAct.apply(t["x"], t["W"], t["bias"], act, t["A"] if rational else None,
+                                      t["B"] if rational else None, 8, t["residual"])
+
+
+@pytest.mark.parametrize("act", ("silu", "rational", "none"))
+@pytest.mark.parametrize("needs", ("x", "W", "bias", "A"))
+def test_the_product_is_kept_for_a_backward_that_reads_it(linear, act, needs):
+    t = linear_inputs(**{needs: True})
+    apply(t, act)
+    asked = act != "none" and (needs != "A" or act == "rational")
+    assert linear[-1]["keep"] is asked
+
+
+@pytest.mark.parametrize("act", ("silu", "rational", "none"))
+def test_the_product_is_not_kept_without_gradients(linear, act):
+    t = linear_inputs(x=True, W=True, bias=True, A=True, B=True, residual=True)
+    with torch.no_grad():
+        z = apply(t, act)
+    assert linear == [{"way": "forward", "keep": False}] and not z.requires_grad
+    t = linear_inputs()
+    z = apply(t, act)
+    assert linear[-1]["keep"] is False and not z.requires_grad
+
+
+@pytest.mark.parametrize("act", ("silu", "none"))
+def test_the_residuals_gradient_alone(linear, act):
+    t = linear_inputs(residual=True)
+    z = apply(t, act)
+    assert linear[-1]["keep"] is False
+    dz = torch.randn(z.shape).to(BF)
+    z.backward(dz)
+    assert torch.equal(t["residual"].grad, dz) and len(linear) == 1
