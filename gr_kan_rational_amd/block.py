@@ -105,6 +105,20 @@ def _given(t, name: str, shape, dtype, dev):
     return t
 
 
+def _wanted(skip, name: str, t, shape, dtype, dev):
+    """A gradient's tensor as _given, or None if it is to be skipped."""
+    if name not in skip:
+        return _given(t, name, shape, dtype, dev)
+    if t is not None:
+        raise ValueError(f"{name} is given and skipped")
+    return None
+
+
+def _skipped(skip, names):
+    if not set(skip) <= set(names):
+        raise ValueError(f"skip takes names among {names}")
+
+
 def _space(ws, need: int, dev):
     """(tensor, pointer, size in bytes) of the workspace: the caller's, or a new one of `need` bytes."""
     if ws is None:
@@ -206,11 +220,13 @@ def grkan_group_norm_forward(x: torch.Tensor, norm_groups: int, weight=None, bia
 def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                               norm_groups: int, weight=None, bias=None, act: str = "none", A=None, B=None,
                               n_groups: int = 8, dx=None, dweight=None, dbias=None, dA=None, dB=None,
-                              workspace=None, stream=None):
+                              workspace=None, stream=None, skip=()):
     """(dx, dweight, dbias, dA, dB) of ``grkan_group_norm_forward`` from its x, mean and rstd
     (``grkan_group_norm_backward``); dweight and dbias also without weight and bias (of ones and zeros),
-    dA and dB None but for the rational."""
+    dA and dB None but for the rational.  ``skip``: names among "dweight" and "dbias" that are not computed
+    (None in their place)."""
     io, code = _io(x), _act(act)
+    _skipped(skip, ("dweight", "dbias"))
     _on_gpu(x)
     n, s, c, xs, xr = _samples(x, "x")
     dev = x.device
@@ -231,13 +247,13 @@ def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Ten
 
     def launch(handle):
         gx = _given(dx, "dx", x.shape, x.dtype, dev)
-        gw = _given(dweight, "dweight", (c,), torch.float32, dev)
-        gb = _given(dbias, "dbias", (c,), torch.float32, dev)
+        gw = _wanted(skip, "dweight", dweight, (c,), torch.float32, dev)
+        gb = _wanted(skip, "dbias", dbias, (c,), torch.float32, dev)
         gA, gB = _coef_grads(code, dA, dB, ng, dev)
         ws, wsp, wsn = _space(workspace, need, dev)
         st = lib.grkan_group_norm_backward(x.data_ptr(), dy.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                           _ptr(weight), _ptr(bias), _ptr(A), _ptr(B), gx.data_ptr(), gw.data_ptr(),
-                                           gb.data_ptr(), _ptr(gA), _ptr(gB), n, s, c, xs, xr, ds, dr, norm_groups,
+                                           _ptr(weight), _ptr(bias), _ptr(A), _ptr(B), gx.data_ptr(), _ptr(gw),
+                                           _ptr(gb), _ptr(gA), _ptr(gB), n, s, c, xs, xr, ds, dr, norm_groups,
                                            ng, code, io, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_group_norm_backward")
@@ -332,11 +348,13 @@ def grkan_linear_act_forward(x: torch.Tensor, W: torch.Tensor, bias=None, act: s
 
 def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor, pre=None, act: str = "none",
                               A=None, B=None, n_groups: int = 8, dx=None, dW=None, dbias=None, dA=None, dB=None,
-                              workspace=None, stream=None):
+                              workspace=None, stream=None, skip=()):
     """(dx, dW, dbias, dA, dB) of ``grkan_linear_act_forward`` from its pre (not needed for act "none")
     (``grkan_linear_act_backward``): bf16 dx and dW, float32 dbias; dA and dB None but for the rational.
-    The residual's gradient is dz."""
+    The residual's gradient is dz.  ``skip``: names among "dx", "dW" and "dbias" that are not computed (None
+    in their place)."""
     code = _act(act)
+    _skipped(skip, ("dx", "dW", "dbias"))
     rows, d_in, d_out, ldx, dev = _linear_dims(x, W)
     if dz.shape != (*x.shape[:-1], d_out):
         raise ValueError(f"dz must be {[*x.shape[:-1], d_out]}")
@@ -352,19 +370,23 @@ def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor
     need = _need("linear_act_backward", rows, d_in, d_out, ng, code)
 
     def launch(handle):
-        gx = _given(dx, "dx", x.shape, torch.bfloat16, dev)
-        gW = _given(dW, "dW", (d_out, d_in), torch.bfloat16, dev)
-        gb = _given(dbias, "dbias", (d_out,), torch.float32, dev)
+        gx = _wanted(skip, "dx", dx, x.shape, torch.bfloat16, dev)
+        gW = _wanted(skip, "dW", dW, (d_out, d_in), torch.bfloat16, dev)
+        gb = _wanted(skip, "dbias", dbias, (d_out,), torch.float32, dev)
         gA, gB = _coef_grads(code, dA, dB, ng, dev)
         ws, wsp, wsn = _space(workspace, need, dev)
         st = lib.grkan_linear_act_backward(x.data_ptr(), W.data_ptr(), dz.data_ptr(), _ptr(pre), _ptr(A), _ptr(B),
-                                           gx.data_ptr(), gW.data_ptr(), gb.data_ptr(), _ptr(gA), _ptr(gB), rows, d_in,
+                                           _ptr(gx), _ptr(gW), _ptr(gb), _ptr(gA), _ptr(gB), rows, d_in,
                                            d_out, ldx, lddz, ng, code, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_linear_act_backward")
         return gx, gW, gb, gA, gB
 
     return _on_stream(stream, dev, launch)
+
+
+def _like(grad, t):
+    return None if grad is None else grad.view_as(t)
 
 
 class GRKANGroupNorm(torch.autograd.Function):
@@ -382,10 +404,10 @@ class GRKANGroupNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, A, B, mean, rstd = ctx.saved_tensors
         norm_groups, act, n_groups = ctx.args
+        skip = [name for name, i in (("dweight", 2), ("dbias", 3)) if not ctx.needs_input_grad[i]]
         dx, dw, db, dA, dB = grkan_group_norm_backward(x, dy.contiguous(), mean, rstd, norm_groups, weight, bias,
-                                                       act, A, B, n_groups)
-        return (dx, None, None if weight is None else dw.view_as(weight), None if bias is None else db.view_as(bias),
-                None, None, None if dA is None else dA.view_as(A), None if dB is None else dB.view_as(B), None)
+                                                       act, A, B, n_groups, skip=skip)
+        return dx, None, _like(dw, weight), _like(db, bias), None, None, _like(dA, A), _like(dB, B), None
 
 
 class GRKANLinearAct(torch.autograd.Function):
@@ -416,6 +438,6 @@ class GRKANLinearAct(torch.autograd.Function):
         if not any(ctx.needs_input_grad[:-1]):
             return (None,) * 7 + (dz,)
         dz = dz.contiguous()
-        dx, dW, db, dA, dB = grkan_linear_act_backward(x, W, dz, pre, act, A, B, n_groups)
-        return (dx, dW, None if bias is None else db.view_as(bias), None, None if dA is None else dA.view_as(A),
-                None if dB is None else dB.view_as(B), None, dz if residual else None)
+        skip = [name for i, name in enumerate(("dx", "dW", "dbias")) if not ctx.needs_input_grad[i]]
+        dx, dW, db, dA, dB = grkan_linear_act_backward(x, W, dz, pre, act, A, B, n_groups, skip=skip)
+        return dx, dW, _like(db, bias), None, _like(dA, A), _like(dB, B), None, dz if residual else None

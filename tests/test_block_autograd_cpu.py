@@ -74,3 +74,49 @@ def test_the_residuals_gradient_alone(linear, act):
     dz = torch.randn(z.shape).to(BF)
     z.backward(dz)
     assert torch.equal(t["residual"].grad, dz) and len(linear) == 1
+
+
+@pytest.mark.parametrize("act", ("silu", "rational", "none"))
+@pytest.mark.parametrize("needs", ("x", "W", "bias"))
+def test_the_linear_backward_forms_what_is_asked_for(linear, act, needs):
+    t = linear_inputs(**{needs: True})
+    apply(t, act).float().sum().backward()
+    grad = {"x": "dx", "W": "dW", "bias": "dbias"}
+    assert sorted(linear[-1]["skip"]) == sorted(grad[k] for k in grad if k != needs)
+    assert t[needs].grad is not None
+
+
+def test_a_missing_bias_has_no_gradient(linear):
+    t = linear_inputs(x=True, W=True)
+    t["bias"] = None
+    apply(t, "silu").float().sum().backward()
+    assert linear[-1]["skip"] == ["dbias"]
+
+
+@pytest.mark.parametrize("needs, skip", [(("x",), ["dweight", "dbias"]), (("x", "w"), ["dbias"]), (("b",), ["dweight"]),
+                                         (("x", "w", "b"), [])])
+def test_the_norms_backward_forms_what_is_asked_for(monkeypatch, needs, skip):
+    calls = []
+    monkeypatch.setattr(block, "grkan_group_norm_forward",
+                        lambda x, g, *a: (x.clone(), torch.zeros(x.shape[0], g), torch.ones(x.shape[0], g)))
+
+    def backward(x, dy, *a, skip=()):
+        calls.append(skip)
+        c = x.shape[-1]
+        return (dy.clone(), *(None if n in skip else torch.ones(c) for n in ("dweight", "dbias")), None, None)
+
+    monkeypatch.setattr(block, "grkan_group_norm_backward", backward)
+    t = {"x": torch.randn(4, 32), "w": torch.ones(32), "b": torch.zeros(32)}
+    for k in needs:
+        t[k].requires_grad_()
+    block.GRKANGroupNorm.apply(t["x"], 4, t["w"], t["b"]).sum().backward()
+    assert calls == [skip]
+    assert all((t[k].grad is not None) == (k in needs) for k in t)
+
+
+def test_skip_names_and_outputs_are_checked():
+    with pytest.raises(ValueError, match="skip"):
+        block._skipped(("dA",), ("dx", "dW", "dbias"))
+    with pytest.raises(ValueError, match="given and skipped"):
+        block._wanted(("dx",), "dx", torch.zeros(3), (3,), torch.float32, torch.device("cpu"))
+    assert block._wanted(["dx"], "dx", None, (3,), torch.float32, torch.device("cpu")) is None

@@ -144,3 +144,31 @@ def test_unaligned_operands_of_aligned_widths(gk, shape, which):
     else:
         dz = off_boundary(dz, 0, 3)
     check_backward(gk, x, W, dz, None, "none", None, None, 1)
+
+
+@pytest.mark.parametrize("act", ("none", "silu", "rational"))
+def test_skipped_gradients(gk, act):
+    """Each subset of dx, dW and dbias left out: None there, the other results unchanged."""
+    x, W, dz, pre, A, B = inputs(300, 96, 80, act, 8, 62)
+    names = ("dx", "dW", "dbias")
+    full = gk.grkan_linear_act_backward(x, W, dz, pre, act, A, B, 8)
+    for bits in range(1, 8):
+        skip = [n for i, n in enumerate(names) if bits >> i & 1]
+        got = gk.grkan_linear_act_backward(x, W, dz, pre, act, A, B, 8, skip=skip)
+        for n, p, q in zip((*names, "dA", "dB"), full, got):
+            assert q is None if n in skip else (p is q is None or torch.equal(p, q)), (skip, n)
+
+
+@pytest.mark.parametrize("shape, groups", [((40, 1, 96), 1), ((3, 50, 96), 4), ((2, 3000, 64), 4)], ids=str)
+@pytest.mark.parametrize("act", ("silu", "rational"))
+def test_skipped_gradients_of_the_norm(gk, shape, groups, act):
+    gen = torch.Generator(device=DEV).manual_seed(63)
+    x, dy = (torch.randn(shape, generator=gen, device=DEV) for _ in range(2))
+    A, B = (torch.randn((8, k), generator=gen, device=DEV) * 0.5 for k in (6, 4)) if act == "rational" else (None, None)
+    _, mean, rstd = gk.grkan_group_norm_forward(x, groups, act=act, A=A, B=B)
+    args = (x, dy, mean, rstd, groups, None, None, act, A, B, 8)
+    full = gk.grkan_group_norm_backward(*args)
+    for skip in (("dweight",), ("dbias",), ("dweight", "dbias")):
+        got = gk.grkan_group_norm_backward(*args, skip=skip)
+        for n, p, q in zip(("dx", "dweight", "dbias", "dA", "dB"), full, got):
+            assert q is None if n in skip else (p is q is None or torch.equal(p, q)), (skip, n)
