@@ -404,7 +404,8 @@ class GRKANGroupNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, A, B, mean, rstd = ctx.saved_tensors
         norm_groups, act, n_groups = ctx.args
-        skip = [name for name, i in (("dweight", 2), ("dbias", 3)) if not ctx.needs_input_grad[i]]
+        needs = *ctx.needs_input_grad, False, False  # as many as apply was given, two at least
+        skip = [name for name, i in (("dweight", 2), ("dbias", 3)) if not needs[i]]
         dx, dw, db, dA, dB = grkan_group_norm_backward(x, dy.contiguous(), mean, rstd, norm_groups, weight, bias,
                                                        act, A, B, n_groups, skip=skip)
         return dx, None, _like(dw, weight), _like(db, bias), None, None, _like(dA, A), _like(dB, B), None

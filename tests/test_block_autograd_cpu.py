@@ -120,3 +120,15 @@ def test_skip_names_and_outputs_are_checked():
     with pytest.raises(ValueError, match="given and skipped"):
         block._wanted(("dx",), "dx", torch.zeros(3), (3,), torch.float32, torch.device("cpu"))
     assert block._wanted(["dx"], "dx", None, (3,), torch.float32, torch.device("cpu")) is None
+
+
+def test_the_norms_arguments_may_be_left_out(monkeypatch):
+    monkeypatch.setattr(block, "grkan_group_norm_forward",
+                        lambda x, g, *a: (x.clone(), torch.zeros(x.shape[0], g), torch.ones(x.shape[0], g)))
+    monkeypatch.setattr(block, "grkan_group_norm_backward",
+                        lambda x, dy, *a, skip=(): (dy.clone(), *(None if n in skip else torch.ones(32)
+                                                                  for n in ("dweight", "dbias")), None, None))
+    x, w = torch.randn(4, 32, requires_grad=True), torch.ones(32, requires_grad=True)
+    block.GRKANGroupNorm.apply(x, 4).sum().backward()
+    block.GRKANGroupNorm.apply(x, 4, w).sum().backward()
+    assert x.grad is not None and w.grad is not None
