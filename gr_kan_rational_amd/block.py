@@ -13,6 +13,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_coefs, _check_out, _on_gpu
@@ -401,6 +402,7 @@ class GRKANGroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable  # the kernels' results carry no graph: a second derivative would silently lack them
     def backward(ctx, dy):
         x, weight, bias, A, B, mean, rstd = ctx.saved_tensors
         norm_groups, act, n_groups = ctx.args
@@ -433,6 +435,7 @@ class GRKANLinearAct(torch.autograd.Function):
         return z
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dz):
         x, W, bias, A, B, pre = ctx.saved_tensors
         act, n_groups, residual = ctx.args

@@ -132,3 +132,21 @@ def test_the_norms_arguments_may_be_left_out(monkeypatch):
     block.GRKANGroupNorm.apply(x, 4).sum().backward()
     block.GRKANGroupNorm.apply(x, 4, w).sum().backward()
     assert x.grad is not None and w.grad is not None
+
+
+def test_a_second_derivative_is_refused(linear, monkeypatch):
+    """The backward's results have no graph of their own: differentiating them raises, where it would leave
+    their part of the second derivative out."""
+    t = linear_inputs(x=True, W=True)
+    z = apply(t, "silu").float()
+    gx, = torch.autograd.grad((z ** 2).sum(), t["x"], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (gx.float() ** 2).sum().backward()
+    monkeypatch.setattr(block, "grkan_group_norm_forward",
+                        lambda x, g, *a: (x.clone(), torch.zeros(x.shape[0], g), torch.ones(x.shape[0], g)))
+    monkeypatch.setattr(block, "grkan_group_norm_backward",
+                        lambda x, dy, *a, skip=(): (dy.clone(), None, None, None, None))
+    x = torch.randn(4, 32, requires_grad=True)
+    gx, = torch.autograd.grad((block.GRKANGroupNorm.apply(x, 4) ** 2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (gx ** 2).sum().backward()
