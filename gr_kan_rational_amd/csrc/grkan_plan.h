@@ -425,11 +425,12 @@ inline SlopePlan plan_slope(int64_t rows, int64_t N, int32_t act, int64_t dga) {
 // ------------------------------------------------------------ linear map
 
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
+constexpr int64_t kMaxRows = INT32_MAX - 256;  // the tiles' row numbers, to the end of the last 256, are 32-bit
 
 inline grkan_status_t linear_shape(int64_t rows, int64_t d_in, int64_t d_out, int32_t n_groups, grkan_act_t act) {
     if (!act_valid(act) || rows < 0 || d_in < 1 || d_out < 1) return GRKAN_ERR_INVALID_ARG;
     if (act == GRKAN_ACT_RATIONAL && (n_groups < 1 || d_out % n_groups != 0)) return GRKAN_ERR_INVALID_ARG;
-    if (rows > INT32_MAX || d_in > kMaxWidth || d_out > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
+    if (rows > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
     // one thread per 8 elements of a result, one launch
     if (rows * ceil_div(d_out, 8) >= (int64_t(1) << 32) || rows * ceil_div(d_in, 8) >= (int64_t(1) << 32) ||
         d_in * ceil_div(d_out, 8) >= (int64_t(1) << 32))

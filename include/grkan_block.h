@@ -142,7 +142,7 @@ GRKAN_API size_t grkan_group_norm_backward_workspace_size(
  *   alignment are served, whole 16-byte vectors in both widths fastest.
  *   workspace grkan_linear_act_forward_workspace_size() bytes (may be 0),
  *             256-byte aligned; enough for any strides and alignment.
- * GRKAN_ERR_UNSUPPORTED: rows >= 2^31, a width or stride above 2^22, rows x
+ * GRKAN_ERR_UNSUPPORTED: rows >= 2^31 - 256, a width or stride above 2^22, rows x
  * d_out past the launch limits, a misaligned pointer.
  */
 GRKAN_API grkan_status_t grkan_linear_act_forward(

@@ -248,3 +248,14 @@ def test_binding_checks_coefficients():
     for bad in (torch.zeros(63), torch.zeros(64, dtype=torch.float64), torch.zeros(128)[::2]):
         with pytest.raises(ValueError):
             block._channel_vector(bad, "weight", 64, dev)
+
+
+@pytest.mark.parametrize("rows", ((1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 256))
+def test_rows_whose_tiles_pass_32_bits_are_refused(lib, rows):
+    """Row numbers of the last tile, 256 past the last row at most, have to fit 32 bits."""
+    one = dict(rows=rows, d_in=1, d_out=1, ldx=1, act=SILU, A=None, B=None)
+    assert lin(lib, **one, r=None) == UNSUPPORTED
+    assert lgrad(lib, **one, lddz=1, dA=None, dB=None) == UNSUPPORTED
+    assert lib.grkan_linear_act_forward_workspace_size(rows, 1, 1, 1, SILU) == 0
+    assert lib.grkan_linear_act_backward_workspace_size(rows, 1, 1, 1, SILU) == 0
+    assert lib.grkan_linear_act_backward_workspace_size((1 << 31) - 257, 1, 1, 1, SILU) > 0
