@@ -240,8 +240,7 @@ bool chunks_aligned(const void *p, int64_t ld, int64_t width) {
 }
 
 __global__ __launch_bounds__(256) void grkan_zero16_kernel(uint16_t *p, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = 0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
 }  // namespace
@@ -339,7 +338,8 @@ extern "C" grkan_status_t grkan_linear_act_backward(const void *x, const void *W
         hipError_t e = hipSuccess;
         if (dW) {
             const int64_t n = d_out * d_in;
-            hipLaunchKernelGGL(grkan_zero16_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, stream,
+            const int64_t blocks = ceil_div(n, 256);
+            hipLaunchKernelGGL(grkan_zero16_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0, stream,
                                static_cast<uint16_t *>(dW), n);
             e = hipGetLastError();
         }

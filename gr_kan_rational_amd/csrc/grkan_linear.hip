@@ -964,14 +964,13 @@ __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel
 // workgroup, then one workgroup per (activation group, coefficient).  5.6 us for
 // 512 rows of 768 columns and 960 coefficient sums: latency.
 template <bool RAT>
-__global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a) {
-    __shared__ double red[1024];
+__device__ static inline void add_columns(const SlopeArgs &a, int b, double *red) {
     const int t = (int)threadIdx.x;
     const int64_t row = a.N + (RAT ? 10 * (int64_t)a.vpr : 0);
     const int colblocks = (a.N + 63) / 64;
     double s = 0.0;
-    if ((int)blockIdx.x < colblocks) {
-        const int c = (int)blockIdx.x * 64 + (t & 63);
+    if (b < colblocks) {
+        const int c = b * 64 + (t & 63);
         if (c < a.N) {
 #pragma unroll 8
             for (int r = t >> 6; r < a.chunks; r += 16) s += (double)a.partials[r * row + c];
@@ -985,7 +984,7 @@ __global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a)
         return;
     }
     if constexpr (RAT) {
-        const int gk = (int)blockIdx.x - colblocks, g = gk / 10, k = gk % 10;
+        const int gk = b - colblocks, g = gk / 10, k = gk % 10;
         const int v0 = g * a.dga / a.vec, w = a.dga / a.vec;
 #pragma unroll 8
         for (int64_t i = t; i < (int64_t)a.chunks * w; i += 1024) {
@@ -1006,6 +1005,14 @@ __global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a)
         }
     }
 }
+template <bool RAT>
+__global__ __launch_bounds__(1024) void grkan_linear_columns_kernel(SlopeArgs a, int total) {
+    __shared__ double red[1024];
+    for (int b = (int)blockIdx.x; b < total; b += (int)gridDim.x) {
+        add_columns<RAT>(a, b, red);
+        __syncthreads();  // the sums in LDS have been read
+    }
+}
 
 }  // namespace
 
@@ -1020,11 +1027,12 @@ hipError_t launch_slope(const SlopeArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((grkan_linear_slope_kernel<1, true>), grid, block, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dbias && !rational)) return e;
-    const dim3 rgrid((unsigned)((a.N + 63) / 64 + (rational ? a.ng * 10 : 0)));
+    const int total = (a.N + 63) / 64 + (rational ? a.ng * 10 : 0);
+    const dim3 rgrid((unsigned)(total < kMaxBlocks ? total : kMaxBlocks));
     if (rational)
-        hipLaunchKernelGGL((grkan_linear_columns_kernel<true>), rgrid, dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((grkan_linear_columns_kernel<true>), rgrid, dim3(1024), 0, s, a, total);
     else
-        hipLaunchKernelGGL((grkan_linear_columns_kernel<false>), rgrid, dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((grkan_linear_columns_kernel<false>), rgrid, dim3(1024), 0, s, a, total);
     return hipGetLastError();
 }
 #endif

@@ -481,6 +481,7 @@ __device__ static inline void add_parts(const NormArgs &a, int64_t ng, double &s
         s0 = red[0][0] + red[0][1] + red[0][2] + red[0][3];
         s1 = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     }
+    __syncthreads();  // the sums in LDS have been read
 }
 
 // Split, few parts: each workgroup of the second pass adds the parts of its
@@ -508,6 +509,10 @@ __device__ static inline void own_parts(const NormArgs &a, const Place &q, int64
     }
     __syncthreads();
 }
+
+// Workgroups of a launch that has one for each (sample, group) while they are
+// not too many.
+unsigned group_blocks(const NormArgs &a) { return (unsigned)(a.N * a.G < kMaxBlocks ? a.N * a.G : kMaxBlocks); }
 
 // Launches KERN with `lds` bytes of dynamic LDS, which may pass the 64 KB a kernel
 // has without asking.
@@ -717,13 +722,14 @@ __global__ __launch_bounds__(1024) void grkan_norm_sums_kernel(NormArgs a) {
 // Split, many parts: a workgroup per (sample, group) adds them (4.1 us for 32
 // groups of 1,024 parts; latency).
 __global__ __launch_bounds__(256) void grkan_norm_stats_kernel(NormArgs a) {
-    const int64_t ng = blockIdx.x;
-    double s0, s1;
-    add_parts(a, ng, s0, s1);
-    if (threadIdx.x == 0) {
-        const float2 st = of_sums(a, s0, s1);
-        a.mean[ng] = st.x;
-        a.rstd[ng] = st.y;
+    for (int64_t ng = blockIdx.x; ng < a.N * a.G; ng += gridDim.x) {
+        double s0, s1;
+        add_parts(a, ng, s0, s1);
+        if (threadIdx.x == 0) {
+            const float2 st = of_sums(a, s0, s1);
+            a.mean[ng] = st.x;
+            a.rstd[ng] = st.y;
+        }
     }
 }
 
@@ -806,7 +812,7 @@ template <int V, int RAT> hipError_t launch_token(const NormArgs &a, hipStream_t
 template <int V, bool RAT, bool MIXED>
 hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
-    const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20))), block((unsigned)p.block);
+    const dim3 grid((unsigned)(p.blocks < kMaxBlocks ? p.blocks : kMaxBlocks)), block((unsigned)p.block);
     if (p.kind == kNormSlab) {
         if (p.regs <= 4) return start<&grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 4>>(a, grid, block, p.lds, s);
         if (p.regs <= 8) return start<&grkan_norm_slab_fwd_kernel<V, RAT, MIXED, 8>>(a, grid, block, p.lds, s);
@@ -814,7 +820,7 @@ hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     }
     hipError_t e = start<&grkan_norm_sums_kernel<V, MIXED>>(a, grid, block, p.lds, s);
     if (e == hipSuccess && !p.fused)
-        e = start<&grkan_norm_stats_kernel>(a, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s);
+        e = start<&grkan_norm_stats_kernel>(a, dim3(group_blocks(a)), dim3(256), 0, s);
     if (e != hipSuccess) return e;
     return start<&grkan_norm_apply_fwd_kernel<V, RAT, MIXED>>(a, grid, block, p.groups * sizeof(float2), s);
 }
@@ -1128,10 +1134,11 @@ __global__ __launch_bounds__(512) void grkan_norm_sums_bwd_kernel(NormArgs a) {
 
 // Split, many parts: <t> and <t xh>, a workgroup per (sample, group).
 __global__ __launch_bounds__(256) void grkan_norm_means_kernel(NormArgs a) {
-    const int64_t ng = blockIdx.x;
-    double s0, s1;
-    add_parts(a, ng, s0, s1);
-    if (threadIdx.x == 0) reinterpret_cast<float2 *>(a.means)[ng] = of_sums(a, s0, s1);
+    for (int64_t ng = blockIdx.x; ng < a.N * a.G; ng += gridDim.x) {
+        double s0, s1;
+        add_parts(a, ng, s0, s1);
+        if (threadIdx.x == 0) reinterpret_cast<float2 *>(a.means)[ng] = of_sums(a, s0, s1);
+    }
 }
 
 // Split, second pass: dx over a row chunk.  The slope is formed again: keeping
@@ -1188,14 +1195,13 @@ __global__ __launch_bounds__(512) void grkan_norm_apply_bwd_kernel(NormArgs a) {
 // coefficient), whose accesses are a contiguous range.  3.9 us for 64 rows of 384
 // columns, 10.5 us for 1,009 rows of 1,536 and 8 x 10 coefficients: latency.
 template <bool RAT>
-__global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
-    __shared__ double red[1024];
+__device__ static inline void add_columns(const NormArgs &a, int64_t b, double *red) {
     const int t = (int)threadIdx.x;
     const NormPlan &p = a.p;
     const int64_t row = p.row, P = p.prows;
     const int64_t colblocks = (2 * (int64_t)a.C + 63) / 64;
-    if ((int64_t)blockIdx.x < colblocks) {
-        const int64_t c = (int64_t)blockIdx.x * 64 + (t & 63);
+    if (b < colblocks) {
+        const int64_t c = b * 64 + (t & 63);
         double s = 0.0;
         if (c < 2 * (int64_t)a.C) {
 #pragma unroll 8
@@ -1214,7 +1220,7 @@ __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
         return;
     }
     if constexpr (RAT) {
-        const int64_t gk = blockIdx.x - colblocks;
+        const int64_t gk = b - colblocks;
         const int g = (int)(gk / 10), k = (int)(gk % 10);
         // The lanes whose first column lies in this group, counted over a row
         // (token: runs of K V columns from each norm group on; else accesses
@@ -1250,10 +1256,21 @@ __global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a) {
     }
 }
 
+template <bool RAT>
+__global__ __launch_bounds__(1024) void grkan_norm_columns_kernel(NormArgs a, int64_t total) {
+    __shared__ double red[1024];
+    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+        add_columns<RAT>(a, b, red);
+        __syncthreads();  // the sums in LDS have been read
+    }
+}
+
 template <bool RAT> hipError_t launch_columns(const NormArgs &a, hipStream_t s) {
     if (!a.dw && !a.db && !RAT) return hipSuccess;
-    const dim3 grid((unsigned)((2 * (int64_t)a.C + 63) / 64 + (RAT ? (int64_t)a.ng * 10 : 0)));
-    return start<&grkan_norm_columns_kernel<RAT>>(a, grid, dim3(1024), 0, s);
+    const int64_t total = (2 * (int64_t)a.C + 63) / 64 + (RAT ? (int64_t)a.ng * 10 : 0);
+    hipLaunchKernelGGL(grkan_norm_columns_kernel<RAT>, dim3((unsigned)(total < kMaxBlocks ? total : kMaxBlocks)), dim3(1024),
+                       0, s, a, total);
+    return hipGetLastError();
 }
 
 template <int V, int RAT, int K> hipError_t launch_token_k(const NormArgs &a, hipStream_t s) {
@@ -1279,7 +1296,7 @@ template <int V, int RAT> hipError_t launch_token(const NormArgs &a, hipStream_t
 template <int V, bool RAT, bool MIXED>
 hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     const NormPlan &p = a.p;
-    const dim3 grid((unsigned)(p.blocks < (1 << 20) ? p.blocks : (1 << 20))), block((unsigned)p.block);
+    const dim3 grid((unsigned)(p.blocks < kMaxBlocks ? p.blocks : kMaxBlocks)), block((unsigned)p.block);
     hipError_t e;
     if (p.kind == kNormSlab) {
         if (p.regs <= 3)
@@ -1291,7 +1308,7 @@ hipError_t launch_blocks(const NormArgs &a, hipStream_t s) {
     } else {
         e = start<&grkan_norm_sums_bwd_kernel<V, RAT, MIXED>>(a, grid, block, p.lds, s);
         if (e == hipSuccess && !p.fused)
-            e = start<&grkan_norm_means_kernel>(a, dim3((unsigned)(a.N * a.G)), dim3(256), 0, s);
+            e = start<&grkan_norm_means_kernel>(a, dim3(group_blocks(a)), dim3(256), 0, s);
         if (e == hipSuccess)
             e = start<&grkan_norm_apply_bwd_kernel<V, RAT, MIXED>>(a, grid, block, p.groups * sizeof(float2), s);
     }

@@ -27,6 +27,10 @@ inline int pow2_at_most(int64_t v) {
     return p;
 }
 
+// Most workgroups of a launch whose kernel walks over what is left: a launch has
+// to stay below 2^32 threads, 1,024 a workgroup.
+constexpr int64_t kMaxBlocks = 1 << 20;
+
 // ------------------------------------------------------------ norm plans
 
 // How a (sample, group)'s positions x D values are covered.
@@ -431,9 +435,9 @@ inline grkan_status_t linear_shape(int64_t rows, int64_t d_in, int64_t d_out, in
     if (!act_valid(act) || rows < 0 || d_in < 1 || d_out < 1) return GRKAN_ERR_INVALID_ARG;
     if (act == GRKAN_ACT_RATIONAL && (n_groups < 1 || d_out % n_groups != 0)) return GRKAN_ERR_INVALID_ARG;
     if (rows > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
-    // one thread per 8 elements of a result, one launch
-    if (rows * ceil_div(d_out, 8) >= (int64_t(1) << 32) || rows * ceil_div(d_in, 8) >= (int64_t(1) << 32) ||
-        d_in * ceil_div(d_out, 8) >= (int64_t(1) << 32))
+    // one thread per 8 elements of a result, in workgroups of 256, one launch
+    const int64_t most = (int64_t(1) << 32) - 256;
+    if (rows * ceil_div(d_out, 8) >= most || rows * ceil_div(d_in, 8) >= most || d_out * ceil_div(d_in, 8) >= most)
         return GRKAN_ERR_UNSUPPORTED;
     return GRKAN_OK;
 }
