@@ -878,8 +878,8 @@ namespace {
 // sums stay in registers over a workgroup's rows.  dpre is rounded to bf16, the
 // matrix cores' operand type for dx and dW (their relative error 0.0023 in place
 // of 0.0017 with fp32 dpre); dbias, dA and dB are summed from the fp32 values.
-// 50,432 x 768, silu: 46 us, 5.0 TB/s, memory.  25,216 x 768, the rational: 34 us,
-// 3.4 TB/s, its 56 instructions an element.
+// 50,432 x 768, silu: 48 us (43 the fastest), 4.8 TB/s, memory.  25,216 x 768, the
+// rational: 35.5 us, 3.3 TB/s, its 58 instructions an element.
 template <int V, bool RAT>
 __global__ __launch_bounds__(kSlopeTx * kSlopeTy) void grkan_linear_slope_kernel(SlopeArgs a) {
     __shared__ float red[kSlopeTy][kSlopeTx * V + 1];

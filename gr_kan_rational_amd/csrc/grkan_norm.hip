@@ -869,11 +869,14 @@ __device__ static inline void store_col_sums(const NormArgs &a, const ColSums<V,
 
 // Token backward: dh and xh of a lane's run in registers, two sums over the
 // group, dx; column and coefficient sums stay in registers over all the
-// samples a workgroup walks over.  201,728 x 768, bf16, the rational: 296 us and
-// 10 for the columns, 3.0 TB/s of 5.0; its 64 instructions an element keep the
-// vector units busy 0.94 of the time, which bounds it.
+// samples a workgroup walks over.  201,728 x 768, bf16, the rational: 306 us a
+// call in a long series, 10 of them the columns', 3.1 TB/s (ten calls from idle,
+// traced: 322 us the fastest, 379 the median); its 64 instructions an element keep
+// the vector units busy 0.94 of the time, which bounds it.
 // The second bound keeps two or three waves on a SIMD: left alone, the compiler
-// evaluates all of a lane's elements side by side, in 270 registers for 12.
+// evaluates all of a lane's elements side by side, in 270 registers for 12.  (The
+// 20 bytes of scratch at K V = 12 are two values put away before the walk and
+// taken back after it; the walk itself touches none.)
 template <int V, int RAT, int K>
 __global__ __launch_bounds__(K * V == 1 ? 1024 : 256, K * V == 1 ? 1 : (RAT == 2 || K * V > 12 ? 2 : 3)) void
 grkan_norm_token_bwd_kernel(NormArgs a) {
@@ -980,7 +983,7 @@ grkan_norm_token_bwd_kernel(NormArgs a) {
 }
 
 // Slab backward: x, dy and dh of a sample's groups in registers, so that x and
-// dy are read once.  128 x 197 x 192 in 8 groups, fp32, gelu: 22 us for 58 MB (2.6
+// dy are read once.  128 x 197 x 192 in 8 groups, fp32, gelu: 23.6 us for 58 MB (2.5
 // TB/s; two samples a workgroup, the loads and the sums of the first exposed);
 // 1,024 samples: 132 us, 3.5 TB/s.
 template <int V, bool RAT, bool MIXED, int R>

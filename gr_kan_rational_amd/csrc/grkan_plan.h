@@ -339,8 +339,9 @@ inline ProductPlan plan_product(int form, int64_t M, int64_t N, int64_t K, bool 
     // 75 us with 7, 16, 24; of 1,003 rows from 768 in tiles of 64: 7.8, 15 us with 1
     // and 2).  The operands reach the XCDs at about 10 TB/s, once or to each of
     // the 8 as the tiles' order has it (768 x 192 from 25,216: 33 us in 7 splits,
-    // all of both to each; 25 us in 16, each k range to one).  No sum runs over
-    // more than 16,384 values of k in fp32.
+    // all of both to each; 25 us in 16, each k range to one).  No sum of a tile
+    // runs over more than 16,384 values of k in fp32 (the few-row kernel's run over
+    // an eighth of K each, whatever it is).
     static const double kAlone[] = {1.5, 0.4, 0.33}, kFull[] = {1.65, 1.2, 0.75}, kTail[] = {7.0, 2.0, 0.5};
     static const int64_t kPlaces[] = {256, 768, 768};
     auto tiles_us = [&](int i, int64_t wgs, int64_t steps) {

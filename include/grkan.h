@@ -331,7 +331,8 @@ GRKAN_API size_t grkan_layer_forward_workspace_size(int64_t rows, int64_t d_in, 
  * The same linear map without the activation: z = y W^T, bf16 y [rows][d_in]
  * (16-byte aligned), W and z as above, the same matrix-core kernel and
  * limits.  With y = grkan_forward(x) (bf16) it is the unfused form of
- * grkan_layer_forward and gives the same bits.
+ * grkan_layer_forward and gives the same bits; for a linear map on its own see
+ * grkan_linear_act_forward (grkan_block.h).
  */
 GRKAN_API grkan_status_t grkan_linear_forward(const void *y, const void *W, void *z, int64_t rows,
                                     int64_t d_in, int64_t d_out, hipStream_t stream);

@@ -140,6 +140,12 @@ GRKAN_API size_t grkan_group_norm_backward_workspace_size(
  *   A, B      with GRKAN_ACT_RATIONAL, channel groups of d_out / n_groups.
  *   rows >= 0 (0 is a no-op), d_in, d_out >= 1; any sizes, strides and element
  *   alignment are served, whole 16-byte vectors in both widths fastest.
+ *
+ * Without bias, activation and residual this is grkan_linear_forward (grkan.h)
+ * for any shape; new callers take this one, which is the faster of the two but at
+ * the largest products (1 x 3,072 from 768: 9 us a call against 22; 197 x 768 from
+ * 3,072: 13 against 69; 50,432 x 768 from 3,072: 252 against 256; 201,728 x 3,072
+ * from 768: 1,096 against 1,025).  Its sums are taken in another order.
  *   workspace grkan_linear_act_forward_workspace_size() bytes (may be 0),
  *             256-byte aligned; enough for any strides and alignment.
  * GRKAN_ERR_UNSUPPORTED: rows >= 2^31 - 256, a width or stride above 2^22, rows x
@@ -161,8 +167,8 @@ GRKAN_API size_t grkan_linear_act_forward_workspace_size(int64_t rows, int64_t d
  *     dx   = dpre W           bf16 [rows][d_in]
  *     dW   = dpre^T x         bf16 [d_out][d_in]
  *     dbias = sum of dpre     fp32 [d_out], from dpre before its rounding
- *     dA, dB                  as grkan_backward's, at pre (its sign decision
- *                             for Q included)
+ *     dA, dB                  as grkan_backward's, at pre (Q in fp64 and the
+ *                             decision of its sign included)
  *
  * and dL/dresidual is dz.  dpre is rounded to bf16 as the operand of the
  * matrix cores; that error is relative to each term, as that of any bf16
