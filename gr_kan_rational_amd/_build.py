@@ -51,6 +51,12 @@ def units() -> list[tuple[str, list[str], str]]:
         for backward in (0, 1):
             out.append(("grkan_norm.hip", [f"-DGRKAN_NORM_BF16={bf16}", f"-DGRKAN_NORM_BACKWARD={backward}"],
                         f"grkan_norm_{bf16}_{backward}.o"))
+    out += [("grkan_train_api.hip", [], "grkan_train_api.o"), ("grkan_quantize.hip", [], "grkan_quantize.o"),
+            ("grkan_product8.hip", [], "grkan_product8.o"), ("grkan_adamw.hip", [], "grkan_adamw.o")]
+    for bf16 in (0, 1):
+        for backward in (0, 1):
+            out.append(("grkan_residual.hip", [f"-DGRKAN_RESIDUAL_BF16={bf16}", f"-DGRKAN_RESIDUAL_BACKWARD={backward}"],
+                        f"grkan_residual_{bf16}_{backward}.o"))
     for al in (0, 1):
         out.append(("grkan_linear.hip", [f"-DGRKAN_LINEAR_ALIGNED={al}"], f"grkan_linear_{al}.o"))
     for m, n in degree_pairs():

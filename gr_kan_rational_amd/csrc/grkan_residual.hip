@@ -1,0 +1,408 @@
+// grkan_residual.hip -- h = x + scale gate post(f), z = norm(h), and the
+// backward (gfx950).
+//
+// Compiled per I/O type (GRKAN_RESIDUAL_BF16) and direction
+// (GRKAN_RESIDUAL_BACKWARD).
+//
+// Bound: memory.  A row is held in registers by one wave (up to 1,024
+// channels), 4 waves or 16, so each tensor is read or written once; the sums of
+// a row stay inside the wave or meet in LDS.
+#include "grkan_residual.h"
+
+#include "grkan_lanes.h"
+
+#ifndef GRKAN_RESIDUAL_BF16
+#error "GRKAN_RESIDUAL_BF16"
+#endif
+
+namespace grkan {
+namespace {
+
+#if GRKAN_RESIDUAL_BF16
+typedef uint16_t io_t;
+#else
+typedef float io_t;
+#endif
+
+// The columns of a lane: 4 from 4 (lane + 64 W k), k < K, over the W waves of a row.
+template <int W, int K> struct Columns {
+    int first, C;
+    __device__ inline Columns(int lane_of_row, int C_) : first(4 * lane_of_row), C(C_) {}
+    __device__ inline int at(int k) const { return first + 256 * W * k; }
+    __device__ inline int nv(int k) const { return min(C - at(k), 4); }  // at most 0: none
+};
+
+// Sums of N values over the W waves of a row, the same bits in every lane.
+template <int W, int N> __device__ static inline void row_sum(float (&v)[N], float (*red)[8], int wave) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = sum64(v[i]);
+    if constexpr (W > 1) {
+        __syncthreads();  // the sums before these have been read
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[wave][i] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) v[i] += red[w][i];
+        }
+    }
+}
+
+// A vector of one value per channel, or `none` for each.
+template <bool VEC> __device__ static inline f32x4 vector4(const float *p, int at, int nv, float none) {
+    return p ? load4<VEC>(p + at, nv) : f32x4{none, none, none, none};
+}
+
+template <bool VEC> __device__ static inline f32x4 gate4(const ResidualArgs &a, int64_t row, int at, int nv) {
+    if (!a.gate) return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+    const int64_t g = row / a.gate_rows;
+    if (a.gate_wide) {
+        if (a.gate_bf16) return load4<VEC>(static_cast<const uint16_t *>(a.gate) + g * a.C + at, nv);
+        return load4<VEC>(static_cast<const float *>(a.gate) + g * a.C + at, nv);
+    }
+    const float v = a.gate_bf16 ? load1(static_cast<const uint16_t *>(a.gate) + g) : static_cast<const float *>(a.gate)[g];
+    return f32x4{v, v, v, v};
+}
+
+// mean and 1 / sqrt(var + eps) of a row held as v (zeros past its columns).
+template <int W, int K>
+__device__ static inline void moments(const f32x4 (&v)[K], const Columns<W, K> &c, int kind, float eps, float (*red)[8],
+                                      int wave, float &mean, float &rstd) {
+    const float inv = 1.0f / (float)c.C;
+    float s[1] = {0.0f};
+    mean = 0.0f;
+    if (kind == GRKAN_NORM_LAYER) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) s[0] += (v[k][0] + v[k][1]) + (v[k][2] + v[k][3]);
+        row_sum<W>(s, red, wave);
+        mean = s[0] * inv;
+    }
+    s[0] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d = e < c.nv(k) ? v[k][e] - mean : 0.0f;
+            s[0] = fmaf(d, d, s[0]);
+        }
+    row_sum<W>(s, red, wave);
+    rstd = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+}
+
+#if !GRKAN_RESIDUAL_BACKWARD
+
+template <int W, int K, bool VEC>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_kernel(ResidualArgs a) {
+    __shared__ float red[W][8];
+    const int wave = (int)threadIdx.x >> 6;
+    const Columns<W, K> c(W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x, a.C);
+    const int per = W == 1 ? 4 : 1;
+    for (int64_t r = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * per) {
+        f32x4 h[K], u[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            h[k] = load4<VEC>(static_cast<const io_t *>(a.x) + r * a.ldx + c.at(k), c.nv(k));
+            u[k] = load4<VEC>(static_cast<const io_t *>(a.f) + r * a.ldf + c.at(k), c.nv(k));
+        }
+        float mean, rstd;
+        if (a.post != GRKAN_NORM_NONE) {
+            moments<W, K>(u, c, a.post, a.eps, red, wave, mean, rstd);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                u[k] = (u[k] - mean) * rstd * vector4<VEC>(a.post_weight, c.at(k), c.nv(k), 1.0f) +
+                       vector4<VEC>(a.post_bias, c.at(k), c.nv(k), 0.0f);
+            if (c.first == 0) {
+                a.stats[2 * a.rows + r] = mean;
+                a.stats[3 * a.rows + r] = rstd;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const f32x4 s = vector4<VEC>(a.scale, c.at(k), c.nv(k), 1.0f) * gate4<VEC>(a, r, c.at(k), c.nv(k));
+            h[k] += s * u[k];
+            store4<VEC>(static_cast<io_t *>(a.h) + r * a.C + c.at(k), c.nv(k), h[k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[k][e] = e < c.nv(k) ? h[k][e] : 0.0f;
+        }
+        moments<W, K>(h, c, a.norm, a.eps, red, wave, mean, rstd);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            store4<VEC>(static_cast<io_t *>(a.z) + r * a.C + c.at(k), c.nv(k),
+                        (h[k] - mean) * rstd * vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f) +
+                            vector4<VEC>(a.bias, c.at(k), c.nv(k), 0.0f));
+        if (c.first == 0) {
+            a.stats[r] = mean;
+            a.stats[a.rows + r] = rstd;
+        }
+    }
+}
+
+template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
+    if (a.vec)
+        hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+#else
+
+// Rows one after another; the column sums of dweight, dbias, dscale (and the
+// post norm's) stay in registers, meet in LDS where a workgroup's waves hold
+// different rows, and leave as one row of partials per workgroup.
+template <int W, int K, bool VEC, bool POST>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward_kernel(ResidualArgs a) {
+    constexpr int S = POST ? 5 : 3;
+    __shared__ float red[W][8];
+    __shared__ f32x4 meet[W == 1 ? 4 : 1][W == 1 ? 64 : 1];
+    const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+    const Columns<W, K> c(W == 1 ? lane : (int)threadIdx.x, a.C);
+    const float inv = 1.0f / (float)a.C;
+    const int per = W == 1 ? 4 : 1;
+    const int64_t walkers = (int64_t)gridDim.x * per;
+    const bool layer = a.norm == GRKAN_NORM_LAYER, post_layer = a.post == GRKAN_NORM_LAYER;
+    const bool by_unit = a.gate && a.gate_wide && a.gate_rows > 1 && a.dgate;
+    f32x4 sum[S][K], gsum[K];
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) sum[i][k] = f32x4{};
+    for (int64_t unit = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0); unit < a.p.units; unit += walkers) {
+        const int64_t run = unit / a.p.units_per_gate, part = unit - run * a.p.units_per_gate;
+        const int64_t run_rows = a.rows / (a.p.units / a.p.units_per_gate);
+        const int64_t r0 = run * run_rows + part * a.p.unit_rows;
+        const int64_t r1 = min(r0 + a.p.unit_rows, (run + 1) * run_rows);
+#pragma unroll
+        for (int k = 0; k < K; ++k) gsum[k] = f32x4{};
+        for (int64_t r = r0; r < r1; ++r) {
+            f32x4 g[K], u[K], t[K], xh[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                xh[k] = load4<VEC>(static_cast<const io_t *>(a.h) + r * a.C + c.at(k), c.nv(k));
+                u[k] = load4<VEC>(static_cast<const io_t *>(a.f) + r * a.ldf + c.at(k), c.nv(k));
+                g[k] = a.dh ? load4<VEC>(static_cast<const io_t *>(a.dh) + r * a.lddh + c.at(k), c.nv(k)) : f32x4{};
+                t[k] = a.dz ? load4<VEC>(static_cast<const io_t *>(a.dz) + r * a.lddz + c.at(k), c.nv(k)) : f32x4{};
+            }
+            const float mean = a.stats[r], rstd = a.stats[a.rows + r];
+            float m[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) xh[k][e] = e < c.nv(k) ? (xh[k][e] - mean) * rstd : 0.0f;
+                sum[0][k] += t[k] * xh[k];
+                sum[1][k] += t[k];
+                t[k] *= vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    m[0] += t[k][e];
+                    m[1] = fmaf(t[k][e], xh[k][e], m[1]);
+                }
+            }
+            row_sum<W>(m, red, wave);
+            const float m0 = layer ? m[0] * inv : 0.0f, m1 = m[1] * inv;
+            float q[3] = {0.0f, 0.0f, 0.0f};
+            float pmean = 0.0f, prstd = 0.0f;
+            if constexpr (POST) {
+                pmean = a.stats[2 * a.rows + r];
+                prstd = a.stats[3 * a.rows + r];
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int at = c.at(k), nv = c.nv(k);
+                g[k] += rstd * (t[k] - m0 - xh[k] * m1);
+                if (a.dx) store4<VEC>(static_cast<io_t *>(a.dx) + r * a.C + at, nv, g[k]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[k][e] = e < nv ? g[k][e] : 0.0f;
+                f32x4 fh = u[k];
+                if constexpr (POST) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fh[e] = e < nv ? (fh[e] - pmean) * prstd : 0.0f;
+                    u[k] = fh * vector4<VEC>(a.post_weight, at, nv, 1.0f) + vector4<VEC>(a.post_bias, at, nv, 0.0f);
+                }
+                const f32x4 s = vector4<VEC>(a.scale, at, nv, 1.0f), gt = gate4<VEC>(a, r, at, nv);
+                const f32x4 gu = g[k] * u[k], gs = gu * s;
+                sum[2][k] += gu * gt;
+                if (a.dgate) {
+                    if (!a.gate_wide) {
+                        q[2] += (gs[0] + gs[1]) + (gs[2] + gs[3]);
+                    } else if (by_unit) {
+                        gsum[k] += gs;
+                    } else if (a.gate_bf16) {
+                        store4<VEC>(static_cast<uint16_t *>(a.dgate) + r * a.C + at, nv, gs);
+                    } else {
+                        store4<VEC>(static_cast<float *>(a.dgate) + r * a.C + at, nv, gs);
+                    }
+                }
+                f32x4 d = g[k] * (s * gt);
+                if constexpr (POST) {
+                    sum[3][k] += d * fh;
+                    sum[4][k] += d;
+                    d *= vector4<VEC>(a.post_weight, at, nv, 1.0f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        q[0] += d[e];
+                        q[1] = fmaf(d[e], fh[e], q[1]);
+                    }
+                    xh[k] = fh;
+                    t[k] = d;
+                } else if (a.df) {
+                    store4<VEC>(static_cast<io_t *>(a.df) + r * a.C + at, nv, d);
+                }
+            }
+            if (POST || (a.dgate && !a.gate_wide)) row_sum<W>(q, red, wave);
+            if (a.dgate && !a.gate_wide && c.first == 0) {
+                if (a.gate_rows > 1)
+                    a.gate_sums[r] = q[2];
+                else if (a.gate_bf16)
+                    store1(static_cast<uint16_t *>(a.dgate) + r, q[2]);
+                else
+                    static_cast<float *>(a.dgate)[r] = q[2];
+            }
+            if constexpr (POST) {
+                const float q0 = post_layer ? q[0] * inv : 0.0f, q1 = q[1] * inv;
+                if (a.df) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        store4<VEC>(static_cast<io_t *>(a.df) + r * a.C + c.at(k), c.nv(k),
+                                    prstd * (t[k] - q0 - xh[k] * q1));
+                }
+            }
+        }
+        if (by_unit) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (a.p.units_per_gate > 1)
+                    store4<VEC>(a.gate_sums + unit * a.C + c.at(k), c.nv(k), gsum[k]);
+                else if (a.gate_bf16)
+                    store4<VEC>(static_cast<uint16_t *>(a.dgate) + run * a.C + c.at(k), c.nv(k), gsum[k]);
+                else
+                    store4<VEC>(static_cast<float *>(a.dgate) + run * a.C + c.at(k), c.nv(k), gsum[k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float *to = a.sums + ((int64_t)blockIdx.x * S + i) * a.C + c.at(k);
+            if constexpr (W == 1) {
+                __syncthreads();
+                meet[wave][lane] = sum[i][k];
+                __syncthreads();
+                if (wave == 0) {
+                    f32x4 v = sum[i][k];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) v += meet[w][lane];
+                    store4<VEC>(to, c.nv(k), v);
+                }
+            } else {
+                store4<VEC>(to, c.nv(k), sum[i][k]);
+            }
+        }
+}
+
+// The workgroups' partials of each column in order of the workgroups, in fp64: 64
+// columns x 16 lanes of workgroups.
+__global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a) {
+    __shared__ double red[1024];
+    const int t = (int)threadIdx.x, cb = (a.C + 63) / 64;
+    const int i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 64 + (t & 63);
+    float *const outs[5] = {a.dweight, a.dbias, a.dscale, a.dpost_weight, a.dpost_bias};
+    float *out = outs[i];
+    if (!out) return;
+    double s = 0.0;
+    if (col < a.C) {
+        const float *p = a.sums + (int64_t)i * a.C + col;
+#pragma unroll 4
+        for (int64_t b = t >> 6; b < a.p.blocks; b += 16) s += (double)p[b * a.p.sums * a.C];
+    }
+    red[t] = s;
+    __syncthreads();
+    if (t < 64 && col < a.C) {
+        for (int q = 1; q < 16; ++q) s += red[t + 64 * q];
+        out[col] = (float)s;
+    }
+}
+
+// dgate of each (gate, channel) from its units, or of each gate from its rows, in order.
+__global__ __launch_bounds__(256) void grkan_residual_gates_kernel(ResidualArgs a, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    double s = 0.0;
+    if (a.gate_wide) {
+        const int64_t g = i / a.C, col = i - g * a.C;
+        for (int64_t k = 0; k < a.p.units_per_gate; ++k) s += (double)a.gate_sums[(g * a.p.units_per_gate + k) * a.C + col];
+    } else {
+        for (int64_t k = 0; k < a.gate_rows; ++k) s += (double)a.gate_sums[i * a.gate_rows + k];
+    }
+    if (a.gate_bf16)
+        store1(static_cast<uint16_t *>(a.dgate) + i, (float)s);
+    else
+        static_cast<float *>(a.dgate)[i] = (float)s;
+}
+
+template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
+    if (a.post != GRKAN_NORM_NONE) {
+        if (a.vec)
+            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, true, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, false, true>), grid, block, 0, s, a);
+    } else {
+        if (a.vec)
+            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, true, false>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, false, false>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+#endif
+
+template <int W> hipError_t launch_waves(const ResidualArgs &a, hipStream_t s) {
+    switch (a.p.K) {
+        case 1: return launch_kernel<W, 1>(a, s);
+        case 2: return launch_kernel<W, 2>(a, s);
+        case 3: return launch_kernel<W, 3>(a, s);
+        case 4: return launch_kernel<W, 4>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_rows(const ResidualArgs &a, hipStream_t s) {
+    switch (a.p.waves) {
+        case 1: return launch_waves<1>(a, s);
+        case 4: return launch_waves<4>(a, s);
+        default: return launch_waves<16>(a, s);
+    }
+}
+
+}  // namespace
+
+#if !GRKAN_RESIDUAL_BACKWARD
+template <> hipError_t launch_residual_forward<io_t>(const ResidualArgs &a, hipStream_t s) { return launch_rows(a, s); }
+#else
+template <> hipError_t launch_residual_backward<io_t>(const ResidualArgs &a, hipStream_t s) {
+    hipError_t e = launch_rows(a, s);
+    if (e != hipSuccess) return e;
+    if (a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias) {
+        const unsigned grid = (unsigned)(a.p.sums * ((a.C + 63) / 64));
+        hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3(grid), dim3(1024), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const bool by_unit = a.gate_wide && a.p.units_per_gate > 1;
+    if (a.dgate && a.gate_rows > 1 && (by_unit || !a.gate_wide)) {
+        const int64_t n = a.rows / a.gate_rows * (a.gate_wide ? a.C : 1);
+        hipLaunchKernelGGL(grkan_residual_gates_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, n);
+        e = hipGetLastError();
+    }
+    return e;
+}
+#endif
+
+}  // namespace grkan
