@@ -12,6 +12,8 @@
 #include "grkan_fp8.h"
 #include "grkan_lanes.h"
 
+#include <type_traits>
+
 namespace grkan {
 namespace {
 
@@ -56,69 +58,546 @@ template <class T> __device__ static inline f32x4 block_product(i32x8 a, i32x8 b
     return c;
 }
 
-// 64 x 64 of the result to a workgroup of 2 x 2 waves, a block of k at a time.
-// The instruction's row operand is b and its column operand a, so a lane holds
-// row lane mod 16 of the result and 4 columns from 4 (lane / 16).
-template <class T>
-__global__ __launch_bounds__(256) void grkan_product8_kernel(Product8Args a) {
-    __shared__ __attribute__((aligned(16))) uint8_t sa[64][kBlock8], sb[64][kBlock8];
-    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int nb = (a.N + 63) / 64, n0 = (int)blockIdx.x % nb * 64, m0 = (int)blockIdx.x / nb * 64;
-    const int mw = wave / 2 * 32, nw = wave % 2 * 32;
-    f32x4 acc[2][2] = {};
-    for (int k0 = 0, kb = 0; k0 < a.K; k0 += kBlock8, ++kb) {
+// ------------------------------------------------------------ tile kernel
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer: reads zeros
+
+// 16 (or 4) bytes per lane from offset `off` of the buffer to LDS, lane after
+// lane from `to` (the same in all lanes; taken from M0).  Written as instructions
+// because they have no result; arrival is waited for by count.  M0 is the
+// compiler's to use nowhere else in these kernels.
+__device__ static inline uint32_t lds_address(const char *to) {
+    return (uint32_t)__builtin_amdgcn_readfirstlane(
+        (int)(uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)to));
+}
+__device__ static inline void fetch16(u32x4 rsrc, uint32_t off, const char *to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds_address(to)), "v"(off), "s"(rsrc) : "memory");
+}
+__device__ static inline void fetch4(u32x4 rsrc, uint32_t off, const char *to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(lds_address(to)), "v"(off), "s"(rsrc) : "memory");
+}
+__device__ static inline u32x4 resource(const void *p, uint32_t bytes) {
+    const uint64_t addr = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)addr),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(addr >> 32)) & 0xffffu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+// s_waitcnt vmcnt(0), lgkmcnt(0), and lgkmcnt(0) alone.
+__device__ static inline void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070); }
+__device__ static inline void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
+__device__ static inline void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Nothing moves across: the compiler would gather the fragments' reads early, in
+// registers that there are not.
+__device__ static inline void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// The chunk (16 bytes) c of a row of 128 bytes sits at c ^ swizzle(row): 8
+// consecutive rows of one chunk column cover 128 bytes of banks and 16 cover 256.
+__device__ static inline int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+// An operand's rows of a tile: ROWS x 128 codes by threads of 16 bytes.  Rows past
+// the end lie past the buffer's (they read zeros).
+template <int ROWS, int T> struct Codes {
+    static constexpr int kChunks = ROWS * 8 / T;
+    static_assert(ROWS * 8 % T == 0 && T / 8 % 16 == 0, "whole chunks, one swizzle a thread");
+    const uint8_t *base;
+    uint32_t bytes;      // from base to the end of the last row
+    uint32_t off;        // of this thread's first chunk; the next lie `step` apart
+    int step;
+    __device__ inline void init(const Operand8 &o, int row0, int rows, int kstart) {
+        const int r0 = (int)threadIdx.x / 8;
+        base = o.p + (int64_t)row0 * o.ld + kstart;
+        bytes = (uint32_t)(min(rows - row0, ROWS) * o.ld - kstart);
+        off = (uint32_t)(r0 * o.ld + first());
+        step = (int)(T / 8 * o.ld);
+    }
+    // k of this thread's chunks
+    __device__ static inline int first() { return (((int)threadIdx.x & 7) ^ swizzle((int)threadIdx.x / 8)) * 16; }
+    // The chunks of step t, `left` values of k before its end.
+    __device__ inline void fetch(char *stage, int t, int left) {
+        const u32x4 rsrc = resource(base + (int64_t)t * kBlock8, left > 0 ? bytes - (uint32_t)t * kBlock8 : 0u);
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const uint32_t from = left >= kBlock8 || first() < left ? off : kNowhere;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int id = t + 256 * i, row = id >> 3, c = id & 7, at = (c ^ (row & 7)) * 16, k = k0 + 16 * c;
-            const int nv = min(a.K - k, 16);
-            *reinterpret_cast<u32x4 *>(&sa[row][at]) = chunk16(a.a.p + (int64_t)(m0 + row) * a.a.ld + k, m0 + row < a.M ? nv : 0);
-            *reinterpret_cast<u32x4 *>(&sb[row][at]) = chunk16(a.b.p + (int64_t)(n0 + row) * a.b.ld + k, n0 + row < a.N ? nv : 0);
+        for (int i = 0; i < kChunks; ++i) fetch16(rsrc, from + (uint32_t)(i * step), stage + (i * T + wave * 64) * 16);
+    }
+};
+
+template <int BM, int BN> struct Tile8 {
+    static constexpr int kWavesM = 2, kWavesN = BN == 256 ? 4 : 2, kThreads = kWavesM * kWavesN * 64;
+    static constexpr int WM = BM / kWavesM, WN = BN / kWavesN, NM = WM / 16, NN = WN / 16;
+    // codes of a, of b, then a scale a thread: BM of a's, BN of b's
+    static constexpr int kScales = (BM + BN) * kBlock8;
+    static constexpr int kStage = kScales + kThreads * 4;
+    static constexpr size_t kLds = 2 * (size_t)kStage;
+    static_assert(BM + BN <= kThreads && BM % 64 == 0, "a scale a thread, one operand's a wave");
+};
+
+// A block of k at a time through two LDS stages.  T: the result's type.
+template <int BM, int BN, class T, bool BTILE, bool PARTIAL>
+__global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_tile_kernel(Product8Args a) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    using Shape = Tile8<BM, BN>;
+    constexpr int TH = Shape::kThreads, WM = Shape::WM, WN = Shape::WN, NM = Shape::NM, NN = Shape::NN;
+    constexpr int kStage = Shape::kStage, kB = BM * kBlock8, kScales = Shape::kScales;
+    const int nb = (a.N + BN - 1) / BN, mb = (a.M + BM - 1) / BM, tiles = mb * nb;
+    const int t = (int)threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int mrow = wave / Shape::kWavesN * WM, ncol = wave % Shape::kWavesN * WN;
+
+    // Tile b of the launch.  Workgroups go to the 8 XCDs in turn, and what an
+    // XCD's workgroups share should stay in its L2, so each XCD takes an eighth
+    // of the tiles (of all splits, those of a split together), its column tiles of
+    // a panel of BM rows one after another.
+    const int all = tiles * (PARTIAL ? a.splits : 1), per = (all + 7) / 8, count = per * 8;
+    int m0, n0, split = 0, kb = 0, len = a.K;
+    auto place = [&](int b) {
+        const int i = (b & 7) * per + (b >> 3), tile = PARTIAL ? i % tiles : i;
+        if constexpr (PARTIAL) {
+            split = i / tiles;
+            kb = split * a.k_split;
+            len = min(a.K - kb, a.k_split);
         }
-        __syncthreads();
-        i32x8 fa[2], fb[2];
+        m0 = tile / nb * BM;
+        n0 = tile % nb * BN;
+    };
+    auto next = [&](int b) {
+        while (b < count && (b & 7) * per + (b >> 3) >= all) b += (int)gridDim.x;
+        return b;
+    };
+
+    // The fetches run a step ahead of the products, on through the tiles of this
+    // workgroup; past the last they read zeros.
+    Codes<BM, TH> ca;
+    Codes<BN, TH> cb;
+    const float *scale_base;
+    uint32_t scale_off;
+    int64_t scale_step;
+    int fetch_tile = next((int)blockIdx.x), fetch_step = 0, fetch_len = 0;
+    if (fetch_tile >= count) return;
+    auto start_tile = [&]() {
+        if (fetch_tile < count) {
+            place(fetch_tile);
+            ca.init(a.a, m0, a.M, kb);
+            cb.init(a.b, n0, a.N, kb);
+            const bool of_a = wave * 64 < BM;   // a wave's scales are one operand's
+            const Operand8 &o = of_a ? a.a : a.b;
+            const int first = of_a ? m0 : n0, i = of_a ? t : t - BM;
+            const bool there = i < (of_a ? BM : BN) && first + i < (of_a ? a.M : a.N);
+            const bool tiled = BTILE && !of_a;
+            const int at = tiled ? (first + i) / kBlock8 - first / kBlock8 : i;
+            scale_base = o.scale + (tiled ? first / kBlock8 : first) * o.srow + kb / kBlock8 * o.sblock;
+            scale_off = there ? (uint32_t)(at * o.srow * 4) : kNowhere;
+            scale_step = o.sblock;
+            fetch_len = len;
+        } else {
+            fetch_len = 0;
+        }
+        fetch_step = 0;
+    };
+    auto fetch = [&](int stage) {
+        const int left = fetch_len - fetch_step * kBlock8;
+        ca.fetch(lds + stage, fetch_step, left);
+        cb.fetch(lds + stage + kB, fetch_step, left);
+        fetch4(resource(scale_base + fetch_step * scale_step, left > 0 ? 0x7ffffff0u : 0u), scale_off,
+               lds + stage + kScales + wave * 256);
+        ++fetch_step;
+        if (fetch_step * kBlock8 >= fetch_len && fetch_tile < count) {
+            fetch_tile = next(fetch_tile + (int)gridDim.x);
+            start_tile();
+        }
+    };
+    // A chunk that reaches past K: what lies there is the caller's, and cleared here.
+    const int ragged = a.K & 15;
+    auto clear_past = [&](int stage) {
+        const int c = (a.K & 127) >> 4;
+        for (int row = t; row < BM + BN; row += TH) {
+            const int r = row < BM ? row : row - BM;
+            u32x4 *p = reinterpret_cast<u32x4 *>(lds + stage + row * kBlock8 + ((c ^ swizzle(r)) << 4));
+            u32x4 v = *p;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            auto read = [&](const uint8_t (*s)[kBlock8], int row) {
-                const i32x4 lo = *reinterpret_cast<const i32x4 *>(&s[row][((2 * (lane >> 4)) ^ (row & 7)) * 16]);
-                const i32x4 hi = *reinterpret_cast<const i32x4 *>(&s[row][((2 * (lane >> 4) + 1) ^ (row & 7)) * 16]);
-                return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            for (int i = 0; i < 4; ++i) {
+                const int left = ragged - 4 * i;
+                v[i] = left <= 0 ? 0u : (left >= 4 ? v[i] : v[i] & ((1u << (8 * (left & 3))) - 1u));
+            }
+            *p = v;
+        }
+        wait_lds();
+        barrier();
+    };
+
+    // Fragments: 32 of the 128 codes of row lane mod 16 to a lane; which 32 does not
+    // matter as long as both operands' lanes hold the same.
+    const int frow = lane & 15, fc = 2 * (lane >> 4);
+    const int f0 = frow * kBlock8 + ((fc ^ swizzle(frow)) << 4), f1 = frow * kBlock8 + (((fc + 1) ^ swizzle(frow)) << 4);
+    auto read = [&](int at) {
+        const i32x4 lo = *reinterpret_cast<const i32x4 *>(lds + at + f0), hi = *reinterpret_cast<const i32x4 *>(lds + at + f1);
+        return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    auto read_a = [&](int stage, int i) { return read(stage + (mrow + 16 * i) * kBlock8); };
+    auto read_b = [&](int stage, int j) { return read(stage + kB + (ncol + 16 * j) * kBlock8); };
+
+    f32x4 acc[NM][NN];
+    // The rows' fragments of a step: X, read during the step before; Y, read at its start,
+    // and once more when multiplied; Z, read at its start.  Z and the second Y are
+    // multiplied after the barrier, while the next step's X and columns are read.
+    constexpr int Y = NM == 8 ? 2 : 0, X = (NM - 2 * Y) / 2, Z = X;
+    static_assert(X + 2 * Y + Z == NM, "all rows");
+    i32x8 fx[X], fy[Y > 0 ? Y : 1], fz[Z], fb[NN];
+    int now = 0;   // the stage of this step
+    start_tile();
+    fetch(0);
+    wait_all();
+    barrier();
+    int tile = next((int)blockIdx.x);
+    place(tile);
+    bool first = true;
+    for (; tile < count; tile = next(tile + (int)gridDim.x)) {
+        place(tile);
+        const int steps = (len + kBlock8 - 1) / kBlock8;
+        const int tm0 = m0, tn0 = n0, tsplit = split;
+        const bool ends = ragged && kb + len == a.K;
+        if (first) {
+            if (ends && steps == 1) clear_past(now);
+            first = false;
+#pragma unroll
+            for (int i = 0; i < X; ++i) fx[i] = read_a(now, i);
+#pragma unroll
+            for (int j = 0; j < NN; ++j) fb[j] = read_b(now, j);
+        }
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+#pragma unroll
+            for (int j = 0; j < NN; ++j) acc[i][j] = f32x4{};
+        for (int st = 0; st < steps; ++st) {
+            const int other = kStage - now;
+            fetch(other);
+            const float *sa = reinterpret_cast<const float *>(lds + now + kScales) + mrow + (lane & 15);
+            const float *sb = reinterpret_cast<const float *>(lds + now + kScales) + BM + ncol + (BTILE ? 0 : 4 * (lane >> 4));
+            f32x4 bs[NN];
+            float as[NM];
+#pragma unroll
+            for (int i = 0; i < Y; ++i) fy[i] = read_a(now, X + i);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) as[i] = sa[16 * i];
+            if constexpr (BTILE) {
+                const float bt = *sb;
+#pragma unroll
+                for (int i = 0; i < NM; ++i) as[i] *= bt;
+            } else {
+#pragma unroll
+                for (int j = 0; j < NN; ++j) bs[j] = *reinterpret_cast<const f32x4 *>(sb + 16 * j);
+            }
+#pragma unroll
+            for (int i = 0; i < Z; ++i) fz[i] = read_a(now, X + Y + i);
+            // Products kAhead of the sums they are added to, so that the matrix unit's
+            // result is there; pinned, or the compiler moves the additions past the
+            // barrier and keeps the products.
+            constexpr int kAhead = 2;
+            f32x4 p[kAhead + 1];
+            auto add = [&](int slot, int i, int j) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    acc[i][j][v] = fmaf(p[slot][v], BTILE ? as[i] : as[i] * bs[j][v], acc[i][j][v]);
+                asm volatile("" : "+v"(acc[i][j]));
             };
-            fa[i] = read(sa, mw + 16 * i + (lane & 15));
-            fb[i] = read(sb, nw + 16 * i + (lane & 15));
+            keep_order();
+            constexpr int kFirst = (X + Y) * NN;
+#pragma unroll
+            for (int q = 0; q < kFirst + kAhead; ++q) {
+                if (q < kFirst) {
+                    const int i = q / NN, j = q % NN;
+                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < X ? fx[i < X ? i : 0] : fy[i < X ? 0 : i - X]);
+                    if (i >= X && j == NN - 1) fy[i - X] = read_a(now, i + Y + Z);
+                }
+                if (q >= kAhead) add((q - kAhead) % (kAhead + 1), (q - kAhead) / NN, (q - kAhead) % NN);
+            }
+            // the next step has arrived, and every wave holds what is left of this one in
+            // registers
+            wait_all();
+            barrier();
+            if (ragged) {
+                // (the next step is this tile's last, or the next tile's only one)
+                const bool here = st + 1 < steps;
+                bool past = here ? ends && st + 2 == steps : false;
+                if (!here) {
+                    const int b = next(tile + (int)gridDim.x);
+                    if (b < count) {
+                        place(b);
+                        past = kb + len == a.K && len <= kBlock8;
+                    }
+                }
+                if (past) clear_past(other);
+            }
+#pragma unroll
+            for (int i = 0; i < X; ++i) fx[i] = read_a(other, i);
+            constexpr int R = Z + Y, kRest = R * NN;
+#pragma unroll
+            for (int q = 0; q < kRest + kAhead; ++q) {
+                if (q < kRest) {
+                    const int j = q / R, i = q % R;
+                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < Z ? fz[i < Z ? i : 0] : fy[i < Z ? 0 : i - Z]);
+                    if (i == R - 1) fb[j] = read_b(other, j);
+                }
+                if (q >= kAhead) add((q - kAhead) % (kAhead + 1), X + Y + (q - kAhead) % R, (q - kAhead) / R);
+            }
+            now = other;
         }
+        // Here `now` holds the next tile's first step (its first fragments are in
+        // registers) and the other stage is free.
+        const int mw = tm0 + mrow + (lane & 15), nw = tn0 + ncol + 4 * (lane >> 4);
+        if constexpr (PARTIAL || sizeof(T) == 4) {
+            // 16 bytes a lane, 64 side by side of a row
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int m = min(m0 + mw + 16 * i + (lane & 15), a.M - 1);
-            const float as = a.a.scale[m * a.a.srow + kb * a.a.sblock];
+            for (int i = 0; i < NM; ++i) {
+                const int m = mw + 16 * i;
+                if (m >= a.M) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const f32x4 p = block_product<T>(fb[j], fa[i]);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = min(n0 + nw + 16 * j + 4 * (lane >> 4) + v, a.N - 1);
-                    const float s = as * a.b.scale[(a.b_tile ? n / kBlock8 : n) * a.b.srow + kb * a.b.sblock];
-                    acc[j][i][v] = fmaf(p[v], s, acc[j][i][v]);
+                for (int j = 0; j < NN; ++j) {
+                    const int n = nw + 16 * j, nv = min(a.N - n, 4);
+                    if (nv <= 0) continue;
+                    f32x4 h = acc[i][j];
+                    float *o;
+                    if constexpr (PARTIAL) {
+                        o = a.partials + ((int64_t)tsplit * a.M + m) * a.N + n;
+                    } else {
+                        o = static_cast<float *>(a.c) + (int64_t)m * a.N + n;
+                        if (a.bias) h += load4<false>(a.bias + n, nv);
+                        if (a.residual) h += load4<false>(static_cast<const float *>(a.residual) + m * a.ldr + n, nv);
+                    }
+                    if (nv == 4)
+                        *reinterpret_cast<f32x4_any *>(o) = h;
+                    else
+                        store4<false>(o, nv, h);
                 }
             }
+        } else {
+            // bf16 results pass through the wave's own corner of the free stage, 16 rows of WN
+            // columns at a time, so that memory sees whole rows.  Chunk c (8 columns) of row r
+            // sits at c ^ (r mod CP).  A residual comes the same way, into the place of its result.
+            constexpr int CP = WN / 8, RP = 64 / CP;
+            static_assert(TH / 64 * 16 * WN * 2 <= kScales, "staging fits");
+            char *own = lds + (kStage - now) + wave * (16 * WN * 2);
+            auto slot = [&](int r, int c) { return own + r * (WN * 2) + ((c ^ (r & (CP - 1))) << 4); };
+            const int row = lane / CP, chunk = lane % CP;
+            const int cn = tn0 + ncol + chunk * 8, cnv = min(max(a.N - cn, 0), 8);
+            auto fence = [] { asm volatile("" ::: "memory"); };  // LDS serves a wave in order
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                const int mh = tm0 + mrow + 16 * i;
+                if (a.residual) {
+#pragma unroll
+                    for (int it = 0; it < 16 / RP; ++it) {
+                        const int r = it * RP + row;
+                        const uint16_t *from = static_cast<const uint16_t *>(a.residual) + (int64_t)(mh + r) * a.ldr + cn;
+                        u32x4 v = {0u, 0u, 0u, 0u};
+                        if (mh + r < a.M) {
+                            if (cnv == 8) {
+                                v = *reinterpret_cast<const u32x4_any *>(from);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (e < cnv) v[e / 2] |= (uint32_t)from[e] << (16 * (e & 1));
+                            }
+                        }
+                        *reinterpret_cast<u32x4 *>(slot(r, chunk)) = v;
+                    }
+                    fence();
+                }
+#pragma unroll
+                for (int j = 0; j < NN; ++j) {
+                    f32x4 h = acc[i][j];
+                    if (a.bias) h += load4<false>(a.bias + nw + 16 * j, min(max(a.N - nw - 16 * j, 0), 4));
+                    char *to = slot(lane & 15, 2 * j + (lane >> 5)) + ((lane >> 4) & 1) * 8;
+                    if (a.residual) {
+                        const u32x2 r = *reinterpret_cast<const u32x2 *>(to);
+                        h += f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
+                                   __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
+                    }
+                    *reinterpret_cast<u32x2 *>(to) = pack4(h);
+                }
+                fence();
+#pragma unroll
+                for (int it = 0; it < 16 / RP; ++it) {
+                    const int r = it * RP + row;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(slot(r, chunk));
+                    if (mh + r >= a.M || cnv <= 0) continue;
+                    uint16_t *to = static_cast<uint16_t *>(a.c) + (int64_t)(mh + r) * a.N + cn;
+                    if (cnv == 8) {
+                        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(to));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < cnv) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                    }
+                }
+                fence();
+            }
+            // the stage goes back to the fetches
+            wait_lds();
+            barrier();
         }
-        __syncthreads();
     }
+    wait_all();  // nothing may still be on its way into LDS when the workgroup ends
+}
+
+// The splits' sums added in order, then bias and residual.
+template <class T> __global__ __launch_bounds__(256) void grkan_product8_finish_kernel(Product8Args a) {
+    const int quads = (a.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)quads * a.M) return;
+    const int64_t m = i / quads, plane = (int64_t)a.M * a.N;
+    const int n = (int)(i - m * quads) * 4, nv = min(a.N - n, 4);
+    const float *p = a.partials + m * a.N + n;
+    f32x4 h = {};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s, p += plane) h += nv == 4 ? *reinterpret_cast<const f32x4_any *>(p) : load4<false>(p, nv);
+    if (a.bias) h += load4<false>(a.bias + n, nv);
+    if (a.residual) h += load4<false>(static_cast<const T *>(a.residual) + m * a.ldr + n, nv);
+    store4<false>(static_cast<T *>(a.c) + m * a.N + n, nv, h);
+}
+
+// ------------------------------------------------------------ few rows
+
+// Few rows of a: a workgroup takes 16 columns of the result (16 rows of b) and
+// 16 MT rows; its waves take the blocks of k in turn, straight from memory into
+// operand registers, the loads of up to kTurns blocks on their way at once.  The
+// waves' sums meet in LDS.  Bound: b's bytes, latency below.
+constexpr int kFewWaves = 8;
+
+template <int MT, class T> __global__ __launch_bounds__(kFewWaves * 64) void grkan_product8_few_kernel(Product8Args a) {
+    constexpr int kTurns = MT == 1 ? 4 : 2;
+    __shared__ float red[kFewWaves][MT * 16][17];
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16 * MT;
+    // rows past the end are the last once more (their results are not stored)
+    const int kl = (lane >> 4) * 32, blocks = (a.K + kBlock8 - 1) / kBlock8;
+    const uint8_t *pb = a.b.p + (int64_t)min(n0 + (lane & 15), a.N - 1) * a.b.ld + kl;
+    const float *sb[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int v = 0; v < 4; ++v) {
+        const int n = min(n0 + 4 * (lane >> 4) + v, a.N - 1);
+        sb[v] = a.b.scale + (a.b_tile ? n / kBlock8 : n) * a.b.srow;
+    }
+    const uint8_t *pa[MT];
+    const float *sa[MT];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int m = m0 + mw + 16 * i + (lane & 15);
-            if (m >= a.M) continue;
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = min(m0 + 16 * i + (lane & 15), a.M - 1);
+        pa[i] = a.a.p + m * a.a.ld + kl;
+        sa[i] = a.a.scale + m * a.a.srow;
+    }
+    f32x4 acc[MT];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int n = n0 + nw + 16 * j + 4 * (lane >> 4) + v;
-                if (n >= a.N) continue;
-                float h = acc[j][i][v];
-                if (a.bias) h += a.bias[n];
-                if (a.residual) h += load1(static_cast<const T *>(a.residual) + m * a.ldr + n);
-                store1(static_cast<T *>(a.c) + (int64_t)m * a.N + n, h);
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{};
+    auto turns = [&](int kb, auto count) {
+        constexpr int U = count();
+        u32x4 b[U][2], x[U][MT][2];
+        f32x4 bs[U];
+        float as[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = (int64_t)(kb + u * kFewWaves) * kBlock8;
+            const int left = (int)min((int64_t)a.K - k - kl, (int64_t)32);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                b[u][h] = chunk16(pb + k + 16 * h, left - 16 * h);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) x[u][i][h] = chunk16(pa[i] + k + 16 * h, left - 16 * h);
+            }
+            const int64_t at = kb + u * kFewWaves;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) bs[u][v] = sb[v][at * a.b.sblock];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) as[u][i] = sa[i][at * a.a.sblock];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            auto whole = [](const u32x4 (&c)[2]) {
+                return i32x8{(int)c[0][0], (int)c[0][1], (int)c[0][2], (int)c[0][3], (int)c[1][0], (int)c[1][1], (int)c[1][2], (int)c[1][3]};
+            };
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const f32x4 p = block_product<T>(whole(b[u]), whole(x[u][i]));
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(p[v], as[u][i] * bs[u][v], acc[i][v]);
             }
         }
+    };
+    int kb = wave;
+    for (; kb + (kTurns - 1) * kFewWaves < blocks; kb += kTurns * kFewWaves) turns(kb, std::integral_constant<int, kTurns>{});
+    for (; kb < blocks; kb += kFewWaves) turns(kb, std::integral_constant<int, 1>{});
+    // lane: row lane mod 16, columns 4 (lane / 16) + v
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[wave][16 * i + (lane & 15)][4 * (lane >> 4) + v] = acc[i][v];
+    __syncthreads();
+    for (int q = t; q < MT * 256; q += kFewWaves * 64) {
+        const int m = q >> 4, c = q & 15, n = n0 + c;
+        if (m0 + m >= a.M || n >= a.N) continue;
+        float h = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) h += red[w][m][c];
+        if (a.bias) h += a.bias[n];
+        if (a.residual) h += load1(static_cast<const T *>(a.residual) + (int64_t)(m0 + m) * a.ldr + n);
+        store1(static_cast<T *>(a.c) + (int64_t)(m0 + m) * a.N + n, h);
+    }
+}
+
+// ------------------------------------------------------------ dispatch
+
+template <int BM, int BN, class T, bool BTILE, bool PARTIAL> hipError_t launch_tile(const Product8Args &a, hipStream_t s) {
+    auto kern = grkan_product8_tile_kernel<BM, BN, T, BTILE, PARTIAL>;
+    using Shape = Tile8<BM, BN>;
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kLds);
+    if (attr != hipSuccess) return attr;
+    const int64_t mb = (a.M + BM - 1) / BM, nb = (a.N + BN - 1) / BN;
+    int64_t grid = (mb * nb * (PARTIAL ? a.splits : 1) + 7) / 8 * 8;
+    // as many workgroups as fit on the 256 CUs at once; each walks over its tiles
+    constexpr int64_t resident = BN == 256 ? 256 : (BN == 128 ? 512 : 1024);
+    if (grid > resident) grid = resident;
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(Shape::kThreads), Shape::kLds, s, a);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, class T> hipError_t launch_kind(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
+    if (p.splits > 1) return a.b_tile ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, false, true>(a, s);
+    return a.b_tile ? launch_tile<BM, BN, T, true, false>(a, s) : launch_tile<BM, BN, T, false, false>(a, s);
+}
+
+template <class T> hipError_t launch_type(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
+    if (p.few > 0) {
+        const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * p.few - 1) / (16 * p.few))), block(kFewWaves * 64);
+        switch (p.few) {
+            case 1: hipLaunchKernelGGL((grkan_product8_few_kernel<1, T>), grid, block, 0, s, a); break;
+            case 2: hipLaunchKernelGGL((grkan_product8_few_kernel<2, T>), grid, block, 0, s, a); break;
+            default: hipLaunchKernelGGL((grkan_product8_few_kernel<4, T>), grid, block, 0, s, a); break;
+        }
+        return hipGetLastError();
+    }
+    hipError_t e;
+    if (p.tile == 256) {
+        if constexpr (sizeof(T) == 2)
+            e = launch_kind<256, 256, T>(p, a, s);
+        else
+            e = hipErrorInvalidValue;
+    } else if (p.tile == 128) {
+        e = launch_kind<128, 128, T>(p, a, s);
+    } else {
+        e = launch_kind<64, 64, T>(p, a, s);
+    }
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t work = (int64_t)((a.N + 3) / 4) * a.M;
+    hipLaunchKernelGGL((grkan_product8_finish_kernel<T>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -127,12 +606,7 @@ hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipS
     Product8Args a = args;
     a.splits = p.splits;
     a.k_split = (int32_t)p.k_split;
-    const unsigned grid = (unsigned)((((int64_t)a.M + 63) / 64) * (((int64_t)a.N + 63) / 64));
-    if (a.bf16)
-        hipLaunchKernelGGL((grkan_product8_kernel<uint16_t>), dim3(grid), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((grkan_product8_kernel<float>), dim3(grid), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return a.bf16 ? launch_type<uint16_t>(p, a, s) : launch_type<float>(p, a, s);
 }
 
 }  // namespace grkan

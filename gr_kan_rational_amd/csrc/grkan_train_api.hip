@@ -82,7 +82,7 @@ extern "C" grkan_status_t grkan_fp8_quantize(const void *x, const float *A, cons
 
 extern "C" size_t grkan_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k) {
     if (product8_shape(m, n, k) != GRKAN_OK || m == 0) return 0;
-    return align256(plan_product8(m, n, k).partials_bytes);
+    return product8_bytes(m, n, k);
 }
 
 extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, const void *b, const float *b_scale,
@@ -98,7 +98,7 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
     if (lda < k || ldb < k || (residual && ldr < n)) return GRKAN_ERR_INVALID_ARG;
     if (a_scale_row < 0 || a_scale_block < 0 || b_scale_row < 0 || b_scale_block < 0) return GRKAN_ERR_INVALID_ARG;
     if (lda > kMaxWidth || ldb > kMaxWidth || (residual && ldr > kMaxWidth)) return GRKAN_ERR_UNSUPPORTED;
-    if (a_scale_row > INT32_MAX || a_scale_block > INT32_MAX || b_scale_row > INT32_MAX || b_scale_block > INT32_MAX)
+    if (a_scale_row > kMaxScaleRow || a_scale_block > INT32_MAX || b_scale_row > kMaxScaleRow || b_scale_block > INT32_MAX)
         return GRKAN_ERR_UNSUPPORTED;
     if (!b || !b_scale) return GRKAN_ERR_INVALID_ARG;
     const int es = io_bytes(out);
@@ -107,7 +107,7 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
         return GRKAN_ERR_UNSUPPORTED;
     if (m == 0) return GRKAN_OK;
     if (!a || !a_scale || !c) return GRKAN_ERR_INVALID_ARG;
-    const Product8Plan p = plan_product8(m, n, k);
+    const Product8Plan p = plan_product8(m, n, k, out == GRKAN_BF16);
     const size_t need = align256(p.partials_bytes);
     const int64_t kb = ceil_div(k, kBlock8), nb = b_tile ? ceil_div(n, kBlock8) : n;
     auto scales = [&](int64_t r, int64_t row, int64_t block) { return (size_t)((r - 1) * row + (kb - 1) * block + 1) * 4; };

@@ -25,7 +25,15 @@ inline grkan_status_t quantize_shape(int64_t rows, int64_t cols, int64_t ldx, in
 
 // ------------------------------------------------------------ 8-bit product
 
+// A scale's row stride: a tile's scales lie within 2^31 bytes.
+constexpr int64_t kMaxScaleRow = int64_t(1) << 20;
+
+// Few rows: `few` blocks of 16 a workgroup.  Else tiles of the result of `tile` x
+// `tile`; with splits > 1 fp32 sums of k ranges go to memory and a second kernel
+// adds them.
 struct Product8Plan {
+    int32_t few;
+    int32_t tile;
     int32_t splits;
     int64_t k_split;         // of a split, whole blocks
     size_t partials_bytes;
@@ -34,15 +42,60 @@ struct Product8Plan {
 inline grkan_status_t product8_shape(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 1 || K < 1) return GRKAN_ERR_INVALID_ARG;
     if (M > kMaxRows || N > kMaxWidth || K > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
-    if (ceil_div(M, 64) * ceil_div(N, 64) >= (int64_t(1) << 24)) return GRKAN_ERR_UNSUPPORTED;
+    // the second kernel's threads, 4 columns each, in one launch
+    if (M * ceil_div(N, 4) >= (int64_t(1) << 32) - 256) return GRKAN_ERR_UNSUPPORTED;
     return GRKAN_OK;
 }
 
-inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K) {
+constexpr int64_t kFewRows = 64;
+
+inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16) {
     Product8Plan p{};
     p.splits = 1;
-    p.k_split = K;
+    p.k_split = ceil_div(K, kBlock8) * kBlock8;
+    if (M <= kFewRows) {
+        p.few = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+        while (p.few > 1 && ceil_div(N, 16) * ceil_div(M, 16 * p.few) < 192) p.few /= 2;
+        return p;
+    }
+    // The tile and the number of k splits with the least estimated time: places are
+    // the workgroups that the CUs hold at once, a step (a block of k) takes a
+    // workgroup `alone` us while few are taken, in proportion to those that are up
+    // to `full`, and a tile's result `tail`.  Splits add a launch, a write and a read
+    // of their sums.
+    static const int kTile[] = {256, 128, 64};
+    static const double kAloneBf[] = {1.0, 0.45, 0.35}, kFullBf[] = {1.25, 0.7, 0.5}, kTail[] = {4.0, 1.5, 0.5};
+    static const double kAloneF[] = {0.0, 0.7, 0.4}, kFullF[] = {0.0, 1.3, 0.7};
+    static const int64_t kPlaces[] = {256, 512, 1024};
+    const double *alone = bf16 ? kAloneBf : kAloneF, *full = bf16 ? kFullBf : kFullF;
+    const int64_t steps = ceil_div(K, kBlock8);
+    double best = 1e30;
+    for (int i = bf16 ? 0 : 1; i < 3; ++i) {
+        const int64_t tiles = ceil_div(M, kTile[i]) * ceil_div(N, kTile[i]);
+        for (int64_t s = 1; s <= 64; ++s) {
+            if (s > 8 && s % 8 != 0) continue;  // eighths: a k range to an XCD
+            if (s > 1 && (steps < 2 * s || (double)s * M * N * 4 > 256e6)) break;
+            const int64_t per = ceil_div(steps, s), wgs = tiles * s, rounds = wgs / kPlaces[i], rest = wgs % kPlaces[i];
+            const double part = full[i] * (double)rest / (double)kPlaces[i];
+            double us = 3.0 + (double)rounds * (per * full[i] + kTail[i]);
+            if (rest) us += per * (part > alone[i] ? part : alone[i]) + kTail[i];
+            if (s > 1) us += 3.0 + 2.0 * (double)s * M * N * 4 / 6e6;
+            if (us < best) {
+                best = us;
+                p.tile = kTile[i];
+                p.k_split = per * kBlock8;
+            }
+        }
+    }
+    p.splits = (int32_t)ceil_div(K, p.k_split);
+    if (p.splits > 1) p.partials_bytes = (size_t)p.splits * (size_t)M * (size_t)N * 4;
     return p;
+}
+
+// Workspace for either type of result.
+inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
+    const size_t a = plan_product8(M, N, K, false).partials_bytes, b = plan_product8(M, N, K, true).partials_bytes;
+    return align256(a > b ? a : b);
 }
 
 // ------------------------------------------------------------ residual path

@@ -78,7 +78,8 @@ GRKAN_API grkan_status_t grkan_fp8_quantize(
  *             if that is dense; any other overlap is GRKAN_ERR_INVALID_ARG.
  *   m >= 0 (0 is a no-op), n, k >= 1.
  *   workspace grkan_fp8_matmul_workspace_size() bytes (may be 0), 256-byte aligned.
- * GRKAN_ERR_UNSUPPORTED: m >= 2^31 - 256, n, k or a leading dimension above 2^22,
+ * GRKAN_ERR_UNSUPPORTED: m >= 2^31 - 256, n, k or a leading dimension above 2^22, a
+ * scale's row stride above 2^20, its block stride above 2^31,
  * m x n past the launch limits, a misaligned pointer or leading dimension.
  */
 GRKAN_API grkan_status_t grkan_fp8_matmul(

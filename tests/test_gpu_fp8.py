@@ -156,6 +156,16 @@ def test_matmul(gk, shape, tile, dtype):
         assert torch.equal(got, gk.grkan_fp8_matmul(a, sa, b, sb, bias=bi, residual=re, dtype=dtype)), "two calls differ"
 
 
+# tiles of 256 rows, whole and odd, one block of k and several; k split, its end inside a block
+LARGE = [(4096, 4096, 128), (4100, 2100, 300), (8200, 2056, 100), (2049, 4107, 777), (300, 264, 20000), (520, 100, 30001)]
+
+
+@pytest.mark.parametrize("dtype, tile", ((BF, True), (BF, False), (torch.float32, False)))
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_matmul_large(gk, shape, dtype, tile):
+    test_matmul(gk, shape, tile, dtype)
+
+
 def test_matmul_layouts(gk):
     """Scales side by side in either order or expanded from one, operands in wider tensors, outputs off their
     16-byte boundary, in place on the residual: the same bits as dense ones; nothing outside the output."""
