@@ -66,27 +66,27 @@ typedef f32x4 f32x4_any __attribute__((aligned(4)));
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer: reads zeros
 
 // 16 (or 4) bytes per lane from offset `off` of the buffer to LDS, lane after
-// lane from `to` (the same in all lanes; taken from M0).  Written as instructions
-// because they have no result; arrival is waited for by count.  M0 is the
-// compiler's to use nowhere else in these kernels.
-__device__ static inline uint32_t lds_address(const char *to) {
-    return (uint32_t)__builtin_amdgcn_readfirstlane(
-        (int)(uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)to));
+// lane from address `to` (the same in all lanes; taken from M0).  Written as
+// instructions because they have no result; arrival is waited for by count.  M0 is
+// the compiler's to use nowhere else in these kernels.
+__device__ static inline uint32_t lds_address(const char *p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char *)p);
 }
-__device__ static inline void fetch16(u32x4 rsrc, uint32_t off, const char *to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(lds_address(to)), "v"(off), "s"(rsrc) : "memory");
+__device__ static inline uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ static inline void fetch16(u32x4 rsrc, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" : : "s"(uniform(to)), "v"(off), "s"(rsrc) : "memory");
 }
-__device__ static inline void fetch4(u32x4 rsrc, uint32_t off, const char *to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(lds_address(to)), "v"(off), "s"(rsrc) : "memory");
+__device__ static inline void fetch4(u32x4 rsrc, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" : : "s"(uniform(to)), "v"(off), "s"(rsrc) : "memory");
 }
 __device__ static inline u32x4 resource(const void *p, uint32_t bytes) {
     const uint64_t addr = reinterpret_cast<uint64_t>(p);
-    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)addr),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(addr >> 32)) & 0xffffu,
-                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+    return u32x4{uniform((uint32_t)addr), uniform((uint32_t)(addr >> 32)) & 0xffffu, uniform(bytes), 0x00020000u};
 }
-// s_waitcnt vmcnt(0), lgkmcnt(0), and lgkmcnt(0) alone.
-__device__ static inline void wait_all() { __builtin_amdgcn_s_waitcnt(0x0070); }
+// s_waitcnt vmcnt(n), lgkmcnt(0), and lgkmcnt(0) alone.
+template <int N> __device__ static inline void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
 __device__ static inline void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 __device__ static inline void barrier() {
     asm volatile("" ::: "memory");
@@ -120,13 +120,16 @@ template <int ROWS, int T> struct Codes {
     }
     // k of this thread's chunks
     __device__ static inline int first() { return (((int)threadIdx.x & 7) ^ swizzle((int)threadIdx.x / 8)) * 16; }
-    // The chunks of step t, `left` values of k before its end.
-    __device__ inline void fetch(char *stage, int t, int left) {
-        const u32x4 rsrc = resource(base + (int64_t)t * kBlock8, left > 0 ? bytes - (uint32_t)t * kBlock8 : 0u);
-        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        const uint32_t from = left >= kBlock8 || first() < left ? off : kNowhere;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) fetch16(rsrc, from + (uint32_t)(i * step), stage + (i * T + wave * 64) * 16);
+    // The chunks of step t, `left` values of k before its end: begin, then each chunk
+    // into its place of a stage.
+    u32x4 rsrc;
+    uint32_t from;
+    __device__ inline void begin(int t, int left) {
+        rsrc = resource(base + (int64_t)t * kBlock8, left > 0 ? bytes - (uint32_t)t * kBlock8 : 0u);
+        from = left >= kBlock8 || first() < left ? off : kNowhere;
+    }
+    __device__ inline void fetch(uint32_t stage, int wave, int i) const {
+        fetch16(rsrc, from + (uint32_t)(i * step), stage + (i * T + wave * 64) * 16);
     }
 };
 
@@ -136,11 +139,19 @@ template <int BM, int BN> struct Tile8 {
     // codes of a, of b, then a scale a thread: BM of a's, BN of b's
     static constexpr int kScales = (BM + BN) * kBlock8;
     static constexpr int kStage = kScales + kThreads * 4;
-    static constexpr size_t kLds = 2 * (size_t)kStage;
+    // two stages, a corner for each wave's 16 rows of bf16 results, the bias of two tiles'
+    // columns
+    static constexpr int kCorner = 16 * WN * 2, kCorners = 2 * kStage;
+    static constexpr int kBias = kCorners + kThreads / 64 * kCorner;
+    static constexpr size_t kLds = kBias + 2 * (size_t)BN * 4;
     static_assert(BM + BN <= kThreads && BM % 64 == 0, "a scale a thread, one operand's a wave");
 };
 
 // A block of k at a time through two LDS stages.  T: the result's type.
+//
+// In the middle of a step every wave holds what is left of it in registers: a barrier
+// there covers both that and the arrival of the next step, and the fetches of the
+// step after that go into the stage just freed, a whole step ahead of their use.
 template <int BM, int BN, class T, bool BTILE, bool PARTIAL>
 __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_tile_kernel(Product8Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -172,8 +183,9 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
         return b;
     };
 
-    // The fetches run a step ahead of the products, on through the tiles of this
-    // workgroup; past the last they read zeros.
+    // The fetches run two steps ahead of the products, on through the tiles of this
+    // workgroup; past the last they read zeros, so the number in flight is fixed.
+    constexpr int kInFlight = Codes<BM, TH>::kChunks + Codes<BN, TH>::kChunks + 1;
     Codes<BM, TH> ca;
     Codes<BN, TH> cb;
     const float *scale_base;
@@ -201,17 +213,34 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
         }
         fetch_step = 0;
     };
-    auto fetch = [&](int stage) {
+    u32x4 scale_rsrc;
+    auto fetch_begin = [&]() {
         const int left = fetch_len - fetch_step * kBlock8;
-        ca.fetch(lds + stage, fetch_step, left);
-        cb.fetch(lds + stage + kB, fetch_step, left);
-        fetch4(resource(scale_base + fetch_step * scale_step, left > 0 ? 0x7ffffff0u : 0u), scale_off,
-               lds + stage + kScales + wave * 256);
+        ca.begin(fetch_step, left);
+        cb.begin(fetch_step, left);
+        scale_rsrc = resource(scale_base + fetch_step * scale_step, left > 0 ? 0x7ffffff0u : 0u);
+    };
+    const uint32_t base = lds_address(lds);
+    auto fetch_part = [&](int stage, int i) {
+        if (i < ca.kChunks)
+            ca.fetch(base + stage, wave, i);
+        else if (i < ca.kChunks + cb.kChunks)
+            cb.fetch(base + stage + kB, wave, i - ca.kChunks);
+        else
+            fetch4(scale_rsrc, scale_off, base + stage + kScales + wave * 256);
+    };
+    auto fetch_end = [&]() {
         ++fetch_step;
         if (fetch_step * kBlock8 >= fetch_len && fetch_tile < count) {
             fetch_tile = next(fetch_tile + (int)gridDim.x);
             start_tile();
         }
+    };
+    auto fetch = [&](int stage) {
+        fetch_begin();
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) fetch_part(stage, i);
+        fetch_end();
     };
     // A chunk that reaches past K: what lies there is the caller's, and cleared here.
     const int ragged = a.K & 15;
@@ -244,67 +273,174 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
     auto read_b = [&](int stage, int j) { return read(stage + kB + (ncol + 16 * j) * kBlock8); };
 
     f32x4 acc[NM][NN];
-    // The rows' fragments of a step: X, read during the step before; Y, read at its start,
-    // and once more when multiplied; Z, read at its start.  Z and the second Y are
-    // multiplied after the barrier, while the next step's X and columns are read.
-    constexpr int Y = NM == 8 ? 2 : 0, X = (NM - 2 * Y) / 2, Z = X;
-    static_assert(X + 2 * Y + Z == NM, "all rows");
-    i32x8 fx[X], fy[Y > 0 ? Y : 1], fz[Z], fb[NN];
+    // The rows' fragments of a step, in the order that they are multiplied: X, read during
+    // the step before; Y and Z, read at its start; W, read into X's registers once those
+    // are through.  Z and W are multiplied after the barrier, while the next step's X and
+    // columns are read, X into Y's registers: the two change places from step to step.
+    constexpr int Y = NM == 8 ? 2 : 0, W = Y, X = (NM - 2 * Y) / 2, Z = X;
+    static_assert(X + Y + Z + W == NM && (Y == 0 || Y == X), "all rows");
+    i32x8 fr[2][X], fz[Z], fb[NN];
+    float as[NM];
+    // The wave's results to memory: rows m0 .., columns n0 ...  WHOLE: all of the tile's
+    // exist.
+    int turn = 0;  // which half of the bias
+    auto finish = [&](auto all_there, int m0, int n0, int split) {
+        constexpr bool WHOLE = all_there();
+        const int mw = m0 + (lane & 15), nw = n0 + 4 * (lane >> 4);
+        const float *bias = reinterpret_cast<const float *>(lds + Shape::kBias) + turn * BN + ncol + 4 * (lane >> 4);
+        if constexpr (PARTIAL || sizeof(T) == 4) {
+            // 16 bytes a lane, 64 side by side of a row
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                const int m = mw + 16 * i;
+                if (!WHOLE && m >= a.M) continue;
+#pragma unroll
+                for (int j = 0; j < NN; ++j) {
+                    const int n = nw + 16 * j, nv = WHOLE ? 4 : min(a.N - n, 4);
+                    if (nv <= 0) continue;
+                    f32x4 h = acc[i][j];
+                    float *o;
+                    if constexpr (PARTIAL) {
+                        o = a.partials + ((int64_t)split * a.M + m) * a.N + n;
+                    } else {
+                        o = static_cast<float *>(a.c) + (int64_t)m * a.N + n;
+                        h += *reinterpret_cast<const f32x4 *>(bias + 16 * j);
+                        if (a.residual) {
+                            const float *r = static_cast<const float *>(a.residual) + m * a.ldr + n;
+                            h += nv == 4 ? f32x4(*reinterpret_cast<const f32x4_any *>(r)) : load4<false>(r, nv);
+                        }
+                    }
+                    if (nv == 4)
+                        *reinterpret_cast<f32x4_any *>(o) = h;
+                    else
+                        store4<false>(o, nv, h);
+                }
+            }
+        } else {
+            // bf16 results pass through the wave's own corner of LDS, 16 rows of WN columns at a
+            // time, so that memory sees whole rows.  Chunk c (8 columns) of row r sits at
+            // c ^ (r mod CP).  A residual comes the same way, into the place of its result.
+            constexpr int CP = WN / 8, RP = 64 / CP;
+            char *own = lds + Shape::kCorners + wave * Shape::kCorner;
+            auto slot = [&](int r, int c) { return own + r * (WN * 2) + ((c ^ (r & (CP - 1))) << 4); };
+            const int row = lane / CP, chunk = lane % CP;
+            const int cn = n0 + chunk * 8, cnv = WHOLE ? 8 : min(max(a.N - cn, 0), 8);
+            auto fence = [] { asm volatile("" ::: "memory"); };  // LDS serves a wave in order
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                const int mh = m0 + 16 * i;
+                if (a.residual) {
+#pragma unroll
+                    for (int it = 0; it < 16 / RP; ++it) {
+                        const int r = it * RP + row;
+                        const uint16_t *from = static_cast<const uint16_t *>(a.residual) + (int64_t)(mh + r) * a.ldr + cn;
+                        u32x4 v = {0u, 0u, 0u, 0u};
+                        if (WHOLE || mh + r < a.M) {
+                            if (WHOLE || cnv == 8) {
+                                v = *reinterpret_cast<const u32x4_any *>(from);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (e < cnv) v[e / 2] |= (uint32_t)from[e] << (16 * (e & 1));
+                            }
+                        }
+                        *reinterpret_cast<u32x4 *>(slot(r, chunk)) = v;
+                    }
+                    fence();
+                }
+#pragma unroll
+                for (int j = 0; j < NN; ++j) {
+                    f32x4 h = acc[i][j] + *reinterpret_cast<const f32x4 *>(bias + 16 * j);
+                    char *to = slot(lane & 15, 2 * j + (lane >> 5)) + ((lane >> 4) & 1) * 8;
+                    if (a.residual) {
+                        const u32x2 r = *reinterpret_cast<const u32x2 *>(to);
+                        h += f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
+                                   __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
+                    }
+                    *reinterpret_cast<u32x2 *>(to) = pack4(h);
+                }
+                fence();
+#pragma unroll
+                for (int it = 0; it < 16 / RP; ++it) {
+                    const int r = it * RP + row;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(slot(r, chunk));
+                    if (!WHOLE && (mh + r >= a.M || cnv <= 0)) continue;
+                    uint16_t *to = static_cast<uint16_t *>(a.c) + (int64_t)(mh + r) * a.N + cn;
+                    if (WHOLE || cnv == 8) {
+                        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(to));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < cnv) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                    }
+                }
+                fence();
+            }
+        }
+    };
     int now = 0;   // the stage of this step
     start_tile();
     fetch(0);
-    wait_all();
+    fetch(kStage);
+    wait_loads<kInFlight>();
     barrier();
     int tile = next((int)blockIdx.x);
-    place(tile);
     bool first = true;
+    bool whole = false;  // the last tile stored by this workgroup had no edge
+    constexpr int kStores = PARTIAL || sizeof(T) == 4 ? NM * NN : NM * WN / 32;
     for (; tile < count; tile = next(tile + (int)gridDim.x)) {
         place(tile);
         const int steps = (len + kBlock8 - 1) / kBlock8;
         const int tm0 = m0, tn0 = n0, tsplit = split;
         const bool ends = ragged && kb + len == a.K;
+        // the bias of this tile's columns: a wave that is a tile ahead writes the other half
+        turn ^= 1;
+        if (!PARTIAL && t < BN)
+            reinterpret_cast<float *>(lds + Shape::kBias)[turn * BN + t] = a.bias && tn0 + t < a.N ? a.bias[tn0 + t] : 0.0f;
+        auto scales_of = [&](int stage, int i) {
+            return reinterpret_cast<const float *>(lds + stage + kScales)[mrow + 16 * i + (lane & 15)];
+        };
         if (first) {
             if (ends && steps == 1) clear_past(now);
             first = false;
 #pragma unroll
-            for (int i = 0; i < X; ++i) fx[i] = read_a(now, i);
+            for (int i = 0; i < X; ++i) fr[0][i] = read_a(now, i);
 #pragma unroll
             for (int j = 0; j < NN; ++j) fb[j] = read_b(now, j);
+#pragma unroll
+            for (int i = 0; i < X + Y; ++i) as[i] = scales_of(now, i);
         }
 #pragma unroll
         for (int i = 0; i < NM; ++i)
 #pragma unroll
             for (int j = 0; j < NN; ++j) acc[i][j] = f32x4{};
-        for (int st = 0; st < steps; ++st) {
+        auto step = [&](int st, auto parity) {
+            constexpr int PX = Y > 0 ? parity() : 0, PY = 1 - PX;
             const int other = kStage - now;
-            fetch(other);
-            const float *sa = reinterpret_cast<const float *>(lds + now + kScales) + mrow + (lane & 15);
             const float *sb = reinterpret_cast<const float *>(lds + now + kScales) + BM + ncol + (BTILE ? 0 : 4 * (lane >> 4));
             f32x4 bs[NN];
-            float as[NM];
-#pragma unroll
-            for (int i = 0; i < Y; ++i) fy[i] = read_a(now, X + i);
-#pragma unroll
-            for (int i = 0; i < NM; ++i) as[i] = sa[16 * i];
+            float bt = 0.0f;
             if constexpr (BTILE) {
-                const float bt = *sb;
-#pragma unroll
-                for (int i = 0; i < NM; ++i) as[i] *= bt;
+                bt = *sb;
             } else {
 #pragma unroll
                 for (int j = 0; j < NN; ++j) bs[j] = *reinterpret_cast<const f32x4 *>(sb + 16 * j);
             }
 #pragma unroll
+            for (int i = 0; i < Y; ++i) fr[PY][i] = read_a(now, X + i);
+#pragma unroll
             for (int i = 0; i < Z; ++i) fz[i] = read_a(now, X + Y + i);
+#pragma unroll
+            for (int i = X + Y; i < NM; ++i) as[i] = scales_of(now, i);
             // Products kAhead of the sums they are added to, so that the matrix unit's
             // result is there; pinned, or the compiler moves the additions past the
             // barrier and keeps the products.
             constexpr int kAhead = 2;
             f32x4 p[kAhead + 1];
             auto add = [&](int slot, int i, int j) {
+                const float s = BTILE ? as[i] * bt : as[i];
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    acc[i][j][v] = fmaf(p[slot][v], BTILE ? as[i] : as[i] * bs[j][v], acc[i][j][v]);
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[slot][v], BTILE ? s : s * bs[j][v], acc[i][j][v]);
                 asm volatile("" : "+v"(acc[i][j]));
             };
             keep_order();
@@ -313,14 +449,18 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
             for (int q = 0; q < kFirst + kAhead; ++q) {
                 if (q < kFirst) {
                     const int i = q / NN, j = q % NN;
-                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < X ? fx[i < X ? i : 0] : fy[i < X ? 0 : i - X]);
-                    if (i >= X && j == NN - 1) fy[i - X] = read_a(now, i + Y + Z);
+                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < X ? fr[PX][i < X ? i : 0] : fr[PY][i < X ? 0 : i - X]);
+                    if (i < W && j == NN - 1) fr[PX][i] = read_a(now, X + Y + Z + i);
                 }
                 if (q >= kAhead) add((q - kAhead) % (kAhead + 1), (q - kAhead) / NN, (q - kAhead) % NN);
             }
-            // the next step has arrived, and every wave holds what is left of this one in
-            // registers
-            wait_all();
+            // memory operations end in the order of their issue: after a whole tile its
+            // kStores stores stand behind the next step's fetches, and need not be waited
+            // for
+            if (st == 0 && whole)
+                wait_loads<kStores>();
+            else
+                wait_loads<0>();
             barrier();
             if (ragged) {
                 // (the next step is this tile's last, or the next tile's only one)
@@ -335,116 +475,55 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
                 }
                 if (past) clear_past(other);
             }
+            fetch_begin();
 #pragma unroll
-            for (int i = 0; i < X; ++i) fx[i] = read_a(other, i);
-            constexpr int R = Z + Y, kRest = R * NN;
+            for (int i = 0; i < X; ++i) fr[Y > 0 ? PY : 0][i] = read_a(other, i);
+            constexpr int R = Z + W, kRest = R * NN;
+            keep_order();
 #pragma unroll
             for (int q = 0; q < kRest + kAhead; ++q) {
                 if (q < kRest) {
                     const int j = q / R, i = q % R;
-                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < Z ? fz[i < Z ? i : 0] : fy[i < Z ? 0 : i - Z]);
+                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < Z ? fz[i < Z ? i : 0] : fr[PX][i < Z ? 0 : i - Z]);
                     if (i == R - 1) fb[j] = read_b(other, j);
+                    // the fetches, spread over the products
+#pragma unroll
+                    for (int k = q * kInFlight / kRest; k < (q + 1) * kInFlight / kRest; ++k) fetch_part(now, k);
                 }
                 if (q >= kAhead) add((q - kAhead) % (kAhead + 1), X + Y + (q - kAhead) % R, (q - kAhead) / R);
+                if (q == kRest / 2) {
+#pragma unroll
+                    for (int i = 0; i < X + Y; ++i) as[i] = scales_of(other, i);
+                }
             }
+            fetch_end();
             now = other;
+        };
+        constexpr std::integral_constant<int, 0> zero;
+        constexpr std::integral_constant<int, 1> one;
+        if constexpr (Y == 0) {
+            for (int st = 0; st < steps; ++st) step(st, zero);
+        } else {
+            int st = 0;
+            for (; st + 1 < steps; st += 2) {
+                step(st, zero);
+                step(st + 1, one);
+            }
+            if (st < steps) {
+                step(st, zero);
+#pragma unroll
+                for (int i = 0; i < X; ++i) fr[0][i] = fr[1][i];
+            }
         }
         // Here `now` holds the next tile's first step (its first fragments are in
-        // registers) and the other stage is free.
-        const int mw = tm0 + mrow + (lane & 15), nw = tn0 + ncol + 4 * (lane >> 4);
-        if constexpr (PARTIAL || sizeof(T) == 4) {
-            // 16 bytes a lane, 64 side by side of a row
-#pragma unroll
-            for (int i = 0; i < NM; ++i) {
-                const int m = mw + 16 * i;
-                if (m >= a.M) continue;
-#pragma unroll
-                for (int j = 0; j < NN; ++j) {
-                    const int n = nw + 16 * j, nv = min(a.N - n, 4);
-                    if (nv <= 0) continue;
-                    f32x4 h = acc[i][j];
-                    float *o;
-                    if constexpr (PARTIAL) {
-                        o = a.partials + ((int64_t)tsplit * a.M + m) * a.N + n;
-                    } else {
-                        o = static_cast<float *>(a.c) + (int64_t)m * a.N + n;
-                        if (a.bias) h += load4<false>(a.bias + n, nv);
-                        if (a.residual) h += load4<false>(static_cast<const float *>(a.residual) + m * a.ldr + n, nv);
-                    }
-                    if (nv == 4)
-                        *reinterpret_cast<f32x4_any *>(o) = h;
-                    else
-                        store4<false>(o, nv, h);
-                }
-            }
-        } else {
-            // bf16 results pass through the wave's own corner of the free stage, 16 rows of WN
-            // columns at a time, so that memory sees whole rows.  Chunk c (8 columns) of row r
-            // sits at c ^ (r mod CP).  A residual comes the same way, into the place of its result.
-            constexpr int CP = WN / 8, RP = 64 / CP;
-            static_assert(TH / 64 * 16 * WN * 2 <= kScales, "staging fits");
-            char *own = lds + (kStage - now) + wave * (16 * WN * 2);
-            auto slot = [&](int r, int c) { return own + r * (WN * 2) + ((c ^ (r & (CP - 1))) << 4); };
-            const int row = lane / CP, chunk = lane % CP;
-            const int cn = tn0 + ncol + chunk * 8, cnv = min(max(a.N - cn, 0), 8);
-            auto fence = [] { asm volatile("" ::: "memory"); };  // LDS serves a wave in order
-#pragma unroll
-            for (int i = 0; i < NM; ++i) {
-                const int mh = tm0 + mrow + 16 * i;
-                if (a.residual) {
-#pragma unroll
-                    for (int it = 0; it < 16 / RP; ++it) {
-                        const int r = it * RP + row;
-                        const uint16_t *from = static_cast<const uint16_t *>(a.residual) + (int64_t)(mh + r) * a.ldr + cn;
-                        u32x4 v = {0u, 0u, 0u, 0u};
-                        if (mh + r < a.M) {
-                            if (cnv == 8) {
-                                v = *reinterpret_cast<const u32x4_any *>(from);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    if (e < cnv) v[e / 2] |= (uint32_t)from[e] << (16 * (e & 1));
-                            }
-                        }
-                        *reinterpret_cast<u32x4 *>(slot(r, chunk)) = v;
-                    }
-                    fence();
-                }
-#pragma unroll
-                for (int j = 0; j < NN; ++j) {
-                    f32x4 h = acc[i][j];
-                    if (a.bias) h += load4<false>(a.bias + nw + 16 * j, min(max(a.N - nw - 16 * j, 0), 4));
-                    char *to = slot(lane & 15, 2 * j + (lane >> 5)) + ((lane >> 4) & 1) * 8;
-                    if (a.residual) {
-                        const u32x2 r = *reinterpret_cast<const u32x2 *>(to);
-                        h += f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
-                                   __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
-                    }
-                    *reinterpret_cast<u32x2 *>(to) = pack4(h);
-                }
-                fence();
-#pragma unroll
-                for (int it = 0; it < 16 / RP; ++it) {
-                    const int r = it * RP + row;
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(slot(r, chunk));
-                    if (mh + r >= a.M || cnv <= 0) continue;
-                    uint16_t *to = static_cast<uint16_t *>(a.c) + (int64_t)(mh + r) * a.N + cn;
-                    if (cnv == 8) {
-                        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(to));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (e < cnv) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
-                    }
-                }
-                fence();
-            }
-            // the stage goes back to the fetches
-            wait_lds();
-            barrier();
-        }
+        // registers) and the other stage waits for its second.
+        whole = tm0 + BM <= a.M && tn0 + BN <= a.N;
+        if (whole)
+            finish(std::true_type{}, tm0 + mrow, tn0 + ncol, tsplit);
+        else
+            finish(std::false_type{}, tm0 + mrow, tn0 + ncol, tsplit);
     }
-    wait_all();  // nothing may still be on its way into LDS when the workgroup ends
+    wait_loads<0>();  // nothing may still be on its way into LDS when the workgroup ends
 }
 
 // The splits' sums added in order, then bias and residual.
@@ -569,8 +648,14 @@ template <int BM, int BN, class T, bool BTILE, bool PARTIAL> hipError_t launch_t
 }
 
 template <int BM, int BN, class T> hipError_t launch_kind(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
-    if (p.splits > 1) return a.b_tile ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, false, true>(a, s);
-    return a.b_tile ? launch_tile<BM, BN, T, true, false>(a, s) : launch_tile<BM, BN, T, false, false>(a, s);
+    if constexpr (BM == 256) {
+        if (!a.b_tile) return hipErrorInvalidValue;  // (has no registers for a scale a column)
+        return p.splits > 1 ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, true, false>(a, s);
+    } else if (p.splits > 1) {
+        return a.b_tile ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, false, true>(a, s);
+    } else {
+        return a.b_tile ? launch_tile<BM, BN, T, true, false>(a, s) : launch_tile<BM, BN, T, false, false>(a, s);
+    }
 }
 
 template <class T> hipError_t launch_type(const Product8Plan &p, const Product8Args &a, hipStream_t s) {

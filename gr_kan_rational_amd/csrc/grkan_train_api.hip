@@ -107,7 +107,7 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
         return GRKAN_ERR_UNSUPPORTED;
     if (m == 0) return GRKAN_OK;
     if (!a || !a_scale || !c) return GRKAN_ERR_INVALID_ARG;
-    const Product8Plan p = plan_product8(m, n, k, out == GRKAN_BF16);
+    const Product8Plan p = plan_product8(m, n, k, out == GRKAN_BF16, b_tile != 0);
     const size_t need = align256(p.partials_bytes);
     const int64_t kb = ceil_div(k, kBlock8), nb = b_tile ? ceil_div(n, kBlock8) : n;
     auto scales = [&](int64_t r, int64_t row, int64_t block) { return (size_t)((r - 1) * row + (kb - 1) * block + 1) * 4; };

@@ -49,7 +49,7 @@ inline grkan_status_t product8_shape(int64_t M, int64_t N, int64_t K) {
 
 constexpr int64_t kFewRows = 64;
 
-inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16) {
+inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile) {
     Product8Plan p{};
     p.splits = 1;
     p.k_split = ceil_div(K, kBlock8) * kBlock8;
@@ -58,28 +58,35 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16) {
         while (p.few > 1 && ceil_div(N, 16) * ceil_div(M, 16 * p.few) < 192) p.few /= 2;
         return p;
     }
-    // The tile and the number of k splits with the least estimated time: places are
-    // the workgroups that the CUs hold at once, a step (a block of k) takes a
-    // workgroup `alone` us while few are taken, in proportion to those that are up
-    // to `full`, and a tile's result `tail`.  Splits add a launch, a write and a read
-    // of their sums.
+    // The tile and the number of k splits with the least estimated time.  A CU holds
+    // 1, 2 or 4 workgroups; a step (a block of k) takes a workgroup `alone` us, or
+    // `full` where the CU holds as many as it can, a tile's result `tail`, `tail_full`.
+    // Splits add a launch, a write and a read of their sums.  Fitted to 603 timings of
+    // 58 shapes: the choice is 1.3% from the best one in the mean, 19% at most
+    // (50,432 x 3,072 from 768, tiles of 256 / 128 / 64: 185 / 182 / 240 us; 8,192 x
+    // 8,192 from 8,192: 537 / 656 / 1,260; 197 x 768 from 3,072 in tiles of 64: 9.7 us
+    // in 4 splits, 20 in one).  256 x 256 is for bf16 results and a scale for each tile
+    // of b alone: it has no registers for the wider products or a scale a column.
     static const int kTile[] = {256, 128, 64};
-    static const double kAloneBf[] = {1.0, 0.45, 0.35}, kFullBf[] = {1.25, 0.7, 0.5}, kTail[] = {4.0, 1.5, 0.5};
-    static const double kAloneF[] = {0.0, 0.7, 0.4}, kFullF[] = {0.0, 1.3, 0.7};
-    static const int64_t kPlaces[] = {256, 512, 1024};
-    const double *alone = bf16 ? kAloneBf : kAloneF, *full = bf16 ? kFullBf : kFullF;
-    const int64_t steps = ceil_div(K, kBlock8);
+    static const double kTimes[2][3][4] = {{{}, {0.9, 2.1, 2.2, 0.0}, {0.61, 1.5, 0.23, 0.0}},
+                                           {{1.6, 1.7, 3.0, 5.5}, {0.5, 1.3, 2.0, 2.3}, {0.38, 1.0, 0.4, 1.9}}};
+    const int64_t steps = ceil_div(K, kBlock8), cus = 256;
     double best = 1e30;
-    for (int i = bf16 ? 0 : 1; i < 3; ++i) {
-        const int64_t tiles = ceil_div(M, kTile[i]) * ceil_div(N, kTile[i]);
+    for (int i = bf16 && b_tile ? 0 : 1; i < 3; ++i) {
+        const double *t = kTimes[bf16][i];
+        const int64_t tiles = ceil_div(M, kTile[i]) * ceil_div(N, kTile[i]), held = 1 << i;
         for (int64_t s = 1; s <= 64; ++s) {
             if (s > 8 && s % 8 != 0) continue;  // eighths: a k range to an XCD
             if (s > 1 && (steps < 2 * s || (double)s * M * N * 4 > 256e6)) break;
-            const int64_t per = ceil_div(steps, s), wgs = tiles * s, rounds = wgs / kPlaces[i], rest = wgs % kPlaces[i];
-            const double part = full[i] * (double)rest / (double)kPlaces[i];
-            double us = 3.0 + (double)rounds * (per * full[i] + kTail[i]);
-            if (rest) us += per * (part > alone[i] ? part : alone[i]) + kTail[i];
-            if (s > 1) us += 3.0 + 2.0 * (double)s * M * N * 4 / 6e6;
+            const int64_t per = ceil_div(steps, s), wgs = tiles * ceil_div(steps, per);
+            const int64_t rounds = wgs / (held * cus), rest = wgs % (held * cus);
+            const double share = (double)ceil_div(rest, cus) / (double)held;
+            double us = 3.5 + (double)rounds * (per * t[1] + t[3]);
+            if (rest) {
+                us += per * (t[1] * share > t[0] ? t[1] * share : t[0]);
+                us += t[3] * share > t[2] ? t[3] * share : t[2];
+            }
+            if (s > 1) us += 3.2 + 2.0 * (double)s * M * N * 4 / 7e6;
             if (us < best) {
                 best = us;
                 p.tile = kTile[i];
@@ -92,10 +99,14 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16) {
     return p;
 }
 
-// Workspace for either type of result.
+// Workspace for every type of result and layout of scales.
 inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
-    const size_t a = plan_product8(M, N, K, false).partials_bytes, b = plan_product8(M, N, K, true).partials_bytes;
-    return align256(a > b ? a : b);
+    size_t most = 0;
+    for (int i = 0; i < 4; ++i) {
+        const size_t n = plan_product8(M, N, K, (i & 1) != 0, (i & 2) != 0).partials_bytes;
+        if (n > most) most = n;
+    }
+    return align256(most);
 }
 
 // ------------------------------------------------------------ residual path
