@@ -32,6 +32,29 @@ template <int W, int K> struct Columns {
     __device__ inline int nv(int k) const { return min(C - at(k), 4); }  // at most 0: none
 };
 
+// Four values as they lie in memory, so that a row on its way takes few registers.
+#if GRKAN_RESIDUAL_BF16
+typedef u32x2 raw4;
+__device__ static inline f32x4 widen(raw4 w) {
+    return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xffff0000u)};
+}
+#else
+typedef f32x4 raw4;
+__device__ static inline f32x4 widen(raw4 w) { return w; }
+#endif
+template <bool VEC> __device__ static inline raw4 load_raw(const io_t *p, int nv) {
+    raw4 w = {};
+    if constexpr (VEC) {
+        if (nv > 0) w = __builtin_nontemporal_load(reinterpret_cast<const raw4 *>(p));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < nv) reinterpret_cast<io_t *>(&w)[e] = p[e];
+    }
+    return w;
+}
+
 // Sums of N values over the W waves of a row, the same bits in every lane.
 template <int W, int N> __device__ static inline void row_sum(float (&v)[N], float (*red)[8], int wave) {
 #pragma unroll
@@ -57,9 +80,13 @@ template <bool VEC> __device__ static inline f32x4 vector4(const float *p, int a
     return p ? load4<VEC>(p + at, nv) : f32x4{none, none, none, none};
 }
 
-template <bool VEC> __device__ static inline f32x4 gate4(const ResidualArgs &a, int64_t row, int at, int nv) {
+// The gate's row of a row (rows fit 31 bits).
+__device__ static inline int64_t gate_row(const ResidualArgs &a, int64_t row) {
+    if (!a.gate || a.gate_rows == 1) return row;
+    return (uint32_t)row / (uint32_t)a.gate_rows;
+}
+template <bool VEC> __device__ static inline f32x4 gate4(const ResidualArgs &a, int64_t g, int at, int nv) {
     if (!a.gate) return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
-    const int64_t g = row / a.gate_rows;
     if (a.gate_wide) {
         if (a.gate_bf16) return load4<VEC>(static_cast<const uint16_t *>(a.gate) + g * a.C + at, nv);
         return load4<VEC>(static_cast<const float *>(a.gate) + g * a.C + at, nv);
@@ -95,35 +122,58 @@ __device__ static inline void moments(const f32x4 (&v)[K], const Columns<W, K> &
 
 #if !GRKAN_RESIDUAL_BACKWARD
 
-template <int W, int K, bool VEC>
+// The vectors of a lane's columns stay in registers over the rows; the next row is
+// on its way while one is worked on.
+template <int W, int K, bool VEC, bool POST>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_kernel(ResidualArgs a) {
     __shared__ float red[W][8];
-    const int wave = (int)threadIdx.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const Columns<W, K> c(W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x, a.C);
     const int per = W == 1 ? 4 : 1;
-    for (int64_t r = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * per) {
+    const int64_t stride = (int64_t)gridDim.x * per;
+    int64_t r = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0);
+    f32x4 weight[K], bias[K], scale[K], pw[POST ? K : 1], pb[POST ? K : 1];
+    raw4 nx[K], nf[K];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            nx[k] = load_raw<VEC>(static_cast<const io_t *>(a.x) + row * a.ldx + c.at(k), c.nv(k));
+            nf[k] = load_raw<VEC>(static_cast<const io_t *>(a.f) + row * a.ldf + c.at(k), c.nv(k));
+        }
+    };
+    if (r < a.rows) fetch(r);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        weight[k] = vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f);
+        bias[k] = vector4<VEC>(a.bias, c.at(k), c.nv(k), 0.0f);
+        scale[k] = vector4<VEC>(a.scale, c.at(k), c.nv(k), 1.0f);
+        if constexpr (POST) {
+            pw[k] = vector4<VEC>(a.post_weight, c.at(k), c.nv(k), 1.0f);
+            pb[k] = vector4<VEC>(a.post_bias, c.at(k), c.nv(k), 0.0f);
+        }
+    }
+    for (; r < a.rows; r += stride) {
         f32x4 h[K], u[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            h[k] = load4<VEC>(static_cast<const io_t *>(a.x) + r * a.ldx + c.at(k), c.nv(k));
-            u[k] = load4<VEC>(static_cast<const io_t *>(a.f) + r * a.ldf + c.at(k), c.nv(k));
+            h[k] = widen(nx[k]);
+            u[k] = widen(nf[k]);
         }
+        if (r + stride < a.rows) fetch(r + stride);
         float mean, rstd;
-        if (a.post != GRKAN_NORM_NONE) {
+        if constexpr (POST) {
             moments<W, K>(u, c, a.post, a.eps, red, wave, mean, rstd);
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                u[k] = (u[k] - mean) * rstd * vector4<VEC>(a.post_weight, c.at(k), c.nv(k), 1.0f) +
-                       vector4<VEC>(a.post_bias, c.at(k), c.nv(k), 0.0f);
+            for (int k = 0; k < K; ++k) u[k] = (u[k] - mean) * rstd * pw[k] + pb[k];
             if (c.first == 0) {
                 a.stats[2 * a.rows + r] = mean;
                 a.stats[3 * a.rows + r] = rstd;
             }
         }
+        const int64_t gr = gate_row(a, r);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const f32x4 s = vector4<VEC>(a.scale, c.at(k), c.nv(k), 1.0f) * gate4<VEC>(a, r, c.at(k), c.nv(k));
-            h[k] += s * u[k];
+            h[k] += scale[k] * gate4<VEC>(a, gr, c.at(k), c.nv(k)) * u[k];
             store4<VEC>(static_cast<io_t *>(a.h) + r * a.C + c.at(k), c.nv(k), h[k]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[k][e] = e < c.nv(k) ? h[k][e] : 0.0f;
@@ -131,9 +181,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
         moments<W, K>(h, c, a.norm, a.eps, red, wave, mean, rstd);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            store4<VEC>(static_cast<io_t *>(a.z) + r * a.C + c.at(k), c.nv(k),
-                        (h[k] - mean) * rstd * vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f) +
-                            vector4<VEC>(a.bias, c.at(k), c.nv(k), 0.0f));
+            store4<VEC>(static_cast<io_t *>(a.z) + r * a.C + c.at(k), c.nv(k), (h[k] - mean) * rstd * weight[k] + bias[k]);
         if (c.first == 0) {
             a.stats[r] = mean;
             a.stats[a.rows + r] = rstd;
@@ -143,10 +191,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
 
 template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
-    if (a.vec)
-        hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false>), grid, block, 0, s, a);
+    if (a.post != GRKAN_NORM_NONE) {
+        if (a.vec)
+            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true, true>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false, true>), grid, block, 0, s, a);
+    } else {
+        if (a.vec)
+            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true, false>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false, false>), grid, block, 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -156,17 +211,40 @@ template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStrea
 // post norm's) stay in registers, meet in LDS where a workgroup's waves hold
 // different rows, and leave as one row of partials per workgroup.
 template <int W, int K, bool VEC, bool POST>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward_kernel(ResidualArgs a) {
-    constexpr int S = POST ? 5 : 3;
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_residual_backward_kernel(ResidualArgs a) {
+    constexpr int S = POST ? 5 : 3, V = POST ? 4 : 2;
     __shared__ float red[W][8];
     __shared__ f32x4 meet[W == 1 ? 4 : 1][W == 1 ? 64 : 1];
-    const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+    __shared__ f32x4 vectors[W == 1 ? V * K : 1][W == 1 ? 64 : 1];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
     const Columns<W, K> c(W == 1 ? lane : (int)threadIdx.x, a.C);
     const float inv = 1.0f / (float)a.C;
     const int per = W == 1 ? 4 : 1;
     const int64_t walkers = (int64_t)gridDim.x * per;
     const bool layer = a.norm == GRKAN_NORM_LAYER, post_layer = a.post == GRKAN_NORM_LAYER;
     const bool by_unit = a.gate && a.gate_wide && a.gate_rows > 1 && a.dgate;
+    // weight, scale, post_weight and post_bias of a lane's columns: from LDS where a wave
+    // holds a row (every wave needs all of them), else from memory
+    const float *const sources[4] = {a.weight, a.scale, a.post_weight, a.post_bias};
+    if constexpr (W == 1) {
+        for (int i = wave; i < V * K; i += 4)
+            vectors[i][lane] = vector4<VEC>(sources[i / K], c.at(i % K), c.nv(i % K), i / K == 3 ? 0.0f : 1.0f);
+        __syncthreads();
+    }
+    auto vector = [&](int v, int k) {
+        if constexpr (W == 1) return vectors[v * K + k][lane];
+        return vector4<VEC>(sources[v], c.at(k), c.nv(k), v == 3 ? 0.0f : 1.0f);
+    };
+    raw4 nh[K], nf[K], ndh[K], ndz[K];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            nh[k] = load_raw<VEC>(static_cast<const io_t *>(a.h) + r * a.C + c.at(k), c.nv(k));
+            nf[k] = load_raw<VEC>(static_cast<const io_t *>(a.f) + r * a.ldf + c.at(k), c.nv(k));
+            ndh[k] = a.dh ? load_raw<VEC>(static_cast<const io_t *>(a.dh) + r * a.lddh + c.at(k), c.nv(k)) : raw4{};
+            ndz[k] = a.dz ? load_raw<VEC>(static_cast<const io_t *>(a.dz) + r * a.lddz + c.at(k), c.nv(k)) : raw4{};
+        }
+    };
     f32x4 sum[S][K], gsum[K];
 #pragma unroll
     for (int i = 0; i < S; ++i)
@@ -179,15 +257,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward
         const int64_t r1 = min(r0 + a.p.unit_rows, (run + 1) * run_rows);
 #pragma unroll
         for (int k = 0; k < K; ++k) gsum[k] = f32x4{};
+        fetch(r0);
         for (int64_t r = r0; r < r1; ++r) {
             f32x4 g[K], u[K], t[K], xh[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                xh[k] = load4<VEC>(static_cast<const io_t *>(a.h) + r * a.C + c.at(k), c.nv(k));
-                u[k] = load4<VEC>(static_cast<const io_t *>(a.f) + r * a.ldf + c.at(k), c.nv(k));
-                g[k] = a.dh ? load4<VEC>(static_cast<const io_t *>(a.dh) + r * a.lddh + c.at(k), c.nv(k)) : f32x4{};
-                t[k] = a.dz ? load4<VEC>(static_cast<const io_t *>(a.dz) + r * a.lddz + c.at(k), c.nv(k)) : f32x4{};
+                xh[k] = widen(nh[k]);
+                u[k] = widen(nf[k]);
+                g[k] = widen(ndh[k]);
+                t[k] = widen(ndz[k]);
             }
+            if (r + 1 < r1) fetch(r + 1);
+            const int64_t gr = gate_row(a, r);
             const float mean = a.stats[r], rstd = a.stats[a.rows + r];
             float m[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -196,7 +277,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward
                 for (int e = 0; e < 4; ++e) xh[k][e] = e < c.nv(k) ? (xh[k][e] - mean) * rstd : 0.0f;
                 sum[0][k] += t[k] * xh[k];
                 sum[1][k] += t[k];
-                t[k] *= vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f);
+                t[k] *= vector(0, k);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     m[0] += t[k][e];
@@ -222,9 +303,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward
                 if constexpr (POST) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) fh[e] = e < nv ? (fh[e] - pmean) * prstd : 0.0f;
-                    u[k] = fh * vector4<VEC>(a.post_weight, at, nv, 1.0f) + vector4<VEC>(a.post_bias, at, nv, 0.0f);
+                    u[k] = fh * vector(2, k) + vector(3, k);
                 }
-                const f32x4 s = vector4<VEC>(a.scale, at, nv, 1.0f), gt = gate4<VEC>(a, r, at, nv);
+                const f32x4 s = vector(1, k), gt = gate4<VEC>(a, gr, at, nv);
                 const f32x4 gu = g[k] * u[k], gs = gu * s;
                 sum[2][k] += gu * gt;
                 if (a.dgate) {
@@ -242,7 +323,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward
                 if constexpr (POST) {
                     sum[3][k] += d * fh;
                     sum[4][k] += d;
-                    d *= vector4<VEC>(a.post_weight, at, nv, 1.0f);
+                    d *= vector(2, k);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         q[0] += d[e];
@@ -306,25 +387,25 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_backward
         }
 }
 
-// The workgroups' partials of each column in order of the workgroups, in fp64: 64
-// columns x 16 lanes of workgroups.
+// The workgroups' partials of each column in order of the workgroups, in fp64: 32
+// columns x 32 lanes of workgroups.
 __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a) {
     __shared__ double red[1024];
-    const int t = (int)threadIdx.x, cb = (a.C + 63) / 64;
-    const int i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 64 + (t & 63);
+    const int t = (int)threadIdx.x, cb = (a.C + 31) / 32;
+    const int i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 32 + (t & 31);
     float *const outs[5] = {a.dweight, a.dbias, a.dscale, a.dpost_weight, a.dpost_bias};
     float *out = outs[i];
     if (!out) return;
     double s = 0.0;
     if (col < a.C) {
         const float *p = a.sums + (int64_t)i * a.C + col;
-#pragma unroll 4
-        for (int64_t b = t >> 6; b < a.p.blocks; b += 16) s += (double)p[b * a.p.sums * a.C];
+#pragma unroll 8
+        for (int64_t b = t >> 5; b < a.p.blocks; b += 32) s += (double)p[b * a.p.sums * a.C];
     }
     red[t] = s;
     __syncthreads();
-    if (t < 64 && col < a.C) {
-        for (int q = 1; q < 16; ++q) s += red[t + 64 * q];
+    if (t < 32 && col < a.C) {
+        for (int q = 1; q < 32; ++q) s += red[t + 32 * q];
         out[col] = (float)s;
     }
 }
@@ -378,6 +459,7 @@ hipError_t launch_rows(const ResidualArgs &a, hipStream_t s) {
     switch (a.p.waves) {
         case 1: return launch_waves<1>(a, s);
         case 4: return launch_waves<4>(a, s);
+        case 8: return launch_waves<8>(a, s);
         default: return launch_waves<16>(a, s);
     }
 }
@@ -391,7 +473,7 @@ template <> hipError_t launch_residual_backward<io_t>(const ResidualArgs &a, hip
     hipError_t e = launch_rows(a, s);
     if (e != hipSuccess) return e;
     if (a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias) {
-        const unsigned grid = (unsigned)(a.p.sums * ((a.C + 63) / 64));
+        const unsigned grid = (unsigned)(a.p.sums * ((a.C + 31) / 32));
         hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3(grid), dim3(1024), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }

@@ -141,12 +141,14 @@ inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_c
                           bool backward, ResidualPlan *p) {
     *p = ResidualPlan{};
     const int64_t quads = ceil_div(C, 4);
-    p->waves = quads <= 256 ? 1 : (quads <= 1024 ? 4 : 16);
+    p->waves = quads <= 256 ? 1 : (quads <= 1024 ? 4 : (quads <= 2048 ? 8 : 16));
     p->K = (int32_t)ceil_div(quads, 64 * p->waves);
     p->per = p->waves == 1 ? 4 : 1;
     if (!backward) {
-        p->blocks = ceil_div(rows, p->per);
-        if (p->blocks > 4096) p->blocks = 4096;
+        p->blocks = ceil_div(rows > 0 ? rows : 1, p->per);
+        // (as many as the CUs hold, each over as many rows as the others)
+        const int64_t most = p->waves == 1 ? 1024 : 2048 / p->waves;
+        p->blocks = ceil_div(p->blocks, ceil_div(p->blocks, most));
         return;
     }
     const bool columns = gates > 0 && gate_channels == C && rows > gates && C > 1;
