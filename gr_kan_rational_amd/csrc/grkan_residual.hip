@@ -25,11 +25,12 @@ typedef float io_t;
 #endif
 
 // The columns of a lane: 4 from 4 (lane + 64 W k), k < K, over the W waves of a row.
+// K is the least that covers them, so only the last k can lie past the end.
 template <int W, int K> struct Columns {
     int first, C;
     __device__ inline Columns(int lane_of_row, int C_) : first(4 * lane_of_row), C(C_) {}
     __device__ inline int at(int k) const { return first + 256 * W * k; }
-    __device__ inline int nv(int k) const { return min(C - at(k), 4); }  // at most 0: none
+    __device__ inline int nv(int k) const { return k < K - 1 ? 4 : min(C - at(k), 4); }  // at most 0: none
 };
 
 // Four values as they lie in memory, so that a row on its way takes few registers.
@@ -75,9 +76,15 @@ template <int W, int N> __device__ static inline void row_sum(float (&v)[N], flo
     }
 }
 
-// A vector of one value per channel, or `none` for each.
+// A vector of one value per channel, or `none` for each; zeros past the end.  With
+// the scale zero there (and x, f, dh and dz read as zeros) what a lane forms past the
+// end adds nothing to a row's sums.
 template <bool VEC> __device__ static inline f32x4 vector4(const float *p, int at, int nv, float none) {
-    return p ? load4<VEC>(p + at, nv) : f32x4{none, none, none, none};
+    if (p) return load4<VEC>(p + at, nv);
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < nv ? none : 0.0f;
+    return v;
 }
 
 // The gate's row of a row (rows fit 31 bits).
@@ -113,7 +120,7 @@ __device__ static inline void moments(const f32x4 (&v)[K], const Columns<W, K> &
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float d = e < c.nv(k) ? v[k][e] - mean : 0.0f;
+            const float d = k < K - 1 || e < c.nv(k) ? v[k][e] - mean : 0.0f;
             s[0] = fmaf(d, d, s[0]);
         }
     row_sum<W>(s, red, wave);
@@ -159,6 +166,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
             h[k] = widen(nx[k]);
             u[k] = widen(nf[k]);
         }
+        // (before the next row's: loads are waited for in their order)
+        const int64_t gr = gate_row(a, r);
+        f32x4 gate[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) gate[k] = gate4<VEC>(a, gr, c.at(k), c.nv(k));
         if (r + stride < a.rows) fetch(r + stride);
         float mean, rstd;
         if constexpr (POST) {
@@ -170,13 +182,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
                 a.stats[3 * a.rows + r] = rstd;
             }
         }
-        const int64_t gr = gate_row(a, r);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            h[k] += scale[k] * gate4<VEC>(a, gr, c.at(k), c.nv(k)) * u[k];
+            h[k] += scale[k] * gate[k] * u[k];
             store4<VEC>(static_cast<io_t *>(a.h) + r * a.C + c.at(k), c.nv(k), h[k]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[k][e] = e < c.nv(k) ? h[k][e] : 0.0f;
         }
         moments<W, K>(h, c, a.norm, a.eps, red, wave, mean, rstd);
 #pragma unroll
@@ -207,12 +216,14 @@ template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStrea
 
 #else
 
-// Rows one after another; the column sums of dweight, dbias, dscale (and the
-// post norm's) stay in registers, meet in LDS where a workgroup's waves hold
-// different rows, and leave as one row of partials per workgroup.
+// Rows one after another; their column sums stay in registers, meet in LDS where a
+// workgroup's waves hold different rows, and leave as one row of partials per
+// workgroup: dz xh, dz, and g gate f (dscale) or, with a post norm, P = g gate fh and
+// Q = g gate, of which, a column's factors being the same in every row,
+// dpost_weight = scale P, dpost_bias = scale Q, dscale = post_weight P + post_bias Q.
 template <int W, int K, bool VEC, bool POST>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_residual_backward_kernel(ResidualArgs a) {
-    constexpr int S = POST ? 5 : 3, V = POST ? 4 : 2;
+    constexpr int S = POST ? 4 : 3, V = POST ? 3 : 2;
     __shared__ float red[W][8];
     __shared__ f32x4 meet[W == 1 ? 4 : 1][W == 1 ? 64 : 1];
     __shared__ f32x4 vectors[W == 1 ? V * K : 1][W == 1 ? 64 : 1];
@@ -220,20 +231,25 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
     const Columns<W, K> c(W == 1 ? lane : (int)threadIdx.x, a.C);
     const float inv = 1.0f / (float)a.C;
     const int per = W == 1 ? 4 : 1;
-    const int64_t walkers = (int64_t)gridDim.x * per;
     const bool layer = a.norm == GRKAN_NORM_LAYER, post_layer = a.post == GRKAN_NORM_LAYER;
     const bool by_unit = a.gate && a.gate_wide && a.gate_rows > 1 && a.dgate;
-    // weight, scale, post_weight and post_bias of a lane's columns: from LDS where a wave
-    // holds a row (every wave needs all of them), else from memory
-    const float *const sources[4] = {a.weight, a.scale, a.post_weight, a.post_bias};
+    // weight, scale x post_weight and scale x post_bias of a lane's columns (with a post
+    // norm; else weight and scale): from LDS where a wave holds a row, since every wave
+    // needs all of them, else from memory
+    auto make = [&](int v, int k) {
+        const int at = c.at(k), nv = c.nv(k);
+        if (v == 0) return vector4<VEC>(a.weight, at, nv, 1.0f);
+        const f32x4 s = vector4<VEC>(a.scale, at, nv, 1.0f);
+        if (!POST) return s;
+        return s * (v == 1 ? vector4<VEC>(a.post_weight, at, nv, 1.0f) : vector4<VEC>(a.post_bias, at, nv, 0.0f));
+    };
     if constexpr (W == 1) {
-        for (int i = wave; i < V * K; i += 4)
-            vectors[i][lane] = vector4<VEC>(sources[i / K], c.at(i % K), c.nv(i % K), i / K == 3 ? 0.0f : 1.0f);
+        for (int i = wave; i < V * K; i += 4) vectors[i][lane] = make(i / K, i % K);
         __syncthreads();
     }
     auto vector = [&](int v, int k) {
         if constexpr (W == 1) return vectors[v * K + k][lane];
-        return vector4<VEC>(sources[v], c.at(k), c.nv(k), v == 3 ? 0.0f : 1.0f);
+        return make(v, k);
     };
     raw4 nh[K], nf[K], ndh[K], ndz[K];
     auto fetch = [&](int64_t r) {
@@ -250,15 +266,36 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
     for (int i = 0; i < S; ++i)
 #pragma unroll
         for (int k = 0; k < K; ++k) sum[i][k] = f32x4{};
-    for (int64_t unit = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0); unit < a.p.units; unit += walkers) {
-        const int64_t run = unit / a.p.units_per_gate, part = unit - run * a.p.units_per_gate;
-        const int64_t run_rows = a.rows / (a.p.units / a.p.units_per_gate);
-        const int64_t r0 = run * run_rows + part * a.p.unit_rows;
-        const int64_t r1 = min(r0 + a.p.unit_rows, (run + 1) * run_rows);
+    // This walker's rows.  Those of a gate row that lie in one walker's leave its sum as
+    // dgate; else each walker leaves what it has, in the first of its two places if the
+    // gate row began before, else in the second.
+    const int64_t walker = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0);
+    const int64_t r0 = walker * a.p.walk, r1 = min(r0 + a.p.walk, a.rows);
+    int64_t gr = by_unit ? gate_row(a, r0) : 0, gate_end = by_unit ? (gr + 1) * a.gate_rows : 0;
+    auto leave = [&]() {
+        const bool before = gr * a.gate_rows < r0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) gsum[k] = f32x4{};
+        for (int k = 0; k < K; ++k) {
+            const int at = c.at(k), nv = c.nv(k);
+            if (before || gate_end > r1)
+                store4<VEC>(a.gate_sums + (2 * walker + !before) * a.C + at, nv, gsum[k]);
+            else if (a.gate_bf16)
+                store4<VEC>(static_cast<uint16_t *>(a.dgate) + gr * a.C + at, nv, gsum[k]);
+            else
+                store4<VEC>(static_cast<float *>(a.dgate) + gr * a.C + at, nv, gsum[k]);
+            gsum[k] = f32x4{};
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) gsum[k] = f32x4{};
+    if (r0 < r1) {
         fetch(r0);
         for (int64_t r = r0; r < r1; ++r) {
+            if (by_unit && r == gate_end) {
+                leave();
+                ++gr;
+                gate_end += a.gate_rows;
+            }
             f32x4 g[K], u[K], t[K], xh[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -267,14 +304,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 g[k] = widen(ndh[k]);
                 t[k] = widen(ndz[k]);
             }
+            // (before the next row's: loads are waited for in their order)
+            const int64_t here = by_unit ? gr : gate_row(a, r);
+            f32x4 gate[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) gate[k] = gate4<VEC>(a, here, c.at(k), c.nv(k));
             if (r + 1 < r1) fetch(r + 1);
-            const int64_t gr = gate_row(a, r);
             const float mean = a.stats[r], rstd = a.stats[a.rows + r];
             float m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) xh[k][e] = e < c.nv(k) ? (xh[k][e] - mean) * rstd : 0.0f;
+                xh[k] = (xh[k] - mean) * rstd;
                 sum[0][k] += t[k] * xh[k];
                 sum[1][k] += t[k];
                 t[k] *= vector(0, k);
@@ -297,33 +337,27 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 const int at = c.at(k), nv = c.nv(k);
                 g[k] += rstd * (t[k] - m0 - xh[k] * m1);
                 if (a.dx) store4<VEC>(static_cast<io_t *>(a.dx) + r * a.C + at, nv, g[k]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[k][e] = e < nv ? g[k][e] : 0.0f;
                 f32x4 fh = u[k];
                 if constexpr (POST) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) fh[e] = e < nv ? (fh[e] - pmean) * prstd : 0.0f;
-                    u[k] = fh * vector(2, k) + vector(3, k);
+                    fh = (fh - pmean) * prstd;
                 }
-                const f32x4 s = vector(1, k), gt = gate4<VEC>(a, gr, at, nv);
-                const f32x4 gu = g[k] * u[k], gs = gu * s;
-                sum[2][k] += gu * gt;
+                const f32x4 s = vector(1, k), gg = g[k] * gate[k];
                 if (a.dgate) {
+                    const f32x4 gu = g[k] * (POST ? fh * s + vector(V - 1, k) : fh * s);
                     if (!a.gate_wide) {
-                        q[2] += (gs[0] + gs[1]) + (gs[2] + gs[3]);
+                        q[2] += (gu[0] + gu[1]) + (gu[2] + gu[3]);
                     } else if (by_unit) {
-                        gsum[k] += gs;
+                        gsum[k] += gu;
                     } else if (a.gate_bf16) {
-                        store4<VEC>(static_cast<uint16_t *>(a.dgate) + r * a.C + at, nv, gs);
+                        store4<VEC>(static_cast<uint16_t *>(a.dgate) + r * a.C + at, nv, gu);
                     } else {
-                        store4<VEC>(static_cast<float *>(a.dgate) + r * a.C + at, nv, gs);
+                        store4<VEC>(static_cast<float *>(a.dgate) + r * a.C + at, nv, gu);
                     }
                 }
-                f32x4 d = g[k] * (s * gt);
+                sum[2][k] += gg * fh;
+                if constexpr (POST) sum[3][k] += gg;
+                const f32x4 d = gg * s;
                 if constexpr (POST) {
-                    sum[3][k] += d * fh;
-                    sum[4][k] += d;
-                    d *= vector(2, k);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         q[0] += d[e];
@@ -354,17 +388,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 }
             }
         }
-        if (by_unit) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (a.p.units_per_gate > 1)
-                    store4<VEC>(a.gate_sums + unit * a.C + c.at(k), c.nv(k), gsum[k]);
-                else if (a.gate_bf16)
-                    store4<VEC>(static_cast<uint16_t *>(a.dgate) + run * a.C + c.at(k), c.nv(k), gsum[k]);
-                else
-                    store4<VEC>(static_cast<float *>(a.dgate) + run * a.C + c.at(k), c.nv(k), gsum[k]);
-            }
-        }
+        if (by_unit) leave();
     }
 #pragma unroll
     for (int i = 0; i < S; ++i)
@@ -387,44 +411,68 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
         }
 }
 
-// The workgroups' partials of each column in order of the workgroups, in fp64: 32
-// columns x 32 lanes of workgroups.
-__global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a) {
+// The second step, sums in fp64 and in order: the workgroups' partials of each
+// column (32 columns x 32 lanes of workgroups); then, from workgroup `columns` on,
+// dgate of each (gate, channel) from what the walkers left, or of each gate from its
+// rows.
+__global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a, int columns, int64_t gates) {
     __shared__ double red[1024];
-    const int t = (int)threadIdx.x, cb = (a.C + 31) / 32;
-    const int i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 32 + (t & 31);
-    float *const outs[5] = {a.dweight, a.dbias, a.dscale, a.dpost_weight, a.dpost_bias};
-    float *out = outs[i];
-    if (!out) return;
+    const int t = (int)threadIdx.x;
     double s = 0.0;
-    if (col < a.C) {
-        const float *p = a.sums + (int64_t)i * a.C + col;
+    if ((int)blockIdx.x >= columns) {
+        const int64_t i = (int64_t)((int)blockIdx.x - columns) * 1024 + t;
+        if (i >= gates) return;
+        if (a.gate_wide) {
+            const int64_t g = i / a.C, col = i - g * a.C, first = g * a.gate_rows / a.p.walk;
+            const int64_t last = ((g + 1) * a.gate_rows - 1) / a.p.walk;
+            if (first == last) return;  // (written by its walker)
+            const bool before = g * a.gate_rows < first * a.p.walk;
+            s = (double)a.gate_sums[(2 * first + !before) * a.C + col];
 #pragma unroll 8
-        for (int64_t b = t >> 5; b < a.p.blocks; b += 32) s += (double)p[b * a.p.sums * a.C];
+            for (int64_t w = first + 1; w <= last; ++w) s += (double)a.gate_sums[2 * w * a.C + col];
+        } else {
+            const float *p = a.gate_sums + i * a.gate_rows;
+#pragma unroll 8
+            for (int64_t k = 0; k < a.gate_rows; ++k) s += (double)p[k];
+        }
+        if (a.gate_bf16)
+            store1(static_cast<uint16_t *>(a.dgate) + i, (float)s);
+        else
+            static_cast<float *>(a.dgate)[i] = (float)s;
+        return;
     }
-    red[t] = s;
+    const int cb = (a.C + 31) / 32, i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 32 + (t & 31);
+    auto column = [&](int k) {
+        double s = 0.0;
+        if (col < a.C) {
+            const float *p = a.sums + (int64_t)k * a.C + col;
+#pragma unroll 8
+            for (int64_t b = t >> 5; b < a.p.blocks; b += 32) s += (double)p[b * a.p.sums * a.C];
+        }
+        red[t] = s;
+        __syncthreads();
+        if (t < 32)
+            for (int q = 1; q < 32; ++q) s += red[t + 32 * q];
+        return s;
+    };
+    const double v = column(i);
+    if (i < 2) {
+        float *out = i == 0 ? a.dweight : a.dbias;
+        if (out && t < 32 && col < a.C) out[col] = (float)v;
+        return;
+    }
+    if (a.post == GRKAN_NORM_NONE) {
+        if (a.dscale && t < 32 && col < a.C) a.dscale[col] = (float)v;
+        return;
+    }
     __syncthreads();
-    if (t < 32 && col < a.C) {
-        for (int q = 1; q < 32; ++q) s += red[t + 32 * q];
-        out[col] = (float)s;
-    }
-}
-
-// dgate of each (gate, channel) from its units, or of each gate from its rows, in order.
-__global__ __launch_bounds__(256) void grkan_residual_gates_kernel(ResidualArgs a, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    double s = 0.0;
-    if (a.gate_wide) {
-        const int64_t g = i / a.C, col = i - g * a.C;
-        for (int64_t k = 0; k < a.p.units_per_gate; ++k) s += (double)a.gate_sums[(g * a.p.units_per_gate + k) * a.C + col];
-    } else {
-        for (int64_t k = 0; k < a.gate_rows; ++k) s += (double)a.gate_sums[i * a.gate_rows + k];
-    }
-    if (a.gate_bf16)
-        store1(static_cast<uint16_t *>(a.dgate) + i, (float)s);
-    else
-        static_cast<float *>(a.dgate)[i] = (float)s;
+    const double w = column(3);
+    if (t >= 32 || col >= a.C) return;
+    const double scale = a.scale ? a.scale[col] : 1.0f;
+    if (a.dpost_weight) a.dpost_weight[col] = (float)(scale * v);
+    if (a.dpost_bias) a.dpost_bias[col] = (float)(scale * w);
+    if (a.dscale)
+        a.dscale[col] = (float)((a.post_weight ? a.post_weight[col] : 1.0f) * v + (a.post_bias ? a.post_bias[col] : 0.0f) * w);
 }
 
 template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
@@ -458,6 +506,7 @@ template <int W> hipError_t launch_waves(const ResidualArgs &a, hipStream_t s) {
 hipError_t launch_rows(const ResidualArgs &a, hipStream_t s) {
     switch (a.p.waves) {
         case 1: return launch_waves<1>(a, s);
+        case 2: return launch_waves<2>(a, s);
         case 4: return launch_waves<4>(a, s);
         case 8: return launch_waves<8>(a, s);
         default: return launch_waves<16>(a, s);
@@ -472,15 +521,14 @@ template <> hipError_t launch_residual_forward<io_t>(const ResidualArgs &a, hipS
 template <> hipError_t launch_residual_backward<io_t>(const ResidualArgs &a, hipStream_t s) {
     hipError_t e = launch_rows(a, s);
     if (e != hipSuccess) return e;
-    if (a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias) {
-        const unsigned grid = (unsigned)(a.p.sums * ((a.C + 31) / 32));
-        hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3(grid), dim3(1024), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    const bool by_unit = a.gate_wide && a.p.units_per_gate > 1;
-    if (a.dgate && a.gate_rows > 1 && (by_unit || !a.gate_wide)) {
-        const int64_t n = a.rows / a.gate_rows * (a.gate_wide ? a.C : 1);
-        hipLaunchKernelGGL(grkan_residual_gates_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, n);
+    const bool sums = a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias;
+    const int columns = sums ? 3 * ((a.C + 31) / 32) : 0;
+    int64_t gates = 0;
+    if (a.dgate && a.gate_rows > 1)
+        gates = a.rows / a.gate_rows * (a.gate_wide ? a.C : 1);
+    const int64_t grid = columns + (gates + 1023) / 1024;
+    if (grid > 0) {
+        hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3((unsigned)grid), dim3(1024), 0, s, a, columns, gates);
         e = hipGetLastError();
     }
     return e;

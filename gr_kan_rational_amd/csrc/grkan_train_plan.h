@@ -114,15 +114,14 @@ inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
 constexpr int64_t kMaxChannels = 16384;
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 
-// A row is held by `waves` waves, 4 K values a lane.  The backward's waves (or
-// workgroups of `waves` > 1) each walk over `unit_rows` rows that share a gate
-// row if the gate has one per channel, so that its sum stays in registers.
+// A row is held by `waves` waves, 4 K values a lane.  The backward's walkers (waves, or
+// workgroups of `waves` > 1) each take `walk` rows one after another.
 struct ResidualPlan {
     int32_t K, waves;
     int32_t per;             // rows that a workgroup holds at a time
     int64_t blocks;
-    int64_t units, unit_rows, units_per_gate;
-    int32_t sums;            // column sums: dweight, dbias, dscale (, dpost_weight, dpost_bias)
+    int64_t walk;
+    int32_t sums;            // column sums that a workgroup leaves
     size_t off_sums, off_gate, total;
 };
 
@@ -134,14 +133,15 @@ inline grkan_status_t residual_shape(int64_t rows, int64_t C, int64_t gates, int
     return GRKAN_OK;
 }
 
-// The backward's rows: about kResidualWalkers waves or workgroups, each a run of rows.
-constexpr int64_t kResidualWalkers = 2048;
-
 inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_channels, grkan_norm_t post,
                           bool backward, ResidualPlan *p) {
     *p = ResidualPlan{};
     const int64_t quads = ceil_div(C, 4);
-    p->waves = quads <= 256 ? 1 : (quads <= 1024 ? 4 : (quads <= 2048 ? 8 : 16));
+    // 16 values a lane for a wave alone, else 12 while 8 waves hold a row so: the
+    // backward's sums and rows have to fit 256 registers
+    p->waves = 1;
+    while (p->waves < 8 && quads > (p->waves == 1 ? 256 : 192) * p->waves) p->waves *= 2;
+    if (quads > 256 * 8) p->waves = 16;
     p->K = (int32_t)ceil_div(quads, 64 * p->waves);
     p->per = p->waves == 1 ? 4 : 1;
     if (!backward) {
@@ -151,26 +151,17 @@ inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_c
         p->blocks = ceil_div(p->blocks, ceil_div(p->blocks, most));
         return;
     }
-    const bool columns = gates > 0 && gate_channels == C && rows > gates && C > 1;
-    const int64_t runs = columns ? gates : 1, run = rows / (runs > 0 ? runs : 1);
-    const int64_t walkers = p->waves == 1 ? kResidualWalkers : kResidualWalkers / (2 * p->waves);
-    int64_t per_run = ceil_div(walkers, runs);
-    if (per_run > ceil_div(run, 4)) per_run = ceil_div(run, 4);
-    if (per_run < 1) per_run = 1;
-    p->unit_rows = ceil_div(run, per_run);
-    if (p->unit_rows < 1) p->unit_rows = 1;
-    p->units_per_gate = ceil_div(run, p->unit_rows);
-    p->units = p->units_per_gate * runs;
-    p->blocks = ceil_div(p->units < walkers ? p->units : walkers, p->per);
-    if (p->blocks < 1) p->blocks = 1;
-    p->sums = post == GRKAN_NORM_NONE ? 3 : 5;
+    // as many walkers as the CUs hold, 8 waves each (16 of the widest rows)
+    const int64_t walkers = p->waves == 16 ? 256 : 2048 / p->waves;
+    p->walk = ceil_div(rows > 0 ? rows : 1, walkers);
+    p->blocks = ceil_div(ceil_div(rows > 0 ? rows : 1, p->walk), p->per);
+    p->sums = post == GRKAN_NORM_NONE ? 3 : 4;
     p->off_sums = 0;
     p->off_gate = align256((size_t)p->blocks * p->sums * (size_t)C * 4);
+    // dgate: two places for each walker, or one for each row
     size_t gate = 0;
-    if (columns)
-        gate = p->units_per_gate > 1 ? (size_t)p->units * (size_t)C * 4 : 0;
-    else if (gates > 0 && rows > gates)
-        gate = (size_t)rows * 4;
+    if (gates > 0 && rows > gates)
+        gate = gate_channels == C && C > 1 ? (size_t)p->blocks * p->per * 2 * (size_t)C * 4 : (size_t)rows * 4;
     p->total = p->off_gate + align256(gate);
 }
 
