@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "grkan_fastdiv.h"
 #include "grkan_train_plan.h"
 
 namespace grkan {
@@ -21,6 +22,7 @@ struct ResidualArgs {
     float *gate_sums;                // [units][C] or [rows]
     int64_t rows, ldx, ldf, lddh, lddz;
     int64_t gate_rows;               // rows that share a gate row
+    FastDiv gate_div;                // division by it
     int32_t C;
     int32_t norm, post;
     bool gate_wide;                  // a gate for each channel

@@ -87,20 +87,66 @@ template <bool VEC> __device__ static inline f32x4 vector4(const float *p, int a
     return v;
 }
 
+// How a kernel takes its gate: known when it is compiled, since a branch inside the
+// rows' loop keeps their loads from overlapping (2,048 channels, one gate a sample:
+// 70 us forward with branches, 50 without).  kAny serves what is rare: rows that are
+// not whole accesses, and fp32 gates of bf16 rows.
+enum GateMode : int { kAny = -1, kNoGate = 0, kNarrow = 1, kShared = 2, kElement = 3 };
+
 // The gate's row of a row (rows fit 31 bits).
 __device__ static inline int64_t gate_row(const ResidualArgs &a, int64_t row) {
-    if (!a.gate || a.gate_rows == 1) return row;
-    return (uint32_t)row / (uint32_t)a.gate_rows;
+    return a.gate_rows == 1 ? row : (int64_t)fastdiv((uint32_t)row, a.gate_div);
 }
-template <bool VEC> __device__ static inline f32x4 gate4(const ResidualArgs &a, int64_t g, int at, int nv) {
-    if (!a.gate) return f32x4{1.0f, 1.0f, 1.0f, 1.0f};
-    if (a.gate_wide) {
-        if (a.gate_bf16) return load4<VEC>(static_cast<const uint16_t *>(a.gate) + g * a.C + at, nv);
-        return load4<VEC>(static_cast<const float *>(a.gate) + g * a.C + at, nv);
+
+// The gate of a lane's columns: per row (narrow, or one for each element) as it lies in
+// memory, fetched with its row; shared by rows that follow each other, loaded
+// where that changes.
+template <int W, int K, bool VEC, int GM> struct Gate {
+    uint32_t narrow;
+    raw4 element[GM == kElement ? K : 1];
+    f32x4 held[GM == kShared || GM == kAny ? K : 1];
+
+    // With row `row`, before its data.
+    __device__ inline void fetch(const ResidualArgs &a, int64_t row, const Columns<W, K> &c) {
+        if constexpr (GM == kNarrow) {
+            const int64_t g = gate_row(a, row);
+            narrow = a.gate_bf16 ? static_cast<const uint16_t *>(a.gate)[g] : static_cast<const uint32_t *>(a.gate)[g];
+        } else if constexpr (GM == kElement) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                element[k] = load_raw<VEC>(static_cast<const io_t *>(a.gate) + row * a.C + c.at(k), c.nv(k));
+        }
     }
-    const float v = a.gate_bf16 ? load1(static_cast<const uint16_t *>(a.gate) + g) : static_cast<const float *>(a.gate)[g];
-    return f32x4{v, v, v, v};
-}
+    // At a row from which it differs.
+    __device__ inline void load(const ResidualArgs &a, int64_t row, const Columns<W, K> &c) {
+        if constexpr (GM == kShared || GM == kAny) {
+            if (GM == kAny && !a.gate) return;
+            const int64_t g = gate_row(a, row);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int at = c.at(k), nv = c.nv(k);
+                if (GM == kShared) {
+                    held[k] = load4<VEC>(static_cast<const io_t *>(a.gate) + g * a.C + at, nv);
+                } else if (!a.gate_wide) {
+                    const float v = a.gate_bf16 ? load1(static_cast<const uint16_t *>(a.gate) + g) : static_cast<const float *>(a.gate)[g];
+                    held[k] = f32x4{v, v, v, v};
+                } else if (a.gate_bf16) {
+                    held[k] = load4<VEC>(static_cast<const uint16_t *>(a.gate) + g * a.C + at, nv);
+                } else {
+                    held[k] = load4<VEC>(static_cast<const float *>(a.gate) + g * a.C + at, nv);
+                }
+            }
+        }
+    }
+    // v gate
+    __device__ inline f32x4 times(const ResidualArgs &a, f32x4 v, int k) const {
+        if constexpr (GM == kNarrow) return v * __uint_as_float(a.gate_bf16 ? narrow << 16 : narrow);
+        if constexpr (GM == kElement) return v * widen(element[k]);
+        if constexpr (GM == kShared) return v * held[k];
+        if constexpr (GM == kAny) return a.gate ? v * held[k] : v;
+        return v;
+    }
+};
 
 // mean and 1 / sqrt(var + eps) of a row held as v (zeros past its columns).
 template <int W, int K>
@@ -129,26 +175,28 @@ __device__ static inline void moments(const f32x4 (&v)[K], const Columns<W, K> &
 
 #if !GRKAN_RESIDUAL_BACKWARD
 
-// The vectors of a lane's columns stay in registers over the rows; the next row is
-// on its way while one is worked on.
-template <int W, int K, bool VEC, bool POST>
+// A walker's rows one after another, the vectors of a lane's columns in registers, the
+// next row on its way while one is worked on.
+template <int W, int K, bool VEC, bool POST, int GM>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_kernel(ResidualArgs a) {
     __shared__ float red[W][8];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const Columns<W, K> c(W == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x, a.C);
-    const int per = W == 1 ? 4 : 1;
-    const int64_t stride = (int64_t)gridDim.x * per;
-    int64_t r = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0);
+    const int64_t walker = W == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    const int64_t r0 = walker * a.p.walk, r1 = min(r0 + a.p.walk, a.rows);
+    if (r0 >= r1) return;
     f32x4 weight[K], bias[K], scale[K], pw[POST ? K : 1], pb[POST ? K : 1];
     raw4 nx[K], nf[K];
+    Gate<W, K, VEC, GM> ng;
     auto fetch = [&](int64_t row) {
+        ng.fetch(a, row, c);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             nx[k] = load_raw<VEC>(static_cast<const io_t *>(a.x) + row * a.ldx + c.at(k), c.nv(k));
             nf[k] = load_raw<VEC>(static_cast<const io_t *>(a.f) + row * a.ldf + c.at(k), c.nv(k));
         }
     };
-    if (r < a.rows) fetch(r);
+    fetch(r0);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         weight[k] = vector4<VEC>(a.weight, c.at(k), c.nv(k), 1.0f);
@@ -159,19 +207,20 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
             pb[k] = vector4<VEC>(a.post_bias, c.at(k), c.nv(k), 0.0f);
         }
     }
-    for (; r < a.rows; r += stride) {
+    int64_t changes = r0;  // the next row whose shared gate is another
+    for (int64_t r = r0; r < r1; ++r) {
         f32x4 h[K], u[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             h[k] = widen(nx[k]);
             u[k] = widen(nf[k]);
         }
-        // (before the next row's: loads are waited for in their order)
-        const int64_t gr = gate_row(a, r);
-        f32x4 gate[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) gate[k] = gate4<VEC>(a, gr, c.at(k), c.nv(k));
-        if (r + stride < a.rows) fetch(r + stride);
+        if ((GM == kShared || GM == kAny) && r == changes) {
+            ng.load(a, r, c);
+            changes = (gate_row(a, r) + 1) * a.gate_rows;
+        }
+        const Gate<W, K, VEC, GM> gate = ng;
+        if (r + 1 < r1) fetch(r + 1);
         float mean, rstd;
         if constexpr (POST) {
             moments<W, K>(u, c, a.post, a.eps, red, wave, mean, rstd);
@@ -184,7 +233,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            h[k] += scale[k] * gate[k] * u[k];
+            h[k] += gate.times(a, scale[k], k) * u[k];
             store4<VEC>(static_cast<io_t *>(a.h) + r * a.C + c.at(k), c.nv(k), h[k]);
         }
         moments<W, K>(h, c, a.norm, a.eps, red, wave, mean, rstd);
@@ -197,22 +246,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void grkan_residual_forward_
         }
     }
 }
-
-template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
-    if (a.post != GRKAN_NORM_NONE) {
-        if (a.vec)
-            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false, true>), grid, block, 0, s, a);
-    } else {
-        if (a.vec)
-            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, true, false>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((grkan_residual_forward_kernel<W, K, false, false>), grid, block, 0, s, a);
-    }
-    return hipGetLastError();
-}
+#define GRKAN_RESIDUAL_KERNEL grkan_residual_forward_kernel
 
 #else
 
@@ -221,7 +255,7 @@ template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStrea
 // workgroup: dz xh, dz, and g gate f (dscale) or, with a post norm, P = g gate fh and
 // Q = g gate, of which, a column's factors being the same in every row,
 // dpost_weight = scale P, dpost_bias = scale Q, dscale = post_weight P + post_bias Q.
-template <int W, int K, bool VEC, bool POST>
+template <int W, int K, bool VEC, bool POST, int GM>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_residual_backward_kernel(ResidualArgs a) {
     constexpr int S = POST ? 4 : 3, V = POST ? 3 : 2;
     __shared__ float red[W][8];
@@ -232,7 +266,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
     const float inv = 1.0f / (float)a.C;
     const int per = W == 1 ? 4 : 1;
     const bool layer = a.norm == GRKAN_NORM_LAYER, post_layer = a.post == GRKAN_NORM_LAYER;
-    const bool by_unit = a.gate && a.gate_wide && a.gate_rows > 1 && a.dgate;
+    const bool narrow = GM == kAny ? a.gate && !a.gate_wide : GM == kNarrow;
+    const bool shared = GM == kAny ? a.gate && a.gate_wide && a.gate_rows > 1 : GM == kShared;
+    const bool element = GM == kAny ? a.gate && a.gate_wide && a.gate_rows == 1 : GM == kElement;
     // weight, scale x post_weight and scale x post_bias of a lane's columns (with a post
     // norm; else weight and scale): from LDS where a wave holds a row, since every wave
     // needs all of them, else from memory
@@ -252,7 +288,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
         return make(v, k);
     };
     raw4 nh[K], nf[K], ndh[K], ndz[K];
+    Gate<W, K, VEC, GM> ng;
     auto fetch = [&](int64_t r) {
+        ng.fetch(a, r, c);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             nh[k] = load_raw<VEC>(static_cast<const io_t *>(a.h) + r * a.C + c.at(k), c.nv(k));
@@ -271,8 +309,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
     // gate row began before, else in the second.
     const int64_t walker = (int64_t)blockIdx.x * per + (W == 1 ? wave : 0);
     const int64_t r0 = walker * a.p.walk, r1 = min(r0 + a.p.walk, a.rows);
-    int64_t gr = by_unit ? gate_row(a, r0) : 0, gate_end = by_unit ? (gr + 1) * a.gate_rows : 0;
+    int64_t gr = 0, gate_end = 0;
     auto leave = [&]() {
+        if (!shared || !a.dgate) return;
         const bool before = gr * a.gate_rows < r0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -291,10 +330,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
     if (r0 < r1) {
         fetch(r0);
         for (int64_t r = r0; r < r1; ++r) {
-            if (by_unit && r == gate_end) {
-                leave();
-                ++gr;
-                gate_end += a.gate_rows;
+            if ((GM == kShared || GM == kAny) && (r == gate_end || r == r0)) {
+                if (r > r0) leave();
+                ng.load(a, r, c);
+                gr = gate_row(a, r);
+                gate_end = (gr + 1) * a.gate_rows;
             }
             f32x4 g[K], u[K], t[K], xh[K];
 #pragma unroll
@@ -304,11 +344,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 g[k] = widen(ndh[k]);
                 t[k] = widen(ndz[k]);
             }
-            // (before the next row's: loads are waited for in their order)
-            const int64_t here = by_unit ? gr : gate_row(a, r);
-            f32x4 gate[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k) gate[k] = gate4<VEC>(a, here, c.at(k), c.nv(k));
+            const Gate<W, K, VEC, GM> gate = ng;
             if (r + 1 < r1) fetch(r + 1);
             const float mean = a.stats[r], rstd = a.stats[a.rows + r];
             float m[2] = {0.0f, 0.0f};
@@ -341,18 +377,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 if constexpr (POST) {
                     fh = (fh - pmean) * prstd;
                 }
-                const f32x4 s = vector(1, k), gg = g[k] * gate[k];
-                if (a.dgate) {
+                const f32x4 s = vector(1, k), gg = gate.times(a, g[k], k);
+                if (narrow || shared || element) {
                     const f32x4 gu = g[k] * (POST ? fh * s + vector(V - 1, k) : fh * s);
-                    if (!a.gate_wide) {
+                    if (narrow)
                         q[2] += (gu[0] + gu[1]) + (gu[2] + gu[3]);
-                    } else if (by_unit) {
+                    else if (shared)
                         gsum[k] += gu;
-                    } else if (a.gate_bf16) {
+                    else if (a.dgate && a.gate_bf16)
                         store4<VEC>(static_cast<uint16_t *>(a.dgate) + r * a.C + at, nv, gu);
-                    } else {
+                    else if (a.dgate)
                         store4<VEC>(static_cast<float *>(a.dgate) + r * a.C + at, nv, gu);
-                    }
                 }
                 sum[2][k] += gg * fh;
                 if constexpr (POST) sum[3][k] += gg;
@@ -369,8 +404,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                     store4<VEC>(static_cast<io_t *>(a.df) + r * a.C + at, nv, d);
                 }
             }
-            if (POST || (a.dgate && !a.gate_wide)) row_sum<W>(q, red, wave);
-            if (a.dgate && !a.gate_wide && c.first == 0) {
+            if (POST || narrow) row_sum<W>(q, red, wave);
+            if (narrow && a.dgate && c.first == 0) {
                 if (a.gate_rows > 1)
                     a.gate_sums[r] = q[2];
                 else if (a.gate_bf16)
@@ -388,7 +423,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
                 }
             }
         }
-        if (by_unit) leave();
+        leave();
     }
 #pragma unroll
     for (int i = 0; i < S; ++i)
@@ -475,41 +510,54 @@ __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs 
         a.dscale[col] = (float)((a.post_weight ? a.post_weight[col] : 1.0f) * v + (a.post_bias ? a.post_bias[col] : 0.0f) * w);
 }
 
-template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
+#define GRKAN_RESIDUAL_KERNEL grkan_residual_backward_kernel
+#endif
+
+template <int W, int K, bool VEC, bool POST> hipError_t launch_gate(const ResidualArgs &a, int mode, hipStream_t s) {
     const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
-    if (a.post != GRKAN_NORM_NONE) {
-        if (a.vec)
-            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, true, true>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, false, true>), grid, block, 0, s, a);
-    } else {
-        if (a.vec)
-            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, true, false>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((grkan_residual_backward_kernel<W, K, false, false>), grid, block, 0, s, a);
+    if constexpr (VEC) {
+        switch (mode) {
+            case kNoGate: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kNoGate>), grid, block, 0, s, a); return hipGetLastError();
+            case kNarrow: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kNarrow>), grid, block, 0, s, a); return hipGetLastError();
+            case kShared: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kShared>), grid, block, 0, s, a); return hipGetLastError();
+            case kElement: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kElement>), grid, block, 0, s, a); return hipGetLastError();
+        }
     }
+    hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, VEC, POST, kAny>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
-#endif
-
-template <int W> hipError_t launch_waves(const ResidualArgs &a, hipStream_t s) {
-    switch (a.p.K) {
-        case 1: return launch_kernel<W, 1>(a, s);
-        case 2: return launch_kernel<W, 2>(a, s);
-        case 3: return launch_kernel<W, 3>(a, s);
-        case 4: return launch_kernel<W, 4>(a, s);
-        default: return hipErrorInvalidValue;
-    }
+template <int W, int K> hipError_t launch_kernel(const ResidualArgs &a, hipStream_t s) {
+    const bool same = a.gate_bf16 == (sizeof(io_t) == 2);
+    int mode = kAny;
+    if (!a.gate)
+        mode = kNoGate;
+    else if (!a.gate_wide)
+        mode = kNarrow;
+    else if (same)
+        mode = a.gate_rows > 1 ? kShared : kElement;
+    if (a.post != GRKAN_NORM_NONE)
+        return a.vec ? launch_gate<W, K, true, true>(a, mode, s) : launch_gate<W, K, false, true>(a, mode, s);
+    return a.vec ? launch_gate<W, K, true, false>(a, mode, s) : launch_gate<W, K, false, false>(a, mode, s);
 }
 
+// The pairs of (waves, K) that plans have.
 hipError_t launch_rows(const ResidualArgs &a, hipStream_t s) {
-    switch (a.p.waves) {
-        case 1: return launch_waves<1>(a, s);
-        case 2: return launch_waves<2>(a, s);
-        case 4: return launch_waves<4>(a, s);
-        case 8: return launch_waves<8>(a, s);
-        default: return launch_waves<16>(a, s);
+    switch (a.p.waves * 8 + a.p.K) {
+        case 8 + 1: return launch_kernel<1, 1>(a, s);
+        case 8 + 2: return launch_kernel<1, 2>(a, s);
+        case 8 + 3: return launch_kernel<1, 3>(a, s);
+        case 8 + 4: return launch_kernel<1, 4>(a, s);
+        case 16 + 2: return launch_kernel<2, 2>(a, s);
+        case 16 + 3: return launch_kernel<2, 3>(a, s);
+        case 32 + 2: return launch_kernel<4, 2>(a, s);
+        case 32 + 3: return launch_kernel<4, 3>(a, s);
+        case 64 + 2: return launch_kernel<8, 2>(a, s);
+        case 64 + 3: return launch_kernel<8, 3>(a, s);
+        case 64 + 4: return launch_kernel<8, 4>(a, s);
+        case 128 + 3: return launch_kernel<16, 3>(a, s);
+        case 128 + 4: return launch_kernel<16, 4>(a, s);
+        default: return hipErrorInvalidValue;
     }
 }
 

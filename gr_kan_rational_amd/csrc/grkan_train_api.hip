@@ -204,6 +204,7 @@ extern "C" grkan_status_t grkan_residual_norm_forward(
     a.ldx = ldx;
     a.ldf = ldf;
     a.gate_rows = gate ? rows / gates : 1;
+    a.gate_div = make_fastdiv((uint32_t)a.gate_rows);
     a.C = (int32_t)channels;
     a.norm = norm;
     a.post = post;
@@ -302,6 +303,7 @@ extern "C" grkan_status_t grkan_residual_norm_backward(
     a.lddh = lddh;
     a.lddz = lddz;
     a.gate_rows = gate ? rows / gates : 1;
+    a.gate_div = make_fastdiv((uint32_t)a.gate_rows);
     a.C = (int32_t)channels;
     a.norm = norm;
     a.post = post;

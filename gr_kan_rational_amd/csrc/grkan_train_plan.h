@@ -114,8 +114,8 @@ inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
 constexpr int64_t kMaxChannels = 16384;
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 
-// A row is held by `waves` waves, 4 K values a lane.  The backward's walkers (waves, or
-// workgroups of `waves` > 1) each take `walk` rows one after another.
+// A row is held by `waves` waves, 4 K values a lane.  The walkers (waves, or workgroups of
+// `waves` > 1) each take `walk` rows one after another.
 struct ResidualPlan {
     int32_t K, waves;
     int32_t per;             // rows that a workgroup holds at a time
@@ -137,24 +137,24 @@ inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_c
                           bool backward, ResidualPlan *p) {
     *p = ResidualPlan{};
     const int64_t quads = ceil_div(C, 4);
-    // 16 values a lane for a wave alone, else 12 while 8 waves hold a row so: the
-    // backward's sums and rows have to fit 256 registers
+    // A wave holds up to 256 accesses of a row, 8 waves as many each, else 192: the
+    // backward's sums and rows then fit 256 registers.  With a post norm's and a gate's
+    // for each channel among them a wave alone takes 192 too (37,824 rows of 1,024
+    // channels: 135 us, 232 with 256); 8 waves do not (4,728 rows of 8,192: 380 us, spilled,
+    // against 531 in 16 waves of half the registers).
+    const bool many = backward && post != GRKAN_NORM_NONE && gates > 0 && gate_channels == C;
+    const int64_t most = many ? 192 : 256;
     p->waves = 1;
-    while (p->waves < 8 && quads > (p->waves == 1 ? 256 : 192) * p->waves) p->waves *= 2;
-    if (quads > 256 * 8) p->waves = 16;
+    while (p->waves < 8 && quads > (p->waves == 1 ? most : 192) * p->waves) p->waves *= 2;
+    if (quads > 2048) p->waves = 16;
     p->K = (int32_t)ceil_div(quads, 64 * p->waves);
     p->per = p->waves == 1 ? 4 : 1;
-    if (!backward) {
-        p->blocks = ceil_div(rows > 0 ? rows : 1, p->per);
-        // (as many as the CUs hold, each over as many rows as the others)
-        const int64_t most = p->waves == 1 ? 1024 : 2048 / p->waves;
-        p->blocks = ceil_div(p->blocks, ceil_div(p->blocks, most));
-        return;
-    }
-    // as many walkers as the CUs hold, 8 waves each (16 of the widest rows)
-    const int64_t walkers = p->waves == 16 ? 256 : 2048 / p->waves;
+    // as many walkers as the CUs hold: 16 waves each, the backward 8 (16 of the widest
+    // rows)
+    const int64_t walkers = (backward && p->waves < 16 ? 2048 : 4096) / p->waves;
     p->walk = ceil_div(rows > 0 ? rows : 1, walkers);
     p->blocks = ceil_div(ceil_div(rows > 0 ? rows : 1, p->walk), p->per);
+    if (!backward) return;
     p->sums = post == GRKAN_NORM_NONE ? 3 : 4;
     p->off_sums = 0;
     p->off_gate = align256((size_t)p->blocks * p->sums * (size_t)C * 4);
