@@ -6,42 +6,119 @@
 #include "grkan_e4m3.h"
 #include "grkan_lanes.h"
 
+#include <type_traits>
+
 namespace grkan {
 namespace {
 
-// A workgroup takes 128 rows x 128 columns, 8 x 8 values a thread in registers.
-// The maxima of rows meet over 16 lanes, those of columns through LDS; the
-// transposed codes pass through LDS, so that both layouts leave as whole rows.
-template <class T>
-__global__ __launch_bounds__(256) void grkan_quantize_tile_kernel(QuantizeArgs a) {
-    __shared__ float colmax[16][kBlock8 + 1];
-    __shared__ float rowmax[kBlock8];
-    __shared__ uint8_t codes[kBlock8][kBlock8 + 8];
+// A lane's 8 columns: their values in a row, F applied.  RAT: 0 no activation, 1 the
+// rational with 8 columns in one activation group, 2 with any groups.
+template <class T, bool VEC, int RAT> struct Columns8 {
+    int c0, nv;   // first column, how many exist (at most 8; 0 or less: none)
+    Coefs<5, 4> coef;
+    __device__ inline Columns8(const QuantizeArgs &a, int c) : c0(c), nv(a.cols - c) {
+        if constexpr (RAT == 1) coef = load_coefs<5, 4>(a.A, a.B, nv > 0 ? c / a.dga : 0);
+    }
+    // As they lie in memory.
+    struct Raw {
+        u32x4 w[sizeof(T) / 2];
+    };
+    __device__ inline Raw fetch(const QuantizeArgs &a, int64_t row) const {
+        Raw r = {};
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx + c0;
+        if (row >= a.rows || nv <= 0) return r;
+        if (VEC && nv >= 8) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x) + i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e >= nv) continue;
+                if constexpr (sizeof(T) == 2)
+                    r.w[0][e / 2] |= (uint32_t)x[e] << (16 * (e & 1));
+                else
+                    r.w[e / 4][e % 4] = __float_as_uint(x[e]);
+            }
+        }
+        return r;
+    }
+    __device__ inline void values(const QuantizeArgs &a, const Raw &r, bool there, float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (sizeof(T) == 2)
+                v[e] = __uint_as_float((e & 1) ? (r.w[0][e / 2] & 0xffff0000u) : (r.w[0][e / 2] << 16));
+            else
+                v[e] = __uint_as_float(r.w[e / 4][e % 4]);
+            // (F(0) need not be 0: what does not exist stays 0)
+            if constexpr (RAT == 1) v[e] = there && e < nv ? rational<5, 4>(v[e], coef) : 0.0f;
+            if constexpr (RAT == 2)
+                v[e] = there && e < nv ? rational<5, 4>(v[e], load_coefs<5, 4>(a.A, a.B, (c0 + e) / a.dga)) : 0.0f;
+        }
+    }
+};
+
+__device__ static inline float finite_max8(const float (&v)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_size(v[e]));
+    return m;
+}
+
+// Rows alone: 16 lanes a block; a workgroup takes a column block of 16 kPasses rows,
+// so that a lane keeps its columns (and the rational's coefficients), all its loads
+// on their way at once.
+constexpr int kPasses = 4;
+
+template <class T, bool VEC, int RAT> __global__ __launch_bounds__(256) void grkan_quantize_rows_kernel(QuantizeArgs a) {
     const int t = (int)threadIdx.x, cl = t & 15, rg = t >> 4;
     const int cb = (a.cols + kBlock8 - 1) / kBlock8;
     const int bc = (int)blockIdx.x % cb, br = (int)blockIdx.x / cb;
-    const int c0 = bc * kBlock8 + cl * 8, r0 = br * kBlock8 + rg * 8;
-    const T *x = static_cast<const T *>(a.x);
-    float v[8][8];
-    Coefs<5, 4> coef;
+    const Columns8<T, VEC, RAT> c(a, bc * kBlock8 + cl * 8);
+    const int64_t r0 = (int64_t)br * (16 * kPasses) + rg;
+    typename Columns8<T, VEC, RAT>::Raw raw[kPasses];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kPasses; ++i) raw[i] = c.fetch(a, r0 + 16 * i);
+    const bool writes = c.c0 < (a.cols + 15) / 16 * 16;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[i][e] = r0 + i < a.rows && c0 + e < a.cols ? load1(x + (int64_t)(r0 + i) * a.ldx + c0 + e) : 0.0f;
-    if (a.A) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (c0 + e >= a.cols) continue;
-            coef = load_coefs<5, 4>(a.A, a.B, (c0 + e) / a.dga);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r0 + i < a.rows) v[i][e] = rational<5, 4>(v[i][e], coef);
-        }
+    for (int i = 0; i < kPasses; ++i) {
+        const int64_t r = r0 + 16 * i;
+        float v[8];
+        c.values(a, raw[i], r < a.rows, v);
+        const float s = block_scale(max16(finite_max8(v)));
+        if (r >= a.rows) continue;
+        if (writes) *reinterpret_cast<u32x2 *>(a.q + r * a.ldq + c.c0) = encode8(v, inverse_scale(s));
+        if (cl == 0) a.scale[(int64_t)bc * a.lds + r] = s;
     }
-    float rm[8], cm[8] = {};
+}
+
+// The larger of v in each lane and in the lanes 16, 32 and 48 away.
+__device__ static inline float max_of_rows(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// Columns, both, or a scale for 128 x 128: a workgroup takes that many, 8 x 8 values
+// a thread in registers, so x is read once.  The maxima of rows meet over 16 lanes,
+// those of columns over the wave's four groups of rows and then through LDS; the
+// transposed codes pass through LDS, so that both layouts leave as whole rows.
+template <class T, bool VEC, int RAT, bool TILE>
+__global__ __launch_bounds__(256) void grkan_quantize_tile_kernel(QuantizeArgs a) {
+    __shared__ __attribute__((aligned(16))) float colmax[4][kBlock8];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kBlock8][kBlock8 + 8];
+    const int t = (int)threadIdx.x, cl = t & 15, rg = t >> 4, wave = t >> 6;
+    const int cb = (a.cols + kBlock8 - 1) / kBlock8;
+    const int bc = (int)blockIdx.x % cb, br = (int)blockIdx.x / cb;
+    const Columns8<T, VEC, RAT> c(a, bc * kBlock8 + cl * 8);
+    const int64_t r0 = (int64_t)br * kBlock8 + rg * 8;
+    typename Columns8<T, VEC, RAT>::Raw raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = c.fetch(a, r0 + i);
+    float v[8][8], rm[8], cm[8] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        c.values(a, raw[i], r0 + i < a.rows, v[i]);
         rm[i] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -49,68 +126,93 @@ __global__ __launch_bounds__(256) void grkan_quantize_tile_kernel(QuantizeArgs a
             rm[i] = fmaxf(rm[i], m);
             cm[e] = fmaxf(cm[e], m);
         }
-        rm[i] = max16(rm[i]);
-        if (cl == 0) rowmax[rg * 8 + i] = rm[i];
     }
+    if constexpr (TILE) {
+        float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) colmax[rg][cl * 8 + e] = cm[e];
-    __syncthreads();
-    float all = 0.0f;
-    if (a.tile) {
-        for (int i = 0; i < kBlock8; ++i) all = fmaxf(all, rowmax[i]);
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, rm[i]);
+        m = max_of_rows(max16(m));
+        if ((t & 63) == 0) colmax[wave][0] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(colmax[0][0], colmax[1][0]), fmaxf(colmax[2][0], colmax[3][0]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rm[i] = cm[i] = m;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cm[e] = 0.0f;
+        for (int i = 0; i < 8; ++i) rm[i] = max16(rm[i]);
+        if (a.qt) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) cm[e] = fmaxf(cm[e], colmax[i][cl * 8 + e]);
+            for (int e = 0; e < 8; ++e) cm[e] = max_of_rows(cm[e]);
+            if ((t & 63) < 16) {
+                *reinterpret_cast<f32x4 *>(&colmax[wave][cl * 8]) = f32x4{cm[0], cm[1], cm[2], cm[3]};
+                *reinterpret_cast<f32x4 *>(&colmax[wave][cl * 8 + 4]) = f32x4{cm[4], cm[5], cm[6], cm[7]};
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                cm[e] = fmaxf(fmaxf(colmax[0][cl * 8 + e], colmax[1][cl * 8 + e]), fmaxf(colmax[2][cl * 8 + e], colmax[3][cl * 8 + e]));
         }
     }
     if (a.q) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float s = block_scale(a.tile ? all : rm[i]), inv = inverse_scale(s);
-            const int r = r0 + i;
+            const int64_t r = r0 + i;
+            const float s = block_scale(rm[i]);
             if (r >= a.rows) continue;
-            const u32x2 w = encode8(v[i], inv);
-            uint8_t *to = a.q + (int64_t)r * a.ldq + c0;
-            if (c0 < (a.cols + 15) / 16 * 16) *reinterpret_cast<u32x2 *>(to) = w;
-            if (cl == 0 && !a.tile) a.scale[(int64_t)bc * a.lds + r] = s;
+            if (c.c0 < (a.cols + 15) / 16 * 16) *reinterpret_cast<u32x2 *>(a.q + r * a.ldq + c.c0) = encode8(v[i], inverse_scale(s));
+            if (cl == 0 && !TILE) a.scale[(int64_t)bc * a.lds + r] = s;
         }
-        if (a.tile && t == 0) a.scale[(int64_t)bc * a.lds + br] = block_scale(all);
+        if (TILE && t == 0) a.scale[(int64_t)bc * a.lds + br] = block_scale(rm[0]);
     }
     if (a.qt) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float s = block_scale(a.tile ? all : cm[e]), inv = inverse_scale(s);
+            const float s = block_scale(cm[e]);
             float u[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) u[i] = v[i][e];
-            *reinterpret_cast<u32x2 *>(&codes[cl * 8 + e][rg * 8]) = encode8(u, inv);
-            if (rg == 0 && !a.tile && c0 + e < a.cols) a.scale_t[(int64_t)br * a.ldst + c0 + e] = s;
+            *reinterpret_cast<u32x2 *>(&codes[cl * 8 + e][rg * 8]) = encode8(u, inverse_scale(s));
+            if (rg == 0 && !TILE && e < c.nv) a.scale_t[(int64_t)br * a.ldst + c.c0 + e] = s;
         }
-        if (a.tile && t == 0) a.scale_t[(int64_t)br * a.ldst + bc] = block_scale(all);
+        if (TILE && t == 0) a.scale_t[(int64_t)br * a.ldst + bc] = block_scale(rm[0]);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = bc * kBlock8 + rg * 8 + i, r = br * kBlock8 + cl * 8;
-            if (c < a.cols && r < (a.rows + 15) / 16 * 16)
-                *reinterpret_cast<u32x2 *>(a.qt + (int64_t)c * a.ldqt + r) =
-                    *reinterpret_cast<const u32x2 *>(&codes[rg * 8 + i][cl * 8]);
+            // 16 columns a pass, 16 lanes to the 128 rows of one
+            const int col = 16 * i + rg, cc = bc * kBlock8 + col;
+            const int64_t r = (int64_t)br * kBlock8 + cl * 8;
+            if (cc < a.cols && r < ((int64_t)a.rows + 15) / 16 * 16)
+                *reinterpret_cast<u32x2 *>(a.qt + (int64_t)cc * a.ldqt + r) = *reinterpret_cast<const u32x2 *>(&codes[col][cl * 8]);
         }
     }
+}
+
+template <class T, bool VEC, int RAT> hipError_t launch_kind(const QuantizeArgs &a, hipStream_t s) {
+    const int64_t cb = (a.cols + kBlock8 - 1) / kBlock8;
+    if (!a.qt && !a.tile) {
+        const int64_t rb = ((int64_t)a.rows + 16 * kPasses - 1) / (16 * kPasses);
+        hipLaunchKernelGGL((grkan_quantize_rows_kernel<T, VEC, RAT>), dim3((unsigned)(cb * rb)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(cb * (((int64_t)a.rows + kBlock8 - 1) / kBlock8)));
+    if (a.tile)
+        hipLaunchKernelGGL((grkan_quantize_tile_kernel<T, VEC, RAT, true>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((grkan_quantize_tile_kernel<T, VEC, RAT, false>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <class T> hipError_t launch_type(const QuantizeArgs &a, hipStream_t s) {
+    const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (int64_t)sizeof(T) % 16 == 0;
+    if (!a.A) return vec ? launch_kind<T, true, 0>(a, s) : launch_kind<T, false, 0>(a, s);
+    if (a.dga % 8 == 0) return vec ? launch_kind<T, true, 1>(a, s) : launch_kind<T, false, 1>(a, s);
+    return launch_kind<T, false, 2>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s) {
-    const unsigned cb = (unsigned)((a.cols + kBlock8 - 1) / kBlock8);
-    const unsigned rb = (unsigned)(((int64_t)a.rows + kBlock8 - 1) / kBlock8);
-    if (a.bf16)
-        hipLaunchKernelGGL((grkan_quantize_tile_kernel<uint16_t>), dim3(cb * rb), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((grkan_quantize_tile_kernel<float>), dim3(cb * rb), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return a.bf16 ? launch_type<uint16_t>(a, s) : launch_type<float>(a, s);
 }
 
 }  // namespace grkan
