@@ -21,37 +21,36 @@ __device__ static inline uint32_t mix(uint32_t h) {
 }
 
 // beta^step by squaring.
-__device__ static inline double power(double beta, int64_t step) {
+__host__ __device__ static inline double power(double beta, int64_t step) {
     double p = 1.0;
     for (uint64_t k = (uint64_t)step; k; k >>= 1, beta *= beta)
         if (k & 1) p *= beta;
     return p;
 }
 
-struct Factors {
-    float beta1, rest1, beta2, rest2, keep, rate, root, eps, clip;
-};
-
-__device__ static inline Factors factors(const AdamwArgs &a, int64_t step) {
-    const double lr = a.lr_ptr ? (double)*a.lr_ptr : a.lr;
-    Factors f;
-    f.beta1 = (float)a.beta1;
-    f.rest1 = (float)(1.0 - a.beta1);
-    f.beta2 = (float)a.beta2;
-    f.rest2 = (float)(1.0 - a.beta2);
-    f.keep = (float)(1.0 - lr * a.decay);
-    f.rate = (float)(lr / (1.0 - power(a.beta1, step)));
-    f.root = (float)(1.0 / sqrt(1.0 - power(a.beta2, step)));
-    f.eps = a.eps;
-    f.clip = a.grad_scale ? *a.grad_scale : 1.0f;
+// The same on the host and on the device: a step that is known before the launch
+// has them among the kernel's arguments (on the device they take 4 us of a workgroup's
+// time).
+__host__ __device__ static inline AdamwFactors factors(double lr, double beta1, double beta2, double decay, double eps,
+                                                       int64_t step) {
+#pragma clang fp contract(off)
+    AdamwFactors f;
+    f.beta1 = (float)beta1;
+    f.rest1 = (float)(1.0 - beta1);
+    f.beta2 = (float)beta2;
+    f.rest2 = (float)(1.0 - beta2);
+    f.keep = (float)(1.0 - lr * decay);
+    f.rate = (float)(lr / (1.0 - power(beta1, step)));
+    f.root = (float)(1.0 / sqrt(1.0 - power(beta2, step)));
+    f.eps = (float)eps;
     return f;
 }
 
 // One value; m is the first moment, v the second.  Each operation is rounded
 // by itself.
-__device__ static inline float update(const Factors &f, bool clip, float w, float g, float &m, float &v) {
+__device__ static inline float update(const AdamwFactors &f, bool clip, float scale, float w, float g, float &m, float &v) {
 #pragma clang fp contract(off)
-    if (clip) g = g * f.clip;
+    if (clip) g = g * scale;
     m = f.beta1 * m + f.rest1 * g;
     v = f.beta2 * v + f.rest2 * g * g;
     const float d = sqrtf(v) * f.root + f.eps;
@@ -70,7 +69,7 @@ __device__ static inline float round_up_sometimes(float y, uint32_t random16) {
 }
 
 template <class T, bool VEC>
-__device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, const Factors &f, int64_t base) {
+__device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, const AdamwFactors &f, float scale, int64_t base) {
 #pragma unroll
     for (int i = 0; i < kAdamwChunk / 1024; ++i) {
         const int64_t at = base + 1024 * i + 4 * (int)threadIdx.x;
@@ -99,7 +98,7 @@ __device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float me = m[e], ve = v[e];
-            w[e] = update(f, a.grad_scale != nullptr, w[e], g[e], me, ve);
+            w[e] = update(f, a.grad_scale != nullptr, scale, w[e], g[e], me, ve);
             m[e] = me;
             v[e] = ve;
         }
@@ -109,7 +108,7 @@ __device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, c
 
 // A lane holds 8 values side by side, 16 lanes a block.
 template <class T, bool VEC>
-__device__ static inline void step8(const AdamwArgs &a, const AdamwTensor &t, const Factors &f, int64_t base,
+__device__ static inline void step8(const AdamwArgs &a, const AdamwTensor &t, const AdamwFactors &f, float scale, int64_t base,
                                     uint32_t block, uint32_t key) {
 #pragma unroll
     for (int i = 0; i < kAdamwChunk / 2048; ++i) {
@@ -141,7 +140,7 @@ __device__ static inline void step8(const AdamwArgs &a, const AdamwTensor &t, co
                 const bool there = e < nv;
                 float me = mv[e] * ms, ve = rv[e] * rs;
                 ve = ve * ve;
-                w[4 * q + e] = update(f, a.grad_scale != nullptr, we[e], ge[e], me, ve);
+                w[4 * q + e] = update(f, a.grad_scale != nullptr, scale, we[e], ge[e], me, ve);
                 m[4 * q + e] = there ? me : 0.0f;
                 r[4 * q + e] = there ? sqrtf(ve) : 0.0f;
             }
@@ -169,9 +168,9 @@ __device__ static inline void step8(const AdamwArgs &a, const AdamwTensor &t, co
             const uint32_t h = mix(bk + place + e);
             const float my = scaled(m[e], minv), ry = scaled(r[e], rinv);
             const float up = round_up_sometimes(ry, h >> 16);
-            // (a NaN's payload does not survive the rounding: it is put back)
-            m[e] = my == my ? round_up_sometimes(my, h & 0xffffu) : my;
-            r[e] = ry == ry ? (ry > 0.0f ? fmaxf(up, 0.001953125f) : up) : ry;
+            // (the one NaN that `scaled` gives survives the rounding)
+            m[e] = round_up_sometimes(my, h & 0xffffu);
+            r[e] = ry > 0.0f ? fmaxf(up, 0.001953125f) : up;
         }
         *reinterpret_cast<u32x2 *>(avg) = u32x2{encode4(m[0], m[1], m[2], m[3]), encode4(m[4], m[5], m[6], m[7])};
         *reinterpret_cast<u32x2 *>(sq) = u32x2{encode4(r[0], r[1], r[2], r[3]), encode4(r[4], r[5], r[6], r[7])};
@@ -191,14 +190,16 @@ template <int BITS> __global__ __launch_bounds__(256) void grkan_adamw_kernel(Ad
     const AdamwTensor t = a.t[it];
     const int64_t base = (int64_t)(blockIdx.x - a.first[it]) * kAdamwChunk;
     const int64_t step = a.step_ptr ? *a.step_ptr : a.step;
-    const Factors f = factors(a, step);
+    AdamwFactors f = a.f;
+    if (a.lr_ptr || a.step_ptr) f = factors(a.lr_ptr ? (double)*a.lr_ptr : a.lr, a.beta1, a.beta2, a.decay, a.eps, step);
+    const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
     const uint8_t flags = a.flags[it];
     auto go = [&](auto type, auto vec) {
         using T = decltype(type);
         if constexpr (BITS == 32)
-            step32<T, vec()>(a, t, f, base);
+            step32<T, vec()>(a, t, f, scale, base);
         else
-            step8<T, vec()>(a, t, f, base, a.block[it], mix(mix(a.seed) + (uint32_t)step));
+            step8<T, vec()>(a, t, f, scale, base, a.block[it], mix(mix(a.seed) + (uint32_t)step));
     };
     if (flags & kAdamwBf16) {
         if (flags & kAdamwVec)
@@ -214,6 +215,8 @@ template <int BITS> __global__ __launch_bounds__(256) void grkan_adamw_kernel(Ad
 }
 
 }  // namespace
+
+void prepare_adamw(AdamwArgs &a) { a.f = factors(a.lr, a.beta1, a.beta2, a.decay, a.eps, a.step); }
 
 hipError_t launch_adamw(const AdamwArgs &a, int bits, hipStream_t s) {
     const unsigned grid = a.first[a.count];

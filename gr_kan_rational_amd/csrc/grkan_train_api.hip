@@ -378,8 +378,9 @@ extern "C" grkan_status_t grkan_adamw_step(const grkan_adamw_tensor_t *tensors, 
     a.lr_ptr = y.lr_ptr;
     a.step_ptr = y.step_ptr;
     a.grad_scale = y.grad_scale;
-    a.eps = (float)y.eps;
+    a.eps = y.eps;
     a.seed = y.seed;
+    if (!a.lr_ptr && !a.step_ptr) prepare_adamw(a);
     // First all launches' overlaps, then the launches.
     for (int pass = 0; pass < 2; ++pass) {
         int64_t groups = 0, block = 0;

@@ -6,7 +6,10 @@ Argument marshalling only, as in block.py: every step of the computation is a HI
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
+from itertools import chain
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -51,7 +54,7 @@ def _library() -> ctypes.CDLL:
     lib.grkan_residual_norm_forward.argtypes = [vp] * 11 + [i64] * 6 + [f32] + [i32] * 4 + [vp]
     lib.grkan_residual_norm_backward.argtypes = [vp] * 18 + [i64] * 7 + [i32] * 4 + [vp, sz, vp]
     lib.grkan_residual_norm_backward_workspace_size.argtypes = [i64] * 4 + [i32] * 2
-    lib.grkan_adamw_step.argtypes = [ctypes.POINTER(grkan_adamw_tensor_t), i64, ctypes.POINTER(grkan_adamw_t), i32, vp]
+    lib.grkan_adamw_step.argtypes = [vp, i64, ctypes.POINTER(grkan_adamw_t), i32, vp]
     for name in ("fp8_quantize", "fp8_matmul", "residual_norm_forward", "residual_norm_backward", "adamw_step"):
         getattr(lib, f"grkan_{name}").restype = ctypes.c_int
     lib.grkan_fp8_matmul_workspace_size.restype = sz
@@ -98,12 +101,14 @@ def _matrix(t: torch.Tensor, name: str, dev=None):
 
 def _codes(rows: int, cols: int, dev):
     """An e4m3 [rows, cols] tensor whose rows start 16 bytes apart or a multiple."""
+    if cols % 16 == 0:
+        return torch.empty((rows, cols), dtype=F8, device=dev)
     return torch.empty((rows, _up(cols, 16)), dtype=F8, device=dev)[:, :cols]
 
 
 def _scales(rows: int, blocks: int, dev):
     """A float32 [rows, blocks] tensor, the rows of a block side by side."""
-    return torch.empty((blocks, rows), dtype=torch.float32, device=dev).t()
+    return torch.empty_strided((rows, blocks), (1, max(rows, 1)), dtype=torch.float32, device=dev)
 
 
 def grkan_fp8_quantize(x: torch.Tensor, outputs: str = "rows", tile: bool = False, act: str = "none", A=None, B=None,
@@ -437,6 +442,53 @@ def _scalar(t, name: str, dtype, dev):
     return t.data_ptr()
 
 
+_dtype, _size, _whole, _place, _at = (operator.attrgetter("dtype"), torch.Tensor.numel, torch.Tensor.is_contiguous,
+                                      torch.Tensor.get_device, torch.Tensor.data_ptr)
+
+
+def _all(want, of, tensors) -> bool:
+    """Whether of(t) is `want` for all."""
+    return all(got == want for got in map(of, tensors))
+
+
+def _adamw_table(params, grads, masters, avgs, sqs, avg_scales, sq_scales, eight: bool, dev) -> array.array:
+    """The tensors as an array of grkan_adamw_tensor_t, checked list by list (hundreds of tensors a step: a
+    check costs as much as a small launch if it is made one tensor at a time)."""
+    n, f32 = len(params), torch.float32
+    state = F8 if eight else f32
+    dtypes, counts = list(map(_dtype, params)), list(map(_size, params))
+    held = [-(-k // BLOCK) * BLOCK for k in counts] if eight else counts
+    scales = [k // BLOCK for k in held]
+    for d in set(dtypes):
+        if d not in _IO:
+            raise TypeError(f"parameters must be float32 or bfloat16, got {d}")
+    if list(map(_dtype, grads)) != dtypes or list(map(_size, grads)) != counts:
+        raise ValueError("each gradient must have its parameter's size and dtype")
+    if not (_all(state, _dtype, avgs) and _all(state, _dtype, sqs) and list(map(_size, avgs)) == held
+            and list(map(_size, sqs)) == held):
+        raise ValueError(f"avgs and sqs must be {state} of the parameters' sizes" + (", whole blocks of 128" if eight else ""))
+    others = [params, grads, avgs, sqs]
+    if eight:
+        for t, name in ((avg_scales, "avg_scales"), (sq_scales, "sq_scales")):
+            if not _all(f32, _dtype, t) or list(map(_size, t)) != scales:
+                raise ValueError(f"{name} must be float32, one for each block of 128")
+        others += [avg_scales, sq_scales]
+    main = [0] * n
+    if masters is not None:
+        kept = [w for w in masters if w is not None]
+        if not _all(f32, _dtype, kept) or any(w is not None and w.numel() != k for w, k in zip(masters, counts)):
+            raise ValueError("masters must be float32 of their parameters' sizes")
+        others.append(kept)
+        main = [0 if w is None else w.data_ptr() for w in masters]
+    if not _all(dev.index, _place, chain(*others)) or not all(map(_whole, chain(*others))):
+        raise ValueError(f"all tensors must be contiguous and on {dev}")
+    none = [0] * n
+    rows = zip(map(_at, params), map(_at, grads), main, map(_at, avgs), map(_at, sqs),
+               map(_at, avg_scales) if eight else none, map(_at, sq_scales) if eight else none, counts,
+               map(_IO.__getitem__, dtypes))
+    return array.array("q", chain.from_iterable(rows))
+
+
 def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, beta2: float = 0.999,
                      eps: float = 1e-8, weight_decay: float = 1e-2, masters=None, avg_scales=None, sq_scales=None,
                      grad_scale=None, seed: int = 0, stream=None) -> None:
@@ -454,43 +506,18 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
     eight = avg_scales is not None or sq_scales is not None
     if eight and (avg_scales is None or sq_scales is None):
         raise ValueError("avg_scales and sq_scales come together")
-    lists = {"grads": grads, "avgs": avgs, "sqs": sqs, "masters": masters, "avg_scales": avg_scales,
-             "sq_scales": sq_scales}
-    for name, got in lists.items():
+    for name, got in (("grads", grads), ("avgs", avgs), ("sqs", sqs), ("masters", masters), ("avg_scales", avg_scales),
+                      ("sq_scales", sq_scales)):
         if got is not None and len(got) != n:
             raise ValueError(f"{name} must be a list of {n}")
     if n == 0:
         return
     _on_gpu(params[0])
     dev = params[0].device
-    table = (grkan_adamw_tensor_t * n)()
-    f32, bf16 = torch.float32, torch.bfloat16
-    state = F8 if eight else f32
-    for i in range(n):
-        p, g, m, v = params[i], grads[i], avgs[i], sqs[i]
-        w = None if masters is None else masters[i]
-        count, dtype = p.numel(), p.dtype
-        if dtype is not f32 and dtype is not bf16:
-            raise TypeError(f"parameters must be float32 or bfloat16, got {dtype}")
-        held = -(-count // BLOCK) * BLOCK if eight else count
-        if not (p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and v.is_contiguous() and g.dtype is dtype
-                and m.dtype is state and v.dtype is state and g.numel() == count and m.numel() == held
-                and v.numel() == held and p.device == dev and g.device == dev and m.device == dev and v.device == dev):
-            raise ValueError(f"tensor {i}: gradient and states must be contiguous, match the parameter's size and be on "
-                             f"{dev}, the gradient in {dtype}, the states in {state}")
-        row = table[i]
-        row.param, row.grad, row.avg, row.sq = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
-        row.n, row.io = count, GRKAN_F32 if dtype is f32 else GRKAN_BF16
-        if w is not None:
-            _check_out(w, "master", f32, count, dev)
-            row.master = w.data_ptr()
-        if eight:
-            for t, name in ((avg_scales[i], "avg_scales"), (sq_scales[i], "sq_scales")):
-                _check_out(t, name, f32, held // BLOCK, dev)
-            row.avg_scale, row.sq_scale = avg_scales[i].data_ptr(), sq_scales[i].data_ptr()
+    table = _adamw_table(params, grads, masters, avgs, sqs, avg_scales, sq_scales, eight, dev)
     hyper = grkan_adamw_t(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, seed=seed & 0xFFFFFFFF)
     if isinstance(lr, torch.Tensor):
-        hyper.lr_ptr = _scalar(lr, "lr", f32, dev)
+        hyper.lr_ptr = _scalar(lr, "lr", torch.float32, dev)
     else:
         hyper.lr = lr
     if isinstance(step, torch.Tensor):
@@ -498,11 +525,11 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
     else:
         hyper.step = step
     if grad_scale is not None:
-        hyper.grad_scale = _scalar(grad_scale, "grad_scale", f32, dev)
+        hyper.grad_scale = _scalar(grad_scale, "grad_scale", torch.float32, dev)
     lib = _library()
 
     def launch(handle):
-        st = lib.grkan_adamw_step(table, n, ctypes.byref(hyper), 8 if eight else 32, handle)
+        st = lib.grkan_adamw_step(table.buffer_info()[0], n, ctypes.byref(hyper), 8 if eight else 32, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_adamw_step")
 

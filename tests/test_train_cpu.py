@@ -212,7 +212,7 @@ def adamw(lib, tensors, bits=32, hyper=None, count=None):
         for k, v in dict(T, **t).items():
             setattr(row, k, v)
     h = train.grkan_adamw_t(**dict(H, **(hyper or {})))
-    return lib.grkan_adamw_step(table, len(tensors) if count is None else count, ctypes.byref(h), bits, None)
+    return lib.grkan_adamw_step(ctypes.addressof(table), len(tensors) if count is None else count, ctypes.byref(h), bits, None)
 
 
 A_BAD = [
