@@ -17,7 +17,7 @@ from torch.autograd.function import once_differentiable
 from . import binding
 from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_out, _on_gpu
 from .block import (_IO, GRKAN_ACT_NONE, GRKAN_ACT_RATIONAL, _act_coefs, _channel_vector, _given, _io, _like,
-                    _on_stream, _ptr, _skipped, _space, _wanted, grkan_linear_act_backward)
+                    _need, _on_stream, _ptr, _skipped, _space, _wanted, grkan_linear_act_backward)
 
 BLOCK = 128  # values that share a scale
 F8 = torch.float8_e4m3fn
@@ -200,7 +200,7 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
             raise ValueError(f"residual must be [{m}, {n}] in {dtype}")
         ldr = _matrix(residual, "residual", dev)[2]
     lib = _library()
-    need = lib.grkan_fp8_matmul_workspace_size(m, n, k)
+    need = _need("fp8_matmul", m, n, k)
 
     def launch(handle):
         c = _given(out, "out", (m, n), dtype, dev)
@@ -316,11 +316,11 @@ def grkan_residual_norm_forward(x: torch.Tensor, f: torch.Tensor, norm: str = "l
     for t, name in ((out, "out"), (normed, "normed")):
         if t is not None and t.shape != x.shape:
             raise ValueError(f"{name} must match x")
-    lib = _library()
+    lib, dense = _library(), x.is_contiguous()
 
     def launch(handle):
-        h = _given(out, "out", x.shape, x.dtype, dev)
-        z = _given(normed, "normed", x.shape, x.dtype, dev)
+        h = _given(out, "out", x.shape, x.dtype, dev) if out is not None or not dense else torch.empty_like(x)
+        z = _given(normed, "normed", x.shape, x.dtype, dev) if normed is not None or not dense else torch.empty_like(x)
         st = _given(stats, "stats", (2 if post == "none" else 4, rows), torch.float32, dev)
         got = lib.grkan_residual_norm_forward(x.data_ptr(), f.data_ptr(), _ptr(weight), _ptr(bias), _ptr(scale),
                                               _ptr(gate), _ptr(post_weight), _ptr(post_bias), h.data_ptr(),
@@ -373,7 +373,7 @@ def grkan_residual_norm_backward(f: torch.Tensor, h: torch.Tensor, dh, dz, stats
         if t is not None and t.shape != h.shape:
             raise ValueError(f"{name} must match h")
     lib = _library()
-    need = lib.grkan_residual_norm_backward_workspace_size(rows, c, gates, gc, _POSTS[post], io)
+    need = _need("residual_norm_backward", rows, c, gates, gc, _POSTS[post], io)
     absent = set(skip)
     for name, t in (("dgate", gate), ("dbias", bias), ("dpost_weight", post_weight), ("dpost_bias", post_bias)):
         if t is None:
