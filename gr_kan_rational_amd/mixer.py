@@ -69,7 +69,8 @@ class GRKANStack(torch.nn.Module):
 
         f = F2(F1(z) W1^T + b1) W2^T + b2,    h = h + scale gate post(f),    z = norm(h)
 
-    and z of the last one is the result.  ``forward(x)`` takes bfloat16 x [..., dim], samples first.  ``products``
+    and z of the last one is the result.  ``forward(x)`` takes bfloat16 x [..., dim], samples first (of x [dim]
+    one).  ``products``
     is "bf16" or "fp8" (e4m3, a scale for each block of 128).  ``post`` is "none", "layer" or "rms".  ``scale``
     is the residual scale's first value.  ``drop`` is the rate at which, in training, a sample's branch is left
     out (the others scaled up to match), rising from 0 at the first mixer.  Weights are bfloat16, all else
@@ -125,8 +126,9 @@ class GRKANStack(torch.nn.Module):
             return [None] * len(self.blocks)
         depth = len(self.blocks)
         rates = torch.arange(depth, device=x.device, dtype=torch.float32).mul_(self.drop / max(depth - 1, 1))
-        kept = torch.rand(depth, x.shape[0], device=x.device) >= rates[:, None]
-        return list((kept / (1.0 - rates)[:, None]).view(depth, x.shape[0], *(1,) * (x.dim() - 1)))
+        samples = (x.shape[0], *(1,) * (x.dim() - 1)) if x.dim() > 1 else (1,)
+        kept = torch.rand(depth, samples[0], device=x.device) >= rates[:, None]
+        return list((kept / (1.0 - rates)[:, None]).view(depth, *samples))
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         x = x.contiguous()

@@ -350,3 +350,12 @@ def test_random_numbers_are_even():
         assert abs(v.mean()) < 5 * 12 ** -0.5 / n ** 0.5
         counts = torch.histc(v, 64, -0.5, 0.5)
         assert (counts - n / 64).abs().max() < 5 * (n / 64) ** 0.5
+
+
+def test_stack_gates_of_one_row():
+    """x without leading dimensions is one sample."""
+    from gr_kan_rational_amd.mixer import GRKANStack
+
+    s = GRKANStack(2, 16, 16, drop=0.5).train()
+    assert [tuple(g.shape) for g in s.gates(torch.zeros(16))] == [(1,), (1,)]
+    assert [tuple(g.shape) for g in s.gates(torch.zeros(3, 5, 16))] == [(3, 1, 1)] * 2
