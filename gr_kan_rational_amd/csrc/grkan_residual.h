@@ -21,7 +21,8 @@ struct ResidualArgs {
     float *sums;                     // [blocks][sums][C]
     float *gate_sums;                // [units][C] or [rows]
     int64_t rows, ldx, ldf, lddh, lddz;
-    int64_t gate_rows;               // rows that share a gate row
+    int64_t gates;                   // gate rows
+    int64_t gate_rows;               // rows that share one
     FastDiv gate_div;                // division by it
     int32_t C;
     int32_t norm, post;

@@ -457,7 +457,7 @@ __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs 
     if ((int)blockIdx.x >= columns) {
         const int64_t i = (int64_t)((int)blockIdx.x - columns) * 1024 + t;
         if (i >= gates) return;
-        if (a.gate_wide) {
+        if (a.gate_wide && a.gate_rows > 0) {
             const int64_t g = i / a.C, col = i - g * a.C, first = g * a.gate_rows / a.p.walk;
             const int64_t last = ((g + 1) * a.gate_rows - 1) / a.p.walk;
             if (first == last) return;  // (written by its walker)
@@ -566,14 +566,13 @@ hipError_t launch_rows(const ResidualArgs &a, hipStream_t s) {
 #if !GRKAN_RESIDUAL_BACKWARD
 template <> hipError_t launch_residual_forward<io_t>(const ResidualArgs &a, hipStream_t s) { return launch_rows(a, s); }
 #else
+// (without rows the sums are all that is left, zeros)
 template <> hipError_t launch_residual_backward<io_t>(const ResidualArgs &a, hipStream_t s) {
-    hipError_t e = launch_rows(a, s);
+    hipError_t e = a.rows > 0 ? launch_rows(a, s) : hipSuccess;
     if (e != hipSuccess) return e;
     const bool sums = a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias;
     const int columns = sums ? 3 * ((a.C + 31) / 32) : 0;
-    int64_t gates = 0;
-    if (a.dgate && a.gate_rows > 1)
-        gates = a.rows / a.gate_rows * (a.gate_wide ? a.C : 1);
+    const int64_t gates = a.dgate && a.gate_rows != 1 ? a.gates * (a.gate_wide ? a.C : 1) : 0;
     const int64_t grid = columns + (gates + 1023) / 1024;
     if (grid > 0) {
         hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3((unsigned)grid), dim3(1024), 0, s, a, columns, gates);

@@ -8,7 +8,6 @@
 #include "grkan_adamw.h"
 #include "grkan_check.h"
 #include "grkan_fp8.h"
-#include "grkan_launch.h"
 #include "grkan_residual.h"
 #include "grkan_train.h"
 
@@ -249,7 +248,8 @@ extern "C" grkan_status_t grkan_residual_norm_backward(
         return GRKAN_ERR_UNSUPPORTED;
     if (rows > 0 && (!f || !h || !stats || (!dh && !dz))) return GRKAN_ERR_INVALID_ARG;
     ResidualArgs a{};
-    if (rows > 0) residual_plan(rows, channels, gate ? gates : 0, gate_channels, post, true, &a.p);
+    residual_plan(rows, channels, gate ? gates : 0, gate_channels, post, true, &a.p);
+    if (rows == 0) a.p.blocks = a.p.total = 0;
     const size_t cb = (size_t)channels * 4, out = (size_t)rows * channels * es;
     const size_t gb = gate ? (size_t)gates * gate_channels * gs : 0;
     const Range rdh{dh, dh ? rows_bytes(rows, channels, lddh, es) : 0};
@@ -268,15 +268,6 @@ extern "C" grkan_status_t grkan_residual_norm_backward(
     if (a.p.total && (!workspace || workspace_bytes < a.p.total)) return GRKAN_ERR_INVALID_ARG;
     if (a.p.total && !aligned(workspace, 256)) return GRKAN_ERR_UNSUPPORTED;
     // ---- validation done; HIP calls from here on
-    if (rows == 0) {
-        float *const sums[] = {dscale, dweight, dbias, dpost_weight, dpost_bias};
-        for (float *s : sums)
-            if (s) {
-                const hipError_t e = launch_zero(s, s, channels, 0, stream);
-                if (e != hipSuccess) return from_hip(e);
-            }
-        return GRKAN_OK;
-    }
     char *ws = static_cast<char *>(workspace);
     a.f = f;
     a.h = const_cast<void *>(h);
@@ -287,10 +278,11 @@ extern "C" grkan_status_t grkan_residual_norm_backward(
     a.dgate = dgate;
     a.stats = const_cast<float *>(stats);
     a.weight = weight;
-    a.scale = scale;
-    a.post_weight = post_weight;
-    a.post_bias = post_bias;
+    a.scale = rows > 0 ? scale : nullptr;  // (may be what no rows leave zero)
+    a.post_weight = rows > 0 ? post_weight : nullptr;
+    a.post_bias = rows > 0 ? post_bias : nullptr;
     a.gate = gate;
+    a.gates = gate ? gates : 0;
     a.dweight = dweight;
     a.dbias = dbias;
     a.dscale = dscale;
@@ -302,8 +294,8 @@ extern "C" grkan_status_t grkan_residual_norm_backward(
     a.ldf = ldf;
     a.lddh = lddh;
     a.lddz = lddz;
-    a.gate_rows = gate ? rows / gates : 1;
-    a.gate_div = make_fastdiv((uint32_t)a.gate_rows);
+    a.gate_rows = a.gates > 0 ? rows / gates : 1;
+    a.gate_div = make_fastdiv((uint32_t)(rows > 0 ? a.gate_rows : 1));
     a.C = (int32_t)channels;
     a.norm = norm;
     a.post = post;

@@ -129,7 +129,7 @@ inline grkan_status_t residual_shape(int64_t rows, int64_t C, int64_t gates, int
     if (io != GRKAN_F32 && io != GRKAN_BF16) return GRKAN_ERR_INVALID_ARG;
     if (rows < 0 || C < 1 || gates < 0) return GRKAN_ERR_INVALID_ARG;
     if (gates > 0 && (rows % gates != 0 || (gate_channels != 1 && gate_channels != C))) return GRKAN_ERR_INVALID_ARG;
-    if (C > kMaxChannels || rows > INT32_MAX) return GRKAN_ERR_UNSUPPORTED;
+    if (C > kMaxChannels || rows > INT32_MAX || gates > INT32_MAX) return GRKAN_ERR_UNSUPPORTED;
     return GRKAN_OK;
 }
 

@@ -283,7 +283,7 @@ def _gate(gate, lead, rows: int, channels: int, io_dtype, dev):
             ended = True
         else:
             raise ValueError(f"gate {list(shape)} does not repeat over whole runs of rows of {[*lead, channels]}")
-    return max(gates, 1) if rows else 1, shape[-1], _IO[gate.dtype]
+    return gates, shape[-1], _IO[gate.dtype]
 
 
 def grkan_residual_norm_forward(x: torch.Tensor, f: torch.Tensor, norm: str = "layer", weight=None, bias=None,

@@ -127,7 +127,7 @@ typedef enum GRKAN_ENUM_INT {
  *   rows >= 0 (0 is a no-op), channels >= 1.
  * Statistics are formed in fp32 about the mean from values held on chip.  A NaN or
  * infinity in a row makes that row's results NaN and touches no other row.
- * GRKAN_ERR_UNSUPPORTED: channels above 16384, rows >= 2^31, a stride above 2^31, a
+ * GRKAN_ERR_UNSUPPORTED: channels above 16384, rows or gates >= 2^31, a stride above 2^31, a
  * misaligned pointer.
  */
 GRKAN_API grkan_status_t grkan_residual_norm_forward(
@@ -156,7 +156,7 @@ GRKAN_API grkan_status_t grkan_residual_norm_forward(
  *             any other overlap is GRKAN_ERR_INVALID_ARG.
  *   d...      fp32 [channels], overwritten; dgate [gates][gate_channels] in gate_io.
  *             dpost_weight and dpost_bias only with a post norm, dgate with a gate.
- *   Each output may be NULL (not computed).  rows = 0 writes zeros to the sums.
+ *   Each output may be NULL (not computed).  rows = 0 writes zeros to the sums and dgate.
  *   workspace grkan_residual_norm_backward_workspace_size() bytes, 256-byte aligned.
  */
 GRKAN_API grkan_status_t grkan_residual_norm_backward(

@@ -222,3 +222,19 @@ def test_autograd(gk):
         want = dict(zip(NAMES, gk.grkan_residual_norm_backward(f.detach(), h, dh, dz, stats, **plain)))
         for name, t in zip(("dx", "df", "dweight", "dbias", "dscale", "dgate", "dpost_weight"), out):
             assert torch.equal(t, want[name]), name
+
+
+@pytest.mark.parametrize("dtype, gate_dtype", ((torch.float32, torch.float32), (BF, BF), (BF, torch.float32)))
+def test_no_rows_of_a_gate(gk, dtype, gate_dtype):
+    """A gate over no rows has a gradient of zeros, whatever lay where it is written."""
+    for shape, lead in (((0, 5, 24), (1, 1)), ((3, 0, 24), (3, 1)), ((0, 24), (1,)), ((0, 5, 24), (0, 1))):
+        for wide in (1, 24):
+            x = torch.empty(shape, dtype=dtype, device=DEV)
+            gate = torch.ones((*lead, wide), dtype=gate_dtype, device=DEV)
+            stats = torch.empty((4, 0), device=DEV)
+            [torch.full((128,), 7.1, device=DEV) for _ in range(200)]  # (freed: the next small tensors have their memory)
+            got = gk.grkan_residual_norm_backward(x, x, x, x, stats, gate=gate, post="rms",
+                                                  post_weight=torch.ones(24, device=DEV))
+            for name, t in zip(NAMES, got):
+                assert t is None or not t.count_nonzero(), (name, shape, lead)
+            assert got[3].shape == gate.shape

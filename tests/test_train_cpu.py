@@ -359,3 +359,10 @@ def test_stack_gates_of_one_row():
     s = GRKANStack(2, 16, 16, drop=0.5).train()
     assert [tuple(g.shape) for g in s.gates(torch.zeros(16))] == [(1,), (1,)]
     assert [tuple(g.shape) for g in s.gates(torch.zeros(3, 5, 16))] == [(3, 1, 1)] * 2
+
+
+def test_binding_reads_gates_of_no_rows(lib):
+    cpu = torch.device("cpu")
+    for lead, gate, want in (((0, 5), (0, 1, 1), 0), ((0, 5), (1, 1, 24), 1), ((3, 0), (3, 1, 1), 3)):
+        assert train._gate(torch.ones(gate), lead, 0, 24, torch.float32, cpu)[:2] == (want, gate[-1])
+    assert residual_grad(lib, rows=0, gates=1 << 31) == UNSUPPORTED
