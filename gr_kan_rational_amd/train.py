@@ -249,6 +249,8 @@ class GRKANFp8Linear(torch.autograd.Function):
         rows, cols = needs[0] or needs[4] or needs[5], needs[1]
         dy = dy.contiguous().view(-1, W.shape[0])
         dx = dW = db = dA = dB = None
+        if cols and not dy.shape[0]:
+            cols, dW = False, torch.zeros(W.shape, dtype=W.dtype, device=W.device)
         if rows or cols:
             got = grkan_fp8_quantize(dy, "both" if rows and cols else ("rows" if rows else "columns"))
         if rows:
@@ -259,7 +261,7 @@ class GRKANFp8Linear(torch.autograd.Function):
             xt, xts = grkan_fp8_quantize(x, "columns", act=act, A=A, B=B, n_groups=n_groups)
             dW = grkan_fp8_matmul(got[-2], got[-1], xt, xts)
         if bias is not None and needs[2]:
-            db = grkan_linear_act_backward(x, W, dy.view(*x.shape[:-1], W.shape[0]), skip=("dx", "dW"))[2]
+            db = grkan_linear_act_backward(x, W.contiguous(), dy.view(*x.shape[:-1], W.shape[0]), skip=("dx", "dW"))[2]
         return (dx, dW, _like(db, bias), None, _like(dA, A), _like(dB, B), None)[:len(ctx.needs_input_grad)]
 
 

@@ -302,3 +302,34 @@ def test_streams_and_graphs(gk):
         torch.cuda.synchronize()
         for a, b in zip(call(), out):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", ("none", "rational"))
+def test_linear_of_no_rows(gk, act):
+    x = normal((0, 7, 64), 71, 1.0, BF).requires_grad_()
+    W = normal((32, 64), 72, 1.0, BF).requires_grad_()
+    b = normal((32,), 73).requires_grad_()
+    A, B = (normal((8, k), 74).requires_grad_() if act == "rational" else None for k in (6, 4))
+    y = gk.GRKANFp8Linear.apply(x, W, b, act, A, B)
+    assert y.shape == (0, 7, 32)
+    y.backward(torch.empty_like(y))
+    for t in (x, W, b, A, B):
+        assert t is None or (t.grad.shape == t.shape and not t.grad.count_nonzero())
+
+
+@pytest.mark.parametrize("d_in, d_out, groups", ((128, 40, 8), (37, 45, 37)))
+def test_linear_of_strided_rows(gk, d_in, d_out, groups):
+    """Rows that are parts of longer ones, and W a part of a larger one, give what dense copies give."""
+    wide, Wide = normal((70, d_in + 64), 75, 1.0, BF), normal((d_out, d_in + 32), 76, 0.1, BF)
+    A, B, b = normal((groups, 6), 77, 0.5), normal((groups, 4), 78, 0.5), normal((d_out,), 79)
+    dy = normal((70, d_out), 80, 0.1, BF)
+    got = []
+    for dense in (False, True):
+        x, W = wide[:, 64:], Wide[:, 16:16 + d_in]
+        if dense:
+            x, W = x.contiguous(), W.contiguous()
+        leaves = [t.detach().requires_grad_() for t in (x, W, b, A, B)]
+        y = gk.GRKANFp8Linear.apply(leaves[0], leaves[1], leaves[2], "rational", leaves[3], leaves[4], groups)
+        got.append([y, *torch.autograd.grad(y, leaves, dy.t().contiguous().t() if not dense else dy)])
+    for one, two in zip(*got):
+        assert torch.equal(one, two)
