@@ -556,17 +556,20 @@ class GRKANAdamW(torch.optim.Optimizer):
 
     Per parameter group: ``lr`` (a number, or one float32 value on the device), ``betas``, ``eps``,
     ``weight_decay``, ``bits`` (32 or 8), ``masters`` (keep bfloat16 parameters in float32 besides; else they are
-    read, stepped and rounded to nearest).  ``seed``: of the 8-bit states' rounding.  ``step(grad_scale=...)``
-    takes one float32 value on the device that every gradient is multiplied with.  Parameters without a gradient
-    are left as they are, and count no step."""
+    read, stepped and rounded to nearest), ``seed`` (of the 8-bit states' rounding; each group adds its number).
+    ``step(grad_scale=...)`` takes one float32 value on the device that every gradient is multiplied with.
+    Parameters without a gradient are left as they are, and count no step.
+
+    Steps are counted on the host, so a step is not captured into a graph (it would repeat its number):
+    ``grkan_adamw_step`` with a step on the device is."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, bits=32, masters=True, seed=0):
         if bits not in (8, 32):
             raise ValueError("bits must be 8 or 32")
         if not isinstance(lr, torch.Tensor) and not lr >= 0.0:
             raise ValueError(f"lr must be at least 0, got {lr}")
-        self.seed = seed
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, bits=bits, masters=masters))
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, bits=bits, masters=masters,
+                                      seed=seed))
 
     def load_state_dict(self, state_dict):
         super().load_state_dict(state_dict)
@@ -580,6 +583,8 @@ class GRKANAdamW(torch.optim.Optimizer):
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step would repeat its number: capture grkan_adamw_step with step on the device")
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -607,5 +612,5 @@ class GRKANAdamW(torch.optim.Optimizer):
                     weight_decay=group["weight_decay"], masters=[s["master"] for _, s in run],
                     avg_scales=[s["avg_scale"] for _, s in run] if eight else None,
                     sq_scales=[s["sq_scale"] for _, s in run] if eight else None, grad_scale=grad_scale,
-                    seed=self.seed + at)
+                    seed=group["seed"] + at)
         return loss

@@ -230,3 +230,43 @@ def test_optimizer(gk):
             assert torch.equal(p, q)
         # the bf16 parameter is its master's rounded copy
         assert torch.equal(a[0], one.state[a[0]]["master"].to(BF)) and one.state[a[0]]["master"].dtype == torch.float32
+
+
+def test_optimizer_refuses_a_capture(gk):
+    """A captured step would hold its step number: refused before anything is launched or counted."""
+    p = torch.nn.Parameter(torch.ones(300, device=DEV))
+    p.grad = torch.ones_like(p)
+    opt = gk.GRKANAdamW([p])
+    opt.step()
+    before = p.detach().clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="captur"):
+            opt.step()
+    assert opt.state[p]["step"] == 1 and torch.equal(p, before)
+
+
+def test_optimizer_copies(gk):
+    """A copy, and one that takes a saved state, round with the seed of the original."""
+    import copy
+
+    def start():
+        p = torch.nn.Parameter(torch.linspace(-1.0, 1.0, 1000, device=DEV))
+        p.grad = torch.linspace(-0.3, 0.7, 1000, device=DEV)
+        return p
+
+    a = start()
+    one = gk.GRKANAdamW([a], bits=8, seed=5)
+    one.step()
+    two = copy.deepcopy(one)
+    b, c = two.param_groups[0]["params"][0], start()
+    b.grad = a.grad.clone()
+    with torch.no_grad():
+        c.copy_(a)
+    three = gk.GRKANAdamW([c], bits=8)
+    three.load_state_dict(one.state_dict())
+    for _ in range(3):
+        for opt in (one, two, three):
+            opt.step()
+    assert torch.equal(a, b) and torch.equal(a, c)
