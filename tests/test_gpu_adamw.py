@@ -270,3 +270,22 @@ def test_optimizer_copies(gk):
         for opt in (one, two, three):
             opt.step()
     assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("bits", (32, 8))
+def test_far_values(gk, bits):
+    """A tensor of more than 2^31 values: its last ones as if they were alone."""
+    n, last = (1 << 31) + 4096 + 77, 1 << 20 | 77
+    p, g = (torch.full((n,), v, device=DEV) for v in (1.0, 0.5))
+    gen = torch.Generator().manual_seed(9)
+    p[-last:], g[-last:] = (torch.randn(last, generator=gen).to(DEV) for _ in range(2))
+    state = gk.grkan_adamw_state(p, bits)
+    one = [t[-last:].clone() for t in (p, g)]
+    alone = gk.grkan_adamw_state(one[0], bits)
+    for (w, grad), (avg, sq, ms, rs) in (((p, g), state), (one, alone)):
+        gk.grkan_adamw_step([w], [grad], [avg], [sq], step=1, avg_scales=None if ms is None else [ms],
+                            sq_scales=None if rs is None else [rs], **HYPER)
+    assert torch.equal(p[-last:], one[0])
+    assert int((p[:-last] != p[0]).count_nonzero()) == 0 and float(p[0]) != 1.0
+    if bits == 32:
+        assert torch.equal(state[0][-last:], alone[0]) and torch.equal(state[1][-last:], alone[1])

@@ -333,3 +333,25 @@ def test_linear_of_strided_rows(gk, d_in, d_out, groups):
         got.append([y, *torch.autograd.grad(y, leaves, dy.t().contiguous().t() if not dense else dy)])
     for one, two in zip(*got):
         assert torch.equal(one, two)
+
+
+def test_far_rows(gk):
+    """Offsets past 2^32 bytes and elements: the last rows as if they were alone."""
+    rows, k, n, last = (1 << 20) + 300, 4096, 4096, 300
+    x = torch.empty((rows, k), dtype=BF, device=DEV)
+    x[:-last] = 1.0
+    x[-last:] = normal((last, k), 81, 1.0, BF)
+    q, s, qt, st = gk.grkan_fp8_quantize(x, "both")
+    del x
+    tail = normal((last, k), 81, 1.0, BF)
+    want = gk.grkan_fp8_quantize(tail, "both")
+    assert torch.equal(q[-last:].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s[-last:], want[1])
+    # (the tail begins at a block of rows)
+    assert torch.equal(qt[:, -last:].view(torch.uint8), want[2].view(torch.uint8)) and torch.equal(st[:, -3:], want[3])
+    del qt, st
+    b, sb = gk.grkan_fp8_quantize(normal((n, k), 82, k ** -0.5, BF), tile=True)
+    c = gk.grkan_fp8_matmul(q, s, b, sb)
+    got, bound = ref.matmul(want[0], want[1], b, sb, True)
+    ref.check("tail", c[-last:], got, bound)
+    one = gk.grkan_fp8_matmul(q[:300], s[:300], b, sb)
+    assert float((c[:300].double() - one.double()).abs().max()) <= 2.0 ** -7 * float(one.double().abs().max())
