@@ -689,9 +689,19 @@ template <class T> hipError_t launch_type(const Product8Plan &p, const Product8A
 
 hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipStream_t s) {
     Product8Args a = args;
+    a.M = (int32_t)p.rows;
     a.splits = p.splits;
     a.k_split = (int32_t)p.k_split;
-    return a.bf16 ? launch_type<uint16_t>(p, a, s) : launch_type<float>(p, a, s);
+    const hipError_t e = a.bf16 ? launch_type<uint16_t>(p, a, s) : launch_type<float>(p, a, s);
+    if (e != hipSuccess || p.rows == args.M) return e;
+    const int64_t es = a.bf16 ? 2 : 4;
+    a = args;
+    a.M -= (int32_t)p.rows;
+    a.a.p += p.rows * a.a.ld;
+    a.a.scale += p.rows * a.a.srow;
+    a.c = static_cast<char *>(a.c) + p.rows * a.N * es;
+    if (a.residual) a.residual = static_cast<const char *>(a.residual) + p.rows * a.ldr * es;
+    return launch_product8(plan_product8_whole(a.M, a.N, a.K, a.bf16, a.b_tile != 0), a, s);
 }
 
 }  // namespace grkan

@@ -30,8 +30,9 @@ constexpr int64_t kMaxScaleRow = int64_t(1) << 20;
 
 // Few rows: `few` blocks of 16 a workgroup.  Else tiles of the result of `tile` x
 // `tile`; with splits > 1 fp32 sums of k ranges go to memory and a second kernel
-// adds them.
+// adds them.  The rows past the first `rows` follow by a plan of their own.
 struct Product8Plan {
+    int64_t rows;
     int32_t few;
     int32_t tile;
     int32_t splits;
@@ -49,8 +50,18 @@ inline grkan_status_t product8_shape(int64_t M, int64_t N, int64_t K) {
 
 constexpr int64_t kFewRows = 64;
 
-inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile) {
+// A CU holds 1, 2 or 4 workgroups of these tiles; a step (a block of k) takes a workgroup
+// `alone` us, or `full` where the CU holds as many as it can, a tile's result `tail`,
+// `tail_full`; by type of the result, fp32 first.
+constexpr int kTiles8[] = {256, 128, 64};
+constexpr double kTimes8[2][3][4] = {{{}, {0.9, 2.1, 2.2, 0.0}, {0.61, 1.5, 0.23, 0.0}},
+                                     {{1.6, 1.7, 3.0, 5.5}, {0.5, 1.3, 2.0, 2.3}, {0.38, 1.0, 0.4, 1.9}}};
+constexpr double kLaunch8 = 3.5;
+
+// One plan for all rows, and its estimated time.
+inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, double *time = nullptr) {
     Product8Plan p{};
+    p.rows = M;
     p.splits = 1;
     p.k_split = ceil_div(K, kBlock8) * kBlock8;
     if (M <= kFewRows) {
@@ -58,30 +69,25 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bo
         while (p.few > 1 && ceil_div(N, 16) * ceil_div(M, 16 * p.few) < 192) p.few /= 2;
         return p;
     }
-    // The tile and the number of k splits with the least estimated time.  A CU holds
-    // 1, 2 or 4 workgroups; a step (a block of k) takes a workgroup `alone` us, or
-    // `full` where the CU holds as many as it can, a tile's result `tail`, `tail_full`.
-    // Splits add a launch, a write and a read of their sums.  Fitted to 603 timings of
+    // The tile and the number of k splits with the least estimated time.  Splits add a
+    // launch, a write and a read of their sums.  Fitted to 603 timings of
     // 58 shapes: the choice is 1.3% from the best one in the mean, 19% at most
     // (50,432 x 3,072 from 768, tiles of 256 / 128 / 64: 185 / 182 / 240 us; 8,192 x
     // 8,192 from 8,192: 537 / 656 / 1,260; 197 x 768 from 3,072 in tiles of 64: 9.7 us
     // in 4 splits, 20 in one).  256 x 256 is for bf16 results and a scale for each tile
     // of b alone: it has no registers for the wider products or a scale a column.
-    static const int kTile[] = {256, 128, 64};
-    static const double kTimes[2][3][4] = {{{}, {0.9, 2.1, 2.2, 0.0}, {0.61, 1.5, 0.23, 0.0}},
-                                           {{1.6, 1.7, 3.0, 5.5}, {0.5, 1.3, 2.0, 2.3}, {0.38, 1.0, 0.4, 1.9}}};
     const int64_t steps = ceil_div(K, kBlock8), cus = 256;
     double best = 1e30;
     for (int i = bf16 && b_tile ? 0 : 1; i < 3; ++i) {
-        const double *t = kTimes[bf16][i];
-        const int64_t tiles = ceil_div(M, kTile[i]) * ceil_div(N, kTile[i]), held = 1 << i;
+        const double *t = kTimes8[bf16][i];
+        const int64_t tiles = ceil_div(M, kTiles8[i]) * ceil_div(N, kTiles8[i]), held = 1 << i;
         for (int64_t s = 1; s <= 64; ++s) {
             if (s > 8 && s % 8 != 0) continue;  // eighths: a k range to an XCD
             if (s > 1 && (steps < 2 * s || (double)s * M * N * 4 > 256e6)) break;
             const int64_t per = ceil_div(steps, s), wgs = tiles * ceil_div(steps, per);
             const int64_t rounds = wgs / (held * cus), rest = wgs % (held * cus);
             const double share = (double)ceil_div(rest, cus) / (double)held;
-            double us = 3.5 + (double)rounds * (per * t[1] + t[3]);
+            double us = kLaunch8 + (double)rounds * (per * t[1] + t[3]);
             if (rest) {
                 us += per * (t[1] * share > t[0] ? t[1] * share : t[0]);
                 us += t[3] * share > t[2] ? t[3] * share : t[2];
@@ -89,13 +95,36 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bo
             if (s > 1) us += 3.2 + 2.0 * (double)s * M * N * 4 / 7e6;
             if (us < best) {
                 best = us;
-                p.tile = kTile[i];
+                p.tile = kTiles8[i];
                 p.k_split = per * kBlock8;
             }
         }
     }
     p.splits = (int32_t)ceil_div(K, p.k_split);
     if (p.splits > 1) p.partials_bytes = (size_t)p.splits * (size_t)M * (size_t)N * 4;
+    if (time) *time = best;
+    return p;
+}
+
+// Tiles of 256 x 256 for as many rows as keep all CUs at work, the others by a plan of their
+// own, if that takes less: a last round of few such tiles takes as long as a full one
+// (50,432 x 768 from 3,072: 138 us whole, 141 in tiles of 128, 127 so; 15,443 x 2,112
+// from 3,648: 160, 151 and 141; 50,432 x 3,072 from 768: 156, 165 and 154).
+inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile) {
+    if (M <= kFewRows || !bf16 || !b_tile) return plan_product8_whole(M, N, K, bf16, b_tile);
+    double whole, rest;
+    Product8Plan p = plan_product8_whole(M, N, K, bf16, b_tile, &whole);
+    const int64_t nb = ceil_div(N, kTiles8[0]), rounds = ceil_div(M, kTiles8[0]) * nb / 256;
+    const int64_t rows = rounds * 256 / nb * kTiles8[0];
+    if (rows < 1 || M - rows <= kFewRows) return p;
+    const Product8Plan r = plan_product8_whole(M - rows, N, K, bf16, b_tile, &rest);
+    const double *t = kTimes8[1][0];
+    if (kLaunch8 + (double)rounds * (ceil_div(K, kBlock8) * t[1] + t[3]) + rest >= whole) return p;
+    p.rows = rows;
+    p.tile = kTiles8[0];
+    p.splits = 1;
+    p.k_split = ceil_div(K, kBlock8) * kBlock8;
+    p.partials_bytes = r.partials_bytes;
     return p;
 }
 

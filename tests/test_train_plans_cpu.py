@@ -19,7 +19,7 @@ def header(monkeypatch):
 
 def test_product_plans(tmp_path):
     """A kernel for every plan: rows of 16 for few, a tile of 64, 128 or (bf16 results and a scale for each tile of b)
-    256; the splits are whole blocks, cover K and leave none empty; the workspace is enough for every type and layout
+    256, the rows past its whole rounds by a plan of their own; the splits are whole blocks, cover K and leave none empty; the workspace is enough for every type and layout
     of scales; an XCD's eighth of the tiles and splits fits 31 bits."""
     run(tmp_path, r"""
     const long ms[] = {1, 16, 17, 33, 64, 65, 100, 197, 1003, 4096, 50432, 201728, 2147483391L};
@@ -32,6 +32,12 @@ def test_product_plans(tmp_path):
                 for (int i = 0; i < 4; ++i) {
                     const bool bf = i & 1, bt = i & 2;
                     const Product8Plan p = plan_product8(m, n, k, bf, bt);
+                    CHECK(p.rows >= 1 && p.rows <= m, "%ld %ld %ld: rows %ld", m, n, k, (long)p.rows);
+                    if (p.rows < m) {
+                        CHECK(p.tile == 256 && p.splits == 1 && p.rows % 256 == 0 && m - p.rows > kFewRows, "rows apart");
+                        const Product8Plan r = plan_product8_whole(m - p.rows, n, k, bf, bt);
+                        CHECK(r.rows == m - p.rows && r.partials_bytes == p.partials_bytes && r.few == 0, "the rest");
+                    }
                     CHECK((p.few > 0) == (m <= kFewRows), "few rows");
                     if (p.few > 0) {
                         CHECK(p.few == 1 || p.few == 2 || p.few == 4, "%ld %ld %ld: few %d", m, n, k, p.few);
