@@ -434,8 +434,11 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
             for (int i = X + Y; i < NM; ++i) as[i] = scales_of(now, i);
             // Products kAhead of the sums they are added to, so that the matrix unit's
             // result is there; pinned, or the compiler moves the additions past the
-            // barrier and keeps the products.
-            constexpr int kAhead = 2;
+            // barrier and keeps the products.  8,192 x 8,192 from 8,192: 484 us with 2, 460
+            // with 3, 770 with 4, for which tiles of 256 have no registers; in tiles of 128
+            // 15,443 x 2,112 from 3,648 149 with 2, 145 with 4, and 3,072 x 768 from
+            // 50,432 in fp32, whose products take longer, 464 with 2, 475 with 4.
+            constexpr int kAhead = sizeof(T) == 4 ? 2 : (BN == 256 ? 3 : 4);
             f32x4 p[kAhead + 1];
             auto add = [&](int slot, int i, int j) {
                 const float s = BTILE ? as[i] * bt : as[i];
