@@ -451,7 +451,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
 // dgate of each (gate, channel) from what the walkers left, or of each gate from its
 // rows.
 __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a, int columns, int64_t gates) {
-    __shared__ double red[1024];
+    __shared__ double red[2][1024];
     const int t = (int)threadIdx.x;
     double s = 0.0;
     if ((int)blockIdx.x >= columns) {
@@ -477,32 +477,41 @@ __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs 
         return;
     }
     const int cb = (a.C + 31) / 32, i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 32 + (t & 31);
-    auto column = [&](int k) {
-        double s = 0.0;
-        if (col < a.C) {
-            const float *p = a.sums + (int64_t)k * a.C + col;
+    // (with a post norm the third and fourth columns' sums together: P and Q)
+    const bool two = i == 2 && a.post != GRKAN_NORM_NONE;
+    double v = 0.0, w = 0.0;
+    if (col < a.C) {
+        const float *p = a.sums + (int64_t)i * a.C + col;
+        const int64_t step = (int64_t)a.p.sums * a.C;
+        if (two) {
 #pragma unroll 8
-            for (int64_t b = t >> 5; b < a.p.blocks; b += 32) s += (double)p[b * a.p.sums * a.C];
+            for (int64_t b = t >> 5; b < a.p.blocks; b += 32) {
+                v += (double)p[b * step];
+                w += (double)p[b * step + a.C];
+            }
+        } else {
+#pragma unroll 16
+            for (int64_t b = t >> 5; b < a.p.blocks; b += 32) v += (double)p[b * step];
         }
-        red[t] = s;
-        __syncthreads();
-        if (t < 32)
-            for (int q = 1; q < 32; ++q) s += red[t + 32 * q];
-        return s;
-    };
-    const double v = column(i);
+    }
+    red[0][t] = v;
+    red[1][t] = w;
+    __syncthreads();
+    if (t >= 32 || col >= a.C) return;
+#pragma unroll
+    for (int q = 1; q < 32; ++q) {
+        v += red[0][t + 32 * q];
+        w += red[1][t + 32 * q];
+    }
     if (i < 2) {
         float *out = i == 0 ? a.dweight : a.dbias;
-        if (out && t < 32 && col < a.C) out[col] = (float)v;
+        if (out) out[col] = (float)v;
         return;
     }
-    if (a.post == GRKAN_NORM_NONE) {
-        if (a.dscale && t < 32 && col < a.C) a.dscale[col] = (float)v;
+    if (!two) {
+        if (a.dscale) a.dscale[col] = (float)v;
         return;
     }
-    __syncthreads();
-    const double w = column(3);
-    if (t >= 32 || col >= a.C) return;
     const double scale = a.scale ? a.scale[col] : 1.0f;
     if (a.dpost_weight) a.dpost_weight[col] = (float)(scale * v);
     if (a.dpost_bias) a.dpost_bias[col] = (float)(scale * w);
