@@ -13,7 +13,7 @@
  * `stream` and the call returns without waiting; arguments are validated
  * before any HIP call; no C++ exception crosses the interface.  Results are
  * bitwise reproducible: every sum is taken in an order that depends on the
- * shape alone.
+ * call's sizes, types, scale layout and norms alone, and no atomics are used.
  */
 #ifndef GRKAN_TRAIN_H
 #define GRKAN_TRAIN_H
@@ -65,10 +65,13 @@ GRKAN_API grkan_status_t grkan_fp8_quantize(
  *     c[m][n] = sum over blocks kb of a_scale(m, kb) b_scale(n, kb)
  *               sum over k in kb of a[m][k] b[n][k]   + bias[n] + residual[m][n]
  *
- * Products and their sums in a block are formed on the matrix cores in fp32,
- * blocks are added in fp32, c is rounded once.
+ * A block's products are summed on the matrix cores; its sum times
+ * (a_scale b_scale), a product that has to be in fp32's range, is added in fp32, and c
+ * is rounded once.  With an fp32 c the block's sum is fp32's own (1e-8 of it); with a
+ * bf16 c the matrix cores cut the products of each 8 values of k off at 2^-13 of the
+ * largest one's power of two, which is a fortieth of the rounding to bf16.
  *   a, b      e4m3 [m][k], [n][k]: 16-byte aligned, lda, ldb multiples of 16 and
- *             >= k.  Bytes past k are not used.
+ *             >= k.  Bytes past k, to the next multiple of 16, are read and not used.
  *   a_scale   fp32, any finite values: (m, kb) at m a_scale_row + kb a_scale_block;
  *             a stride may be 0 (one scale for all).
  *   b_scale   likewise; with b_tile (0 or 1) row block n / 128 in the place of n.
