@@ -73,14 +73,15 @@ def _matrix(t: torch.Tensor, name: str, dev=None):
     """(rows, width, row stride) of [..., width] whose rows are equally spaced, any dtype."""
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
-    if t.dim() < 1:
+    size = t.shape
+    if not size:
         raise ValueError(f"{name} must be [..., width]")
-    size, stride = t.shape, t.stride()
     w, rows = size[-1], 1
     for k in size[:-1]:
         rows *= k
     if t.is_contiguous():
         return rows, w, w
+    stride = t.stride()
     if w > 1 and stride[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     row, run = None, 0
@@ -151,13 +152,15 @@ def grkan_fp8_quantize(x: torch.Tensor, outputs: str = "rows", tile: bool = Fals
 
 
 def _operand8(t: torch.Tensor, name: str, dev):
-    if t.dtype != F8:
+    if t.dtype is not F8:
         raise TypeError(f"{name} must be float8_e4m3fn, got {t.dtype}")
-    if t.dim() != 2:
+    size, stride = t.shape, t.stride()
+    if len(size) != 2:
         raise ValueError(f"{name} must be [rows, k]")
-    rows, k, ld = _matrix(t, name, dev)
-    if rows <= 1:  # (the stride of a single row is not used)
-        ld = _up(k, 16)
+    rows, k = size
+    if rows <= 1 or (stride[1] != 1 and k > 1) or stride[0] < k or t.device != dev:
+        _matrix(t, name, dev)  # (raises unless there is but one row)
+    ld = _up(k, 16) if rows <= 1 else stride[0]  # (the stride of a single row is not used)
     if ld % 16 or t.data_ptr() % 16:
         raise ValueError(f"the rows of {name} must start at multiples of 16 bytes, as grkan_fp8_quantize's do")
     return rows, k, ld
@@ -165,11 +168,11 @@ def _operand8(t: torch.Tensor, name: str, dev):
 
 def _scale8(t: torch.Tensor, name: str, rows, k: int, dev):
     """(row stride, block stride) of the scales of an operand with `rows` rows (or, one of two, row blocks)."""
-    if t.dtype != torch.float32 or t.device != dev or t.dim() != 2 or t.shape[1] != _up(k, BLOCK) // BLOCK or \
-            t.shape[0] not in rows:
+    size, blocks = t.shape, _up(k, BLOCK) // BLOCK
+    if t.dtype is not torch.float32 or len(size) != 2 or size[1] != blocks or size[0] not in rows or t.device != dev:
         raise ValueError(f"{name} must be a float32 tensor [{' or '.join(map(str, rows))}, "
-                         f"{_up(k, BLOCK) // BLOCK}] on {dev}")
-    return t.stride(0), t.stride(1)
+                         f"{blocks}] on {dev}")
+    return t.stride()
 
 
 def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, bias=None,
@@ -311,7 +314,8 @@ def grkan_residual_norm_forward(x: torch.Tensor, f: torch.Tensor, norm: str = "l
         raise ValueError("x must have a channel")
     for t, name in ((weight, "weight"), (bias, "bias"), (scale, "scale"), (post_weight, "post_weight"),
                     (post_bias, "post_bias")):
-        _channel_vector(t, name, c, dev)
+        if t is not None:
+            _channel_vector(t, name, c, dev)
     if post == "none" and (post_weight is not None or post_bias is not None):
         raise ValueError("post_weight and post_bias need a post norm")
     gates, gc, gio = _gate(gate, x.shape[:-1], rows, c, x.dtype, dev)
@@ -366,7 +370,8 @@ def grkan_residual_norm_backward(f: torch.Tensor, h: torch.Tensor, dh, dz, stats
         lds.append(0 if t is None else _matrix(t, name)[2])
     for t, name in ((weight, "weight"), (bias, "bias"), (scale, "scale"), (post_weight, "post_weight"),
                     (post_bias, "post_bias")):
-        _channel_vector(t, name, c, dev)
+        if t is not None:
+            _channel_vector(t, name, c, dev)
     if post == "none" and (post_weight is not None or post_bias is not None):
         raise ValueError("post_weight and post_bias need a post norm")
     _check_out(stats, "stats", torch.float32, rows * (2 if post == "none" else 4), dev)
