@@ -653,9 +653,18 @@ template <int MT, class T> __global__ __launch_bounds__(kFewWaves * 64) void grk
 template <int BM, int BN, class T, bool BTILE, bool PARTIAL> hipError_t launch_tile(const Product8Args &a, hipStream_t s) {
     auto kern = grkan_product8_tile_kernel<BM, BN, T, BTILE, PARTIAL>;
     using Shape = Tile8<BM, BN>;
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kLds);
-    if (attr != hipSuccess) return attr;
+    // Once on each device (twice if two threads come first: the same value).
+    static uint64_t told = 0;
+    int device = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (!(__atomic_load_n(&told, __ATOMIC_RELAXED) & bit)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Shape::kLds);
+        if (e != hipSuccess) return e;
+        __atomic_fetch_or(&told, bit, __ATOMIC_RELAXED);
+    }
     const int64_t mb = (a.M + BM - 1) / BM, nb = (a.N + BN - 1) / BN;
     int64_t grid = (mb * nb * (PARTIAL ? a.splits : 1) + 7) / 8 * 8;
     // as many workgroups as fit on the 256 CUs at once; each walks over its tiles
