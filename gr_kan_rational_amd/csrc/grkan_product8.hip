@@ -561,7 +561,7 @@ template <class T> __global__ __launch_bounds__(256) void grkan_product8_finish_
 
 // ------------------------------------------------------------ few rows
 
-// Few rows of a: a workgroup takes 16 columns of the result (16 rows of b) and
+// Few rows of a, or a small result: a workgroup takes 16 columns of the result (16 rows of b) and
 // 16 MT rows; its waves take the blocks of k in turn, straight from memory into
 // operand registers, the loads of up to kTurns blocks on their way at once.  The
 // waves' sums meet in LDS.  Bound: b's bytes, latency below (1 x 3,072 from 768: 3.3 us,

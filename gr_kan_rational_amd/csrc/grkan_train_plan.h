@@ -28,7 +28,7 @@ inline grkan_status_t quantize_shape(int64_t rows, int64_t cols, int64_t ldx, in
 // A scale's row stride: a tile's scales lie within 2^31 bytes.
 constexpr int64_t kMaxScaleRow = int64_t(1) << 20;
 
-// Few rows: `few` blocks of 16 a workgroup.  Else tiles of the result of `tile` x
+// Few rows, or a small result: `few` blocks of 16 rows a workgroup.  Else tiles of the result of `tile` x
 // `tile`; with splits > 1 fp32 sums of k ranges go to memory and a second kernel
 // adds them.  The rows past the first `rows` follow by a plan of their own.
 struct Product8Plan {
@@ -100,7 +100,22 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
             }
         }
     }
-    p.splits = (int32_t)ceil_div(K, p.k_split);
+    // The kernel of few rows, as long as a CU has one workgroup, with the fewest rows for
+    // which that is so (160 x 768 from 3,072 7.2 us, in tiles 9.7; 256 x 512 from 2,048 5.5
+    // and 9.3; 197 x 768 from 3,072 10.4 and 9.7).
+    static const double kFewTimes[3][2] = {{2.6, 0.105}, {2.8, 0.185}, {3.0, 0.31}};
+    for (int i = 0; i < 3; ++i) {
+        if (ceil_div(N, 16) * ceil_div(M, 16 << i) > cus) continue;
+        const double us = kFewTimes[i][0] + kFewTimes[i][1] * (double)steps;
+        if (us < best) {
+            best = us;
+            p.few = 1 << i;
+            p.tile = 0;
+            p.k_split = steps * kBlock8;
+        }
+        break;
+    }
+    p.splits = p.few > 0 ? 1 : (int32_t)ceil_div(K, p.k_split);
     if (p.splits > 1) p.partials_bytes = (size_t)p.splits * (size_t)M * (size_t)N * 4;
     if (time) *time = best;
     return p;
@@ -121,6 +136,7 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bo
     const double *t = kTimes8[1][0];
     if (kLaunch8 + (double)rounds * (ceil_div(K, kBlock8) * t[1] + t[3]) + rest >= whole) return p;
     p.rows = rows;
+    p.few = 0;
     p.tile = kTiles8[0];
     p.splits = 1;
     p.k_split = ceil_div(K, kBlock8) * kBlock8;

@@ -156,8 +156,9 @@ def test_matmul(gk, shape, tile, dtype):
         assert torch.equal(got, gk.grkan_fp8_matmul(a, sa, b, sb, bias=bi, residual=re, dtype=dtype)), "two calls differ"
 
 
-# tiles of 256 rows, whole and odd, one block of k and several, the last rows apart; k split, its end inside a block
-LARGE = [(9000, 2304, 1000), (4096, 4096, 128), (4100, 2100, 300), (8200, 2056, 100), (2049, 4107, 777), (300, 264, 20000), (520, 100, 30001)]
+# tiles of 64; of 256 rows, whole and odd, one block of k and several, the last rows apart; k split, its end inside a block
+LARGE = [(700, 1100, 200), (513, 1025, 333), (9000, 2304, 1000),
+         (4096, 4096, 128), (4100, 2100, 300), (8200, 2056, 100), (2049, 4107, 777), (300, 264, 20000), (520, 100, 30001)]
 
 
 @pytest.mark.parametrize("dtype, tile", ((BF, True), (BF, False), (torch.float32, False)))

@@ -18,7 +18,7 @@ def header(monkeypatch):
 
 
 def test_product_plans(tmp_path):
-    """A kernel for every plan: rows of 16 for few, a tile of 64, 128 or (bf16 results and a scale for each tile of b)
+    """A kernel for every plan: rows of 16 for few or small results, a tile of 64, 128 or (bf16 results and a scale for each tile of b)
     256, the rows past its whole rounds by a plan of their own; the splits are whole blocks, cover K and leave none empty; the workspace is enough for every type and layout
     of scales; an XCD's eighth of the tiles and splits fits 31 bits."""
     run(tmp_path, r"""
@@ -36,9 +36,9 @@ def test_product_plans(tmp_path):
                     if (p.rows < m) {
                         CHECK(p.tile == 256 && p.splits == 1 && p.rows % 256 == 0 && m - p.rows > kFewRows, "rows apart");
                         const Product8Plan r = plan_product8_whole(m - p.rows, n, k, bf, bt);
-                        CHECK(r.rows == m - p.rows && r.partials_bytes == p.partials_bytes && r.few == 0, "the rest");
+                        CHECK(r.rows == m - p.rows && r.partials_bytes == p.partials_bytes, "the rest");
                     }
-                    CHECK((p.few > 0) == (m <= kFewRows), "few rows");
+                    CHECK(p.few > 0 || m > kFewRows, "few rows");
                     if (p.few > 0) {
                         CHECK(p.few == 1 || p.few == 2 || p.few == 4, "%ld %ld %ld: few %d", m, n, k, p.few);
                         CHECK(p.splits == 1 && p.partials_bytes == 0, "few rows are not split");
