@@ -39,6 +39,7 @@ struct Product8Args {
     int32_t splits, k_split;
     int32_t b_tile;
     bool bf16;
+    bool sums32;             // bf16: block sums in fp32
 };
 hipError_t launch_product8(const Product8Plan &p, const Product8Args &a, hipStream_t s);
 

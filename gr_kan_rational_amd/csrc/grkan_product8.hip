@@ -2,13 +2,18 @@
 // of 128 values of k, on the matrix cores (gfx950).
 //
 // A block's products are summed from zero; its sum times both scales is added
-// to the accumulators in fp32.  For a bf16 result one v_mfma_f32_16x16x128_f8f6f4
-// sums a block: that instruction cuts the products of each 8 values of k off at
-// 2^-13 of the largest one's power of two before adding them (measured; the groups
-// of 8 are added in fp32), which put results 1.5e-5 to 5e-5 of their norm off, a
-// fortieth of the rounding to bf16 (at most 2^-9 of each value).  For an fp32
-// result the values are widened to bf16, exactly, and four
-// v_mfma_f32_16x16x32_bf16 sum them in fp32 (1e-8), at half the rate.
+// to the accumulators in fp32.  Two ways to sum a block (the kernels' CUT):
+//
+// one v_mfma_f32_16x16x128_f8f6f4.  It cuts the products of each 8 values of k off at
+// 2^-13 of the largest one's power of two before adding them (measured; the groups of 8
+// are added in fp32; v_mfma_f32_16x16x32_fp8_fp8 does the same).  Results are 1.5e-5
+// to 5e-5 of their norm off, a fortieth of the rounding to bf16 in the mean; a value whose
+// large products cancel may be off by more than its own rounding.
+//
+// the values widened to bf16, exactly, and four v_mfma_f32_16x16x32_bf16, whose sums
+// are fp32's (1e-7), at half the rate: fp32 results, and bf16 ones whose caller asks for it
+// (50,432 x 3,072 from 768: 248 us against 150; 4,096 x 768 from 3,072: 34 and 21.5; 1,003 x
+// 1,501 from 777: 10.9 and 9.1).
 //
 // Bound, large products: LDS (of a 256 x 256 tile's step 192 KB are read and 64 KB written,
 // 2,048 cycles of a CU) and the matrix cores (2,048 cycles) side by side, with the
@@ -56,9 +61,9 @@ __device__ static inline bf16x8 widen(uint32_t lo, uint32_t hi) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A block's sum of products.
-template <class T> __device__ static inline f32x4 block_product(i32x8 a, i32x8 b) {
-    if constexpr (sizeof(T) == 2) return mfma8(a, b, f32x4{});
+// A block's sum of products, cut as above or fp32's own.
+template <bool CUT> __device__ static inline f32x4 block_product(i32x8 a, i32x8 b) {
+    if constexpr (CUT) return mfma8(a, b, f32x4{});
     f32x4 c = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -158,14 +163,14 @@ template <int BM, int BN> struct Tile8 {
 // A block of k at a time through two LDS stages.  T: the result's type.  A 256 x 256
 // tile in 8 waves of 128 x 64 leaves each byte of LDS the most products that the
 // accumulators' registers allow (128 of 256); 128 x 128 and 64 x 64, 4 waves, give two and
-// four workgroups to a CU where there are fewer tiles.  fp32 results: the widening, 128
+// four workgroups to a CU where there are fewer tiles.  fp32 sums: the widening, 128
 // conversions beside 64 matrix instructions in a step of a wave, is the bound (3,072 x 768
 // from 50,432 in 7 splits: 256 us, 930 TFLOP/s).
 //
 // In the middle of a step every wave holds what is left of it in registers: a barrier
 // there covers both that and the arrival of the next step, and the fetches of the
 // step after that go into the stage just freed, a whole step ahead of their use.
-template <int BM, int BN, class T, bool BTILE, bool PARTIAL>
+template <int BM, int BN, class T, bool CUT, bool BTILE, bool PARTIAL>
 __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_tile_kernel(Product8Args a) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     using Shape = Tile8<BM, BN>;
@@ -451,7 +456,7 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
             // with 3, 770 with 4, for which tiles of 256 have no registers; in tiles of 128
             // 15,443 x 2,112 from 3,648 149 with 2, 145 with 4, and 3,072 x 768 from
             // 50,432 in fp32, whose products take longer, 464 with 2, 475 with 4.
-            constexpr int kAhead = sizeof(T) == 4 ? 2 : (BN == 256 ? 3 : 4);
+            constexpr int kAhead = CUT ? (BN == 256 ? 3 : 4) : 2;
             f32x4 p[kAhead + 1];
             auto add = [&](int slot, int i, int j) {
                 const float s = BTILE ? as[i] * bt : as[i];
@@ -465,7 +470,7 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
             for (int q = 0; q < kFirst + kAhead; ++q) {
                 if (q < kFirst) {
                     const int i = q / NN, j = q % NN;
-                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < X ? fr[PX][i < X ? i : 0] : fr[PY][i < X ? 0 : i - X]);
+                    p[q % (kAhead + 1)] = block_product<CUT>(fb[j], i < X ? fr[PX][i < X ? i : 0] : fr[PY][i < X ? 0 : i - X]);
                     if (i < W && j == NN - 1) fr[PX][i] = read_a(now, X + Y + Z + i);
                 }
                 if (q >= kAhead) add((q - kAhead) % (kAhead + 1), (q - kAhead) / NN, (q - kAhead) % NN);
@@ -500,7 +505,7 @@ __global__ __launch_bounds__((Tile8<BM, BN>::kThreads), 2) void grkan_product8_t
             for (int q = 0; q < kRest + kAhead; ++q) {
                 if (q < kRest) {
                     const int j = q / R, i = q % R;
-                    p[q % (kAhead + 1)] = block_product<T>(fb[j], i < Z ? fz[i < Z ? i : 0] : fr[PX][i < Z ? 0 : i - Z]);
+                    p[q % (kAhead + 1)] = block_product<CUT>(fb[j], i < Z ? fz[i < Z ? i : 0] : fr[PX][i < Z ? 0 : i - Z]);
                     if (i == R - 1) fb[j] = read_b(other, j);
                     // the fetches, spread over the products
 #pragma unroll
@@ -568,7 +573,7 @@ template <class T> __global__ __launch_bounds__(256) void grkan_product8_finish_
 // the floor of a launch).
 constexpr int kFewWaves = 8;
 
-template <int MT, class T> __global__ __launch_bounds__(kFewWaves * 64) void grkan_product8_few_kernel(Product8Args a) {
+template <int MT, class T, bool CUT> __global__ __launch_bounds__(kFewWaves * 64) void grkan_product8_few_kernel(Product8Args a) {
     constexpr int kTurns = MT == 1 ? 4 : 2;
     __shared__ float red[kFewWaves][MT * 16][17];
     const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -621,7 +626,7 @@ template <int MT, class T> __global__ __launch_bounds__(kFewWaves * 64) void grk
             };
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const f32x4 p = block_product<T>(whole(b[u]), whole(x[u][i]));
+                const f32x4 p = block_product<CUT>(whole(b[u]), whole(x[u][i]));
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(p[v], as[u][i] * bs[u][v], acc[i][v]);
             }
@@ -650,8 +655,8 @@ template <int MT, class T> __global__ __launch_bounds__(kFewWaves * 64) void grk
 
 // ------------------------------------------------------------ dispatch
 
-template <int BM, int BN, class T, bool BTILE, bool PARTIAL> hipError_t launch_tile(const Product8Args &a, hipStream_t s) {
-    auto kern = grkan_product8_tile_kernel<BM, BN, T, BTILE, PARTIAL>;
+template <int BM, int BN, class T, bool CUT, bool BTILE, bool PARTIAL> hipError_t launch_tile(const Product8Args &a, hipStream_t s) {
+    auto kern = grkan_product8_tile_kernel<BM, BN, T, CUT, BTILE, PARTIAL>;
     using Shape = Tile8<BM, BN>;
     // Once on each device (twice if two threads come first: the same value).
     static uint64_t told = 0;
@@ -674,37 +679,37 @@ template <int BM, int BN, class T, bool BTILE, bool PARTIAL> hipError_t launch_t
     return hipGetLastError();
 }
 
-template <int BM, int BN, class T> hipError_t launch_kind(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
+template <int BM, int BN, class T, bool CUT> hipError_t launch_kind(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
     if constexpr (BM == 256) {
         if (!a.b_tile) return hipErrorInvalidValue;  // (has no registers for a scale a column)
-        return p.splits > 1 ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, true, false>(a, s);
+        return p.splits > 1 ? launch_tile<BM, BN, T, CUT, true, true>(a, s) : launch_tile<BM, BN, T, CUT, true, false>(a, s);
     } else if (p.splits > 1) {
-        return a.b_tile ? launch_tile<BM, BN, T, true, true>(a, s) : launch_tile<BM, BN, T, false, true>(a, s);
+        return a.b_tile ? launch_tile<BM, BN, T, CUT, true, true>(a, s) : launch_tile<BM, BN, T, CUT, false, true>(a, s);
     } else {
-        return a.b_tile ? launch_tile<BM, BN, T, true, false>(a, s) : launch_tile<BM, BN, T, false, false>(a, s);
+        return a.b_tile ? launch_tile<BM, BN, T, CUT, true, false>(a, s) : launch_tile<BM, BN, T, CUT, false, false>(a, s);
     }
 }
 
-template <class T> hipError_t launch_type(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
+template <class T, bool CUT> hipError_t launch_type(const Product8Plan &p, const Product8Args &a, hipStream_t s) {
     if (p.few > 0) {
         const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * p.few - 1) / (16 * p.few))), block(kFewWaves * 64);
         switch (p.few) {
-            case 1: hipLaunchKernelGGL((grkan_product8_few_kernel<1, T>), grid, block, 0, s, a); break;
-            case 2: hipLaunchKernelGGL((grkan_product8_few_kernel<2, T>), grid, block, 0, s, a); break;
-            default: hipLaunchKernelGGL((grkan_product8_few_kernel<4, T>), grid, block, 0, s, a); break;
+            case 1: hipLaunchKernelGGL((grkan_product8_few_kernel<1, T, CUT>), grid, block, 0, s, a); break;
+            case 2: hipLaunchKernelGGL((grkan_product8_few_kernel<2, T, CUT>), grid, block, 0, s, a); break;
+            default: hipLaunchKernelGGL((grkan_product8_few_kernel<4, T, CUT>), grid, block, 0, s, a); break;
         }
         return hipGetLastError();
     }
     hipError_t e;
     if (p.tile == 256) {
-        if constexpr (sizeof(T) == 2)
-            e = launch_kind<256, 256, T>(p, a, s);
+        if constexpr (CUT)   // (has no registers for the wider products)
+            e = launch_kind<256, 256, T, CUT>(p, a, s);
         else
             e = hipErrorInvalidValue;
     } else if (p.tile == 128) {
-        e = launch_kind<128, 128, T>(p, a, s);
+        e = launch_kind<128, 128, T, CUT>(p, a, s);
     } else {
-        e = launch_kind<64, 64, T>(p, a, s);
+        e = launch_kind<64, 64, T, CUT>(p, a, s);
     }
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t work = (int64_t)((a.N + 3) / 4) * a.M;
@@ -719,7 +724,11 @@ hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipS
     a.M = (int32_t)p.rows;
     a.splits = p.splits;
     a.k_split = (int32_t)p.k_split;
-    const hipError_t e = a.bf16 ? launch_type<uint16_t>(p, a, s) : launch_type<float>(p, a, s);
+    hipError_t e;
+    if (!a.bf16)
+        e = launch_type<float, false>(p, a, s);
+    else
+        e = a.sums32 ? launch_type<uint16_t, false>(p, a, s) : launch_type<uint16_t, true>(p, a, s);
     if (e != hipSuccess || p.rows == args.M) return e;
     const int64_t es = a.bf16 ? 2 : 4;
     a = args;
@@ -728,7 +737,7 @@ hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipS
     a.a.scale += p.rows * a.a.srow;
     a.c = static_cast<char *>(a.c) + p.rows * a.N * es;
     if (a.residual) a.residual = static_cast<const char *>(a.residual) + p.rows * a.ldr * es;
-    return launch_product8(plan_product8_whole(a.M, a.N, a.K, a.bf16, a.b_tile != 0), a, s);
+    return launch_product8(plan_product8_whole(a.M, a.N, a.K, a.bf16, a.b_tile != 0, a.sums32), a, s);
 }
 
 }  // namespace grkan

@@ -52,14 +52,16 @@ constexpr int64_t kFewRows = 64;
 
 // A CU holds 1, 2 or 4 workgroups of these tiles; a step (a block of k) takes a workgroup
 // `alone` us, or `full` where the CU holds as many as it can, a tile's result `tail`,
-// `tail_full`; by type of the result, fp32 first.
+// `tail_full`; by how blocks are summed, in fp32 first.
 constexpr int kTiles8[] = {256, 128, 64};
 constexpr double kTimes8[2][3][4] = {{{}, {0.9, 2.1, 2.2, 0.0}, {0.61, 1.5, 0.23, 0.0}},
                                      {{1.6, 1.7, 3.0, 5.5}, {0.5, 1.3, 2.0, 2.3}, {0.38, 1.0, 0.4, 1.9}}};
 constexpr double kLaunch8 = 3.5;
 
 // One plan for all rows, and its estimated time.
-inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, double *time = nullptr) {
+inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool sums32 = false,
+                                        double *time = nullptr) {
+    const bool cut = bf16 && !sums32;   // blocks summed by the 8-bit matrix instruction
     Product8Plan p{};
     p.rows = M;
     p.splits = 1;
@@ -74,12 +76,12 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
     // 58 shapes: the choice is 1.3% from the best one in the mean, 19% at most
     // (50,432 x 3,072 from 768, tiles of 256 / 128 / 64: 185 / 182 / 240 us; 8,192 x
     // 8,192 from 8,192: 537 / 656 / 1,260; 197 x 768 from 3,072 in tiles of 64: 9.7 us
-    // in 4 splits, 20 in one).  256 x 256 is for bf16 results and a scale for each tile
-    // of b alone: it has no registers for the wider products or a scale a column.
+    // in 4 splits, 20 in one).  256 x 256 is for sums by the 8-bit instruction and a
+    // scale for each tile of b alone: it has no registers for the wider products or a scale a column.
     const int64_t steps = ceil_div(K, kBlock8), cus = 256;
     double best = 1e30;
-    for (int i = bf16 && b_tile ? 0 : 1; i < 3; ++i) {
-        const double *t = kTimes8[bf16][i];
+    for (int i = cut && b_tile ? 0 : 1; i < 3; ++i) {
+        const double *t = kTimes8[cut][i];
         const int64_t tiles = ceil_div(M, kTiles8[i]) * ceil_div(N, kTiles8[i]), held = 1 << i;
         for (int64_t s = 1; s <= 64; ++s) {
             if (s > 8 && s % 8 != 0) continue;  // eighths: a k range to an XCD
@@ -125,14 +127,14 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
 // own, if that takes less: a last round of few such tiles takes as long as a full one
 // (50,432 x 768 from 3,072: 138 us whole, 141 in tiles of 128, 127 so; 15,443 x 2,112
 // from 3,648: 160, 151 and 141; 50,432 x 3,072 from 768: 156, 165 and 154).
-inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile) {
-    if (M <= kFewRows || !bf16 || !b_tile) return plan_product8_whole(M, N, K, bf16, b_tile);
+inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool sums32 = false) {
+    if (M <= kFewRows || !bf16 || sums32 || !b_tile) return plan_product8_whole(M, N, K, bf16, b_tile, sums32);
     double whole, rest;
-    Product8Plan p = plan_product8_whole(M, N, K, bf16, b_tile, &whole);
+    Product8Plan p = plan_product8_whole(M, N, K, bf16, b_tile, false, &whole);
     const int64_t nb = ceil_div(N, kTiles8[0]), rounds = ceil_div(M, kTiles8[0]) * nb / 256;
     const int64_t rows = rounds * 256 / nb * kTiles8[0];
     if (rows < 1 || M - rows <= kFewRows) return p;
-    const Product8Plan r = plan_product8_whole(M - rows, N, K, bf16, b_tile, &rest);
+    const Product8Plan r = plan_product8_whole(M - rows, N, K, bf16, b_tile, false, &rest);
     const double *t = kTimes8[1][0];
     if (kLaunch8 + (double)rounds * (ceil_div(K, kBlock8) * t[1] + t[3]) + rest >= whole) return p;
     p.rows = rows;
@@ -144,7 +146,7 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bo
     return p;
 }
 
-// Workspace for every type of result and layout of scales.
+// Workspace for every type of result (bf16 with fp32 sums takes fp32's plan) and layout of scales.
 inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
     size_t most = 0;
     for (int i = 0; i < 4; ++i) {

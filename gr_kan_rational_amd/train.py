@@ -24,6 +24,7 @@ F8 = torch.float8_e4m3fn
 GRKAN_NORM_NONE, GRKAN_NORM_LAYER, GRKAN_NORM_RMS = 0, 1, 2
 _NORMS = {"layer": GRKAN_NORM_LAYER, "rms": GRKAN_NORM_RMS}
 _POSTS = {"none": GRKAN_NORM_NONE, **_NORMS}
+GRKAN_FP8_SUMS_F32 = 16
 
 _lib = None
 
@@ -175,15 +176,22 @@ def _scale8(t: torch.Tensor, name: str, rows, k: int, dev):
     return t.stride()
 
 
+_SUMS = {"fast": 0, "fp32": GRKAN_FP8_SUMS_F32}
+
+
 def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, bias=None,
-                     residual=None, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+                     residual=None, dtype=torch.bfloat16, out=None, workspace=None, stream=None, sums: str = "fast"):
     """a b^T + bias + residual [m, n] in ``dtype`` (bfloat16 or float32) for e4m3 a [m, k], b [n, k]
     (``grkan_fp8_matmul``).
 
     ``a_scale`` is float32 [m, k / 128] (rounded up), ``b_scale`` [n, k / 128], or [n / 128, k / 128] for 128 x
     128 tiles (if n / 128 rounded up is n itself, n = 1, the two are the same); any strides, expanded ones
     too.  The codes' rows start at multiples of 16 bytes, as the quantiser's do.  float32 ``bias`` [n];
-    ``residual`` [m, n] in ``dtype``; ``out`` may be the residual itself."""
+    ``residual`` [m, n] in ``dtype``; ``out`` may be the residual itself.  ``sums``: how the products of a block
+    are summed for a bfloat16 result, "fp32", or "fast": twice the rate, products cut off at 2^-13 of the largest
+    of each 8, which values whose large products cancel can show.  A float32 result has fp32 sums always."""
+    if sums not in _SUMS:
+        raise ValueError(f"sums must be one of {sorted(_SUMS)}")
     _on_gpu(a)
     dev = a.device
     if dtype not in _IO:
@@ -209,7 +217,8 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
         c = _given(out, "out", (m, n), dtype, dev)
         ws, wsp, wsn = _space(workspace, need, dev)
         st = lib.grkan_fp8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(bias),
-                                  _ptr(residual), c.data_ptr(), m, n, k, lda, ar, ab, ldb, br, bb, int(tile), ldr,
+                                  _ptr(residual), c.data_ptr(), m, n, k, lda, ar, ab, ldb, br, bb,
+                                  int(tile) | _SUMS[sums], ldr,
                                   _IO[dtype], wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_fp8_matmul")
@@ -219,15 +228,15 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
 
 
 class GRKANFp8Linear(torch.autograd.Function):
-    """Autograd wrapper: y = F(x) W^T + bias with 8-bit operands, ``apply(x, W, bias, act, A, B, n_groups)``,
-    act "none" (F the identity) or "rational".
+    """Autograd wrapper: y = F(x) W^T + bias with 8-bit operands, ``apply(x, W, bias, act, A, B, n_groups, sums)``,
+    act "none" (F the identity) or "rational"; ``sums`` of all three products as ``grkan_fp8_matmul``'s.
 
     bf16 x [..., d_in] and W [d_out, d_in], float32 bias.  F(x) and the incoming gradient are quantised in blocks
     of 128 along the axis that each product sums over, W in tiles of 128 x 128 (one set of values for both of its
     products).  x is kept for the backward, which quantises F(x) along the rows."""
 
     @staticmethod
-    def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8):
+    def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, sums="fast"):
         if W.dim() != 2 or W.shape[1] != x.shape[-1]:
             raise ValueError(f"W must be [d_out, {x.shape[-1]}], got {list(W.shape)}")
         if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
@@ -238,16 +247,16 @@ class GRKANFp8Linear(torch.autograd.Function):
             wq, ws, wt, wts = grkan_fp8_quantize(W, "both", tile=True)
         else:
             (wq, ws), wt, wts = grkan_fp8_quantize(W, "rows", tile=True), None, None
-        y = grkan_fp8_matmul(q, s, wq, ws, bias=bias)
+        y = grkan_fp8_matmul(q, s, wq, ws, bias=bias, sums=sums)
         ctx.save_for_backward(x, W, bias, A, B, wt, wts)
-        ctx.args = act, n_groups
+        ctx.args = act, n_groups, sums
         return y.view(*x.shape[:-1], W.shape[0])
 
     @staticmethod
     @once_differentiable  # the kernels' results carry no graph: a second derivative would silently lack them
     def backward(ctx, dy):
         x, W, bias, A, B, wt, wts = ctx.saved_tensors
-        act, n_groups = ctx.args
+        act, n_groups, sums = ctx.args
         needs = (*ctx.needs_input_grad, False, False, False, False)  # as many as apply was given, three at least
         rows, cols = needs[0] or needs[4] or needs[5], needs[1]
         dy = dy.contiguous().view(-1, W.shape[0])
@@ -257,15 +266,15 @@ class GRKANFp8Linear(torch.autograd.Function):
         if rows or cols:
             got = grkan_fp8_quantize(dy, "both" if rows and cols else ("rows" if rows else "columns"))
         if rows:
-            dx = grkan_fp8_matmul(got[0], got[1], wt, wts).view(x.shape)
+            dx = grkan_fp8_matmul(got[0], got[1], wt, wts, sums=sums).view(x.shape)
             if act == "rational":
                 dx, dA, dB = binding.grkan_backward(x.contiguous(), dx, A, B, n_groups)
         if cols:
             xt, xts = grkan_fp8_quantize(x, "columns", act=act, A=A, B=B, n_groups=n_groups)
-            dW = grkan_fp8_matmul(got[-2], got[-1], xt, xts)
+            dW = grkan_fp8_matmul(got[-2], got[-1], xt, xts, sums=sums)
         if bias is not None and needs[2]:
             db = grkan_linear_act_backward(x, W.contiguous(), dy.view(*x.shape[:-1], W.shape[0]), skip=("dx", "dW"))[2]
-        return (dx, dW, _like(db, bias), None, _like(dA, A), _like(dB, B), None)[:len(ctx.needs_input_grad)]
+        return (dx, dW, _like(db, bias), None, _like(dA, A), _like(dB, B), None, None)[:len(ctx.needs_input_grad)]
 
 
 # ---------------------------------------------------------------- residual path
