@@ -13,6 +13,7 @@ from itertools import chain
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import binding
 from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_out, _on_gpu
@@ -517,7 +518,10 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
     moment's root, whole blocks of 128 (``grkan_adamw_state`` makes them).  ``step`` (from 1) and ``lr`` are numbers,
     or one int64 and one float32 value on the device, which the kernel reads (and a captured graph reads again at
     each replay).  ``grad_scale``: one float32 value on the device that every gradient is multiplied with.
-    ``seed``: of the 8-bit states' rounding."""
+    ``seed``: of the 8-bit states' rounding.
+
+    What is written counts as modified in place: a backward that still needs it raises (a graph's replays
+    write without being noticed)."""
     n = len(params)
     eight = avg_scales is not None or sq_scales is not None
     if eight and (avg_scales is None or sq_scales is None):
@@ -550,6 +554,8 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
             raise GRKANError(st, "grkan_adamw_step")
 
     _on_stream(stream, dev, launch)
+    kept = () if masters is None else (w for w in masters if w is not None)
+    increment_version(chain(params, kept, avgs, sqs, avg_scales or (), sq_scales or ()))
 
 
 def grkan_adamw_state(param: torch.Tensor, bits: int = 32):
