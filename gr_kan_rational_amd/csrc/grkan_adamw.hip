@@ -70,6 +70,18 @@ __device__ static inline float round_up_sometimes(float y, uint32_t random16) {
     return copysignf(__uint_as_float(bits & 0xfff00000u) - low, y);
 }
 
+// The weights to step: the master's, but where the parameter is not the master rounded it has
+// been written by another (loaded, clamped, set anew) and counts.
+template <class T> __device__ static inline f32x4 latest(f32x4 master, f32x4 param) {
+    f32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float rounded = sizeof(T) == 2 ? (float)(__bf16)master[e] : master[e];
+        w[e] = rounded == param[e] ? master[e] : param[e];
+    }
+    return w;
+}
+
 template <class T, bool VEC>
 __device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, const AdamwFactors &f, float scale, int64_t base) {
 #pragma unroll
@@ -85,7 +97,8 @@ __device__ static inline void step32(const AdamwArgs &a, const AdamwTensor &t, c
         auto load = [&](auto vec) {
             constexpr bool V = vec();
             g = load4<V>(grad, nv);
-            w = t.master ? load4<V>(t.master + at, nv) : load4<V>(param, nv);
+            w = load4<V>(param, nv);
+            if (t.master) w = latest<T>(load4<V>(t.master + at, nv), w);
             m = load4<V>(avg, nv);
             v = load4<V>(sq, nv);
         };
@@ -129,11 +142,8 @@ __device__ static inline void step8(const AdamwArgs &a, const AdamwTensor &t, co
             const int nv = (int)min(t.n - p, (int64_t)4);
             const bool whole = VEC && nv == 4;
             const f32x4 ge = whole ? load4<true>(grad + 4 * q, 4) : load4<false>(grad + 4 * q, nv);
-            f32x4 we;
-            if (t.master)
-                we = whole ? load4<true>(t.master + p, 4) : load4<false>(t.master + p, nv);
-            else
-                we = whole ? load4<true>(param + 4 * q, 4) : load4<false>(param + 4 * q, nv);
+            f32x4 we = whole ? load4<true>(param + 4 * q, 4) : load4<false>(param + 4 * q, nv);
+            if (t.master) we = latest<T>(whole ? load4<true>(t.master + p, 4) : load4<false>(t.master + p, nv), we);
             const f32x2 m01 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[q], false), m23 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[q], true);
             const f32x2 r01 = __builtin_amdgcn_cvt_pk_f32_fp8(rc[q], false), r23 = __builtin_amdgcn_cvt_pk_f32_fp8(rc[q], true);
             const float mv[4] = {m01[0], m01[1], m23[0], m23[1]}, rv[4] = {r01[0], r01[1], r23[0], r23[1]};

@@ -513,7 +513,7 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
 
     ``params`` and ``grads`` are contiguous float32 or bfloat16 tensors (a gradient in its parameter's dtype);
     ``masters``: the weights in float32 for some (None for the others), their parameter then being the rounded
-    copy.  ``avgs`` and ``sqs`` are float32 tensors of the parameters' sizes, or, with ``avg_scales`` and
+    copy; where it is not, a program has written it since, and the parameter's value is stepped.  ``avgs`` and ``sqs`` are float32 tensors of the parameters' sizes, or, with ``avg_scales`` and
     ``sq_scales`` (float32, one for each 128 values), float8_e4m3fn codes of the first moment and of the second
     moment's root, whole blocks of 128 (``grkan_adamw_state`` makes them).  ``step`` (from 1) and ``lr`` are numbers,
     or one int64 and one float32 value on the device, which the kernel reads (and a captured graph reads again at
@@ -575,8 +575,9 @@ class GRKANAdamW(torch.optim.Optimizer):
     parameters.
 
     Per parameter group: ``lr`` (a number, or one float32 value on the device), ``betas``, ``eps``,
-    ``weight_decay``, ``bits`` (32 or 8), ``masters`` (keep bfloat16 parameters in float32 besides; else they are
-    read, stepped and rounded to nearest), ``seed`` (of the 8-bit states' rounding; each group adds its number).
+    ``weight_decay``, ``bits`` (32 or 8), ``masters`` (keep bfloat16 parameters in float32 besides; what a program
+    writes into a parameter between steps goes into its master with the next; without, parameters are stepped and
+    rounded to nearest), ``seed`` (of the 8-bit states' rounding; each group adds its number).
     ``step(grad_scale=...)`` takes one float32 value on the device that every gradient is multiplied with.
     Parameters without a gradient are left as they are, and count no step.
 

@@ -186,8 +186,9 @@ GRKAN_API size_t grkan_residual_norm_backward_workspace_size(int64_t rows, int64
 typedef struct {
     void *param;       /* dtype io [n]; the weights                                          */
     const void *grad;  /* dtype io [n]                                                       */
-    float *master;     /* fp32 [n]: the weights in 32 bits, `param` their rounded copy; or
-                          NULL: `param` is read, and rounded to nearest even                 */
+    float *master;     /* fp32 [n]: the weights in 32 bits, `param` their copy rounded to nearest
+                          even (where it is not, another has written it, and `param` is taken);
+                          or NULL: `param` is stepped and rounded to nearest even            */
     void *avg;         /* first moment: fp32 [n], or e4m3 [n to whole blocks of 128]         */
     void *sq;          /* second moment: fp32 [n], or its root in e4m3, as avg               */
     float *avg_scale;  /* 8 bits: fp32, one for each block of 128; else NULL                 */
