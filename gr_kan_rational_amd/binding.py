@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.graph import increment_version
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgrkan.so")
@@ -143,6 +144,14 @@ def _check_out(t: torch.Tensor, name: str, dtype, numel: int, dev) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {dev}")
 
 
+def _written(*given) -> None:
+    """What a call has written of the caller's own tensors (None among them: not given) counts as modified in
+    place, so that a backward that still needs what was there raises."""
+    for t in given:
+        if t is not None:
+            increment_version(t)
+
+
 def _workspace(ws, dev):
     """(pointer, size in bytes) of an optional caller-supplied workspace on dev."""
     if ws is None:
@@ -192,6 +201,7 @@ def _forward(x, A, B, n_groups, m, n, out, stream, pau, repeat=None):
         st = lib.grkan_forward(_ptr(x), _ptr(y), _ptr(A), _ptr(B), rows, d, n_groups, io, s)
     if st != GRKAN_OK:
         raise GRKANError(st, name)
+    _written(out)
     return y
 
 
@@ -258,6 +268,7 @@ def _backward(x, dy, A, B, n_groups, m, n, mode, dx, dA, dB, workspace, stream, 
     if mode not in _MODES:
         raise ValueError(f"mode must be one of {sorted(_MODES)}")
     flags = _MODES[mode]
+    given = dx, dA, dB
     dx, dA, dB = _grad_outputs(x, n_groups, m, n, dx, dA, dB)
     if pau:
         ws_bytes = lib.grkan_pau_backward_workspace_size(rows, d, n_groups, m, n, io, flags)
@@ -281,6 +292,7 @@ def _backward(x, dy, A, B, n_groups, m, n, mode, dx, dA, dB, workspace, stream, 
                                 rows, d, n_groups, io, flags, wsp, wsn, s)
     if st != GRKAN_OK:
         raise GRKANError(st, name)
+    _written(*given)
     return dx, dA, dB
 
 
@@ -312,11 +324,13 @@ def grkan_backward_noalloc(x: torch.Tensor, dy: torch.Tensor, A: torch.Tensor, B
         raise ValueError("dy must match x")
     _check_coefs(A, B, n_groups, x.device)
     rows, d = _rows_d(x)
+    given = dx, dA, dB
     dx, dA, dB = _grad_outputs(x, n_groups, GRKAN_M, GRKAN_N, dx, dA, dB)
     st = lib.grkan_backward_noalloc(_ptr(x), _ptr(dy), _ptr(A), _ptr(B), _ptr(dx), _ptr(dA), _ptr(dB),
                                     rows, d, n_groups, io, ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_backward_noalloc")
+    _written(*given)
     return dx, dA, dB
 
 
@@ -331,6 +345,7 @@ def grkan_stream_probe(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | Non
     if a.numel() * a.element_size() != b.numel() * b.element_size() or not (a.is_contiguous() and b.is_contiguous()) \
             or b.device != a.device:
         raise ValueError("a and b must be contiguous tensors of the same byte size on one device")
+    given = out
     out = torch.empty_like(a) if out is None else out
     nbytes = a.numel() * a.element_size()
     if out.numel() * out.element_size() != nbytes or not out.is_contiguous() or out.device != a.device:
@@ -338,6 +353,7 @@ def grkan_stream_probe(a: torch.Tensor, b: torch.Tensor, out: torch.Tensor | Non
     st = load_library().grkan_stream_probe(_ptr(a), _ptr(b), _ptr(out), nbytes, ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_stream_probe")
+    _written(given)
     return out
 
 
@@ -390,6 +406,7 @@ def grkan_layer_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, W: to
                                             d_out, n_groups, ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_layer_forward")
+    _written(out)
     return z
 
 
@@ -413,6 +430,7 @@ def grkan_layer_forward_ws(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, W:
                                     wsp, wsn, ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_layer_forward_ws")
+    _written(out)
     return z
 
 
@@ -424,6 +442,7 @@ def grkan_linear_forward(y: torch.Tensor, W: torch.Tensor, out: torch.Tensor | N
                                              ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_linear_forward")
+    _written(out)
     return z
 
 
@@ -441,6 +460,7 @@ def grkan_layer_backward(x: torch.Tensor, dz: torch.Tensor, A: torch.Tensor, B: 
     _check_coefs(A, B, n_groups, x.device)
     rows, d_in, d_out = _layer_dims(x, W)
     _check_out(dz, "dz", torch.bfloat16, rows * d_out, x.device)
+    given = dx, dA, dB, dW
     dx, dA, dB = _grad_outputs(x, n_groups, GRKAN_M, GRKAN_N, dx, dA, dB)
     dW = torch.empty((d_out, d_in), dtype=torch.float32, device=x.device) if dW is None else dW
     _check_out(dW, "dW", torch.float32, d_out * d_in, x.device)
@@ -454,6 +474,7 @@ def grkan_layer_backward(x: torch.Tensor, dz: torch.Tensor, A: torch.Tensor, B: 
                                   ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_layer_backward")
+    _written(*given)
     return dx, dA, dB, dW
 
 
@@ -481,6 +502,7 @@ def grkan_chebykan_forward(x: torch.Tensor, C: torch.Tensor, degree: int = CHEBY
                                                ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_chebykan_forward")
+    _written(out)
     return y
 
 
@@ -494,6 +516,7 @@ def grkan_chebykan_backward(x: torch.Tensor, dy: torch.Tensor, C: torch.Tensor, 
     """(dx, dC) of the Chebyshev-KAN layer (``grkan_chebykan_backward``): dx bf16, dC fp32."""
     rows, d_in, d_out = _cheby_dims(x, C, degree)
     _check_out(dy, "dy", torch.bfloat16, rows * d_out, x.device)
+    given = dx, dC
     if dx is None:
         dx = torch.empty_like(x)
     _check_out(dx, "dx", torch.bfloat16, x.numel(), x.device)
@@ -508,6 +531,7 @@ def grkan_chebykan_backward(x: torch.Tensor, dy: torch.Tensor, C: torch.Tensor, 
                                      wsp, wsn, ctypes.c_void_p(_stream(stream)))
     if st != GRKAN_OK:
         raise GRKANError(st, "grkan_chebykan_backward")
+    _written(*given)
     return dx, dC
 
 

@@ -16,7 +16,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
-from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_coefs, _check_out, _on_gpu
+from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_coefs, _check_out, _on_gpu, _written
 
 GRKAN_ACT_NONE, GRKAN_ACT_SILU, GRKAN_ACT_GELU, GRKAN_ACT_RATIONAL = 0, 1, 2, 3
 _ACTS = {"none": GRKAN_ACT_NONE, "silu": GRKAN_ACT_SILU, "gelu": GRKAN_ACT_GELU, "rational": GRKAN_ACT_RATIONAL}
@@ -213,6 +213,7 @@ def grkan_group_norm_forward(x: torch.Tensor, norm_groups: int, weight=None, bia
                                           io, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_group_norm_forward")
+        _written(out, mean, rstd)
         return y, mu, rs
 
     return _on_stream(stream, dev, launch)
@@ -258,6 +259,7 @@ def grkan_group_norm_backward(x: torch.Tensor, dy: torch.Tensor, mean: torch.Ten
                                            ng, code, io, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_group_norm_backward")
+        _written(dx, dweight, dbias, dA, dB)
         return gx, gw, gb, gA, gB
 
     return _on_stream(stream, dev, launch)
@@ -342,6 +344,7 @@ def grkan_linear_act_forward(x: torch.Tensor, W: torch.Tensor, bias=None, act: s
                                           handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_linear_act_forward")
+        _written(out, pre)
         return z, h
 
     return _on_stream(stream, dev, launch)
@@ -381,6 +384,7 @@ def grkan_linear_act_backward(x: torch.Tensor, W: torch.Tensor, dz: torch.Tensor
                                            d_out, ldx, lddz, ng, code, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_linear_act_backward")
+        _written(dx, dW, dbias, dA, dB)
         return gx, gW, gb, gA, gB
 
     return _on_stream(stream, dev, launch)

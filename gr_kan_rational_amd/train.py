@@ -16,7 +16,7 @@ from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import binding
-from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_out, _on_gpu
+from .binding import GRKAN_BF16, GRKAN_F32, GRKAN_OK, GRKANError, _check_out, _on_gpu, _written
 from .block import (_IO, GRKAN_ACT_NONE, GRKAN_ACT_RATIONAL, _act_coefs, _channel_vector, _given, _io, _like,
                     _need, _on_stream, _ptr, _skipped, _space, _wanted, grkan_linear_act_backward)
 
@@ -223,6 +223,7 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
                                   _IO[dtype], wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_fp8_matmul")
+        _written(out)
         return c
 
     return _on_stream(stream, dev, launch)
@@ -344,6 +345,7 @@ def grkan_residual_norm_forward(x: torch.Tensor, f: torch.Tensor, norm: str = "l
                                               _NORMS[norm], _POSTS[post], io, gio, handle)
         if got != GRKAN_OK:
             raise GRKANError(got, "grkan_residual_norm_forward")
+        _written(out, normed, stats)
         return h, z, st
 
     return _on_stream(stream, dev, launch)
@@ -410,6 +412,7 @@ def grkan_residual_norm_backward(f: torch.Tensor, h: torch.Tensor, dh, dz, stats
                                               _POSTS[post], io, gio, wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_residual_norm_backward")
+        _written(dx, df)
         return gx, gf, gs, gg, gw, gb, gpw, gpb
 
     return _on_stream(stream, dev, launch)
