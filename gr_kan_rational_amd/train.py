@@ -592,6 +592,10 @@ class GRKANAdamW(torch.optim.Optimizer):
             raise ValueError("bits must be 8 or 32")
         if not isinstance(lr, torch.Tensor) and not lr >= 0.0:
             raise ValueError(f"lr must be at least 0, got {lr}")
+        if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
+            raise ValueError(f"betas must be two numbers in [0, 1), got {betas}")
+        if not eps >= 0.0 or not weight_decay >= 0.0:
+            raise ValueError(f"eps and weight_decay must be at least 0, got {eps} and {weight_decay}")
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, bits=bits, masters=masters,
                                       seed=seed))
 
@@ -625,8 +629,7 @@ class GRKANAdamW(torch.optim.Optimizer):
                         grkan_adamw_state(p, group["bits"])
                     state["master"] = p.detach().float().contiguous() \
                         if group["masters"] and p.dtype == torch.bfloat16 else None
-                state["step"] += 1
-                runs.setdefault((state["step"], p.device), []).append((p, state))
+                runs.setdefault((state["step"] + 1, p.device), []).append((p, state))
             for (step, _), run in runs.items():
                 eight = run[0][1]["avg_scale"] is not None
                 grkan_adamw_step(
@@ -637,4 +640,6 @@ class GRKANAdamW(torch.optim.Optimizer):
                     avg_scales=[s["avg_scale"] for _, s in run] if eight else None,
                     sq_scales=[s["sq_scale"] for _, s in run] if eight else None, grad_scale=grad_scale,
                     seed=group["seed"] + at)
+                for _, state in run:  # (counted once it has run: a refused step may be tried again)
+                    state["step"] = step
         return loss

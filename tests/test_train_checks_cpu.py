@@ -21,3 +21,35 @@ def test_kind_of_sums(lib):  # noqa: F811
 
     with pytest.raises(ValueError, match="sums"):
         GRKANStack(1, 16, 16, products="fp8", sums="bf16")
+
+
+def test_optimizer_checks_its_numbers():
+    w = torch.nn.Parameter(torch.zeros(4))
+    for kw in (dict(betas=(0.9, 1.0)), dict(betas=(-0.1, 0.9)), dict(betas=(0.9,)), dict(betas=(float("nan"), 0.9)),
+               dict(eps=-1e-8), dict(eps=float("nan")), dict(weight_decay=-0.1), dict(weight_decay=float("nan"))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            train.GRKANAdamW([w], **kw)
+    train.GRKANAdamW([w], betas=[0, 0.5], eps=0.0, weight_decay=0)
+
+
+def test_a_refused_step_is_not_counted(monkeypatch):
+    """Parameters that the step has taken count it, those behind a refusal do not, and a second try goes on from there."""
+    a, b = (torch.nn.Parameter(torch.zeros(4)) for _ in range(2))
+    a.grad, b.grad = torch.ones(4), torch.ones(4)
+    opt = train.GRKANAdamW([{"params": [a]}, {"params": [b], "weight_decay": 0.5}])
+    seen, refuse = [], [True]
+
+    def step(params, *args, step, weight_decay, **kw):
+        if weight_decay == 0.5 and refuse[0]:
+            raise ValueError("refused")
+        seen.append((params[0].data_ptr(), step))
+
+    monkeypatch.setattr(train, "grkan_adamw_step", step)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    with pytest.raises(ValueError, match="refused"):
+        opt.step()
+    assert opt.state[a]["step"] == 1 and opt.state[b]["step"] == 0
+    refuse[0] = False
+    opt.step()
+    assert opt.state[a]["step"] == 2 and opt.state[b]["step"] == 1
+    assert seen == [(a.data_ptr(), 1), (a.data_ptr(), 2), (b.data_ptr(), 1)]
