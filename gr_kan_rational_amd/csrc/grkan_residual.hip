@@ -455,27 +455,27 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W, W <= 8 ? 2 : 1) void grkan_r
 __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs a, int columns, int64_t gates) {
     __shared__ double red[2][1024];
     const int t = (int)threadIdx.x;
-    double s = 0.0;
     if ((int)blockIdx.x >= columns) {
-        const int64_t i = (int64_t)((int)blockIdx.x - columns) * 1024 + t;
-        if (i >= gates) return;
-        if (a.gate_wide && a.gate_rows > 0) {
-            const int64_t g = i / a.C, col = i - g * a.C, first = g * a.gate_rows / a.p.walk;
-            const int64_t last = ((g + 1) * a.gate_rows - 1) / a.p.walk;
-            if (first == last) return;  // (written by its walker)
-            const bool before = g * a.gate_rows < first * a.p.walk;
-            s = (double)a.gate_sums[(2 * first + !before) * a.C + col];
+        for (int64_t i = (int64_t)((int)blockIdx.x - columns) * 1024 + t; i < gates; i += (int64_t)((int)gridDim.x - columns) * 1024) {
+            double s = 0.0;
+            if (a.gate_wide && a.gate_rows > 0) {
+                const int64_t g = i / a.C, col = i - g * a.C, first = g * a.gate_rows / a.p.walk;
+                const int64_t last = ((g + 1) * a.gate_rows - 1) / a.p.walk;
+                if (first == last) continue;  // (written by its walker)
+                const bool before = g * a.gate_rows < first * a.p.walk;
+                s = (double)a.gate_sums[(2 * first + !before) * a.C + col];
 #pragma unroll 8
-            for (int64_t w = first + 1; w <= last; ++w) s += (double)a.gate_sums[2 * w * a.C + col];
-        } else {
-            const float *p = a.gate_sums + i * a.gate_rows;
+                for (int64_t w = first + 1; w <= last; ++w) s += (double)a.gate_sums[2 * w * a.C + col];
+            } else {
+                const float *p = a.gate_sums + i * a.gate_rows;
 #pragma unroll 8
-            for (int64_t k = 0; k < a.gate_rows; ++k) s += (double)p[k];
+                for (int64_t k = 0; k < a.gate_rows; ++k) s += (double)p[k];
+            }
+            if (a.gate_bf16)
+                store1(static_cast<uint16_t *>(a.dgate) + i, (float)s);
+            else
+                static_cast<float *>(a.dgate)[i] = (float)s;
         }
-        if (a.gate_bf16)
-            store1(static_cast<uint16_t *>(a.dgate) + i, (float)s);
-        else
-            static_cast<float *>(a.dgate)[i] = (float)s;
         return;
     }
     const int cb = (a.C + 31) / 32, i = (int)blockIdx.x / cb, col = ((int)blockIdx.x - i * cb) * 32 + (t & 31);
@@ -582,11 +582,10 @@ template <> hipError_t launch_residual_backward<io_t>(const ResidualArgs &a, hip
     hipError_t e = a.rows > 0 ? launch_rows(a, s) : hipSuccess;
     if (e != hipSuccess) return e;
     const bool sums = a.dweight || a.dbias || a.dscale || a.dpost_weight || a.dpost_bias;
-    const int columns = sums ? 3 * ((a.C + 31) / 32) : 0;
     const int64_t gates = a.dgate && a.gate_rows != 1 ? a.gates * (a.gate_wide ? a.C : 1) : 0;
-    const int64_t grid = columns + (gates + 1023) / 1024;
-    if (grid > 0) {
-        hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3((unsigned)grid), dim3(1024), 0, s, a, columns, gates);
+    const ResidualSums grid = residual_sums(a.C, sums, gates);
+    if (grid.blocks > 0) {
+        hipLaunchKernelGGL(grkan_residual_sums_kernel, dim3((unsigned)grid.blocks), dim3(1024), 0, s, a, grid.columns, gates);
         e = hipGetLastError();
     }
     return e;

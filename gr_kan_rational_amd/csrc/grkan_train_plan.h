@@ -212,4 +212,17 @@ inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_c
     p->total = p->off_gate + align256(gate);
 }
 
+// The last kernel of the backward, 1,024 threads a workgroup: 32 columns of the three kinds of sums a
+// workgroup, then `gates` values of dgate, a value a thread, which walks on where they are more than a
+// launch holds.
+struct ResidualSums {
+    int32_t columns;
+    int64_t blocks;
+};
+
+inline ResidualSums residual_sums(int64_t C, bool sums, int64_t gates) {
+    const int64_t columns = sums ? 3 * ceil_div(C, 32) : 0, more = ceil_div(gates, 1024);
+    return ResidualSums{(int32_t)columns, columns + (more < kMaxBlocks ? more : kMaxBlocks)};
+}
+
 }  // namespace grkan
