@@ -66,17 +66,17 @@ __device__ static inline float finite_max8(const float (&v)[8]) {
     return m;
 }
 
-// Rows alone: 16 lanes a block; a workgroup takes a column block of 16 kPasses rows,
+// Rows alone: 16 lanes a block; a workgroup takes a column block of kQuantizeRows rows,
 // so that a lane keeps its columns (and the rational's coefficients), all its loads
 // on their way at once.
-constexpr int kPasses = 4;
+constexpr int kPasses = kQuantizeRows / 16;
 
 template <class T, bool VEC, int RAT> __global__ __launch_bounds__(256) void grkan_quantize_rows_kernel(QuantizeArgs a) {
     const int t = (int)threadIdx.x, cl = t & 15, rg = t >> 4;
     const int cb = (a.cols + kBlock8 - 1) / kBlock8;
     const int bc = (int)blockIdx.x % cb, br = (int)blockIdx.x / cb;
     const Columns8<T, VEC, RAT> c(a, bc * kBlock8 + cl * 8);
-    const int64_t r0 = (int64_t)br * (16 * kPasses) + rg;
+    const int64_t r0 = (int64_t)br * kQuantizeRows + rg;
     typename Columns8<T, VEC, RAT>::Raw raw[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) raw[i] = c.fetch(a, r0 + 16 * i);
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void grkan_quantize_tile_kernel(QuantizeArgs a
 template <class T, bool VEC, int RAT> hipError_t launch_kind(const QuantizeArgs &a, hipStream_t s) {
     const int64_t cb = (a.cols + kBlock8 - 1) / kBlock8;
     if (!a.qt && !a.tile) {
-        const int64_t rb = ((int64_t)a.rows + 16 * kPasses - 1) / (16 * kPasses);
+        const int64_t rb = ((int64_t)a.rows + kQuantizeRows - 1) / kQuantizeRows;
         hipLaunchKernelGGL((grkan_quantize_rows_kernel<T, VEC, RAT>), dim3((unsigned)(cb * rb)), dim3(256), 0, s, a);
         return hipGetLastError();
     }

@@ -11,6 +11,9 @@ constexpr int kBlock8 = 128;  // values that share a scale
 
 // ------------------------------------------------------------ quantiser
 
+// Rows of a workgroup that takes rows alone (the others take 128), 128 columns each, 256 threads.
+constexpr int kQuantizeRows = 64;
+
 inline grkan_status_t quantize_shape(int64_t rows, int64_t cols, int64_t ldx, int32_t n_groups, grkan_act_t act,
                                      grkan_dtype_t io) {
     if (io != GRKAN_F32 && io != GRKAN_BF16) return GRKAN_ERR_INVALID_ARG;
@@ -18,8 +21,8 @@ inline grkan_status_t quantize_shape(int64_t rows, int64_t cols, int64_t ldx, in
     if (rows < 0 || cols < 1 || ldx < cols) return GRKAN_ERR_INVALID_ARG;
     if (act == GRKAN_ACT_RATIONAL && (n_groups < 1 || cols % n_groups != 0)) return GRKAN_ERR_INVALID_ARG;
     if (rows > kMaxRows || cols > kMaxWidth || ldx > kMaxWidth) return GRKAN_ERR_UNSUPPORTED;
-    // a workgroup for at least 16 rows of 128 columns, in one launch
-    if (ceil_div(rows, 16) * ceil_div(cols, kBlock8) >= (int64_t(1) << 24)) return GRKAN_ERR_UNSUPPORTED;
+    // one launch, below 2^32 threads
+    if (ceil_div(rows, kQuantizeRows) * ceil_div(cols, kBlock8) >= (int64_t(1) << 24)) return GRKAN_ERR_UNSUPPORTED;
     return GRKAN_OK;
 }
 

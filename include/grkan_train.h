@@ -50,8 +50,8 @@ extern "C" {
  *   scale_t   fp32; column c's block b (of rows) at scale_t[b ld_scale_t + c], with
  *             tile column block c of 128.
  *   rows >= 0 (0 is a no-op), cols >= 1.
- * GRKAN_ERR_UNSUPPORTED: rows >= 2^31 - 256, cols or ldx above 2^22, a misaligned
- * pointer or leading dimension.
+ * GRKAN_ERR_UNSUPPORTED: rows >= 2^31 - 256, cols or ldx above 2^22, 2^24 or more blocks of
+ * 64 rows x 128 columns, a misaligned pointer or leading dimension.
  */
 GRKAN_API grkan_status_t grkan_fp8_quantize(
     const void *x, const float *A, const float *B, void *q, float *scale, void *qt, float *scale_t,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gr_kan_rational_amd import train
-from test_train_cpu import F32, INVALID, lib, matmul  # noqa: F401
+from test_train_cpu import BF16, F32, INVALID, NONE, UNSUPPORTED, lib, matmul, quantize  # noqa: F401
 
 
 def test_kind_of_sums(lib):  # noqa: F811
@@ -53,3 +53,13 @@ def test_a_refused_step_is_not_counted(monkeypatch):
     opt.step()
     assert opt.state[a]["step"] == 2 and opt.state[b]["step"] == 1
     assert seen == [(a.data_ptr(), 1), (a.data_ptr(), 2), (b.data_ptr(), 1)]
+
+
+def test_quantiser_sizes(lib):  # noqa: F811
+    """The header's limit, 2^24 blocks of 64 rows x 128 columns, is the one that is kept: a size below it passes to the
+    next check (no x)."""
+    for rows, cols, want in (((1 << 30) - 64, 128, INVALID), ((1 << 30) - 63, 128, UNSUPPORTED), (1 << 28, 129, INVALID),
+                             ((1 << 29) - 64, 129, INVALID), (1 << 29, 129, UNSUPPORTED), (64, 1 << 22, INVALID)):
+        ld = -(-rows // 16) * 16
+        assert quantize(lib, x=None, A=None, B=None, act=NONE, rows=rows, cols=cols, ldx=cols, ldq=-(-cols // 16) * 16,
+                        ls=rows, ldqt=ld, lst=cols, io=BF16) == want, (rows, cols)
