@@ -135,7 +135,9 @@ typedef enum GRKAN_ENUM_INT {
  *   eps       > 0.
  *   rows >= 0 (0 is a no-op), channels >= 1.
  * Statistics are formed in fp32 about the mean from values held on chip.  A NaN or
- * infinity in a row makes that row's results NaN and touches no other row.
+ * infinity touches no row but its own.  There h is what its formula gives, channel by channel (in
+ * all channels where a post norm's statistics become NaN); z is NaN throughout, but for an rms norm
+ * of infinities without a NaN, whose rstd is 0: NaN at them and 0 elsewhere.
  * GRKAN_ERR_UNSUPPORTED: channels above 16384, rows or gates >= 2^31, a stride above 2^31, a
  * misaligned pointer.
  */
