@@ -376,6 +376,8 @@ extern "C" grkan_status_t grkan_adamw_step(const grkan_adamw_tensor_t *tensors, 
     a.eps = y.eps;
     a.seed = y.seed;
     if (!a.lr_ptr && !a.step_ptr) prepare_adamw(a);
+    // What every workgroup reads: nothing that one of them writes.
+    const Range scalars[] = {{y.lr_ptr, 4}, {y.step_ptr, 8}, {y.grad_scale, 4}};
     // First all launches' overlaps, then the launches.
     for (int pass = 0; pass < 2; ++pass) {
         int64_t groups = 0, block = 0;
@@ -409,8 +411,13 @@ extern "C" grkan_status_t grkan_adamw_step(const grkan_adamw_tensor_t *tensors, 
                 const Range own[] = {{t.param, (size_t)t.n * es}, {t.grad, (size_t)t.n * es},
                                      {t.master, t.master ? (size_t)t.n * 4 : 0}, {t.avg, state}, {t.sq, state},
                                      {t.avg_scale, sc}, {t.sq_scale, sc}};
-                for (const Range &o : own)
-                    if (o.p && o.n) r[n++] = o;
+                const Range gradient = own[1];
+                for (const Range &o : own) {
+                    if (!o.p || !o.n) continue;
+                    r[n++] = o;
+                    for (const Range &s : scalars)
+                        if (o.p != gradient.p && overlap(o, s)) return GRKAN_ERR_INVALID_ARG;
+                }
             }
             AdamwTensor &d = a.t[a.count];
             d = AdamwTensor{t.param, t.grad, t.master, t.avg, t.sq, t.avg_scale, t.sq_scale, t.n};

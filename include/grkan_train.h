@@ -236,7 +236,8 @@ typedef struct {
  * scale.  Codes past n in the last block are zeros.
  *   tensors   host array, read before the call returns.  All on the current device; no
  *             two of their pointers share memory (checked among the tensors of a launch,
- *             48 at a time; GRKAN_ERR_INVALID_ARG, before anything is launched).
+ *             48 at a time; GRKAN_ERR_INVALID_ARG, before anything is launched), and lr_ptr,
+ *             step_ptr and grad_scale lie in nothing that the step writes (likewise).
  *   Pointers are aligned to their element size; avg and sq in 8 bits to 16 bytes.
  *   lr >= 0, 0 <= beta < 1, eps >= 0, weight_decay >= 0, step >= 1 (host values; the
  *   device's are not checked), bits 8 or 32.

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gr_kan_rational_amd import train
-from test_train_cpu import BF16, F32, INVALID, NONE, UNSUPPORTED, lib, matmul, quantize  # noqa: F401
+from test_train_cpu import A8, BF16, F32, INVALID, NONE, UNSUPPORTED, T, adamw, lib, matmul, p, quantize  # noqa: F401
 
 
 def test_kind_of_sums(lib):  # noqa: F811
@@ -63,3 +63,14 @@ def test_quantiser_sizes(lib):  # noqa: F811
         ld = -(-rows // 16) * 16
         assert quantize(lib, x=None, A=None, B=None, act=NONE, rows=rows, cols=cols, ldx=cols, ldq=-(-cols // 16) * 16,
                         ls=rows, ldqt=ld, lst=cols, io=BF16) == want, (rows, cols)
+
+
+def test_adamw_scalars_lie_apart(lib):  # noqa: F811
+    """A scalar on the device that the step itself would write, by any of its tensors, in a first or a later launch."""
+    many = [{k: p(100 + 8 * i + j) for j, k in enumerate(("param", "grad", "master", "avg", "sq"))} for i in range(60)]
+    for name in ("lr_ptr", "step_ptr", "grad_scale"):
+        for at in (p(1), p(1, 1992), p(3, 16), p(3, 3992), p(4), p(5, 800)):
+            assert adamw(lib, [T], hyper={name: at}) == INVALID, (name, at)
+        assert adamw(lib, many, hyper={name: p(100 + 8 * 59)}) == INVALID
+        for at in (p(4), p(5, 8), p(6), p(7, 16)):
+            assert adamw(lib, [dict(T, **A8)], 8, hyper={name: at}) == INVALID, (name, at)
