@@ -527,11 +527,20 @@ __global__ __launch_bounds__(1024) void grkan_residual_sums_kernel(ResidualArgs 
 template <int W, int K, bool VEC, bool POST> hipError_t launch_gate(const ResidualArgs &a, int mode, hipStream_t s) {
     const dim3 grid((unsigned)a.p.blocks), block(W == 1 ? 256 : 64 * W);
     if constexpr (VEC) {
+        // (a wave alone takes no four accesses of these: see residual_plan)
+        constexpr bool planned = !(GRKAN_RESIDUAL_BACKWARD && POST && W == 1 && K == 4);
+        if constexpr (!planned) {
+            if (mode == kShared || mode == kElement) return hipErrorInvalidValue;
+        }
         switch (mode) {
             case kNoGate: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kNoGate>), grid, block, 0, s, a); return hipGetLastError();
             case kNarrow: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kNarrow>), grid, block, 0, s, a); return hipGetLastError();
-            case kShared: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kShared>), grid, block, 0, s, a); return hipGetLastError();
-            case kElement: hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kElement>), grid, block, 0, s, a); return hipGetLastError();
+            case kShared:
+                if constexpr (planned) hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kShared>), grid, block, 0, s, a);
+                return hipGetLastError();
+            case kElement:
+                if constexpr (planned) hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, true, POST, kElement>), grid, block, 0, s, a);
+                return hipGetLastError();
         }
     }
     hipLaunchKernelGGL((GRKAN_RESIDUAL_KERNEL<W, K, VEC, POST, kAny>), grid, block, 0, s, a);

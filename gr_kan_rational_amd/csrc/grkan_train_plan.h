@@ -187,11 +187,14 @@ inline void residual_plan(int64_t rows, int64_t C, int64_t gates, int64_t gate_c
                           bool backward, ResidualPlan *p) {
     *p = ResidualPlan{};
     const int64_t quads = ceil_div(C, 4);
-    // A wave holds up to 256 accesses of a row, 8 waves as many each, else 192: the
-    // backward's sums and rows then fit 256 registers.  With a post norm's and a gate's
-    // for each channel among them a wave alone takes 192 too (37,824 rows of 1,024
-    // channels: 135 us, 232 with 256); 8 waves do not (4,728 rows of 8,192: 380 us, spilled,
-    // against 531 in 16 waves of half the registers).
+    // A wave holds up to 256 accesses of a row, 8 waves as many each, else 192, whatever the
+    // type.  With a post norm's sums and a gate's for each channel in the backward a wave
+    // alone takes 192 too (37,824 rows of 1,024 channels: 135 us, 232 with 256); 8 waves do not
+    // (4,728 rows of 8,192: 380 us, spilled, against 531 in 16 waves of half the registers).
+    // The backward's bf16 rows then fit 256 registers up to 6,144 channels, but for both norms with a
+    // shared gate in three accesses.  What spills, in bytes of scratch a lane: that 44 to 176, in
+    // fp32 144 to 260; fp32 rows of 769 to 1,024 channels 40 to 132; 8 waves of four accesses
+    // up to 684; 16 waves (above 8,192 channels) 192 to 1,292.
     const bool many = backward && post != GRKAN_NORM_NONE && gates > 0 && gate_channels == C;
     const int64_t most = many ? 192 : 256;
     p->waves = 1;
