@@ -235,7 +235,8 @@ class GRKANFp8Linear(torch.autograd.Function):
 
     bf16 x [..., d_in] and W [d_out, d_in], float32 bias.  F(x) and the incoming gradient are quantised in blocks
     of 128 along the axis that each product sums over, W in tiles of 128 x 128 (one set of values for both of its
-    products).  x is kept for the backward, which quantises F(x) along the rows."""
+    products).  x is kept for the backward, which quantises F(x) along the rows: W's gradient sums over at most
+    2^22 of them."""
 
     @staticmethod
     def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, sums="fast"):
@@ -243,6 +244,8 @@ class GRKANFp8Linear(torch.autograd.Function):
             raise ValueError(f"W must be [d_out, {x.shape[-1]}], got {list(W.shape)}")
         if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
             raise TypeError(f"x and W must be bfloat16, got {x.dtype} and {W.dtype}")
+        if ctx.needs_input_grad[1] and x.shape[:-1].numel() > 1 << 22:
+            raise ValueError(f"W's gradient sums over at most {1 << 22} rows, got {x.shape[:-1].numel()}")
         q, s = grkan_fp8_quantize(x, act=act, A=A, B=B, n_groups=n_groups)
         needs = (*ctx.needs_input_grad, False, False, False, False)
         if needs[0] or needs[4] or needs[5]:

@@ -74,3 +74,20 @@ def test_adamw_scalars_lie_apart(lib):  # noqa: F811
         assert adamw(lib, many, hyper={name: p(100 + 8 * 59)}) == INVALID
         for at in (p(4), p(5, 8), p(6), p(7, 16)):
             assert adamw(lib, [dict(T, **A8)], 8, hyper={name: at}) == INVALID, (name, at)
+
+
+def test_linear_refuses_rows_that_its_backward_would(monkeypatch):
+    """W's gradient is a product over the rows, of which one takes 2^22: refused in the forward, unless W asks for
+    none."""
+    def reached(*args, **kw):
+        raise InterruptedError
+
+    monkeypatch.setattr(train, "grkan_fp8_quantize", reached)
+    BF = torch.bfloat16
+    x, few = torch.empty((3, (1 << 22) // 3 + 1, 8), dtype=BF), torch.empty((1 << 22, 8), dtype=BF)
+    W = torch.empty((16, 8), dtype=BF, requires_grad=True)
+    with pytest.raises(ValueError, match="rows"):
+        train.GRKANFp8Linear.apply(x, W)
+    for a, b in ((few, W), (x, W.detach())):
+        with pytest.raises(InterruptedError):
+            train.GRKANFp8Linear.apply(a, b)
