@@ -39,7 +39,7 @@ struct Product8Args {
     int32_t splits, k_split;
     int32_t b_tile;
     bool bf16;
-    bool sums32;             // bf16: block sums in fp32
+    bool cut;                // bf16: blocks summed by the 8-bit matrix instruction, which cuts products
 };
 hipError_t launch_product8(const Product8Plan &p, const Product8Args &a, hipStream_t s);
 

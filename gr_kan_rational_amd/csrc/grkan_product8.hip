@@ -4,18 +4,18 @@
 // A block's products are summed from zero; its sum times both scales is added
 // to the accumulators in fp32.  Two ways to sum a block (the kernels' CUT):
 //
-// one v_mfma_f32_16x16x128_f8f6f4.  It cuts the products of each 8 values of k off at
-// 2^-13 of the largest one's power of two before adding them (measured; the groups of 8
-// are added in fp32; v_mfma_f32_16x16x32_fp8_fp8 does the same).  Results are 1.5e-5
-// to 5e-5 of their norm off, a fortieth of the rounding to bf16 in the mean; a value whose
-// large products cancel may be off by more than its own rounding.
-//
 // the values widened to bf16, exactly, and four v_mfma_f32_16x16x32_bf16, whose sums
-// are fp32's (1e-7), at half the rate: fp32 results, and bf16 ones whose caller asks for it
-// (50,432 x 3,072 from 768: 248 us against 150; 4,096 x 768 from 3,072: 34 and 21.5; 1,003 x
-// 1,501 from 777: 10.9 and 9.1).
+// are fp32's (1e-7);
 //
-// Bound, large products: LDS (of a 256 x 256 tile's step 192 KB are read and 64 KB written,
+// where the caller of a bf16 result asks for it, one v_mfma_f32_16x16x128_f8f6f4, at twice the
+// rate.  It cuts the products of each 8 values of k off at 2^-13 of the largest one's power
+// of two before adding them (measured; the groups of 8 are added in fp32;
+// v_mfma_f32_16x16x32_fp8_fp8 does the same).  Results are 1.5e-5 to 5e-5 of their norm
+// off, a fortieth of the rounding to bf16 in the mean; a value whose large products cancel may
+// be off by more than its own rounding.  50,432 x 3,072 from 768: 150 us against 248; 4,096 x
+// 768 from 3,072: 21.5 and 34; 1,003 x 1,501 from 777: 9.1 and 10.9.
+//
+// Bound, large products, cut sums: LDS (of a 256 x 256 tile's step 192 KB are read and 64 KB written,
 // 2,048 cycles of a CU) and the matrix cores (2,048 cycles) side by side, with the
 // additions (1,360 cycles of a SIMD) between them, at the clock that the power allows
 // (1.95 GHz).  8,192 x 8,192 from 8,192: 460 us, 2,390 TFLOP/s (a library product with
@@ -728,7 +728,7 @@ hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipS
     if (!a.bf16)
         e = launch_type<float, false>(p, a, s);
     else
-        e = a.sums32 ? launch_type<uint16_t, false>(p, a, s) : launch_type<uint16_t, true>(p, a, s);
+        e = a.cut ? launch_type<uint16_t, true>(p, a, s) : launch_type<uint16_t, false>(p, a, s);
     if (e != hipSuccess || p.rows == args.M) return e;
     const int64_t es = a.bf16 ? 2 : 4;
     a = args;
@@ -737,7 +737,7 @@ hipError_t launch_product8(const Product8Plan &p, const Product8Args &args, hipS
     a.a.scale += p.rows * a.a.srow;
     a.c = static_cast<char *>(a.c) + p.rows * a.N * es;
     if (a.residual) a.residual = static_cast<const char *>(a.residual) + p.rows * a.ldr * es;
-    return launch_product8(plan_product8_whole(a.M, a.N, a.K, a.bf16, a.b_tile != 0, a.sums32), a, s);
+    return launch_product8(plan_product8_whole(a.M, a.N, a.K, a.bf16, a.b_tile != 0, a.cut), a, s);
 }
 
 }  // namespace grkan

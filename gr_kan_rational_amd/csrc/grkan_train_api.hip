@@ -93,8 +93,8 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
     grkan_status_t st = product8_shape(m, n, k);
     if (st != GRKAN_OK) return st;
     if (out != GRKAN_F32 && out != GRKAN_BF16) return GRKAN_ERR_INVALID_ARG;
-    const bool sums32 = (b_tile & GRKAN_FP8_SUMS_F32) != 0;
-    b_tile &= ~GRKAN_FP8_SUMS_F32;
+    const bool cut = (b_tile & GRKAN_FP8_SUMS_CUT) != 0;
+    b_tile &= ~GRKAN_FP8_SUMS_CUT;
     if (b_tile != 0 && b_tile != 1) return GRKAN_ERR_INVALID_ARG;
     if (lda < k || ldb < k || (residual && ldr < n)) return GRKAN_ERR_INVALID_ARG;
     if (a_scale_row < 0 || a_scale_block < 0 || b_scale_row < 0 || b_scale_block < 0) return GRKAN_ERR_INVALID_ARG;
@@ -108,7 +108,7 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
         return GRKAN_ERR_UNSUPPORTED;
     if (m == 0) return GRKAN_OK;
     if (!a || !a_scale || !c) return GRKAN_ERR_INVALID_ARG;
-    const Product8Plan p = plan_product8(m, n, k, out == GRKAN_BF16, b_tile != 0, sums32);
+    const Product8Plan p = plan_product8(m, n, k, out == GRKAN_BF16, b_tile != 0, cut);
     const size_t need = align256(p.partials_bytes);
     const int64_t kb = ceil_div(k, kBlock8), nb = b_tile ? ceil_div(n, kBlock8) : n;
     auto scales = [&](int64_t r, int64_t row, int64_t block) { return (size_t)((r - 1) * row + (kb - 1) * block + 1) * 4; };
@@ -136,7 +136,7 @@ extern "C" grkan_status_t grkan_fp8_matmul(const void *a, const float *a_scale, 
     g.K = (int32_t)k;
     g.b_tile = b_tile;
     g.bf16 = out == GRKAN_BF16;
-    g.sums32 = sums32;
+    g.cut = cut;
     return from_hip(launch_product8(p, g, stream));
 }
 

@@ -62,9 +62,9 @@ constexpr double kTimes8[2][3][4] = {{{}, {0.9, 2.1, 2.2, 0.0}, {0.61, 1.5, 0.23
 constexpr double kLaunch8 = 3.5;
 
 // One plan for all rows, and its estimated time.
-inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool sums32 = false,
+inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool cut = false,
                                         double *time = nullptr) {
-    const bool cut = bf16 && !sums32;   // blocks summed by the 8-bit matrix instruction
+    cut = cut && bf16;   // (fp32 results have fp32 sums)
     Product8Plan p{};
     p.rows = M;
     p.splits = 1;
@@ -130,14 +130,14 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
 // own, if that takes less: a last round of few such tiles takes as long as a full one
 // (50,432 x 768 from 3,072: 138 us whole, 141 in tiles of 128, 127 so; 15,443 x 2,112
 // from 3,648: 160, 151 and 141; 50,432 x 3,072 from 768: 156, 165 and 154).
-inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool sums32 = false) {
-    if (M <= kFewRows || !bf16 || sums32 || !b_tile) return plan_product8_whole(M, N, K, bf16, b_tile, sums32);
+inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bool b_tile, bool cut = false) {
+    if (M <= kFewRows || !bf16 || !cut || !b_tile) return plan_product8_whole(M, N, K, bf16, b_tile, cut);
     double whole, rest;
-    Product8Plan p = plan_product8_whole(M, N, K, bf16, b_tile, false, &whole);
+    Product8Plan p = plan_product8_whole(M, N, K, bf16, b_tile, true, &whole);
     const int64_t nb = ceil_div(N, kTiles8[0]), rounds = ceil_div(M, kTiles8[0]) * nb / 256;
     const int64_t rows = rounds * 256 / nb * kTiles8[0];
     if (rows < 1 || M - rows <= kFewRows) return p;
-    const Product8Plan r = plan_product8_whole(M - rows, N, K, bf16, b_tile, false, &rest);
+    const Product8Plan r = plan_product8_whole(M - rows, N, K, bf16, b_tile, true, &rest);
     const double *t = kTimes8[1][0];
     if (kLaunch8 + (double)rounds * (ceil_div(K, kBlock8) * t[1] + t[3]) + rest >= whole) return p;
     p.rows = rows;
@@ -149,11 +149,11 @@ inline Product8Plan plan_product8(int64_t M, int64_t N, int64_t K, bool bf16, bo
     return p;
 }
 
-// Workspace for every type of result (bf16 with fp32 sums takes fp32's plan) and layout of scales.
+// Workspace for every kind of sums and layout of scales (bf16 results with fp32 sums take fp32's plan).
 inline size_t product8_bytes(int64_t M, int64_t N, int64_t K) {
     size_t most = 0;
     for (int i = 0; i < 4; ++i) {
-        const size_t n = plan_product8(M, N, K, (i & 1) != 0, (i & 2) != 0).partials_bytes;
+        const size_t n = plan_product8(M, N, K, true, (i & 2) != 0, (i & 1) != 0).partials_bytes;
         if (n > most) most = n;
     }
     return align256(most);

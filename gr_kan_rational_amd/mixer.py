@@ -71,20 +71,20 @@ class GRKANStack(torch.nn.Module):
 
     and z of the last one is the result.  ``forward(x)`` takes bfloat16 x [..., dim], samples first (of x [dim]
     one).  ``products``
-    is "bf16" or "fp8" (e4m3, a scale for each block of 128; ``sums`` "fast" or "fp32" as ``grkan_fp8_matmul``'s).  ``post`` is "none", "layer" or "rms".  ``scale``
+    is "bf16" or "fp8" (e4m3, a scale for each block of 128; ``sums`` "fp32" or "fast" as ``grkan_fp8_matmul``'s).  ``post`` is "none", "layer" or "rms".  ``scale``
     is the residual scale's first value.  ``drop`` is the rate at which, in training, a sample's branch is left
     out (the others scaled up to match), rising from 0 at the first mixer.  Weights are bfloat16, all else
     float32."""
 
     def __init__(self, depth: int, dim: int, hidden: int, n_groups: int = 8, products: str = "bf16", post: str = "none",
-                 scale: float = 0.1, drop: float = 0.0, device=None, sums: str = "fast"):
+                 scale: float = 0.1, drop: float = 0.0, device=None, sums: str = "fp32"):
         super().__init__()
         if dim % n_groups or hidden % n_groups:
             raise ValueError("dim and hidden must be multiples of n_groups")
         if products not in ("bf16", "fp8"):
             raise ValueError('products must be "bf16" or "fp8"')
-        if sums not in ("fast", "fp32"):
-            raise ValueError('sums must be "fast" or "fp32"')
+        if sums not in ("fp32", "fast"):
+            raise ValueError('sums must be "fp32" or "fast"')
         if not 0.0 <= drop < 1.0:
             raise ValueError("drop must be in [0, 1)")
         self.n_groups, self.products, self.post, self.drop, self.sums = n_groups, products, post, drop, sums

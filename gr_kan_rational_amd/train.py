@@ -25,7 +25,7 @@ F8 = torch.float8_e4m3fn
 GRKAN_NORM_NONE, GRKAN_NORM_LAYER, GRKAN_NORM_RMS = 0, 1, 2
 _NORMS = {"layer": GRKAN_NORM_LAYER, "rms": GRKAN_NORM_RMS}
 _POSTS = {"none": GRKAN_NORM_NONE, **_NORMS}
-GRKAN_FP8_SUMS_F32 = 16
+GRKAN_FP8_SUMS_CUT = 16
 
 _lib = None
 
@@ -177,11 +177,11 @@ def _scale8(t: torch.Tensor, name: str, rows, k: int, dev):
     return t.stride()
 
 
-_SUMS = {"fast": 0, "fp32": GRKAN_FP8_SUMS_F32}
+_SUMS = {"fp32": 0, "fast": GRKAN_FP8_SUMS_CUT}
 
 
 def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, bias=None,
-                     residual=None, dtype=torch.bfloat16, out=None, workspace=None, stream=None, sums: str = "fast"):
+                     residual=None, dtype=torch.bfloat16, out=None, workspace=None, stream=None, sums: str = "fp32"):
     """a b^T + bias + residual [m, n] in ``dtype`` (bfloat16 or float32) for e4m3 a [m, k], b [n, k]
     (``grkan_fp8_matmul``).
 
@@ -189,8 +189,8 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
     128 tiles (if n / 128 rounded up is n itself, n = 1, the two are the same); any strides, expanded ones
     too.  The codes' rows start at multiples of 16 bytes, as the quantiser's do.  float32 ``bias`` [n];
     ``residual`` [m, n] in ``dtype``; ``out`` may be the residual itself.  ``sums``: how the products of a block
-    are summed for a bfloat16 result, "fp32", or "fast": twice the rate, products cut off at 2^-13 of the largest
-    of each 8, which values whose large products cancel can show.  A float32 result has fp32 sums always."""
+    are summed, "fp32", or for a bfloat16 result "fast": twice the rate, products cut off at 2^-13 of the largest of
+    each 8, which values whose large products cancel can show (a float32 result's sums stay fp32's)."""
     if sums not in _SUMS:
         raise ValueError(f"sums must be one of {sorted(_SUMS)}")
     _on_gpu(a)
@@ -239,7 +239,7 @@ class GRKANFp8Linear(torch.autograd.Function):
     2^22 of them."""
 
     @staticmethod
-    def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, sums="fast"):
+    def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, sums="fp32"):
         if W.dim() != 2 or W.shape[1] != x.shape[-1]:
             raise ValueError(f"W must be [d_out, {x.shape[-1]}], got {list(W.shape)}")
         if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:

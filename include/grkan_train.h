@@ -68,17 +68,17 @@ GRKAN_API grkan_status_t grkan_fp8_quantize(
  * A block's products are summed on the matrix cores; its sum times
  * (a_scale b_scale), a product that has to be in fp32's range, is added in fp32, and c
  * is rounded once.  How a block is summed:
- *     fp32 c, or GRKAN_FP8_SUMS_F32: in fp32 (1e-7 of the sum of the products' sizes);
- *     bf16 c otherwise: the matrix cores cut the products of each 8 values of k off at
- *     2^-13 of the largest one's power of two.  Over a result that is a fortieth of the rounding
- *     to bf16; a single value whose large products cancel may be off by up to 7 x 2^-13
- *     of the largest of each 8, which can exceed its own rounding.  Twice the rate.
+ *     in fp32 (1e-7 of the sum of the products' sizes);
+ *     or, bf16 c with GRKAN_FP8_SUMS_CUT, twice the rate: the matrix cores cut the products
+ *     of each 8 values of k off at 2^-13 of the largest one's power of two.  Over a result
+ *     that is a fortieth of the rounding to bf16; a single value whose large products cancel may
+ *     be off by up to 7 x 2^-13 of the largest of each 8, which can exceed its own rounding.
  *   a, b      e4m3 [m][k], [n][k]: 16-byte aligned, lda, ldb multiples of 16 and
  *             >= k.  Bytes past k, to the next multiple of 16, are read and not used.
  *   a_scale   fp32, any finite values: (m, kb) at m a_scale_row + kb a_scale_block;
  *             a stride may be 0 (one scale for all).
  *   b_scale   likewise; with b_tile (0 or 1) row block n / 128 in the place of n.
- *   b_tile    0 or 1, and GRKAN_FP8_SUMS_F32 or'ed in for fp32 sums of a bf16 c.
+ *   b_tile    0 or 1, and GRKAN_FP8_SUMS_CUT or'ed in (without effect on an fp32 c).
  *   bias      fp32 [n], or NULL.
  *   residual  dtype out [m][n], row r at residual + r ldr (ldr >= n), or NULL.
  *   c         dtype out (fp32 or bf16) [m][n], dense; may be the residual itself
@@ -89,7 +89,7 @@ GRKAN_API grkan_status_t grkan_fp8_quantize(
  * scale's row stride above 2^20, its block stride above 2^31,
  * m x n past the launch limits, a misaligned pointer or leading dimension.
  */
-#define GRKAN_FP8_SUMS_F32 16
+#define GRKAN_FP8_SUMS_CUT 16
 
 GRKAN_API grkan_status_t grkan_fp8_matmul(
     const void *a, const float *a_scale, const void *b, const float *b_scale, const float *bias,

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 BF = torch.bfloat16
 F8 = torch.float8_e4m3fn
-KINDS = {"f32": (torch.float32, "fast"), "sums": (BF, "fp32"), "cut": (BF, "fast")}
+KINDS = {"f32": (torch.float32, "fp32"), "sums": (BF, "fp32"), "cut": (BF, "fast")}
 
 
 @pytest.fixture(scope="module")

@@ -35,20 +35,21 @@ def test_sums_that_cancel(gk, shape):
     s = [torch.ones((t.shape[0], ref.ceil(k, 128)), device=DEV) for t in (a, b)]
     want = torch.full((m, n), 2.0 ** -6 * ((k + 5) // 8), device=DEV)
     for dtype in (BF, torch.float32):
-        got = gk.grkan_fp8_matmul(q[0], s[0], q[1], s[1], dtype=dtype, sums="fp32")
-        assert torch.equal(got, want.to(dtype))
-    cut = gk.grkan_fp8_matmul(q[0], s[0], q[1], s[1])
+        assert torch.equal(gk.grkan_fp8_matmul(q[0], s[0], q[1], s[1], dtype=dtype), want.to(dtype))
+    assert torch.equal(gk.grkan_fp8_matmul(q[0], s[0], q[1], s[1], dtype=torch.float32, sums="fast"), want)
+    cut = gk.grkan_fp8_matmul(q[0], s[0], q[1], s[1], sums="fast")
     ref.check("cut", cut, *ref.matmul(q[0], s[0], q[1], s[1], False))
 
 
-def test_linear_with_fp32_sums(gk):
+def test_linear_with_either_sums(gk):
     """The layer's three products take the kind of sums: each result is that of the products by themselves."""
     gen = torch.Generator(device=DEV).manual_seed(5)
     x = torch.randn((70, 200), generator=gen, device=DEV).to(BF).requires_grad_()
     W = (torch.randn((90, 200), generator=gen, device=DEV) * 0.1).to(BF).requires_grad_()
     dy = torch.randn((70, 90), generator=gen, device=DEV).to(BF)
-    for sums in ("fp32", "fast"):
-        y = gk.GRKANFp8Linear.apply(x, W, None, "none", None, None, 8, sums)
+    for sums in ("fp32", "fast", None):
+        y = gk.GRKANFp8Linear.apply(x, W, *((None, "none", None, None, 8, sums) if sums else ()))
+        sums = sums or "fp32"
         dx, dW = torch.autograd.grad(y, (x, W), dy)
         q, s, qt, st = gk.grkan_fp8_quantize(x.detach(), "both")
         wq, ws, wt, wst = gk.grkan_fp8_quantize(W.detach(), "both", tile=True)
@@ -58,12 +59,12 @@ def test_linear_with_fp32_sums(gk):
         assert torch.equal(dW, gk.grkan_fp8_matmul(gt, gst, qt, st, sums=sums))
 
 
-def test_stack_with_fp32_sums(gk):
+def test_stack_with_either_sums(gk):
     from gr_kan_rational_amd.mixer import GRKANStack
 
     torch.manual_seed(3)
-    one = GRKANStack(2, 64, 128, products="fp8", device=DEV)
-    two = GRKANStack(2, 64, 128, products="fp8", sums="fp32", device=DEV)
+    one = GRKANStack(2, 64, 128, products="fp8", sums="fast", device=DEV)
+    two = GRKANStack(2, 64, 128, products="fp8", device=DEV)
     two.load_state_dict(one.state_dict())
     x = torch.randn((3, 20, 64), device=DEV).to(BF)
     a, b = one(x).detach().double(), two(x).detach().double()

@@ -14,10 +14,10 @@ static std::string one(const Product8Plan &p, long m, long n) {
     return std::to_string(p.tile) + (p.splits > 1 ? " split" : "") + (tiles > most ? " several" : "");
 }
 static std::string kind(long m, long n, long k, int type, int tile) {
-    const bool bf16 = type > 0, sums32 = type == 1;
-    const Product8Plan p = plan_product8(m, n, k, bf16, tile, sums32);
+    const bool bf16 = type > 0, cut = type == 2;
+    const Product8Plan p = plan_product8(m, n, k, bf16, tile, cut);
     std::string s = std::to_string(type) + (tile ? " tiles " : " columns ") + one(p, p.rows, n);
-    if (p.rows < m) s += ", then " + one(plan_product8_whole(m - p.rows, n, k, bf16, tile, sums32), m - p.rows, n);
+    if (p.rows < m) s += ", then " + one(plan_product8_whole(m - p.rows, n, k, bf16, tile, cut), m - p.rows, n);
     return s;
 }
 """)

@@ -10,7 +10,7 @@ from test_train_cpu import A8, BF16, F32, INVALID, NONE, UNSUPPORTED, T, adamw, 
 def test_kind_of_sums(lib):  # noqa: F811
     """One of two names; in the C ABI a flag beside b_tile, which does not hide other values of it."""
     assert open(__file__.replace("tests/test_train_checks_cpu.py", "include/grkan_train.h")).read().count(
-        f"#define GRKAN_FP8_SUMS_F32 {train.GRKAN_FP8_SUMS_F32}\n") == 1
+        f"#define GRKAN_FP8_SUMS_CUT {train.GRKAN_FP8_SUMS_CUT}\n") == 1
     for tile in (18, 19, 15, 32, -1, -16):
         assert matmul(lib, tile=tile) == INVALID
     assert matmul(lib, tile=17, c=None) == INVALID and matmul(lib, tile=16, m=0, a=None, sa=None, c=None, out=F32) == 0
