@@ -4,8 +4,8 @@
 // The tensors' addresses travel as the kernel's arguments; a workgroup takes 4,096
 // elements of one tensor, which it finds from the first workgroups of all (one per
 // lane).  Bound: memory with 32-bit states (57 million parameters in bf16 with masters
-// 302 us, 5.3 TB/s); with 8-bit ones vector arithmetic beside it, 100 instructions a value
-// (division, root, hash, two roundings; busy 0.78), 220 us, 4.1 TB/s.
+// 332 us, 5.1 TB/s); with 8-bit ones vector arithmetic beside it, 105 instructions a value
+// (division, root, hash, two roundings; busy 0.73), 246 us, 4.2 TB/s.
 #include "grkan_adamw.h"
 
 #include <type_traits>

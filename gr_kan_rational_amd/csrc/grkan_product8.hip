@@ -163,9 +163,13 @@ template <int BM, int BN> struct Tile8 {
 // A block of k at a time through two LDS stages.  T: the result's type.  A 256 x 256
 // tile in 8 waves of 128 x 64 leaves each byte of LDS the most products that the
 // accumulators' registers allow (128 of 256); 128 x 128 and 64 x 64, 4 waves, give two and
-// four workgroups to a CU where there are fewer tiles.  fp32 sums: the widening, 128
-// conversions beside 64 matrix instructions in a step of a wave, is the bound (3,072 x 768
-// from 50,432 in 7 splits: 256 us, 930 TFLOP/s).
+// four workgroups to a CU where there are fewer tiles.  The 256 x 256 tile spills 21 vector and 69 scalar
+// registers (88 bytes a lane).  fp32 sums: a step of a wave is 128 conversions, 64 matrix
+// instructions and 64 to 128 additions, which follow one another more than they overlap: matrix cores
+// busy 0.46 (3,072 x 768 from 50,432 in 7 splits: 256 us, 930 TFLOP/s).  Not the
+// conversions alone: a form of it with every conversion between two matrix instructions took 249,
+// and one with 32 x 32 x 16 instructions and codes read a step ahead 255, of which 208 were left
+// without the additions, 221 without the fetches and no less without the conversions.
 //
 // In the middle of a step every wave holds what is left of it in registers: a barrier
 // there covers both that and the arrival of the next step, and the fetches of the

@@ -76,8 +76,9 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
     }
     // The tile and the number of k splits with the least estimated time.  Splits add a
     // launch, a write and a read of their sums.  Fitted to 603 timings of
-    // 58 shapes: the choice is 1.3% from the best one in the mean, 19% at most
-    // (50,432 x 3,072 from 768, tiles of 256 / 128 / 64: 185 / 182 / 240 us; 8,192 x
+    // 58 shapes: the choice is 1.3% from the best one in the mean, 19% at most, of bf16
+    // results with fp32 sums, planned as fp32 ones, 2.0% and 24%
+    // (cut sums, 50,432 x 3,072 from 768, tiles of 256 / 128 / 64: 185 / 182 / 240 us; 8,192 x
     // 8,192 from 8,192: 537 / 656 / 1,260; 197 x 768 from 3,072 in tiles of 64: 9.7 us
     // in 4 splits, 20 in one).  256 x 256 is for sums by the 8-bit instruction and a
     // scale for each tile of b alone: it has no registers for the wider products or a scale a column.
@@ -106,7 +107,7 @@ inline Product8Plan plan_product8_whole(int64_t M, int64_t N, int64_t K, bool bf
         }
     }
     // The kernel of few rows, as long as a CU has one workgroup, with the fewest rows for
-    // which that is so (160 x 768 from 3,072 7.2 us, in tiles 9.7; 256 x 512 from 2,048 5.5
+    // which that is so (cut sums, 160 x 768 from 3,072 7.2 us, in tiles 9.7; 256 x 512 from 2,048 5.5
     // and 9.3; 197 x 768 from 3,072 10.4 and 9.7).
     static const double kFewTimes[3][2] = {{2.6, 0.105}, {2.8, 0.185}, {3.0, 0.31}};
     for (int i = 0; i < 3; ++i) {
