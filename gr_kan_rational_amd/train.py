@@ -238,14 +238,19 @@ class GRKANFp8Linear(torch.autograd.Function):
     products).  x is kept for the backward, which quantises F(x) along the rows: W's gradient sums over at most
     2^22 of them."""
 
+    @classmethod
+    def apply(cls, x, W, *args):
+        # (inside forward the grad mode is off and needs_input_grad does not know of it)
+        if torch.is_grad_enabled() and W.requires_grad and x.shape[:-1].numel() > 1 << 22:
+            raise ValueError(f"W's gradient sums over at most {1 << 22} rows, got {x.shape[:-1].numel()}")
+        return super().apply(x, W, *args)
+
     @staticmethod
     def forward(ctx, x, W, bias=None, act="none", A=None, B=None, n_groups=8, sums="fp32"):
         if W.dim() != 2 or W.shape[1] != x.shape[-1]:
             raise ValueError(f"W must be [d_out, {x.shape[-1]}], got {list(W.shape)}")
         if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
             raise TypeError(f"x and W must be bfloat16, got {x.dtype} and {W.dtype}")
-        if ctx.needs_input_grad[1] and x.shape[:-1].numel() > 1 << 22:
-            raise ValueError(f"W's gradient sums over at most {1 << 22} rows, got {x.shape[:-1].numel()}")
         q, s = grkan_fp8_quantize(x, act=act, A=A, B=B, n_groups=n_groups)
         needs = (*ctx.needs_input_grad, False, False, False, False)
         if needs[0] or needs[4] or needs[5]:

@@ -91,3 +91,5 @@ def test_linear_refuses_rows_that_its_backward_would(monkeypatch):
     for a, b in ((few, W), (x, W.detach())):
         with pytest.raises(InterruptedError):
             train.GRKANFp8Linear.apply(a, b)
+    with torch.no_grad(), pytest.raises(InterruptedError):
+        train.GRKANFp8Linear.apply(x, W)
