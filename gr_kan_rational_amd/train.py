@@ -219,8 +219,7 @@ def grkan_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
         ws, wsp, wsn = _space(workspace, need, dev)
         st = lib.grkan_fp8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(bias),
                                   _ptr(residual), c.data_ptr(), m, n, k, lda, ar, ab, ldb, br, bb,
-                                  int(tile) | _SUMS[sums], ldr,
-                                  _IO[dtype], wsp, wsn, handle)
+                                  int(tile) | _SUMS[sums], ldr, _IO[dtype], wsp, wsn, handle)
         if st != GRKAN_OK:
             raise GRKANError(st, "grkan_fp8_matmul")
         _written(out)
@@ -524,12 +523,12 @@ def grkan_adamw_step(params, grads, avgs, sqs, *, step, lr, beta1: float = 0.9, 
 
     ``params`` and ``grads`` are contiguous float32 or bfloat16 tensors (a gradient in its parameter's dtype);
     ``masters``: the weights in float32 for some (None for the others), their parameter then being the rounded
-    copy; where it is not, a program has written it since, and the parameter's value is stepped.  ``avgs`` and ``sqs`` are float32 tensors of the parameters' sizes, or, with ``avg_scales`` and
-    ``sq_scales`` (float32, one for each 128 values), float8_e4m3fn codes of the first moment and of the second
-    moment's root, whole blocks of 128 (``grkan_adamw_state`` makes them).  ``step`` (from 1) and ``lr`` are numbers,
-    or one int64 and one float32 value on the device, which the kernel reads (and a captured graph reads again at
-    each replay).  ``grad_scale``: one float32 value on the device that every gradient is multiplied with.
-    ``seed``: of the 8-bit states' rounding.
+    copy; where it is not, a program has written it since, and the parameter's value is stepped.  ``avgs`` and
+    ``sqs`` are float32 tensors of the parameters' sizes, or, with ``avg_scales`` and ``sq_scales`` (float32, one
+    for each 128 values), float8_e4m3fn codes of the first moment and of the second moment's root, whole blocks of
+    128 (``grkan_adamw_state`` makes them).  ``step`` (from 1) and ``lr`` are numbers, or one int64 and one float32
+    value on the device, which the kernel reads (and a captured graph reads again at each replay).  ``grad_scale``:
+    one float32 value on the device that every gradient is multiplied with.  ``seed``: of the 8-bit states' rounding.
 
     What is written counts as modified in place: a backward that still needs it raises (a graph's replays
     write without being noticed)."""
